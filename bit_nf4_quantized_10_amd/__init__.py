@@ -7,6 +7,7 @@ not built, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -20,14 +21,15 @@ NF4_COMPUTE_BF16, NF4_COMPUTE_F16 = 0, 1
 KERNEL_IDS = {
     "quant_pass1": 0, "quant_mean": 1, "quant_pass2": 2, "dequant": 3, "lora_down": 4,
     "fwd_gemm": 5, "fwd_gemv": 6, "bwd_dz": 7, "bwd_dx": 8, "bwd_colsum": 9, "dequant_bf16": 10,
-    "reduce": 11, "merge": 12, "sgd": 13,
+    "reduce": 11, "merge": 12, "sgd": 13, "act8_encode": 14, "act8_decode": 15,
 }
 C_FUNCTIONS = [
     "nf4_sizes", "nf4_quantize", "nf4_dequantize", "qlora_workspace_bytes",
     "qlora_linear_fwd", "qlora_linear_bwd", "nf4_status_read", "qlora_timer_enable",
     "qlora_timer_read", "qlora_merge", "qlora_sgd_step", "qlora_grouped_workspace_bytes",
     "qlora_grouped_fwd", "qlora_grouped_bwd", "qlora_linear_fwd_dt", "qlora_linear_bwd_dt", "qlora_sgd_step_dt",
-    "qlora_linear_fwd_noalloc", "qlora_grouped_fwd_dt", "qlora_grouped_bwd_dt", "nf4_error_string",
+    "qlora_linear_fwd_noalloc", "qlora_grouped_fwd_dt", "qlora_grouped_bwd_dt",
+    "act8_encode", "act8_decode", "qlora_linear_bwd_ex", "nf4_error_string",
 ]
 NF4_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 
@@ -41,6 +43,10 @@ class NF4Error(RuntimeError):
 class _State(ctypes.Structure):
     _fields_ = [("numel", ctypes.c_int64), ("codes", ctypes.c_void_p), ("qabsmax", ctypes.c_void_p),
                 ("absmax2", ctypes.c_void_p), ("offset", ctypes.c_void_p), ("absmax", ctypes.c_void_p)]
+
+
+class _Act8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("absmax", ctypes.c_void_p)]
 
 
 _lib = None
@@ -85,6 +91,11 @@ def lib() -> ctypes.CDLL:
         L.qlora_linear_fwd_noalloc.argtypes = [i64, i64, i64, i64, vp, sp, vp, vp, ctypes.c_float, vp, vp, vp]
         L.qlora_grouped_fwd_dt.argtypes = [ctypes.c_int] + L.qlora_grouped_fwd.argtypes
         L.qlora_grouped_bwd_dt.argtypes = [ctypes.c_int] + L.qlora_grouped_bwd.argtypes
+        a8 = ctypes.POINTER(_Act8)
+        L.act8_encode.argtypes = [ctypes.c_int, i64, i64, vp, i64, a8, vp]
+        L.act8_decode.argtypes = [ctypes.c_int, i64, i64, a8, vp, i64, vp]
+        L.qlora_linear_bwd_ex.argtypes = [ctypes.c_int, ctypes.c_int, i64, i64, i64, i64, vp, vp, a8, vp, sp, vp, vp,
+                                          ctypes.c_float, vp, vp, vp, vp, i64, vp]
         L.nf4_error_string.argtypes = [ctypes.c_int]
         L.nf4_error_string.restype = ctypes.c_char_p
         for name in C_FUNCTIONS[:-1]:
@@ -115,6 +126,121 @@ def _require_cuda(t, name: str, dtype=None) -> None:
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+@contextlib.contextmanager
+def _on(t, stream=None, *others):
+    """The scope in which a call on tensor t allocates and launches: t's
+    device current and, where one is given, `stream` current, so that outputs
+    and workspaces belong to the stream that the kernels run on.  Yields that
+    stream's handle.  The other tensors must be on the same device."""
+    import torch
+    for o in others:
+        if o is not None and o.device != t.device:
+            raise ValueError(f"tensors on {t.device} and {o.device}")
+    if stream is None:
+        if t.device.index == torch.cuda.current_device():
+            yield torch.cuda.current_stream().cuda_stream
+        else:
+            with torch.cuda.device(t.device):
+                yield torch.cuda.current_stream().cuda_stream
+        return
+    if stream.device != t.device:
+        raise ValueError(f"tensors on {t.device}, stream on {stream.device}")
+    with torch.cuda.stream(stream):
+        yield stream.cuda_stream
+
+
+def _require_shape(t, name: str, *shape) -> None:
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {' x '.join(map(str, shape))}, got {tuple(t.shape)}")
+
+
+@dataclass
+class Act8:
+    """An M x K matrix of activations kept in 8 bits (device tensors): int8
+    codes and, per row and block of 64 columns, the largest magnitude in the
+    activations' 16-bit type.  Made by act8_encode."""
+    codes: "torch.Tensor"     # int8, M x K
+    absmax: "torch.Tensor"    # bf16 or fp16, M x ceil(K / 64)
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+    @property
+    def dtype(self):
+        return self.absmax.dtype
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def c_struct(self) -> _Act8:
+        return _Act8(self.codes.data_ptr(), self.absmax.data_ptr())
+
+    def check(self, name: str) -> None:
+        import torch
+        _require_cuda(self.codes, f"{name}.codes", torch.int8)
+        if self.codes.dim() != 2:
+            raise ValueError(f"{name}.codes must be a matrix")
+        _require_cuda(self.absmax, f"{name}.absmax", _compute_dtype(self.absmax))
+        _require_shape(self.absmax, f"{name}.absmax", self.codes.shape[0], (self.codes.shape[1] + 63) // 64)
+        if self.absmax.device != self.codes.device:
+            raise ValueError(f"{name}'s tensors must be on one device")
+
+
+def empty_act8(rows: int, cols: int, dtype, device="cuda") -> Act8:
+    import torch
+    return Act8(torch.empty(rows, cols, dtype=torch.int8, device=device),
+                torch.empty(rows, (cols + 63) // 64, dtype=dtype, device=device))
+
+
+def _require_matrix(t, name: str) -> int:
+    """A device matrix of the compute types whose rows are contiguous; returns
+    its row stride."""
+    _compute_dtype(t)
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a matrix with contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def act8_encode(X, out: Act8 | None = None, stream=None) -> Act8:
+    """Keep the bf16 or fp16 matrix X (M x K, K % 8 == 0; rows may be strided
+    by a multiple of 8 elements) in 8 bits."""
+    ld = _require_matrix(X, "X")
+    M, K = X.shape
+    if out is not None:
+        out.check("out")
+        _require_shape(out.codes, "out.codes", M, K)
+        _require_cuda(out.absmax, "out.absmax", X.dtype)
+    with _on(X, stream, None if out is None else out.codes) as s:
+        if out is None:
+            out = empty_act8(M, K, X.dtype, X.device)
+        st = out.c_struct()
+        _check(lib().act8_encode(_COMPUTE[X.dtype], M, K, X.data_ptr(), ld, ctypes.byref(st), s), "act8_encode")
+    return out
+
+
+def act8_decode(kept: Act8, out=None, stream=None):
+    """The M x K values that `kept` stands for, in its 16-bit type."""
+    import torch
+    kept.check("kept")
+    M, K = kept.shape
+    if out is not None:
+        if out.dtype != kept.dtype:
+            raise ValueError(f"out must be {kept.dtype}, got {out.dtype}")
+        _require_matrix(out, "out")
+        _require_shape(out, "out", M, K)
+    with _on(kept.codes, stream, out) as s:
+        if out is None:
+            out = torch.empty(M, K, dtype=kept.dtype, device=kept.device)
+        st = kept.c_struct()
+        _check(lib().act8_decode(_COMPUTE[kept.dtype], M, K, ctypes.byref(st), out.data_ptr(),
+                                 _require_matrix(out, "out"), s), "act8_decode")
+    return out
 
 
 @dataclass
@@ -383,10 +509,14 @@ def qlora_linear_fwd_noalloc(X, state: NF4State, A, B, c: float, K: int, N: int,
 
 
 def qlora_linear_bwd(G, X, Z, state: NF4State, A, B, c: float, K: int, N: int, need_dx: bool = True,
-                     dX=None, dA=None, dB=None, workspace=None, stream=None):
+                     dX=None, dA=None, dB=None, workspace=None, stream=None, grad_dtype=None):
     """dZ = c G Bᵀ, dA = Xᵀ dZ, dB = c Zᵀ G, dX = G Ŵᵀ + dZ Aᵀ.  Returns (dX, dA, dB).
-    Z = None recomputes Z = X A in the workspace."""
+    Z = None recomputes Z = X A in the workspace.  X may be an Act8 (kept in 8
+    bits; Z is then required).  grad_dtype: of dA and dB, float32 (the default)
+    or X's dtype."""
     import torch
+    if isinstance(X, Act8) or grad_dtype not in (None, torch.float32):
+        return _linear_bwd_ex(G, X, Z, state, A, B, c, K, N, need_dx, dX, dA, dB, workspace, stream, grad_dtype)
     M, r = X.shape[0], A.shape[1]
     dt = _compute_dtype(X)
     for t, n in ((G, "G"), (X, "X"), (Z, "Z"), (A, "A"), (B, "B")):
@@ -407,6 +537,71 @@ def qlora_linear_bwd(G, X, Z, state: NF4State, A, B, c: float, K: int, N: int, n
                                      _ptr(dX if need_dx else None), dA.data_ptr(), dB.data_ptr(),
                                      workspace.data_ptr(), workspace.numel(), _stream(stream)), "qlora_linear_bwd_dt")
     return (dX if need_dx else None), dA, dB
+
+
+def _grad_code(grad_dtype, dt) -> tuple:
+    """(torch dtype, NF4_AB_* code) of adapter gradients for compute type dt."""
+    import torch
+    if grad_dtype in (None, torch.float32):
+        return torch.float32, NF4_AB_F32
+    if grad_dtype != dt:
+        raise ValueError(f"grad_dtype is float32 or the compute type {dt}, got {grad_dtype}")
+    return dt, NF4_AB_F16 if dt == torch.float16 else NF4_AB_BF16
+
+
+def _out(t, name: str, dtype, device, *shape):
+    """A given output, checked, or a new one."""
+    import torch
+    if t is None:
+        return torch.empty(*shape, dtype=dtype, device=device)
+    _require_cuda(t, name, dtype)
+    _require_shape(t, name, *shape)
+    return t
+
+
+def _workspace(workspace, need: int, device):
+    import torch
+    return torch.empty(max(need, 256), dtype=torch.uint8, device=device) if workspace is None else workspace
+
+
+def _kept_or_dense(X, M: int, K: int, name: str):
+    """(device pointer or None, _Act8 or None) of an input given in 16 or 8 bits."""
+    if isinstance(X, Act8):
+        X.check(name)
+        _require_shape(X.codes, f"{name}.codes", M, K)
+        return None, X.c_struct()
+    _require_shape(X, name, M, K)
+    return X.data_ptr(), None
+
+
+def _ref(struct):
+    return None if struct is None else ctypes.byref(struct)
+
+
+def _linear_bwd_ex(G, X, Z, state, A, B, c, K, N, need_dx, dX, dA, dB, workspace, stream, grad_dtype):
+    M, r = X.shape[0], A.shape[1]
+    dt = _compute_dtype(X)
+    for t, n, shape in ((G, "G", (M, N)), (Z, "Z", (M, r)), (A, "A", (K, r)), (B, "B", (r, N))):
+        if t is not None or n != "Z":
+            _require_cuda(t, n, dt)
+            _require_shape(t, n, *shape)
+    if not isinstance(X, Act8):
+        _require_cuda(X, "X", dt)
+    elif Z is None:
+        raise ValueError("Z is required where X is kept in 8 bits")
+    xp, x8 = _kept_or_dense(X, M, K, "X")
+    gdt, gcode = _grad_code(grad_dtype, dt)
+    with _on(G, stream, X, Z, A, B, state.codes, dX, dA, dB, workspace) as s:
+        dX = _out(dX, "dX", dt, G.device, M, K) if need_dx else None
+        dA = _out(dA, "dA", gdt, G.device, K, r)
+        dB = _out(dB, "dB", gdt, G.device, r, N)
+        ws = _workspace(workspace, qlora_workspace_bytes(M, K, N, r)[1], G.device)
+        st = state.c_struct()
+        _check(lib().qlora_linear_bwd_ex(_COMPUTE[dt], gcode, M, K, N, r, G.data_ptr(), xp, _ref(x8), _ptr(Z),
+                                         ctypes.byref(st), A.data_ptr(), B.data_ptr(), float(c), _ptr(dX),
+                                         dA.data_ptr(), dB.data_ptr(), ws.data_ptr(), ws.numel(), s),
+               "qlora_linear_bwd_ex")
+    return dX, dA, dB
 
 
 def qlora_timer_enable(kernel: str, enable: bool = True) -> None:

@@ -208,6 +208,53 @@ int qlora_linear_fwd(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t*
   return qlora_linear_fwd_dt(NF4_COMPUTE_BF16, M, K, N, r, X, W, A, B, c, Y, Z, workspace, workspace_bytes, stream);
 }
 
+// dA / dB element type: fp32, or the layer's own 16-bit type.
+static bool grad_dtype_ok(int grad_dtype, int compute_dtype) {
+  return grad_dtype == NF4_AB_F32 || grad_dtype == (compute_dtype == NF4_COMPUTE_F16 ? NF4_AB_F16 : NF4_AB_BF16);
+}
+
+static bool act8_ok(const act8_t* a) {
+  return a != nullptr && a->codes != nullptr && a->absmax != nullptr && aligned16(a->codes) &&
+         (reinterpret_cast<uintptr_t>(a->absmax) & 1u) == 0;
+}
+
+static bool act8_shape_ok(int dtype, int64_t rows, int64_t cols, const void* X, int64_t ld) {
+  return dtype_ok(dtype) && rows >= 1 && cols >= 8 && cols % 8 == 0 && ld >= cols && ld % 8 == 0 &&
+         rows < kMaxOperandElems / 8 && ld < kMaxOperandElems && rows * ld < kMaxOperandElems && X != nullptr &&
+         aligned16(X);
+}
+
+int act8_encode(int dtype, int64_t rows, int64_t cols, const uint16_t* X, int64_t ld, const act8_t* out, void* stream) {
+  if (!act8_shape_ok(dtype, rows, cols, X, ld) || !act8_ok(out)) return NF4_EINVAL;
+  hipError_t e = qn::launch_act8_encode(rows, cols, X, ld, out->codes, out->absmax, static_cast<hipStream_t>(stream), dtype);
+  return e == hipSuccess ? NF4_OK : NF4_EHIP;
+}
+
+int act8_decode(int dtype, int64_t rows, int64_t cols, const act8_t* in, uint16_t* X, int64_t ld, void* stream) {
+  if (!act8_shape_ok(dtype, rows, cols, X, ld) || !act8_ok(in)) return NF4_EINVAL;
+  hipError_t e = qn::launch_act8_decode(rows, cols, in->codes, in->absmax, X, ld, static_cast<hipStream_t>(stream), dtype);
+  return e == hipSuccess ? NF4_OK : NF4_EHIP;
+}
+
+int qlora_linear_bwd_ex(int compute_dtype, int grad_dtype, int64_t M, int64_t K, int64_t N, int64_t r,
+                        const uint16_t* G, const uint16_t* X, const act8_t* X8, const uint16_t* Z,
+                        const nf4_state_t* W, const uint16_t* A, const uint16_t* B, float c, uint16_t* dX, void* dA,
+                        void* dB, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!dtype_ok(compute_dtype) || !grad_dtype_ok(grad_dtype, compute_dtype)) return NF4_EINVAL;
+  if (!layer_shape_ok(M, K, N, r) || !state_ok(W) || W->numel != K * N) return NF4_EINVAL;
+  if ((X == nullptr) == (X8 == nullptr) || (X8 != nullptr && (!act8_ok(X8) || Z == nullptr))) return NF4_EINVAL;
+  if (!G || !A || !B || !dA || !dB || !workspace) return NF4_EINVAL;   // with X, Z may be NULL
+  if (!aligned16(G) || (X && !aligned16(X)) || (Z && !aligned16(Z)) || !aligned16(A) || !aligned16(B) ||
+      !aligned16(dA) || !aligned16(dB) || (dX && !aligned16(dX)) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return NF4_EINVAL;
+  if (workspace_bytes < qn::bwd_workspace_bytes(M, K, N, r)) return NF4_EINVAL;
+  qn::Act8View x8;
+  if (X8 != nullptr) x8 = qn::Act8View{X8->codes, X8->absmax};
+  hipError_t e = qn::launch_bwd(M, K, N, r, G, X, Z, view_of(W), A, B, c, dX, dA, dB, workspace,
+                                static_cast<hipStream_t>(stream), compute_dtype, grad_dtype != NF4_AB_F32, x8);
+  return e == hipSuccess ? NF4_OK : NF4_EHIP;
+}
+
 int qlora_linear_bwd_dt(int compute_dtype, int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t* G,
                         const uint16_t* X,
                      const uint16_t* Z, const nf4_state_t* W, const uint16_t* A, const uint16_t* B, float c,

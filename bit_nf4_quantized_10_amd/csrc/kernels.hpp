@@ -49,6 +49,18 @@ struct NF4View {
   const float* absmax;
 };
 
+// A matrix kept as an 8-bit checkpoint (act8.hip): codes rows x cols, absmax
+// rows x ceil(cols / 64) in the 16-bit type.  codes null: none given.
+struct Act8View {
+  const int8_t* codes = nullptr;
+  const uint16_t* absmax = nullptr;
+};
+// ld: row stride of X in elements (a multiple of 8, at least cols).
+hipError_t launch_act8_encode(int64_t rows, int64_t cols, const uint16_t* X, int64_t ld, int8_t* codes,
+                              uint16_t* absmax, hipStream_t stream, int dtype);
+hipError_t launch_act8_decode(int64_t rows, int64_t cols, const int8_t* codes, const uint16_t* absmax, uint16_t* X,
+                              int64_t ld, hipStream_t stream, int dtype);
+
 // absmax_out non-null: single-level encoding (the fp32 first-level scales are
 // the stored state; qabsmax, absmax2 and offset are not written).
 hipError_t launch_quantize(const float* W, int64_t P, uint8_t* codes, int8_t* qabsmax,
@@ -77,8 +89,8 @@ hipError_t launch_grouped_fwd(int64_t M, int64_t K, int g, const int64_t* Ns, in
                               uint16_t* Z, void* ws, hipStream_t stream, int dtype = kDtypeBf16);
 hipError_t launch_grouped_bwd(int64_t M, int64_t K, int g, const int64_t* Ns, int64_t r, const uint16_t* G,
                               const uint16_t* X, const uint16_t* Z, const NF4View* W, const uint16_t* A,
-                              const uint16_t* B, float c, uint16_t* dX, float* dA, float* dB, void* ws,
-                              hipStream_t stream, int dtype = kDtypeBf16);
+                              const uint16_t* B, float c, uint16_t* dX, void* dA, void* dB, void* ws,
+                              hipStream_t stream, int dtype = kDtypeBf16, bool grad16 = false, Act8View x8 = {});
 
 // Workspace needs (bytes) of the layer kernels; the C ABI adds them up.
 int64_t fwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t r);
@@ -117,8 +129,8 @@ hipError_t launch_dz_grouped(int64_t M, int g, const int64_t* Ns, int64_t Ntot, 
                              hipStream_t stream, int dtype = 0, RdJob* defer = nullptr);
 hipError_t launch_colsums_grouped(int64_t M, int64_t K, int g, const int64_t* Ns, int64_t Ntot, int64_t r,
                                   const uint16_t* X, const uint16_t* G, const uint16_t* Z, const uint16_t* dZ, float c,
-                                  float* dA, float* dB, const GroupPlan& gp, void* da_ws, void* db_ws,
-                                  hipStream_t stream, int dtype = 0);
+                                  void* dA, void* dB, const GroupPlan& gp, void* da_ws, void* db_ws,
+                                  hipStream_t stream, int dtype = 0, bool grad16 = false, Act8View x8 = {});
 // Small-M forward (M <= 16) in two launches: the split-K partials of X Ŵ and
 // of Z = X A (extra workgroups of the same launch), then their fixed-order
 // sums, Z (written out) and Y = X Ŵ + c Z B.  part_ws: gv_part + gv_zpart.
@@ -129,9 +141,12 @@ hipError_t launch_gemv(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_
 // is not launched but returned, for the caller to run in a later launch).
 hipError_t launch_dz(int64_t M, int64_t N, int64_t r, const uint16_t* G, const uint16_t* B, float c, uint16_t* dZ,
                      const SkinnyPlan& p, void* part_ws, hipStream_t stream, int dtype = 0, RdJob* defer = nullptr);
+// dA and dB: fp32, or with grad16 of the layer's 16-bit type.  x8 (codes
+// non-null): X is kept in 8 bits, and the X argument is not read.
 hipError_t launch_colsums(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t* X, const uint16_t* G,
-                          const uint16_t* Z, const uint16_t* dZ, float c, float* dA, float* dB, const SkinnyPlan& p,
-                          void* da_ws, void* db_ws, hipStream_t stream, int dtype = 0);
+                          const uint16_t* Z, const uint16_t* dZ, float c, void* dA, void* dB, const SkinnyPlan& p,
+                          void* da_ws, void* db_ws, hipStream_t stream, int dtype = 0, bool grad16 = false,
+                          Act8View x8 = {});
 
 hipError_t launch_fwd(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t* X, NF4View W,
                       const uint16_t* A, const uint16_t* B, float c, uint16_t* Y, uint16_t* Z,
@@ -139,8 +154,8 @@ hipError_t launch_fwd(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t
 
 hipError_t launch_bwd(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t* G,
                       const uint16_t* X, const uint16_t* Z, NF4View W, const uint16_t* A,
-                      const uint16_t* B, float c, uint16_t* dX, float* dA, float* dB, void* ws,
-                      hipStream_t stream, int dtype = 0);
+                      const uint16_t* B, float c, uint16_t* dX, void* dA, void* dB, void* ws,
+                      hipStream_t stream, int dtype = 0, bool grad16 = false, Act8View x8 = {});
 
 // Split-K plan of the 256 x 256-tile GEMMs for an M x cols output reduced
 // over red: splits (1: none), elements per split, fp32 partial bytes.

@@ -91,7 +91,7 @@ hipError_t launch_fwd(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t
 
 hipError_t launch_bwd(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t* G, const uint16_t* X,
                       const uint16_t* Z, NF4View W, const uint16_t* A, const uint16_t* B, float c, uint16_t* dX,
-                      float* dA, float* dB, void* ws, hipStream_t stream, int dtype) {
+                      void* dA, void* dB, void* ws, hipStream_t stream, int dtype, bool grad16, Act8View x8) {
   const SkinnyPlan p = plan_skinny(M, K, N, r);
   char* base = static_cast<char*>(ws);
   void* dz_part = base;
@@ -115,12 +115,15 @@ hipError_t launch_bwd(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t
     RdJob jz;
     if ((e = launch_dz(M, N, r, G, B, c, dz16, p, dz_part, stream, dtype, &jz)) != hipSuccess) return e;
     if ((e = launch_dequant_bf16(W, K, N, false, wd, stream, 0, dtype, nullptr, &jz)) != hipSuccess) return e;
-    if ((e = launch_colsums(M, K, N, r, X, G, Z, dz16, c, dA, dB, p, da_part, db_part, stream, dtype)) != hipSuccess)
+    if ((e = launch_colsums(M, K, N, r, X, G, Z, dz16, c, dA, dB, p, da_part, db_part, stream, dtype, grad16, x8)) !=
+        hipSuccess)
       return e;
     return launch_dx_dense(M, K, N, r, G, wd, dz16, A, dX, stream, dtype, split_ws);
   }
   if ((e = launch_dz(M, N, r, G, B, c, dz16, p, dz_part, stream, dtype)) != hipSuccess) return e;
-  if ((e = launch_colsums(M, K, N, r, X, G, Z, dz16, c, dA, dB, p, da_part, db_part, stream, dtype)) != hipSuccess) return e;
+  if ((e = launch_colsums(M, K, N, r, X, G, Z, dz16, c, dA, dB, p, da_part, db_part, stream, dtype, grad16, x8)) !=
+      hipSuccess)
+    return e;
   if (dX == nullptr) return hipGetLastError();
   return launch_dx_big(M, K, N, r, G, W, dz16, A, dX, stream, dtype, split_ws);
 }
@@ -182,8 +185,8 @@ hipError_t launch_grouped_fwd(int64_t M, int64_t K, int g, const int64_t* Ns, in
 
 hipError_t launch_grouped_bwd(int64_t M, int64_t K, int g, const int64_t* Ns, int64_t r, const uint16_t* G,
                               const uint16_t* X, const uint16_t* Z, const NF4View* W, const uint16_t* A,
-                              const uint16_t* B, float c, uint16_t* dX, float* dA, float* dB, void* ws,
-                              hipStream_t stream, int dtype) {
+                              const uint16_t* B, float c, uint16_t* dX, void* dA, void* dB, void* ws,
+                              hipStream_t stream, int dtype, bool grad16, Act8View x8) {
   const GroupPlan gp = plan_grouped(M, K, g, Ns, r);
   int64_t Ntot = 0;
   for (int i = 0; i < g; ++i) Ntot += Ns[i];
@@ -206,8 +209,8 @@ hipError_t launch_grouped_bwd(int64_t M, int64_t K, int g, const int64_t* Ns, in
       off += Ns[i];
     }
   }
-  if ((e = launch_colsums_grouped(M, K, g, Ns, Ntot, r, X, G, Z, dz16, c, dA, dB, gp, da_ws, db_ws, stream, dtype)) !=
-      hipSuccess)
+  if ((e = launch_colsums_grouped(M, K, g, Ns, Ntot, r, X, G, Z, dz16, c, dA, dB, gp, da_ws, db_ws, stream, dtype,
+                                  grad16, x8)) != hipSuccess)
     return e;
   if (dX == nullptr) return hipGetLastError();
   return launch_dx_dense(M, K, Ntot, g * r, G, wd, dz16, A, dX, stream, dtype,

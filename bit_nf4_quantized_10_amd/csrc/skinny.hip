@@ -12,6 +12,7 @@
 //     write dA and dB themselves; otherwise a reduce kernel adds the splits.
 // (The small-M dequant-GEMV is in gemv.hip.)
 // Every reduction is in a fixed order, so results are run-to-run identical.
+#include "act8.hpp"
 #include "common.hpp"
 #include "kernels.hpp"
 #include "side_jobs.hpp"
@@ -193,6 +194,11 @@ struct CsJob {
   // r x cols (row j, column c) instead of as a partial
   int transposed = 0;
   float scale = 1.0f;
+  // act kept in 8 bits (q8 non-null, act unused): codes M x cols and the
+  // blocks' magnitudes M x nb8
+  const int8_t* q8 = nullptr;
+  const uint16_t* am8 = nullptr;
+  int64_t nb8 = 0;
 };
 
 typedef short v4i16 __attribute__((ext_vector_type(4)));
@@ -243,7 +249,87 @@ __device__ __forceinline__ void cs_block(float* blk, bool tr, const f32x16 (&acc
       }
 }
 
+// The streaming loop of a job whose activations are kept in 8 bits.  A
+// 64-column block is one checkpoint block per token, so a step is 16 rows of
+// 64 code bytes (one 16-byte load a lane: row lane/4, columns 16 (lane & 3)
+// ..), each with one magnitude, and 16 rows of v (two loads a lane).  kCs8Depth
+// steps are in flight in registers; a step is decoded to the 16-bit values
+// RNE(q fl32(a / 127)) on its way into the wave's own LDS slot, from where the
+// transposing reads and products are those of the 16-bit loop: the sums have
+// the same bits as with the decoded matrix.
+#ifndef QN_CS8_DEPTH
+#define QN_CS8_DEPTH 4
+#endif
+constexpr int kCs8Depth = QN_CS8_DEPTH;
+struct Cs8Step {
+  uint4 q, v[2];
+  uint32_t am;
+};
 template <class T>
+__device__ __forceinline__ void colsum_act8(const CsJob& J, int64_t M, int64_t c0, int64_t jb, int64_t wb, int64_t we,
+                                            int64_t nsteps, int lane, char* slot, const int (&toff)[2][2],
+                                            f32x16 (&acc)[2][2]) {
+  const int64_t nb = J.nb8;
+  const Rsrc rq = make_rsrc(J.q8, M * J.cols), rm = make_rsrc(J.am8, M * nb * 2);
+  const Rsrc rv = make_rsrc(J.v, ((M - 1) * J.v_ld + J.r) * 2);
+  const int row = lane >> 2, quarter = lane & 3;
+  // columns past the row's end only reach sums that are not stored
+  const uint32_t qv = c0 + 16 * quarter < J.cols
+                          ? static_cast<uint32_t>((wb + row) * J.cols + c0 + 16 * quarter) : kMasked;
+  const uint32_t mv = static_cast<uint32_t>(((wb + row) * nb + (c0 >> 6)) * 2);
+  uint32_t vv[2];
+  int vdst[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int R = 8 * i + (lane >> 3), c = lane & 7;
+    vv[i] = jb + 8 * c < J.r ? static_cast<uint32_t>(((wb + R) * J.v_ld + jb + 8 * c) * 2) : kMasked;
+    vdst[i] = 2048 + cs_off(R, c);
+  }
+  const int rows_left = static_cast<int>(we - wb);
+  auto load = [&](Cs8Step& S, int64_t s) {
+    const int m = static_cast<int>(16 * s);   // steps past the last one read nothing: all masked
+    const bool in = m + row < rows_left;
+    S.q = ld_b128(rq, in && qv != kMasked ? qv + static_cast<uint32_t>(m * J.cols) : kMasked);
+    S.am = __builtin_amdgcn_raw_buffer_load_b16(rm, in ? mv + static_cast<uint32_t>(m * nb * 2) : kMasked, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      S.v[i] = ld_b128(rv, (m + 8 * i + (lane >> 3) < rows_left && vv[i] != kMasked)
+                               ? vv[i] + static_cast<uint32_t>(m * J.v_ld * 2) : kMasked);
+  };
+  Cs8Step S[kCs8Depth];
+#pragma unroll
+  for (int u = 0; u < kCs8Depth; ++u) load(S[u], u);
+  for (int64_t s0 = 0; s0 < nsteps; s0 += kCs8Depth) {
+#pragma unroll
+    for (int u = 0; u < kCs8Depth; ++u) {
+      if (s0 + u >= nsteps) break;
+      const float step = act8_step<T>(S[u].am & 0xffffu);
+      const uint2 d0 = act8_values4<T>(S[u].q.x, step), d1 = act8_values4<T>(S[u].q.y, step);
+      const uint2 d2 = act8_values4<T>(S[u].q.z, step), d3 = act8_values4<T>(S[u].q.w, step);
+      *reinterpret_cast<uint4*>(slot + cs_off(row, 2 * quarter)) = make_uint4(d0.x, d0.y, d1.x, d1.y);
+      *reinterpret_cast<uint4*>(slot + cs_off(row, 2 * quarter + 1)) = make_uint4(d2.x, d2.y, d3.x, d3.y);
+      *reinterpret_cast<uint4*>(slot + vdst[0]) = S[u].v[0];
+      *reinterpret_cast<uint4*>(slot + vdst[1]) = S[u].v[1];
+      load(S[u], s0 + u + kCs8Depth);
+      // LDS operations of one wave complete in order, and the slot is its own
+      asm volatile("" ::: "memory");
+      typename T::v8 fa[2], fv[2];
+#pragma unroll
+      for (int ti = 0; ti < 2; ++ti) {
+        fa[ti] = tr_read2<T>(slot + toff[ti][0], slot + toff[ti][1]);
+        fv[ti] = tr_read2<T>(slot + 2048 + toff[ti][0], slot + 2048 + toff[ti][1]);
+      }
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int vj = 0; vj < 2; ++vj)
+#pragma unroll
+        for (int ci = 0; ci < 2; ++ci) acc[vj][ci] = T::mfma32(fv[vj], fa[ci], acc[vj][ci]);
+    }
+  }
+}
+
+// kA8: some job's activations are kept in 8 bits.
+template <class T, bool kA8>
 __global__ __launch_bounds__(256) void colsum_kernel(CsJobs jobs, int64_t M) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   int64_t blk = blockIdx.x;
@@ -308,11 +394,16 @@ __global__ __launch_bounds__(256) void colsum_kernel(CsJobs jobs, int64_t M) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
   constexpr int S = kCsSlots;
+  const bool a8 = kA8 && J.q8 != nullptr;
+  const int64_t nsteps16 = a8 ? 0 : nsteps;
+  if constexpr (kA8) {
+    if (a8) colsum_act8<T>(J, M, c0, jb, wb, we, nsteps, lane, ring, toff, acc);
+  }
   for (int x = 0; x < S - 1; ++x)
-    if (x < nsteps) copy(x, x);
-  for (int64_t s = 0; s < nsteps; ++s) {
+    if (x < nsteps16) copy(x, x);
+  for (int64_t s = 0; s < nsteps16; ++s) {
     const int b = static_cast<int>(s % S);
-    if (s + S - 1 < nsteps) {
+    if (s + S - 1 < nsteps16) {
       copy(s + S - 1, static_cast<int>((s + S - 1) % S));   // slot of step s-1, read in full already
       __builtin_amdgcn_s_waitcnt(waitcnt_imm(4 * (S - 1), 15));
     } else {
@@ -386,6 +477,20 @@ RdJob rdjob(const float* part, int64_t splits, int64_t rows, int64_t cols, float
   return make_rdjob(part, splits, rows, cols, scale, transpose, out_f32, out_bf16, dtype == kDtypeF16 ? 1 : 0);
 }
 
+// The split sum of an adapter gradient, into fp32 or (grad16) the layer's type.
+RdJob grad_job(const float* part, int64_t splits, int64_t rows, int64_t cols, float scale, bool transpose, void* out,
+               bool grad16, int dtype) {
+  return grad16 ? rdjob(part, splits, rows, cols, scale, transpose, nullptr, static_cast<uint16_t*>(out), dtype)
+                : rdjob(part, splits, rows, cols, scale, transpose, static_cast<float*>(out), nullptr);
+}
+
+void set_act8(CsJob& j, const Act8View& x8) {
+  if (x8.codes == nullptr) return;
+  j.q8 = x8.codes;
+  j.am8 = x8.absmax;
+  j.nb8 = cdiv(j.cols, 64);
+}
+
 hipError_t launch_reduce(const RdJob& ja, const RdJob* jb, hipStream_t stream) {
   RdJob second = jb != nullptr ? *jb : ja;
   if (jb == nullptr) second.nblk = 0;
@@ -415,24 +520,29 @@ hipError_t launch_rowsum(const uint16_t* act, const uint16_t* wt, int64_t M, int
   return dtype == kDtypeF16 ? rowsum_launch_t<F16>(a, splits, stream) : rowsum_launch_t<Bf16>(a, splits, stream);
 }
 
-template <class T>
+template <class T, bool kA8>
 hipError_t colsum_launch_t(const CsJobs& jobs, int64_t M, hipStream_t stream) {
   // raised once per process; the initialisation of a function-local static
   // is thread-safe, so concurrent first calls do not race
-  static const hipError_t lds_limit = hipFuncSetAttribute(reinterpret_cast<const void*>(&colsum_kernel<T>),
+  static const hipError_t lds_limit = hipFuncSetAttribute(reinterpret_cast<const void*>(&colsum_kernel<T, kA8>),
                                                           hipFuncAttributeMaxDynamicSharedMemorySize, kCsLds);
   if (lds_limit != hipSuccess) return lds_limit;
   int64_t blocks = 0;
   for (int i = 0; i < kCsJobs; ++i) blocks += jobs.j[i].nblk;
-  hipLaunchKernelGGL(colsum_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(256), kCsLds, stream, jobs, M);
+  hipLaunchKernelGGL((colsum_kernel<T, kA8>), dim3(static_cast<unsigned>(blocks)), dim3(256), kCsLds, stream, jobs, M);
   return hipGetLastError();
 }
 
 // jobs[0 .. n-1] (n <= kCsJobs) in one launch.
 hipError_t launch_colsum(const CsJob* jobs, int n, int64_t M, hipStream_t stream, int dtype) {
   CsJobs js{};
-  for (int i = 0; i < n; ++i) js.j[i] = jobs[i];
-  return dtype == kDtypeF16 ? colsum_launch_t<F16>(js, M, stream) : colsum_launch_t<Bf16>(js, M, stream);
+  bool a8 = false;
+  for (int i = 0; i < n; ++i) {
+    js.j[i] = jobs[i];
+    a8 = a8 || jobs[i].q8 != nullptr;
+  }
+  if (a8) return dtype == kDtypeF16 ? colsum_launch_t<F16, true>(js, M, stream) : colsum_launch_t<Bf16, true>(js, M, stream);
+  return dtype == kDtypeF16 ? colsum_launch_t<F16, false>(js, M, stream) : colsum_launch_t<Bf16, false>(js, M, stream);
 }
 
 }  // namespace
@@ -507,19 +617,20 @@ hipError_t launch_dz(int64_t M, int64_t N, int64_t r, const uint16_t* G, const u
 
 // dA = Xᵀ dZ (K x r) and dB = c Zᵀ G (r x N).
 hipError_t launch_colsums(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t* X, const uint16_t* G,
-                          const uint16_t* Z, const uint16_t* dZ, float c, float* dA, float* dB, const SkinnyPlan& p,
-                          void* da_ws, void* db_ws, hipStream_t stream, int dtype) {
+                          const uint16_t* Z, const uint16_t* dZ, float c, void* dA, void* dB, const SkinnyPlan& p,
+                          void* da_ws, void* db_ws, hipStream_t stream, int dtype, bool grad16, Act8View x8) {
   const int64_t jc = cdiv(r, 64);
   CsJob ja{X, K, K, dZ, static_cast<float*>(da_ws), cdiv(K, 64), jc, p.da_per, 0, r, r};
+  set_act8(ja, x8);
   CsJob jb{G, N, N, Z, static_cast<float*>(db_ws), cdiv(N, 64), jc, p.db_per, 0, r, r};
   ja.nblk = ja.col_blocks * jc * p.da_splits;
   jb.nblk = jb.col_blocks * jc * p.db_splits;
   // with one token split the sums are final: dA is written in place, dB
   // scaled and transposed, and no reduce launch follows
-  const bool direct = p.da_splits == 1 && p.db_splits == 1;
+  const bool direct = p.da_splits == 1 && p.db_splits == 1 && !grad16;
   if (direct) {
-    ja.part = dA;
-    jb.part = dB;
+    ja.part = static_cast<float*>(dA);
+    jb.part = static_cast<float*>(dB);
     jb.transposed = 1;
     jb.scale = c;
   }
@@ -528,8 +639,8 @@ hipError_t launch_colsums(int64_t M, int64_t K, int64_t N, int64_t r, const uint
   hipError_t e = launch_colsum(both, 2, M, stream, dtype);
   tm.stop();
   if (e != hipSuccess || direct) return e;
-  const RdJob ra = rdjob(static_cast<float*>(da_ws), p.da_splits, K, r, 1.0f, false, dA, nullptr);
-  const RdJob rb = rdjob(static_cast<float*>(db_ws), p.db_splits, N, r, c, true, dB, nullptr);
+  const RdJob ra = grad_job(static_cast<float*>(da_ws), p.da_splits, K, r, 1.0f, false, dA, grad16, dtype);
+  const RdJob rb = grad_job(static_cast<float*>(db_ws), p.db_splits, N, r, c, true, dB, grad16, dtype);
   return launch_reduce(ra, &rb, stream);
 }
 
@@ -595,18 +706,20 @@ hipError_t launch_dz_grouped(int64_t M, int g, const int64_t* Ns, int64_t Ntot, 
 // into columns off_i .. of dB (r x Ntot); two column-sum jobs per launch.
 hipError_t launch_colsums_grouped(int64_t M, int64_t K, int g, const int64_t* Ns, int64_t Ntot, int64_t r,
                                   const uint16_t* X, const uint16_t* G, const uint16_t* Z, const uint16_t* dZ, float c,
-                                  float* dA, float* dB, const GroupPlan& gp, void* da_ws, void* db_ws,
-                                  hipStream_t stream, int dtype) {
+                                  void* dA, void* dB, const GroupPlan& gp, void* da_ws, void* db_ws,
+                                  hipStream_t stream, int dtype, bool grad16, Act8View x8) {
   const int64_t rt = g * r;
   CsJob jobs[kMaxGroupMembers + 1];
   RdJob rds[kMaxGroupMembers + 1];
   jobs[0] = CsJob{X, K, K, dZ, static_cast<float*>(da_ws), cdiv(K, 64), cdiv(rt, 64), gp.cs_per, 0, rt, rt};
-  rds[0] = rdjob(static_cast<float*>(da_ws), gp.cs_splits, K, rt, 1.0f, false, dA, nullptr);
+  set_act8(jobs[0], x8);
+  rds[0] = grad_job(static_cast<float*>(da_ws), gp.cs_splits, K, rt, 1.0f, false, dA, grad16, dtype);
   int64_t off = 0;
   for (int i = 0; i < g; ++i) {
     float* part = reinterpret_cast<float*>(static_cast<char*>(db_ws) + gp.db_off[i]);
     jobs[i + 1] = CsJob{G + off, Ntot, Ns[i], Z + i * r, part, cdiv(Ns[i], 64), cdiv(r, 64), gp.cs_per, 0, r, rt};
-    rds[i + 1] = rdjob(part, gp.cs_splits, Ns[i], r, c, true, dB + off, nullptr);
+    void* db = grad16 ? static_cast<void*>(static_cast<uint16_t*>(dB) + off) : static_cast<float*>(dB) + off;
+    rds[i + 1] = grad_job(part, gp.cs_splits, Ns[i], r, c, true, db, grad16, dtype);
     rds[i + 1].out_ld = Ntot;
     off += Ns[i];
   }

@@ -260,6 +260,41 @@ int qlora_grouped_bwd_dt(int compute_dtype, int64_t M, int64_t K, int g, const i
                          const uint16_t* A, const uint16_t* B, float c, uint16_t* dX, float* dA, float* dB,
                          void* workspace, int64_t workspace_bytes, void* stream);
 
+/* 8-bit checkpoints of 16-bit activations: what a backward pass needs of a
+ * forward input, in 1.03 bytes an element instead of 2.  Per row, blocks of 64
+ * consecutive columns (the last block of a row may be shorter):
+ *   a = max |x| of the block, kept exactly in the activations' 16-bit type;
+ *   q = the integer nearest to 127 x / a, ties to even (0 where a = 0);
+ *   the kept value is x^ = RNE_T(fl32(q * fl32(a / 127))).
+ * The element of magnitude a is kept exactly, the others within a / 254 and
+ * the last rounding.  A block holding an infinity or a NaN is kept as a = NaN,
+ * q = 0 and decodes to NaN in all its columns. */
+typedef struct act8 {
+  int8_t*   codes;    /* rows x cols, row-major, dense, 16-byte aligned        */
+  uint16_t* absmax;   /* rows x ceil(cols / 64), bit patterns of the 16-bit type, 2-byte aligned */
+} act8_t;
+
+/* Encode the rows x cols matrix X of the 16-bit type dtype (NF4_COMPUTE_*)
+ * with row stride ld (elements), or decode into such a matrix.  rows >= 1,
+ * cols >= 8, cols % 8 == 0, ld >= cols, ld % 8 == 0, rows * ld and 8 rows
+ * below 2^29, X 16-byte aligned; NF4_EINVAL otherwise.  Columns cols .. ld-1
+ * are neither read nor written.  One launch, no workspace. */
+int act8_encode(int dtype, int64_t rows, int64_t cols, const uint16_t* X, int64_t ld, const act8_t* out, void* stream);
+int act8_decode(int dtype, int64_t rows, int64_t cols, const act8_t* in, uint16_t* X, int64_t ld, void* stream);
+
+/* qlora_linear_bwd_dt whose input was kept in 8 bits, or whose adapter
+ * gradients are wanted in the layer's 16-bit type.  Exactly one of X (16 bits)
+ * and X8 is given (the other NULL).  With X8, dA = x^ᵀ dZ for the kept values
+ * x^ - the bits of the same call on the decoded matrix - which is read in 8
+ * bits and never decoded to memory; Z must then be given (it was computed from
+ * the input before it was kept).  grad_dtype: NF4_AB_F32, or NF4_AB_BF16 /
+ * NF4_AB_F16 matching compute_dtype; dA and dB are of that type (the fp32 sum
+ * rounded once).  Workspace, requirements and the rest as qlora_linear_bwd. */
+int qlora_linear_bwd_ex(int compute_dtype, int grad_dtype, int64_t M, int64_t K, int64_t N, int64_t r,
+                        const uint16_t* G, const uint16_t* X, const act8_t* X8, const uint16_t* Z,
+                        const nf4_state_t* W, const uint16_t* A, const uint16_t* B, float c, uint16_t* dX, void* dA,
+                        void* dB, void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Synchronise `stream`, then copy the device status word to *host_value.
  * Returns NF4_EHIP if the copy fails, else NF4_OK. */
 int nf4_status_read(const int32_t* status, int32_t* host_value, void* stream);
@@ -279,7 +314,9 @@ int nf4_status_read(const int32_t* status, int32_t* host_value, void* stream);
 #define QK_REDUCE       11  /* fixed-order split reductions             */
 #define QK_MERGE        12  /* adapter merge W' = fl32(ŵ + cAB)          */
 #define QK_SGD          13  /* adapter SGD step                          */
-#define QK_NUM_KERNELS  14
+#define QK_ACT8_ENCODE  14  /* 8-bit activation checkpoint               */
+#define QK_ACT8_DECODE  15  /* its 16-bit values                         */
+#define QK_NUM_KERNELS  16
 
 /* When enabled, the library records a pair of hipEvents on the launch
  * stream around every launch of kernel `kernel_id`.  qlora_timer_read
