@@ -21,7 +21,7 @@ NF4_COMPUTE_BF16, NF4_COMPUTE_F16 = 0, 1
 KERNEL_IDS = {
     "quant_pass1": 0, "quant_mean": 1, "quant_pass2": 2, "dequant": 3, "lora_down": 4,
     "fwd_gemm": 5, "fwd_gemv": 6, "bwd_dz": 7, "bwd_dx": 8, "bwd_colsum": 9, "dequant_bf16": 10,
-    "reduce": 11, "merge": 12, "sgd": 13, "act8_encode": 14, "act8_decode": 15,
+    "reduce": 11, "merge": 12, "sgd": 13, "act8_encode": 14, "act8_decode": 15, "gated_fwd": 16, "gated_dy": 17,
 }
 C_FUNCTIONS = [
     "nf4_sizes", "nf4_quantize", "nf4_dequantize", "qlora_workspace_bytes",
@@ -29,7 +29,8 @@ C_FUNCTIONS = [
     "qlora_timer_read", "qlora_merge", "qlora_sgd_step", "qlora_grouped_workspace_bytes",
     "qlora_grouped_fwd", "qlora_grouped_bwd", "qlora_linear_fwd_dt", "qlora_linear_bwd_dt", "qlora_sgd_step_dt",
     "qlora_linear_fwd_noalloc", "qlora_grouped_fwd_dt", "qlora_grouped_bwd_dt",
-    "act8_encode", "act8_decode", "qlora_linear_bwd_ex", "nf4_error_string",
+    "act8_encode", "act8_decode", "qlora_linear_bwd_ex",
+    "qlora_gated_workspace_bytes", "qlora_gated_fwd", "qlora_gated_bwd", "nf4_error_string",
 ]
 NF4_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 
@@ -96,6 +97,11 @@ def lib() -> ctypes.CDLL:
         L.act8_decode.argtypes = [ctypes.c_int, i64, i64, a8, vp, i64, vp]
         L.qlora_linear_bwd_ex.argtypes = [ctypes.c_int, ctypes.c_int, i64, i64, i64, i64, vp, vp, a8, vp, sp, vp, vp,
                                           ctypes.c_float, vp, vp, vp, vp, i64, vp]
+        L.qlora_gated_workspace_bytes.argtypes = L.qlora_workspace_bytes.argtypes
+        L.qlora_gated_fwd.argtypes = [ctypes.c_int, ctypes.c_int, i64, i64, i64, i64, vp, sp, vp, vp, ctypes.c_float,
+                                      vp, vp, vp, a8, vp, i64, vp]
+        L.qlora_gated_bwd.argtypes = [ctypes.c_int] * 3 + [i64, i64, i64, i64, vp, vp, a8, vp, vp, a8, sp, vp, vp,
+                                                           ctypes.c_float, vp, vp, vp, vp, i64, vp]
         L.nf4_error_string.argtypes = [ctypes.c_int]
         L.nf4_error_string.restype = ctypes.c_char_p
         for name in C_FUNCTIONS[:-1]:
@@ -601,6 +607,103 @@ def _linear_bwd_ex(G, X, Z, state, A, B, c, K, N, need_dx, dX, dA, dB, workspace
                                          ctypes.byref(st), A.data_ptr(), B.data_ptr(), float(c), _ptr(dX),
                                          dA.data_ptr(), dB.data_ptr(), ws.data_ptr(), ws.numel(), s),
                "qlora_linear_bwd_ex")
+    return dX, dA, dB
+
+
+NF4_ACT_SILU, NF4_ACT_GELU = 0, 1
+_ACTS = {"silu": NF4_ACT_SILU, "gelu": NF4_ACT_GELU}
+
+
+def qlora_gated_workspace_bytes(M: int, K: int, F: int, r: int) -> tuple[int, int]:
+    f, b = ctypes.c_int64(), ctypes.c_int64()
+    _check(lib().qlora_gated_workspace_bytes(M, K, F, r, ctypes.byref(f), ctypes.byref(b)),
+           "qlora_gated_workspace_bytes")
+    return f.value, b.value
+
+
+def _gated_args(X, states, A, B, K: int, F: int, act: str):
+    """Checks shared by the gated calls: (M, r, compute dtype, states array, act code)."""
+    if act not in _ACTS:
+        raise ValueError(f"act is one of {sorted(_ACTS)}, got {act!r}")
+    if len(states) != 2:
+        raise ValueError("two states: the gate's weight and the up weight")
+    M, r2 = X.shape[0], A.shape[1]
+    dt = _compute_dtype(X)
+    if r2 % 2:
+        raise ValueError("A must be K x 2r: the gate's adapter and the up adapter side by side")
+    _require_cuda(A, "A", dt)
+    _require_cuda(B, "B", dt)
+    _require_shape(A, "A", K, r2)
+    _require_shape(B, "B", r2 // 2, 2 * F)
+    return M, r2 // 2, dt, (_State * 2)(*[s.c_struct() for s in states]), _ACTS[act]
+
+
+def _gated_kept(saved, M: int, F: int, dt):
+    """(GU pointer or None, _Act8 or None) of a gated forward's kept pair."""
+    if saved is None:
+        return None, None
+    if saved.dtype != dt:
+        raise ValueError(f"saved must be of {dt}, got {saved.dtype}")
+    if not isinstance(saved, Act8):
+        _require_cuda(saved, "saved")
+    return _kept_or_dense(saved, M, 2 * F, "saved")
+
+
+def qlora_gated_fwd(X, states, A, B, c: float, K: int, F: int, act: str = "silu", save: str = "none", H=None, Z=None,
+                    saved=None, workspace=None, stream=None, return_z: bool = True):
+    """H = act(G) * U with G = X Ŵ0 + c Zg Bg, U = X Ŵ1 + c Zu Bu, [Zg | Zu] = X A.
+    X: M x K, A = [Ag | Au] (K x 2r), B = [Bg | Bu] (r x 2F), all bf16 or all
+    fp16; states: the gate's and the up weight (K x F).  save: what is kept of
+    [G | U] (M x 2F) for the backward: "none", "16" (a tensor) or "8" (an
+    Act8); a given `saved` of either kind is filled instead.  Returns
+    (H, Z, saved); with return_z=False and no Z given, Z is None."""
+    if save not in ("none", "16", "8"):
+        raise ValueError(f'save is "none", "16" or "8", got {save!r}')
+    M, r, dt, st, code = _gated_args(X, states, A, B, K, F, act)
+    _require_cuda(X, "X", dt)
+    _require_shape(X, "X", M, K)
+    import torch
+    with _on(X, stream, A, B, states[0].codes, states[1].codes, H, Z, saved, workspace) as s:
+        H = _out(H, "H", dt, X.device, M, F)
+        if Z is not None or return_z:
+            Z = _out(Z, "Z", dt, X.device, M, 2 * r)
+        if saved is None and save == "16":
+            saved = torch.empty(M, 2 * F, dtype=dt, device=X.device)
+        elif saved is None and save == "8":
+            saved = empty_act8(M, 2 * F, dt, X.device)
+        gu, gu8 = _gated_kept(saved, M, F, dt)
+        ws = _workspace(workspace, qlora_gated_workspace_bytes(M, K, F, r)[0], X.device)
+        _check(lib().qlora_gated_fwd(_COMPUTE[dt], code, M, K, F, r, X.data_ptr(), st, A.data_ptr(), B.data_ptr(),
+                                     float(c), H.data_ptr(), _ptr(Z), gu, _ref(gu8), ws.data_ptr(), ws.numel(), s),
+               "qlora_gated_fwd")
+    return H, Z, saved
+
+
+def qlora_gated_bwd(dH, X, Z, saved, states, A, B, c: float, K: int, F: int, act: str = "silu", need_dx: bool = True,
+                    grad_dtype=None, dX=None, dA=None, dB=None, workspace=None, stream=None):
+    """Backward of qlora_gated_fwd given dH (M x F): (dX or None, dA (K x 2r),
+    dB (r x 2F)).  saved: the forward's (None: G and U are computed again from
+    X).  X may be an Act8 where saved is given.  grad_dtype: of dA and
+    dB, float32 (the default) or X's dtype."""
+    M, r, dt, st, code = _gated_args(X, states, A, B, K, F, act)
+    for t, n, shape in ((dH, "dH", (M, F)), (Z, "Z", (M, 2 * r))):
+        _require_cuda(t, n, dt)
+        _require_shape(t, n, *shape)
+    if not isinstance(X, Act8):
+        _require_cuda(X, "X", dt)
+    elif saved is None:
+        raise ValueError("saved is required where X is kept in 8 bits")
+    xp, x8 = _kept_or_dense(X, M, K, "X")
+    gu, gu8 = _gated_kept(saved, M, F, dt)
+    gdt, gcode = _grad_code(grad_dtype, dt)
+    with _on(dH, stream, X, Z, saved, A, B, states[0].codes, states[1].codes, dX, dA, dB, workspace) as s:
+        dX = _out(dX, "dX", dt, dH.device, M, K) if need_dx else None
+        dA = _out(dA, "dA", gdt, dH.device, K, 2 * r)
+        dB = _out(dB, "dB", gdt, dH.device, r, 2 * F)
+        ws = _workspace(workspace, qlora_gated_workspace_bytes(M, K, F, r)[1], dH.device)
+        _check(lib().qlora_gated_bwd(_COMPUTE[dt], code, gcode, M, K, F, r, dH.data_ptr(), xp, _ref(x8), Z.data_ptr(),
+                                     gu, _ref(gu8), st, A.data_ptr(), B.data_ptr(), float(c), _ptr(dX), dA.data_ptr(),
+                                     dB.data_ptr(), ws.data_ptr(), ws.numel(), s), "qlora_gated_bwd")
     return dX, dA, dB
 
 

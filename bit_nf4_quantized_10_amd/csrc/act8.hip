@@ -76,12 +76,7 @@ __global__ __launch_bounds__(kThreads) void act8_encode_kernel(A8Args a) {
 #pragma unroll
     for (int u = 0; u < kU; ++u) {
       // every lane of the block's eight takes part: a chunk past the row's end counts as zeros
-      uint32_t m = act8_max4(v[u]);
-      m = act8_max2(m, __shfl_xor(m, 1, 64));
-      m = act8_max2(m, __shfl_xor(m, 2, 64));
-      m = act8_max2(m, __shfl_xor(m, 4, 64));
-      const uint32_t amax = max(m & 0xffffu, m >> 16);
-      const Act8Scale sc = act8_scale<T>(amax);
+      const Act8Scale sc = act8_scale<T>(act8_block_max(v[u]));
       const uint2 q = act8_codes8<T>(v[u], sc);
       if (!ok[u]) continue;
       *reinterpret_cast<uint2*>(a.codes + static_cast<int64_t>(row[u]) * a.cols + col[u]) = q;

@@ -17,6 +17,15 @@ __device__ __forceinline__ uint32_t act8_max4(const uint4& v) {
   return act8_max2(act8_max2(v.x & kAbs, v.y & kAbs), act8_max2(v.z & kAbs, v.w & kAbs));
 }
 
+// The same over a block that eight neighbouring lanes hold, 8 values each.
+__device__ __forceinline__ uint32_t act8_block_max(const uint4& v) {
+  uint32_t m = act8_max4(v);
+  m = act8_max2(m, __shfl_xor(m, 1, 64));
+  m = act8_max2(m, __shfl_xor(m, 2, 64));
+  m = act8_max2(m, __shfl_xor(m, 4, 64));
+  return max(m & 0xffffu, m >> 16);
+}
+
 // What encoding a block needs of its largest magnitude (16-bit pattern).
 struct Act8Scale {
   float k, a, inv;   // quotient = (k x) / a, both scaled by a power of two into fp32's middle; inv ~ 1 / a

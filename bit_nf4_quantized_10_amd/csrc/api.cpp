@@ -7,6 +7,7 @@
 #include <vector>
 
 #include "../../include/qlora_nf4.h"
+#include "gated.hpp"
 #include "kernels.hpp"
 
 namespace {
@@ -360,6 +361,75 @@ int qlora_grouped_bwd(int64_t M, int64_t K, int g, const int64_t* N, int64_t r, 
                       uint16_t* dX, float* dA, float* dB, void* workspace, int64_t workspace_bytes, void* stream) {
   return qlora_grouped_bwd_dt(NF4_COMPUTE_BF16, M, K, g, N, r, G, X, Z, W, A, B, c, dX, dA, dB, workspace,
                               workspace_bytes, stream);
+}
+
+static bool act_ok(int act) { return act == NF4_ACT_SILU || act == NF4_ACT_GELU; }
+
+static bool gated_shape_ok(int64_t M, int64_t K, int64_t F, int64_t r) {
+  return F >= 64 && F % 64 == 0 && F <= (int64_t(1) << 23) && r >= 8 && r % 8 == 0 && r <= 128 &&
+         layer_shape_ok(M, K, 2 * F, 2 * r);
+}
+
+// What the forward keeps (or the backward reads): none, 16 bits or 8.
+static bool gated_keep_ok(const uint16_t* GU, const act8_t* GU8) {
+  if (GU != nullptr && GU8 != nullptr) return false;
+  return (GU == nullptr || aligned16(GU)) && (GU8 == nullptr || act8_ok(GU8));
+}
+static qn::GatedKeep gated_keep(const uint16_t* GU, const act8_t* GU8) {
+  qn::GatedKeep k;
+  k.gu = const_cast<uint16_t*>(GU);
+  if (GU8 != nullptr) {
+    k.codes = GU8->codes;
+    k.absmax = GU8->absmax;
+  }
+  return k;
+}
+
+int qlora_gated_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t r, int64_t* fwd_bytes, int64_t* bwd_bytes) {
+  if (!gated_shape_ok(M, K, F, r)) return NF4_EINVAL;
+  if (fwd_bytes) *fwd_bytes = qn::gated_fwd_workspace_bytes(M, K, F, r);
+  if (bwd_bytes) *bwd_bytes = qn::gated_bwd_workspace_bytes(M, K, F, r);
+  return NF4_OK;
+}
+
+int qlora_gated_fwd(int compute_dtype, int act, int64_t M, int64_t K, int64_t F, int64_t r, const uint16_t* X,
+                    const nf4_state_t* W, const uint16_t* A, const uint16_t* B, float c, uint16_t* H, uint16_t* Z,
+                    uint16_t* GU, const act8_t* GU8, void* workspace, int64_t workspace_bytes, void* stream) {
+  const int64_t Ns[2] = {F, F};
+  qn::NF4View views[2];
+  if (!dtype_ok(compute_dtype) || !act_ok(act) || !gated_shape_ok(M, K, F, r)) return NF4_EINVAL;
+  if (!grouped_states_ok(W, 2, K, Ns, views) || !gated_keep_ok(GU, GU8)) return NF4_EINVAL;
+  if (!X || !A || !B || !H || !workspace) return NF4_EINVAL;   // Z may be NULL
+  if (!aligned16(X) || !aligned16(A) || !aligned16(B) || !aligned16(H) || (Z && !aligned16(Z)) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return NF4_EINVAL;
+  if (workspace_bytes < qn::gated_fwd_workspace_bytes(M, K, F, r)) return NF4_EINVAL;
+  hipError_t e = qn::launch_gated_fwd(M, K, F, r, X, views, A, B, c, act == NF4_ACT_GELU, H, Z, gated_keep(GU, GU8),
+                                      workspace, static_cast<hipStream_t>(stream), compute_dtype);
+  return e == hipSuccess ? NF4_OK : NF4_EHIP;
+}
+
+int qlora_gated_bwd(int compute_dtype, int act, int grad_dtype, int64_t M, int64_t K, int64_t F, int64_t r,
+                    const uint16_t* dH, const uint16_t* X, const act8_t* X8, const uint16_t* Z, const uint16_t* GU,
+                    const act8_t* GU8, const nf4_state_t* W, const uint16_t* A, const uint16_t* B, float c,
+                    uint16_t* dX, void* dA, void* dB, void* workspace, int64_t workspace_bytes, void* stream) {
+  const int64_t Ns[2] = {F, F};
+  qn::NF4View views[2];
+  if (!dtype_ok(compute_dtype) || !act_ok(act) || !grad_dtype_ok(grad_dtype, compute_dtype)) return NF4_EINVAL;
+  if (!gated_shape_ok(M, K, F, r) || !grouped_states_ok(W, 2, K, Ns, views) || !gated_keep_ok(GU, GU8)) return NF4_EINVAL;
+  if ((X == nullptr) == (X8 == nullptr)) return NF4_EINVAL;
+  if (X8 != nullptr && (!act8_ok(X8) || (GU == nullptr && GU8 == nullptr))) return NF4_EINVAL;
+  if (!dH || !Z || !A || !B || !dA || !dB || !workspace) return NF4_EINVAL;
+  if (!aligned16(dH) || (X && !aligned16(X)) || !aligned16(Z) || !aligned16(A) || !aligned16(B) || !aligned16(dA) ||
+      !aligned16(dB) || (dX && !aligned16(dX)) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return NF4_EINVAL;
+  if (workspace_bytes < qn::gated_bwd_workspace_bytes(M, K, F, r)) return NF4_EINVAL;
+  qn::Act8View x8;
+  if (X8 != nullptr) x8 = qn::Act8View{X8->codes, X8->absmax};
+  hipError_t e = qn::launch_gated_bwd(M, K, F, r, dH, X, x8, Z, gated_keep(GU, GU8), views, A, B, c,
+                                      act == NF4_ACT_GELU, dX, dA, dB, workspace, static_cast<hipStream_t>(stream),
+                                      compute_dtype, grad_dtype != NF4_AB_F32);
+  return e == hipSuccess ? NF4_OK : NF4_EHIP;
 }
 
 int qlora_merge(int64_t K, int64_t N, int64_t r, const nf4_state_t* W, const void* A, const void* B, int ab_dtype,

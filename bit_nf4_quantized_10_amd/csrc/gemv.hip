@@ -18,6 +18,7 @@
 // row ranges of a strip are added in LDS in a fixed order; the split-K
 // partials and the LoRA term are added by gemv_finish_kernel.
 #include "common.hpp"
+#include "gated.hpp"
 #include "kernels.hpp"
 
 namespace qn {
@@ -168,17 +169,20 @@ struct GvStep {
 // one byte-select add and one 16-bit table lookup, pairs packed with v_perm;
 // column t of the lane feeds the MFMA of tile t.  part[split][m][n] = sum of
 // the 4 waves (fixed order).
-template <class T>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3, 3))) void gemv_kernel(const uint16_t* __restrict__ X, int64_t M, NF4View W, int64_t K,
+// kTwo: two weights of N columns each (the gated block's), `pairs` strip pairs
+// of the first, then of the second; the partials are M x 2N, side by side.
+template <class T, bool kTwo>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3, 3))) void gemv_kernel(const uint16_t* __restrict__ X, int64_t M, NF4View W_, int64_t K,
                                                    int64_t N, int64_t rpw, int64_t pairs, float* __restrict__ part,
                                                    const uint16_t* __restrict__ A, int64_t r,
-                                                   float* __restrict__ zpart) {
+                                                   float* __restrict__ zpart, NF4View W2) {
   __shared__ float q2t[256];
   __shared__ __attribute__((aligned(16))) char lds[kGvWaves * kGvWaveLds];
   const int t = threadIdx.x, lane = t & 63, q = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int64_t splits = (K + 2 * rpw - 1) / (2 * rpw);
-  const int64_t gv = pairs * splits;
+  const int64_t row_pairs = kTwo ? 2 * pairs : pairs;
+  const int64_t gv = row_pairs * splits;
   if (blockIdx.x >= gv) {
     // the last `splits` workgroups: Z partials over the same row ranges
     gemv_zpart<T>(X, M, K, rpw / 2, A, r, zpart, blockIdx.x - gv, reinterpret_cast<float*>(lds));
@@ -191,8 +195,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3, 3))) voi
   // whose L2 then fetches the lines of int8 scale codes they share once.
   const int64_t per = gv / 8, rem = gv % 8, xcd = blockIdx.x % 8;
   const int64_t L = xcd * per + min(xcd, rem) + blockIdx.x / 8;
-  const int64_t split = L / pairs;
-  const int64_t n0 = (2 * (L % pairs) + (wave & 1)) * kGvCols;
+  const int64_t split = L / row_pairs;
+  const bool second = kTwo && L % row_pairs >= pairs;
+  const NF4View W = second ? W2 : W_;
+  const int64_t n0 = (2 * (L % row_pairs - (second ? pairs : 0)) + (wave & 1)) * kGvCols;
   const int64_t kw0 = (split * 2 + (wave >> 1)) * rpw;
   const int64_t kend = min(K, kw0 + rpw);   // this wave's rows; nothing past them is fetched
   const int64_t rows = kend > kw0 ? kend - kw0 : 0;
@@ -302,7 +308,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3, 3))) voi
   }
   __syncthreads();
   if (wave < 2) {
-    float* out = part + split * M * N;
+    const int64_t ldn = kTwo ? 2 * N : N;
+    float* out = part + split * M * ldn + (second ? N : 0);
     const int64_t n = n0 + 8 * q;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -311,8 +318,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3, 3))) voi
 #pragma unroll
       for (int tile = 0; tile < 8; ++tile) v[tile] = acc[tile][e] + red[(wave * 32 + tile * 4 + e) * 64 + lane];
       if (m < M && n < N) {
-        *reinterpret_cast<float4*>(out + m * N + n) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4*>(out + m * N + n + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        *reinterpret_cast<float4*>(out + m * ldn + n) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(out + m * ldn + n + 4) = make_float4(v[4], v[5], v[6], v[7]);
       }
     }
   }
@@ -346,38 +353,47 @@ __device__ __forceinline__ void fin_add8(float (&s)[8], const uint4 (&a)[8], con
     s[6] += __builtin_bit_cast(float, b[k].z); s[7] += __builtin_bit_cast(float, b[k].w);
   }
 }
-template <class T>
+// kTwo (the gated block; N = F columns per weight, r per member, Z M x 2r): a
+// workgroup owns 256 columns, waves 0 and 1 of G, waves 2 and 3 of U; the U
+// waves hand their values over in LDS and the G waves store Y = act(G) * U and
+// what is kept of G and U.
+template <class T, bool kTwo, bool kGelu>
 __global__ __launch_bounds__(256) void gemv_finish_kernel(const float* __restrict__ part, int splits, int64_t M,
                                                           int64_t N, const float* __restrict__ zpart,
                                                           uint16_t* __restrict__ Z, const uint16_t* __restrict__ B,
-                                                          int64_t r, float c, uint16_t* __restrict__ Y) {
+                                                          int64_t r, float c, uint16_t* __restrict__ Y,
+                                                          GatedKeep keep) {
   __shared__ __attribute__((aligned(16))) uint16_t zl[16 * 256];   // Z, M x r (M <= 16, r <= 256)
   const int t = threadIdx.x, lane = t & 63, q = lane & 15, g = lane >> 4, wave = t >> 6;
   const int e = blockIdx.y;
-  const int64_t n = static_cast<int64_t>(blockIdx.x) * kFinCols + 128 * wave + 8 * q;
-  const bool n_ok = n < N;
+  const int member = kTwo ? wave >> 1 : 0;
+  const int64_t ncol = kTwo ? static_cast<int64_t>(blockIdx.x) * (kFinCols / 2) + 128 * (wave & 1) + 8 * q
+                            : static_cast<int64_t>(blockIdx.x) * kFinCols + 128 * wave + 8 * q;
+  const bool n_ok = ncol < N;
+  const int64_t ldn = kTwo ? 2 * N : N, n = ncol + member * N;
+  const int64_t rt = kTwo ? 2 * r : r;   // Z's row length
   const int64_t m = 4 * g + e;
   const bool out_ok = m < M && n_ok;
-  const int64_t MR = M * r;
-  const Rsrc rb = make_rsrc(B, r * N * 2);
+  const int64_t MR = M * rt;
+  const Rsrc rb = make_rsrc(B, r * ldn * 2);
   const Rsrc rzp = make_rsrc(zpart, static_cast<int64_t>(splits) * MR * 4);
-  const Rsrc rp = make_rsrc(part, static_cast<int64_t>(splits) * M * N * 4);
+  const Rsrc rp = make_rsrc(part, static_cast<int64_t>(splits) * M * ldn * 4);
   auto load_b = [&](int64_t j0, uint4 (&rows8)[8]) {
     const int64_t jb = j0 + 8 * g;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      rows8[i] = ld_b128(rb, (jb + i < r && n_ok) ? static_cast<uint32_t>(((jb + i) * N + n) * 2) : kMasked);
+      rows8[i] = ld_b128(rb, (jb + i < r && n_ok) ? static_cast<uint32_t>(((jb + i) * ldn + n) * 2) : kMasked);
   };
   auto load_part = [&](int s0, uint4 (&pa)[8], uint4 (&pb)[8]) {
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const uint32_t off = (out_ok && s0 + k < splits) ? static_cast<uint32_t>((((s0 + k) * M + m) * N + n) * 4) : kMasked;
+      const uint32_t off = (out_ok && s0 + k < splits) ? static_cast<uint32_t>((((s0 + k) * M + m) * ldn + n) * 4) : kMasked;
       pa[k] = ld_b128(rp, off);
       pb[k] = ld_b128(rp, off == kMasked ? kMasked : off + 16);
     }
   };
-  // thread t sums elements idx .. idx+3 of the row-major M x r matrix Z
-  // (r % 8 == 0, so a group of 4 never leaves its row)
+  // thread t sums elements idx .. idx+3 of the row-major M x rt matrix Z
+  // (rt % 8 == 0, so a group of 4 never leaves its row)
   auto load_z = [&](int s0, int64_t idx, uint4 (&za)[8]) {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
@@ -417,7 +433,7 @@ __global__ __launch_bounds__(256) void gemv_finish_kernel(const float* __restric
   for (int i = 0; i < 8; ++i) accl[i] = f32x4{0, 0, 0, 0};
   auto lora_step = [&](int64_t j0, const uint4 (&rows8)[8]) {
     const int64_t jb = j0 + 8 * g;
-    const uint4 zv = (q < M && jb < r) ? *reinterpret_cast<const uint4*>(zl + q * r + jb) : make_uint4(0, 0, 0, 0);
+    const uint4 zv = (q < M && jb < r) ? *reinterpret_cast<const uint4*>(zl + q * rt + member * r + jb) : make_uint4(0, 0, 0, 0);
     uint4 cols8[8];
     transpose8x8_bf16(rows8, cols8);
 #pragma unroll
@@ -430,12 +446,29 @@ __global__ __launch_bounds__(256) void gemv_finish_kernel(const float* __restric
     load_b(j0, b0);
     lora_step(j0, b0);
   }
-  if (!out_ok) return;
+  if (!kTwo && !out_ok) return;
   float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
   fin_add8(v, pa, pb);
   for (int s0 = 8; s0 < splits; s0 += 8) {
     load_part(s0, pa, pb);
     fin_add8(v, pa, pb);
+  }
+  if constexpr (kTwo) {
+    __shared__ float us[2 * 64 * 9];   // U of the two strips, 8 values a lane (rows of 9: no bank is hit twice)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += c * accl[i][e];
+    float* mine = us + ((wave & 1) * 64 + lane) * 9;
+    if (member == 1) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mine[i] = v[i];
+    }
+    __syncthreads();
+    if (member == 1 || !out_ok) return;   // n_ok is the same for the eight lanes of a 64-column block
+    float u[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) u[i] = mine[i];
+    gated_store8<T, kGelu>(v, u, m, ncol, N, Y, keep);
+    return;
   }
   uint4 o;
   o.x = T::pack2(v[0] + c * accl[0][e], v[1] + c * accl[1][e]);
@@ -472,14 +505,46 @@ hipError_t launch_gemv(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_
   float* part = static_cast<float*>(part_ws);
   float* zpart = reinterpret_cast<float*>(static_cast<char*>(part_ws) + p.gv_part);
   Timer tm(QK_FWD_GEMV, stream);
-  hipLaunchKernelGGL(dtype == kDtypeF16 ? gemv_kernel<F16> : gemv_kernel<Bf16>, dim3(static_cast<unsigned>((pairs + 1) * p.gv_splits)), dim3(kGvWaves * 64), 0,
-                     stream, X, M, W, K, N, p.gv_rows_per_wave, pairs, part, A, r, zpart);
+  hipLaunchKernelGGL((dtype == kDtypeF16 ? gemv_kernel<F16, false> : gemv_kernel<Bf16, false>), dim3(static_cast<unsigned>((pairs + 1) * p.gv_splits)), dim3(kGvWaves * 64), 0,
+                     stream, X, M, W, K, N, p.gv_rows_per_wave, pairs, part, A, r, zpart, W);
   tm.stop();
   Timer te(QK_REDUCE, stream);
   const unsigned phases = static_cast<unsigned>(M < 4 ? M : 4);   // rows 4g + e, e < phases
-  hipLaunchKernelGGL(dtype == kDtypeF16 ? gemv_finish_kernel<F16> : gemv_finish_kernel<Bf16>, dim3(static_cast<unsigned>(cdiv(N, kFinCols)), phases), dim3(256), 0, stream,
+  hipLaunchKernelGGL((dtype == kDtypeF16 ? gemv_finish_kernel<F16, false, false> : gemv_finish_kernel<Bf16, false, false>), dim3(static_cast<unsigned>(cdiv(N, kFinCols)), phases), dim3(256), 0, stream,
                      static_cast<const float*>(part), static_cast<int>(p.gv_splits), M, N,
-                     static_cast<const float*>(zpart), Z, B, r, c, Y);
+                     static_cast<const float*>(zpart), Z, B, r, c, Y, GatedKeep{});
+  te.stop();
+  return hipGetLastError();
+}
+
+// The gated block's two weights share a launch: twice the strips, so half the
+// row ranges of one weight's plan.
+GatedGemvPlan plan_gated_gemv(int64_t M, int64_t K, int64_t F, int64_t r) {
+  const int64_t pairs = 2 * cdiv(F, 2 * kGvCols);
+  const int64_t groups = cdiv(QN_GV_WAVES, pairs * kGvWaves);
+  const int64_t rpw = round_up(cdiv(K, groups * 2), 64), splits = cdiv(K, 2 * rpw);
+  return GatedGemvPlan{rpw, splits, round_up(splits * M * 2 * F * 4, 256), round_up(splits * M * 2 * r * 4, 256)};
+}
+
+hipError_t launch_gated_gemv(int64_t M, int64_t K, int64_t F, int64_t r, const uint16_t* X, const NF4View* W,
+                             const uint16_t* A, const uint16_t* B, float c, bool gelu, uint16_t* H, uint16_t* Z,
+                             const GatedKeep& keep, void* ws, hipStream_t stream, int dtype) {
+  const GatedGemvPlan p = plan_gated_gemv(M, K, F, r);
+  const int64_t pairs = cdiv(F, 2 * kGvCols);
+  float* part = static_cast<float*>(ws);
+  float* zpart = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part);
+  Timer tm(QK_FWD_GEMV, stream);
+  hipLaunchKernelGGL((dtype == kDtypeF16 ? gemv_kernel<F16, true> : gemv_kernel<Bf16, true>),
+                     dim3(static_cast<unsigned>((2 * pairs + 1) * p.splits)), dim3(kGvWaves * 64), 0, stream, X, M,
+                     W[0], K, F, p.rows_per_wave, pairs, part, A, 2 * r, zpart, W[1]);
+  tm.stop();
+  Timer te(QK_REDUCE, stream);
+  const unsigned phases = static_cast<unsigned>(M < 4 ? M : 4);   // rows 4g + e, e < phases
+  auto* fin = dtype == kDtypeF16 ? (gelu ? gemv_finish_kernel<F16, true, true> : gemv_finish_kernel<F16, true, false>)
+                                 : (gelu ? gemv_finish_kernel<Bf16, true, true> : gemv_finish_kernel<Bf16, true, false>);
+  hipLaunchKernelGGL(fin, dim3(static_cast<unsigned>(cdiv(F, kFinCols / 2)), phases), dim3(256), 0, stream,
+                     static_cast<const float*>(part), static_cast<int>(p.splits), M, F,
+                     static_cast<const float*>(zpart), Z, B, r, c, H, keep);
   te.stop();
   return hipGetLastError();
 }

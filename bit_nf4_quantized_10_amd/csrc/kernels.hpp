@@ -81,7 +81,8 @@ hipError_t launch_merge(int64_t K, int64_t N, int64_t r, NF4View W, const void* 
 hipError_t launch_sgd(int64_t K, int64_t N, int64_t r, uint16_t* A, uint16_t* B, const float* dA, const float* dB,
                       float lr, float* A_master, float* B_master, hipStream_t stream, int dtype = 0);
 
-// Grouped linears sharing X (see layer.hip).
+// Grouped linears sharing X (see layer.hip).  dZ_lo (scratch, M x g r): dA is
+// formed from dZ before its rounding to 16 bits.
 int64_t grouped_fwd_workspace_bytes(int64_t M, int64_t K, int g, const int64_t* Ns, int64_t r);
 int64_t grouped_bwd_workspace_bytes(int64_t M, int64_t K, int g, const int64_t* Ns, int64_t r);
 hipError_t launch_grouped_fwd(int64_t M, int64_t K, int g, const int64_t* Ns, int64_t r, const uint16_t* X,
@@ -90,7 +91,8 @@ hipError_t launch_grouped_fwd(int64_t M, int64_t K, int g, const int64_t* Ns, in
 hipError_t launch_grouped_bwd(int64_t M, int64_t K, int g, const int64_t* Ns, int64_t r, const uint16_t* G,
                               const uint16_t* X, const uint16_t* Z, const NF4View* W, const uint16_t* A,
                               const uint16_t* B, float c, uint16_t* dX, void* dA, void* dB, void* ws,
-                              hipStream_t stream, int dtype = kDtypeBf16, bool grad16 = false, Act8View x8 = {});
+                              hipStream_t stream, int dtype = kDtypeBf16, bool grad16 = false, Act8View x8 = {},
+                              uint16_t* dZ_lo = nullptr);
 
 // Workspace needs (bytes) of the layer kernels; the C ABI adds them up.
 int64_t fwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t r);
@@ -110,11 +112,12 @@ SkinnyPlan plan_skinny(int64_t M, int64_t K, int64_t N, int64_t r);
 void lora_transposes(int64_t K, int64_t r, const uint16_t* A, uint16_t* At, int64_t N, const uint16_t* B, float c,
                      uint16_t* cbt, int64_t rb, int dtype, TJob out[2]);
 // Z = X A: the transposes above (one launch, unless pre_transposed: another
-// launch already ran them), then the split partials and their sum.
+// launch already ran them), then the split partials and their sum.  z_ext: also
+// c Z before its rounding as [hi | lo] (M x 2r, hi + lo to 2^-17).
 hipError_t launch_lora_down(int64_t M, int64_t K, int64_t r, const uint16_t* X, const uint16_t* A, uint16_t* Z,
                             const SkinnyPlan& p, void* at_ws, void* part_ws, hipStream_t stream, int64_t N = 0,
                             const uint16_t* B = nullptr, float c = 1.0f, uint16_t* cbt = nullptr, int64_t rb = 0,
-                            int dtype = 0, bool pre_transposed = false);
+                            int dtype = 0, bool pre_transposed = false, uint16_t* z_ext = nullptr);
 
 // Split plans of a group of g linears sharing X (column counts Ns[i], rank r
 // each); zp covers Z = X A over all g r columns.
@@ -126,11 +129,12 @@ struct GroupPlan {
 GroupPlan plan_grouped(int64_t M, int64_t K, int g, const int64_t* Ns, int64_t r);
 hipError_t launch_dz_grouped(int64_t M, int g, const int64_t* Ns, int64_t Ntot, int64_t r, const uint16_t* G,
                              const uint16_t* B, float c, uint16_t* dZ, const GroupPlan& gp, void* part_ws,
-                             hipStream_t stream, int dtype = 0, RdJob* defer = nullptr);
+                             hipStream_t stream, int dtype = 0, RdJob* defer = nullptr, uint16_t* dZ_lo = nullptr);
 hipError_t launch_colsums_grouped(int64_t M, int64_t K, int g, const int64_t* Ns, int64_t Ntot, int64_t r,
                                   const uint16_t* X, const uint16_t* G, const uint16_t* Z, const uint16_t* dZ, float c,
                                   void* dA, void* dB, const GroupPlan& gp, void* da_ws, void* db_ws,
-                                  hipStream_t stream, int dtype = 0, bool grad16 = false, Act8View x8 = {});
+                                  hipStream_t stream, int dtype = 0, bool grad16 = false, Act8View x8 = {},
+                                  const uint16_t* dZ_lo = nullptr);
 // Small-M forward (M <= 16) in two launches: the split-K partials of X Ŵ and
 // of Z = X A (extra workgroups of the same launch), then their fixed-order
 // sums, Z (written out) and Y = X Ŵ + c Z B.  part_ws: gv_part + gv_zpart.
@@ -190,6 +194,34 @@ hipError_t launch_fwd_dense_grouped(int64_t M, int64_t K, int64_t Ntot, int64_t 
 hipError_t launch_dx_dense(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t* G, const uint16_t* What,
                            const uint16_t* dZ, const uint16_t* A, uint16_t* dX, hipStream_t stream, int dtype = 0,
                            void* split_ws = nullptr);
+
+// The gated feed-forward front (gated.hip; up to 16 rows gemv.hip): W[0], W[1]
+// the K x F weights, A K x 2r, B r x 2F, H M x F (null in launch_gated_dense:
+// not wanted), Z M x 2r.
+struct GatedKeep;
+int64_t gated_fwd_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t r);
+int64_t gated_bwd_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t r);
+hipError_t launch_gated_fwd(int64_t M, int64_t K, int64_t F, int64_t r, const uint16_t* X, const NF4View* W,
+                            const uint16_t* A, const uint16_t* B, float c, bool gelu, uint16_t* H, uint16_t* Z,
+                            const GatedKeep& keep, void* ws, hipStream_t stream, int dtype);
+// kept: the forward's; with neither kept, G and U are computed again from X.
+hipError_t launch_gated_bwd(int64_t M, int64_t K, int64_t F, int64_t r, const uint16_t* dH, const uint16_t* X,
+                            Act8View x8, const uint16_t* Z, const GatedKeep& kept, const NF4View* W, const uint16_t* A,
+                            const uint16_t* B, float c, bool gelu, uint16_t* dX, void* dA, void* dB, void* ws,
+                            hipStream_t stream, int dtype, bool grad16);
+hipError_t launch_gated_dense(int64_t M, int64_t K, int64_t F, int64_t r, const uint16_t* X, const uint16_t* WhatT,
+                              const uint16_t* Zext, const uint16_t* Bt, bool gelu, uint16_t* H, const GatedKeep& keep,
+                              hipStream_t stream, int dtype, void* split_ws);
+hipError_t launch_gated_dy(int64_t M, int64_t F, const uint16_t* dH, const GatedKeep& kept, bool gelu, uint16_t* dY,
+                           hipStream_t stream, int dtype);
+// Up to 16 rows: split-K partials of both weights and of Z, then their sums.
+struct GatedGemvPlan {
+  int64_t rows_per_wave, splits, part, zpart;
+};
+GatedGemvPlan plan_gated_gemv(int64_t M, int64_t K, int64_t F, int64_t r);
+hipError_t launch_gated_gemv(int64_t M, int64_t K, int64_t F, int64_t r, const uint16_t* X, const NF4View* W,
+                             const uint16_t* A, const uint16_t* B, float c, bool gelu, uint16_t* H, uint16_t* Z,
+                             const GatedKeep& keep, void* ws, hipStream_t stream, int dtype);
 
 // Dequantize a K x N weight to the 16-bit compute type (dtype), either as
 // stored (K x N) or transposed (N x K).

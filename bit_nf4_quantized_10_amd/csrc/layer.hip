@@ -12,7 +12,10 @@
 //             same launch, before dA and dB; then a dense GEMM).
 // Either GEMM splits its reduction when its output has too few 256 x 256
 // tiles to occupy the device (plan_split), with a fixed-order sum after.
+#include <cmath>
+
 #include "common.hpp"
+#include "gated.hpp"
 #include "kernels.hpp"
 
 namespace qn {
@@ -186,7 +189,7 @@ hipError_t launch_grouped_fwd(int64_t M, int64_t K, int g, const int64_t* Ns, in
 hipError_t launch_grouped_bwd(int64_t M, int64_t K, int g, const int64_t* Ns, int64_t r, const uint16_t* G,
                               const uint16_t* X, const uint16_t* Z, const NF4View* W, const uint16_t* A,
                               const uint16_t* B, float c, uint16_t* dX, void* dA, void* dB, void* ws,
-                              hipStream_t stream, int dtype, bool grad16, Act8View x8) {
+                              hipStream_t stream, int dtype, bool grad16, Act8View x8, uint16_t* dZ_lo) {
   const GroupPlan gp = plan_grouped(M, K, g, Ns, r);
   int64_t Ntot = 0;
   for (int i = 0; i < g; ++i) Ntot += Ns[i];
@@ -198,7 +201,7 @@ hipError_t launch_grouped_bwd(int64_t M, int64_t K, int g, const int64_t* Ns, in
   // with dX wanted, member i's dZ sum rides along in member i's dequantize launch
   RdJob jz[kMaxGroupMembers];
   hipError_t e = launch_dz_grouped(M, g, Ns, Ntot, r, G, B, c, dz16, gp, base, stream, dtype,
-                                   dX != nullptr ? jz : nullptr);
+                                   dX != nullptr ? jz : nullptr, dZ_lo);
   if (e != hipSuccess) return e;
   if (dX != nullptr) {
     int64_t off = 0;
@@ -210,11 +213,99 @@ hipError_t launch_grouped_bwd(int64_t M, int64_t K, int g, const int64_t* Ns, in
     }
   }
   if ((e = launch_colsums_grouped(M, K, g, Ns, Ntot, r, X, G, Z, dz16, c, dA, dB, gp, da_ws, db_ws, stream, dtype,
-                                  grad16, x8)) != hipSuccess)
+                                  grad16, x8, dZ_lo)) != hipSuccess)
     return e;
   if (dX == nullptr) return hipGetLastError();
   return launch_dx_dense(M, K, Ntot, g * r, G, wd, dz16, A, dX, stream, dtype,
                          reinterpret_cast<char*>(wd) + align256(K * Ntot * 2));
+}
+
+// --------------------------------------------------- gated feed-forward front
+// The forward is a grouped linear of two members whose last kernel combines
+// them (gated.hip; up to 16 rows: gemv.hip).  The backward turns dH into the
+// grouped linear's dY = [dG | dU] and runs that linear's backward.
+int64_t gated_fwd_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t r) {
+  const int64_t z = align256(M * 2 * r * 2);
+  if (M <= 16) {
+    const GatedGemvPlan p = plan_gated_gemv(M, K, F, r);
+    return p.part + p.zpart + z;
+  }
+  const SkinnyPlan zp = plan_skinny(M, K, 2 * F, 2 * r);
+  return zp.at_bytes + zp.z_part + align256(2 * F * r * 2) + align256(2 * F * K * 2) + plan_split(M, 2 * F, K).part_bytes +
+         align256(M * 4 * r * 2) + z;
+}
+
+int64_t gated_bwd_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t r) {
+  const int64_t Ns[2] = {F, F};
+  const int64_t grouped = grouped_bwd_workspace_bytes(M, K, 2, Ns, r);
+  // G and U computed again: the forward's scratch and the kept pair
+  const int64_t again = gated_fwd_workspace_bytes(M, K, F, r) + align256(M * 2 * F * 2);
+  return align256(M * 2 * F * 2) + align256(M * 2 * r * 2) + (grouped > again ? grouped : again);
+}
+
+// H may be null only together with a 16-bit keep.  The adapter's term enters
+// the GEMM as c Z in two 16-bit parts over Bᵀ: G and U then carry
+// none of Z's rounding, which would move many of their 8-bit codes.
+static hipError_t gated_fwd(int64_t M, int64_t K, int64_t F, int64_t r, const uint16_t* X, const NF4View* W,
+                            const uint16_t* A, const uint16_t* B, float c, bool gelu, uint16_t* H, uint16_t* Z,
+                            const GatedKeep& keep, void* ws, hipStream_t stream, int dtype) {
+  char* base = static_cast<char*>(ws);
+  const SkinnyPlan zp = plan_skinny(M, K, 2 * F, 2 * r);
+  uint16_t* at = reinterpret_cast<uint16_t*>(base);
+  char* zpart = base + zp.at_bytes;
+  uint16_t* zext = reinterpret_cast<uint16_t*>(zpart + zp.z_part);
+  uint16_t* bt = reinterpret_cast<uint16_t*>(reinterpret_cast<char*>(zext) + align256(M * 4 * r * 2));
+  uint16_t* wt = reinterpret_cast<uint16_t*>(reinterpret_cast<char*>(bt) + align256(2 * F * r * 2));
+  // c is at most 1 in Z (which must not leave fp16's range for it); a power of
+  // two, exact, goes to B
+  float cz = c, cb = 1.0f;
+  if (std::isfinite(c) && std::fabs(c) > 1.0f) {
+    int ex;
+    cz = std::frexp(c, &ex);
+    cb = std::ldexp(1.0f, ex);
+  }
+  TJob tj[2];
+  lora_transposes(K, 2 * r, A, at, 2 * F, B, cb, bt, r, dtype, tj);
+  hipError_t e;
+  for (int i = 0; i < 2; ++i)
+    if ((e = launch_dequant_bf16(W[i], K, F, true, wt + i * F * K, stream, 0, dtype, i == 0 ? tj : nullptr)) != hipSuccess)
+      return e;
+  if ((e = launch_lora_down(M, K, 2 * r, X, A, Z, zp, base, zpart, stream, 2 * F, B, cz, bt, r, dtype, true, zext)) !=
+      hipSuccess)
+    return e;
+  return launch_gated_dense(M, K, F, r, X, wt, zext, bt, gelu, H, keep, stream, dtype,
+                            reinterpret_cast<char*>(wt) + align256(2 * F * K * 2));
+}
+
+hipError_t launch_gated_fwd(int64_t M, int64_t K, int64_t F, int64_t r, const uint16_t* X, const NF4View* W,
+                            const uint16_t* A, const uint16_t* B, float c, bool gelu, uint16_t* H, uint16_t* Z,
+                            const GatedKeep& keep, void* ws, hipStream_t stream, int dtype) {
+  if (Z == nullptr)
+    Z = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + gated_fwd_workspace_bytes(M, K, F, r) - align256(M * 2 * r * 2));
+  if (M <= 16) return launch_gated_gemv(M, K, F, r, X, W, A, B, c, gelu, H, Z, keep, ws, stream, dtype);
+  return gated_fwd(M, K, F, r, X, W, A, B, c, gelu, H, Z, keep, ws, stream, dtype);
+}
+
+hipError_t launch_gated_bwd(int64_t M, int64_t K, int64_t F, int64_t r, const uint16_t* dH, const uint16_t* X,
+                            Act8View x8, const uint16_t* Z, const GatedKeep& kept, const NF4View* W, const uint16_t* A,
+                            const uint16_t* B, float c, bool gelu, uint16_t* dX, void* dA, void* dB, void* ws,
+                            hipStream_t stream, int dtype, bool grad16) {
+  char* base = static_cast<char*>(ws);
+  uint16_t* dY = reinterpret_cast<uint16_t*>(base);
+  uint16_t* dZ_lo = reinterpret_cast<uint16_t*>(base + align256(M * 2 * F * 2));
+  char* rest = reinterpret_cast<char*>(dZ_lo) + align256(M * 2 * r * 2);
+  GatedKeep from = kept;
+  hipError_t e;
+  if (from.gu == nullptr && from.codes == nullptr) {
+    from.gu = reinterpret_cast<uint16_t*>(rest);
+    // the forward's kernels again, their Z at the end of the scratch
+    if ((e = launch_gated_fwd(M, K, F, r, X, W, A, B, c, gelu, nullptr, nullptr, from, rest + align256(M * 2 * F * 2),
+                              stream, dtype)) != hipSuccess)
+      return e;
+  }
+  if ((e = launch_gated_dy(M, F, dH, from, gelu, dY, stream, dtype)) != hipSuccess) return e;
+  const int64_t Ns[2] = {F, F};
+  return launch_grouped_bwd(M, K, 2, Ns, r, dY, X, Z, W, A, B, c, dX, dA, dB, rest, stream, dtype, grad16, x8, dZ_lo);
 }
 
 }  // namespace qn

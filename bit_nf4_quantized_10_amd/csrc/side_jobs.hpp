@@ -64,14 +64,32 @@ struct RdJob {
   int64_t nblk;
   int64_t out_ld;   // row stride of the output (cols, or rows when transposed, for a dense result)
   int f16;          // the 16-bit output is fp16 (else bf16)
+  // What the 16-bit rounding of ext_scale * sum leaves out, as more 16-bit
+  // matrices of row stride ext_ld: `hi` the rounding itself (null where
+  // out_bf16 is it), `lo` the rounded rest, so hi + lo holds the sum to 2^-17.
+  uint16_t* ext_hi = nullptr;
+  uint16_t* ext_lo = nullptr;
+  int64_t ext_ld = 0;
+  float ext_scale = 1.0f;
 };
 
 inline RdJob make_rdjob(const float* part, int64_t splits, int64_t rows, int64_t cols, float scale, bool transpose,
                         float* out_f32, uint16_t* out_16, int f16) {
   int64_t blocks = (rows * cols + 255) / 256;
   if (blocks > 2048) blocks = 2048;
-  return RdJob{part, splits, rows, cols, scale, transpose ? 1 : 0, out_f32, out_16, blocks, transpose ? rows : cols,
-               f16};
+  RdJob j{};
+  j.part = part;
+  j.splits = splits;
+  j.rows = rows;
+  j.cols = cols;
+  j.scale = scale;
+  j.transpose = transpose ? 1 : 0;
+  j.out_f32 = out_f32;
+  j.out_bf16 = out_16;
+  j.nblk = blocks;
+  j.out_ld = transpose ? rows : cols;
+  j.f16 = f16;
+  return j;
 }
 
 // Block blk of job J (grid-stride over J.nblk blocks).
@@ -92,6 +110,15 @@ __device__ __forceinline__ void reduce_block(const RdJob& J, int64_t blk) {
     const int64_t o = J.transpose ? (i % J.cols) * J.out_ld + i / J.cols : (i / J.cols) * J.out_ld + i % J.cols;
     if (J.out_f32) J.out_f32[o] = s;
     if (J.out_bf16) J.out_bf16[o] = half_of(s, J.f16);
+    if (J.ext_lo) {
+      const int64_t x = (i / J.cols) * J.ext_ld + i % J.cols;
+      const float v = s * J.ext_scale;
+      const uint16_t hi = half_of(v, J.f16);
+      if (J.ext_hi) J.ext_hi[x] = hi;
+      // an infinite rounding has no rest
+      const float rest = v - widen_of(hi, J.f16);
+      J.ext_lo[x] = half_of(__builtin_fabsf(rest) < __builtin_inff() ? rest : 0.0f, J.f16);
+    }
   }
 }
 

@@ -180,6 +180,7 @@ constexpr int kCsSlots = QN_CS_SLOTS;
 constexpr int kCsSlot = 2 * 16 * 128;
 constexpr int kCsRing = kCsSlots * kCsSlot;
 constexpr int kCsBlock = 64 * 64 * 4;   // one wave's 64 x 64 fp32 sums, for the epilogue
+static_assert(kCsRing >= 3 * 2048, "column sums: a staged step (act, v, v_lo) lives in the wave's own ring");
 static_assert(kCsRing >= kCsBlock, "column sums: each wave's epilogue block lives in its own ring");
 constexpr int kCsLds = 4 * kCsRing;
 
@@ -199,6 +200,7 @@ struct CsJob {
   const int8_t* q8 = nullptr;
   const uint16_t* am8 = nullptr;
   int64_t nb8 = 0;
+  const uint16_t* v_lo = nullptr;   // what v's 16-bit rounding left out (same shape and stride), or none
 };
 
 typedef short v4i16 __attribute__((ext_vector_type(4)));
@@ -249,87 +251,109 @@ __device__ __forceinline__ void cs_block(float* blk, bool tr, const f32x16 (&acc
       }
 }
 
-// The streaming loop of a job whose activations are kept in 8 bits.  A
-// 64-column block is one checkpoint block per token, so a step is 16 rows of
+// The streaming loop of a job whose operands pass through registers: one whose
+// activations are kept in 8 bits, or whose v comes with a second matrix v_lo of
+// what its rounding left out (the sums are then act^T (v + v_lo)).
+// A 64-column block is one checkpoint block per token, so a step is 16 rows of
 // 64 code bytes (one 16-byte load a lane: row lane/4, columns 16 (lane & 3)
-// ..), each with one magnitude, and 16 rows of v (two loads a lane).  kCs8Depth
-// steps are in flight in registers; a step is decoded to the 16-bit values
+// ..), each with one magnitude, and 16 rows of v (two loads a lane).  kCsDepth
+// steps are in flight; a step is decoded to the 16-bit values
 // RNE(q fl32(a / 127)) on its way into the wave's own LDS slot, from where the
-// transposing reads and products are those of the 16-bit loop: the sums have
+// transposing reads and products are those of the plain loop: the sums have
 // the same bits as with the decoded matrix.
 #ifndef QN_CS8_DEPTH
 #define QN_CS8_DEPTH 4
 #endif
-constexpr int kCs8Depth = QN_CS8_DEPTH;
-struct Cs8Step {
-  uint4 q, v[2];
+constexpr int kCsDepth = QN_CS8_DEPTH;
+template <bool kA8, bool kLo>
+struct CsStep {
+  uint4 a[kA8 ? 1 : 2], v[2], lo[kLo ? 2 : 1];
   uint32_t am;
 };
-template <class T>
-__device__ __forceinline__ void colsum_act8(const CsJob& J, int64_t M, int64_t c0, int64_t jb, int64_t wb, int64_t we,
-                                            int64_t nsteps, int lane, char* slot, const int (&toff)[2][2],
-                                            f32x16 (&acc)[2][2]) {
+template <class T, bool kA8, bool kLo>
+__device__ __forceinline__ void colsum_staged(const CsJob& J, int64_t M, int64_t c0, int64_t jb, int64_t wb, int64_t we,
+                                              int64_t nsteps, int lane, char* slot, const int (&toff)[2][2],
+                                              f32x16 (&acc)[2][2]) {
   const int64_t nb = J.nb8;
-  const Rsrc rq = make_rsrc(J.q8, M * J.cols), rm = make_rsrc(J.am8, M * nb * 2);
+  const Rsrc ra = kA8 ? make_rsrc(J.q8, M * J.cols) : make_rsrc(J.act, ((M - 1) * J.ld + J.cols) * 2);
+  const Rsrc rm = make_rsrc(J.am8, kA8 ? M * nb * 2 : 0);
   const Rsrc rv = make_rsrc(J.v, ((M - 1) * J.v_ld + J.r) * 2);
+  const Rsrc rl = make_rsrc(J.v_lo, kLo ? ((M - 1) * J.v_ld + J.r) * 2 : 0);
   const int row = lane >> 2, quarter = lane & 3;
-  // columns past the row's end only reach sums that are not stored
+  // 8 bits: columns past the row's end only reach sums that are not stored
   const uint32_t qv = c0 + 16 * quarter < J.cols
                           ? static_cast<uint32_t>((wb + row) * J.cols + c0 + 16 * quarter) : kMasked;
   const uint32_t mv = static_cast<uint32_t>(((wb + row) * nb + (c0 >> 6)) * 2);
-  uint32_t vv[2];
-  int vdst[2];
+  uint32_t av[2], vv[2];
+  int dst[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int R = 8 * i + (lane >> 3), c = lane & 7;
+    av[i] = c0 + 8 * c < J.cols ? static_cast<uint32_t>(((wb + R) * J.ld + c0 + 8 * c) * 2) : kMasked;
     vv[i] = jb + 8 * c < J.r ? static_cast<uint32_t>(((wb + R) * J.v_ld + jb + 8 * c) * 2) : kMasked;
-    vdst[i] = 2048 + cs_off(R, c);
+    dst[i] = cs_off(R, c);
   }
   const int rows_left = static_cast<int>(we - wb);
-  auto load = [&](Cs8Step& S, int64_t s) {
+  auto load = [&](CsStep<kA8, kLo>& S, int64_t s) {
     const int m = static_cast<int>(16 * s);   // steps past the last one read nothing: all masked
-    const bool in = m + row < rows_left;
-    S.q = ld_b128(rq, in && qv != kMasked ? qv + static_cast<uint32_t>(m * J.cols) : kMasked);
-    S.am = __builtin_amdgcn_raw_buffer_load_b16(rm, in ? mv + static_cast<uint32_t>(m * nb * 2) : kMasked, 0, 0);
+    if (kA8) {
+      const bool in = m + row < rows_left;
+      S.a[0] = ld_b128(ra, in && qv != kMasked ? qv + static_cast<uint32_t>(m * J.cols) : kMasked);
+      S.am = __builtin_amdgcn_raw_buffer_load_b16(rm, in ? mv + static_cast<uint32_t>(m * nb * 2) : kMasked, 0, 0);
+    }
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      S.v[i] = ld_b128(rv, (m + 8 * i + (lane >> 3) < rows_left && vv[i] != kMasked)
-                               ? vv[i] + static_cast<uint32_t>(m * J.v_ld * 2) : kMasked);
+    for (int i = 0; i < 2; ++i) {
+      const bool in = m + 8 * i + (lane >> 3) < rows_left;
+      if (!kA8) S.a[i] = ld_b128(ra, in && av[i] != kMasked ? av[i] + static_cast<uint32_t>(m * J.ld * 2) : kMasked);
+      const uint32_t off = in && vv[i] != kMasked ? vv[i] + static_cast<uint32_t>(m * J.v_ld * 2) : kMasked;
+      S.v[i] = ld_b128(rv, off);
+      if (kLo) S.lo[i] = ld_b128(rl, off);
+    }
   };
-  Cs8Step S[kCs8Depth];
+  CsStep<kA8, kLo> S[kCsDepth];
 #pragma unroll
-  for (int u = 0; u < kCs8Depth; ++u) load(S[u], u);
-  for (int64_t s0 = 0; s0 < nsteps; s0 += kCs8Depth) {
+  for (int u = 0; u < kCsDepth; ++u) load(S[u], u);
+  for (int64_t s0 = 0; s0 < nsteps; s0 += kCsDepth) {
 #pragma unroll
-    for (int u = 0; u < kCs8Depth; ++u) {
+    for (int u = 0; u < kCsDepth; ++u) {
       if (s0 + u >= nsteps) break;
-      const float step = act8_step<T>(S[u].am & 0xffffu);
-      const uint2 d0 = act8_values4<T>(S[u].q.x, step), d1 = act8_values4<T>(S[u].q.y, step);
-      const uint2 d2 = act8_values4<T>(S[u].q.z, step), d3 = act8_values4<T>(S[u].q.w, step);
-      *reinterpret_cast<uint4*>(slot + cs_off(row, 2 * quarter)) = make_uint4(d0.x, d0.y, d1.x, d1.y);
-      *reinterpret_cast<uint4*>(slot + cs_off(row, 2 * quarter + 1)) = make_uint4(d2.x, d2.y, d3.x, d3.y);
-      *reinterpret_cast<uint4*>(slot + vdst[0]) = S[u].v[0];
-      *reinterpret_cast<uint4*>(slot + vdst[1]) = S[u].v[1];
-      load(S[u], s0 + u + kCs8Depth);
+      if (kA8) {
+        const float step = act8_step<T>(S[u].am & 0xffffu);
+        const uint2 d0 = act8_values4<T>(S[u].a[0].x, step), d1 = act8_values4<T>(S[u].a[0].y, step);
+        const uint2 d2 = act8_values4<T>(S[u].a[0].z, step), d3 = act8_values4<T>(S[u].a[0].w, step);
+        *reinterpret_cast<uint4*>(slot + cs_off(row, 2 * quarter)) = make_uint4(d0.x, d0.y, d1.x, d1.y);
+        *reinterpret_cast<uint4*>(slot + cs_off(row, 2 * quarter + 1)) = make_uint4(d2.x, d2.y, d3.x, d3.y);
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (!kA8) *reinterpret_cast<uint4*>(slot + dst[i]) = S[u].a[i];
+        *reinterpret_cast<uint4*>(slot + 2048 + dst[i]) = S[u].v[i];
+        if (kLo) *reinterpret_cast<uint4*>(slot + 4096 + dst[i]) = S[u].lo[i];
+      }
+      load(S[u], s0 + u + kCsDepth);
       // LDS operations of one wave complete in order, and the slot is its own
       asm volatile("" ::: "memory");
-      typename T::v8 fa[2], fv[2];
+      typename T::v8 fa[2], fv[2], fl[2];
 #pragma unroll
       for (int ti = 0; ti < 2; ++ti) {
         fa[ti] = tr_read2<T>(slot + toff[ti][0], slot + toff[ti][1]);
         fv[ti] = tr_read2<T>(slot + 2048 + toff[ti][0], slot + 2048 + toff[ti][1]);
+        if (kLo) fl[ti] = tr_read2<T>(slot + 4096 + toff[ti][0], slot + 4096 + toff[ti][1]);
       }
       asm volatile("" ::: "memory");
 #pragma unroll
       for (int vj = 0; vj < 2; ++vj)
 #pragma unroll
-        for (int ci = 0; ci < 2; ++ci) acc[vj][ci] = T::mfma32(fv[vj], fa[ci], acc[vj][ci]);
+        for (int ci = 0; ci < 2; ++ci) {
+          acc[vj][ci] = T::mfma32(fv[vj], fa[ci], acc[vj][ci]);
+          if (kLo) acc[vj][ci] = T::mfma32(fl[vj], fa[ci], acc[vj][ci]);
+        }
     }
   }
 }
 
-// kA8: some job's activations are kept in 8 bits.
-template <class T, bool kA8>
+// kStaged: some job's operands pass through registers (colsum_staged).
+template <class T, bool kStaged>
 __global__ __launch_bounds__(256) void colsum_kernel(CsJobs jobs, int64_t M) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   int64_t blk = blockIdx.x;
@@ -394,10 +418,12 @@ __global__ __launch_bounds__(256) void colsum_kernel(CsJobs jobs, int64_t M) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
   constexpr int S = kCsSlots;
-  const bool a8 = kA8 && J.q8 != nullptr;
-  const int64_t nsteps16 = a8 ? 0 : nsteps;
-  if constexpr (kA8) {
-    if (a8) colsum_act8<T>(J, M, c0, jb, wb, we, nsteps, lane, ring, toff, acc);
+  const bool a8 = kStaged && J.q8 != nullptr, lo = kStaged && J.v_lo != nullptr;
+  const int64_t nsteps16 = a8 || lo ? 0 : nsteps;
+  if constexpr (kStaged) {
+    if (a8 && lo) colsum_staged<T, true, true>(J, M, c0, jb, wb, we, nsteps, lane, ring, toff, acc);
+    else if (a8) colsum_staged<T, true, false>(J, M, c0, jb, wb, we, nsteps, lane, ring, toff, acc);
+    else if (lo) colsum_staged<T, false, true>(J, M, c0, jb, wb, we, nsteps, lane, ring, toff, acc);
   }
   for (int x = 0; x < S - 1; ++x)
     if (x < nsteps16) copy(x, x);
@@ -520,28 +546,28 @@ hipError_t launch_rowsum(const uint16_t* act, const uint16_t* wt, int64_t M, int
   return dtype == kDtypeF16 ? rowsum_launch_t<F16>(a, splits, stream) : rowsum_launch_t<Bf16>(a, splits, stream);
 }
 
-template <class T, bool kA8>
+template <class T, bool kStaged>
 hipError_t colsum_launch_t(const CsJobs& jobs, int64_t M, hipStream_t stream) {
   // raised once per process; the initialisation of a function-local static
   // is thread-safe, so concurrent first calls do not race
-  static const hipError_t lds_limit = hipFuncSetAttribute(reinterpret_cast<const void*>(&colsum_kernel<T, kA8>),
+  static const hipError_t lds_limit = hipFuncSetAttribute(reinterpret_cast<const void*>(&colsum_kernel<T, kStaged>),
                                                           hipFuncAttributeMaxDynamicSharedMemorySize, kCsLds);
   if (lds_limit != hipSuccess) return lds_limit;
   int64_t blocks = 0;
   for (int i = 0; i < kCsJobs; ++i) blocks += jobs.j[i].nblk;
-  hipLaunchKernelGGL((colsum_kernel<T, kA8>), dim3(static_cast<unsigned>(blocks)), dim3(256), kCsLds, stream, jobs, M);
+  hipLaunchKernelGGL((colsum_kernel<T, kStaged>), dim3(static_cast<unsigned>(blocks)), dim3(256), kCsLds, stream, jobs, M);
   return hipGetLastError();
 }
 
 // jobs[0 .. n-1] (n <= kCsJobs) in one launch.
 hipError_t launch_colsum(const CsJob* jobs, int n, int64_t M, hipStream_t stream, int dtype) {
   CsJobs js{};
-  bool a8 = false;
+  bool staged = false;
   for (int i = 0; i < n; ++i) {
     js.j[i] = jobs[i];
-    a8 = a8 || jobs[i].q8 != nullptr;
+    staged = staged || jobs[i].q8 != nullptr || jobs[i].v_lo != nullptr;
   }
-  if (a8) return dtype == kDtypeF16 ? colsum_launch_t<F16, true>(js, M, stream) : colsum_launch_t<Bf16, true>(js, M, stream);
+  if (staged) return dtype == kDtypeF16 ? colsum_launch_t<F16, true>(js, M, stream) : colsum_launch_t<Bf16, true>(js, M, stream);
   return dtype == kDtypeF16 ? colsum_launch_t<F16, false>(js, M, stream) : colsum_launch_t<Bf16, false>(js, M, stream);
 }
 
@@ -583,7 +609,8 @@ void lora_transposes(int64_t K, int64_t r, const uint16_t* A, uint16_t* At, int6
 
 hipError_t launch_lora_down(int64_t M, int64_t K, int64_t r, const uint16_t* X, const uint16_t* A, uint16_t* Z,
                             const SkinnyPlan& p, void* at_ws, void* part_ws, hipStream_t stream, int64_t N,
-                            const uint16_t* B, float c, uint16_t* cbt, int64_t rb, int dtype, bool pre_transposed) {
+                            const uint16_t* B, float c, uint16_t* cbt, int64_t rb, int dtype, bool pre_transposed,
+                            uint16_t* z_ext) {
   uint16_t* At = static_cast<uint16_t*>(at_ws);
   if (!pre_transposed) {
     TJob tj[2];
@@ -596,7 +623,13 @@ hipError_t launch_lora_down(int64_t M, int64_t K, int64_t r, const uint16_t* X, 
   hipError_t e = launch_rowsum(X, At, M, r, K, p.z_splits, p.z_per, part, stream, 0, 0, dtype);
   tm.stop();
   if (e != hipSuccess) return e;
-  const RdJob jz = rdjob(part, p.z_splits, M, r, 1.0f, false, nullptr, Z, dtype);
+  RdJob jz = rdjob(part, p.z_splits, M, r, 1.0f, false, nullptr, Z, dtype);
+  if (z_ext != nullptr) {
+    jz.ext_hi = z_ext;
+    jz.ext_lo = z_ext + r;
+    jz.ext_ld = 2 * r;
+    jz.ext_scale = c;
+  }
   return launch_reduce(jz, nullptr, stream);
 }
 
@@ -684,7 +717,7 @@ GroupPlan plan_grouped(int64_t M, int64_t K, int g, const int64_t* Ns, int64_t r
 // With defer != nullptr the g sums are not launched but returned there.
 hipError_t launch_dz_grouped(int64_t M, int g, const int64_t* Ns, int64_t Ntot, int64_t r, const uint16_t* G,
                              const uint16_t* B, float c, uint16_t* dZ, const GroupPlan& gp, void* part_ws,
-                             hipStream_t stream, int dtype, RdJob* defer) {
+                             hipStream_t stream, int dtype, RdJob* defer, uint16_t* dZ_lo) {
   int64_t off = 0;
   for (int i = 0; i < g; ++i) {
     float* part = reinterpret_cast<float*>(static_cast<char*>(part_ws) + gp.dz_off[i]);
@@ -695,6 +728,10 @@ hipError_t launch_dz_grouped(int64_t M, int g, const int64_t* Ns, int64_t Ntot, 
     if (e != hipSuccess) return e;
     RdJob jz = rdjob(part, gp.dz_splits[i], M, r, c, false, nullptr, dZ + i * r, dtype);
     jz.out_ld = g * r;
+    if (dZ_lo != nullptr) {
+      jz.ext_lo = dZ_lo + i * r;
+      jz.ext_ld = g * r;
+    }
     if (defer != nullptr) defer[i] = jz;
     else if ((e = launch_reduce(jz, nullptr, stream)) != hipSuccess) return e;
     off += Ns[i];
@@ -707,12 +744,13 @@ hipError_t launch_dz_grouped(int64_t M, int g, const int64_t* Ns, int64_t Ntot, 
 hipError_t launch_colsums_grouped(int64_t M, int64_t K, int g, const int64_t* Ns, int64_t Ntot, int64_t r,
                                   const uint16_t* X, const uint16_t* G, const uint16_t* Z, const uint16_t* dZ, float c,
                                   void* dA, void* dB, const GroupPlan& gp, void* da_ws, void* db_ws,
-                                  hipStream_t stream, int dtype, bool grad16, Act8View x8) {
+                                  hipStream_t stream, int dtype, bool grad16, Act8View x8, const uint16_t* dZ_lo) {
   const int64_t rt = g * r;
   CsJob jobs[kMaxGroupMembers + 1];
   RdJob rds[kMaxGroupMembers + 1];
   jobs[0] = CsJob{X, K, K, dZ, static_cast<float*>(da_ws), cdiv(K, 64), cdiv(rt, 64), gp.cs_per, 0, rt, rt};
   set_act8(jobs[0], x8);
+  jobs[0].v_lo = dZ_lo;
   rds[0] = grad_job(static_cast<float*>(da_ws), gp.cs_splits, K, rt, 1.0f, false, dA, grad16, dtype);
   int64_t off = 0;
   for (int i = 0; i < g; ++i) {

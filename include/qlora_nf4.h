@@ -295,6 +295,42 @@ int qlora_linear_bwd_ex(int compute_dtype, int grad_dtype, int64_t M, int64_t K,
                         const nf4_state_t* W, const uint16_t* A, const uint16_t* B, float c, uint16_t* dX, void* dA,
                         void* dB, void* workspace, int64_t workspace_bytes, void* stream);
 
+/* The gated feed-forward front: two linears of one input and the gated
+ * activation of their outputs,
+ *   [Zg | Zu] = X A,  G = X Ŵ0 + c Zg Bg,  U = X Ŵ1 + c Zu Bu,  H = act(G) * U,
+ * act one of NF4_ACT_*.  X: M x K, W: host array of two states of K x F
+ * weights (gate, up), A = [Ag | Au] (K x 2r), B = [Bg | Bu] (r x 2F), Z M x 2r
+ * (the backward's; may be NULL), H M x F, all of compute_dtype.  H is formed
+ * from the fp32 sums and rounded once.  For the backward G and U can be kept
+ * side by side ([G | U], M x 2F): rounded to 16 bits in GU, or that rounding
+ * as an 8-bit checkpoint in GU8 (act8_t with cols = 2F: the bits act8_encode
+ * makes of GU).  At most one of the two is given; with neither, nothing is
+ * kept.  Requirements: F % 64 == 0, K % 8 == 0, r % 8 == 0, r <= 128, and
+ * qlora_linear_fwd's on (M, K, 2F, 2r); all pointers 16-byte aligned
+ * (GU8->absmax 2-byte); workspace 256-byte aligned, at least fwd_bytes.  M <= 16
+ * reads the packed weights once, as a dequant-GEMV; above, both weights are
+ * dequantized into the workspace and multiplied by one GEMM whose epilogue is
+ * the activation. */
+#define NF4_ACT_SILU 0   /* g / (1 + e^-g)                                                 */
+#define NF4_ACT_GELU 1   /* the tanh form 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)))   */
+int qlora_gated_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t r, int64_t* fwd_bytes, int64_t* bwd_bytes);
+int qlora_gated_fwd(int compute_dtype, int act, int64_t M, int64_t K, int64_t F, int64_t r, const uint16_t* X,
+                    const nf4_state_t* W, const uint16_t* A, const uint16_t* B, float c, uint16_t* H, uint16_t* Z,
+                    uint16_t* GU, const act8_t* GU8, void* workspace, int64_t workspace_bytes, void* stream);
+/* Its backward given dH (M x F):
+ *   dG = dH U act'(G), dU = dH act(G) (rounded to 16 bits), then the grouped
+ *   linear's backward of dY = [dG | dU]: dZ_i = c dY_i B_iᵀ, dA = Xᵀ [dZg | dZu],
+ *   dB = [c Zgᵀ dG | c Zuᵀ dU], dX = sum_i (dY_i Ŵ_iᵀ + dZ_i A_iᵀ) (skipped when NULL).
+ * G and U come from GU or GU8, whichever the forward filled; with neither they
+ * are computed again from X (one more forward product).  The input is X
+ * in 16 bits or X8 in 8 (exactly one; X8 needs GU or GU8).  Z is required.
+ * grad_dtype as in qlora_linear_bwd_ex; the rest as the forward, workspace at
+ * least bwd_bytes. */
+int qlora_gated_bwd(int compute_dtype, int act, int grad_dtype, int64_t M, int64_t K, int64_t F, int64_t r,
+                    const uint16_t* dH, const uint16_t* X, const act8_t* X8, const uint16_t* Z, const uint16_t* GU,
+                    const act8_t* GU8, const nf4_state_t* W, const uint16_t* A, const uint16_t* B, float c,
+                    uint16_t* dX, void* dA, void* dB, void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Synchronise `stream`, then copy the device status word to *host_value.
  * Returns NF4_EHIP if the copy fails, else NF4_OK. */
 int nf4_status_read(const int32_t* status, int32_t* host_value, void* stream);
@@ -316,7 +352,9 @@ int nf4_status_read(const int32_t* status, int32_t* host_value, void* stream);
 #define QK_SGD          13  /* adapter SGD step                          */
 #define QK_ACT8_ENCODE  14  /* 8-bit activation checkpoint               */
 #define QK_ACT8_DECODE  15  /* its 16-bit values                         */
-#define QK_NUM_KERNELS  16
+#define QK_GATED_FWD    16  /* gated block's GEMM with its activation    */
+#define QK_GATED_DY     17  /* dG and dU from dH                         */
+#define QK_NUM_KERNELS  18
 
 /* When enabled, the library records a pair of hipEvents on the launch
  * stream around every launch of kernel `kernel_id`.  qlora_timer_read

@@ -1,0 +1,232 @@
+"""The gated feed-forward front on the GPU against its 64-bit reference: both
+activations, both types, the decode, split and unsplit paths, everything the
+backward may be given.  Bounds are elementwise and counted from the roundings:
+half a step (d) for every value held in 16 bits on the way, 2^-24 per added
+term for fp32 sums."""
+import numpy as np
+import pytest
+
+import bit_nf4_quantized_10_amd as qn
+from oracle import nf4_oracle as o
+from oracle import ops_oracle as oo
+from tests.gpu_util import dev_f32, host, say
+
+pytestmark = pytest.mark.gpu
+HALF = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+# fp16 values below its normal range are off by up to half its smallest step
+TINY = {"bf16": 0.0, "f16": 2.0 ** -25}
+F32 = 2.0 ** -24
+ACT = 1e-5      # exp2, reciprocal and the argument's fp32 rounding: below 1e-5 for |argument| < 80
+
+
+def _torch_type(name):
+    import torch
+    return {"bf16": torch.bfloat16, "f16": torch.float16}[name]
+
+
+def _dev(x, name):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(x, dtype=np.float32)).to(_torch_type(name)).cuda()
+
+
+class Case:
+    def __init__(self, M, K, F, r, name, c=0.5, single=False, seed=None):
+        rng = np.random.default_rng(M * 31 + K + F if seed is None else seed)
+        self.M, self.K, self.F, self.r, self.c, self.name = M, K, F, r, c, name
+        self.W, self.states = [], []
+        for _ in range(2):
+            w = (rng.standard_normal((K, F)) / np.sqrt(K) * 1.5).astype(np.float32)
+            state, status = qn.nf4_quantize(dev_f32(w), double_quant=not single)
+            assert qn.nf4_status_read(status) == 0
+            self.states.append(state)
+            self.W.append(host(qn.nf4_dequantize(state, name)).reshape(K, F).astype(np.float64))
+        self.X, self.A, self.B, self.dH = (_dev(rng.standard_normal(s) * std, name) for s, std in (
+            ((M, K), 1.0), ((K, 2 * r), 1.0 / np.sqrt(K)), ((r, 2 * F), 0.3), ((M, F), 1.0)))
+        self.x, self.a, self.b, self.dh = (host(t).astype(np.float64) for t in (self.X, self.A, self.B, self.dH))
+
+    def forward(self, act, save="none", **kw):
+        return qn.qlora_gated_fwd(self.X, self.states, self.A, self.B, self.c, self.K, self.F, act=act, save=save, **kw)
+
+    def backward(self, act, X, Z, saved, **kw):
+        return qn.qlora_gated_bwd(self.dH, X, Z, saved, self.states, self.A, self.B, self.c, self.K, self.F, act=act, **kw)
+
+
+def _close(got, want, bound, what):
+    got = host(got).astype(np.float64)
+    assert np.isfinite(got).all(), what
+    worst = np.max(np.abs(got - want) / bound)
+    say(f"  {what}: worst error / bound {worst:.3f}")
+    assert worst <= 1.0, what
+
+
+def _check_forward(k, act, H, Z):
+    d, n = HALF[k.name], k.K + 2 * k.r
+    H0, Z0, G0, U0 = oo.gated_forward(k.x, k.W[0], k.W[1], k.a, k.b, k.c, act)
+    zabs = np.abs(k.x) @ np.abs(k.a)
+    _close(Z, Z0, d * np.abs(Z0) + n * F32 * zabs + TINY[k.name] + 1e-30, "Z")
+    dG = []
+    for i in range(2):
+        b, z = np.abs(k.b[:, i * k.F:(i + 1) * k.F]), zabs[:, i * k.r:(i + 1) * k.r]
+        z16 = np.abs(Z0[:, i * k.r:(i + 1) * k.r])
+        # Z and c B are rounded to 16 bits, the sums are fp32
+        dG.append(k.c * (z16 @ b) * (2.01 * d) + (n + 2) * F32 * (np.abs(k.x) @ np.abs(k.W[i]) + k.c * (z @ b))
+                  + k.c * TINY[k.name] * (b.sum(0)[None] + z16.sum(1)[:, None]))
+    f = oo.act(act, G0)[0]
+    # |act'| <= 1.13
+    bound = 1.13 * dG[0] * (np.abs(U0) + dG[1]) + np.abs(f) * dG[1] + (d + ACT) * (np.abs(H0) + dG[0] * dG[1]) \
+        + 1e-6 * np.abs(U0) + TINY[k.name] + 1e-30
+    _close(H, H0, bound, "H")
+
+
+def _check_backward(k, act, x, Z, G, U, got, gdt):
+    d = HALF[k.name]
+    z = host(Z).astype(np.float64)
+    dX0, dA0, dB0 = oo.gated_backward(k.dh, x, z, G, U, k.W[0], k.W[1], k.a, k.b, k.c, act)
+    f, df = oo.act(act, G)
+    dY = (np.abs(k.dh * U * df), np.abs(k.dh * f))
+    # each of dG, dU: the activation's error, at most 2e-5 of the factors, and one rounding
+    eY = (d * dY[0] + 2e-5 * np.abs(k.dh * U) + TINY[k.name], d * dY[1] + 2e-5 * np.abs(k.dh * G) + TINY[k.name])
+    dX = np.zeros_like(dX0)
+    dA, dB = [], []
+    n = 2 * k.F + 2 * k.r + 8
+    for i in range(2):
+        w, b = np.abs(k.W[i]), np.abs(k.b[:, i * k.F:(i + 1) * k.F])
+        a, zi = np.abs(k.a[:, i * k.r:(i + 1) * k.r]), np.abs(z[:, i * k.r:(i + 1) * k.r])
+        zabs, ez = k.c * (dY[i] @ b.T), k.c * (eY[i] @ b.T)
+        ez = ez * 1.01 + (d + n * F32) * zabs + TINY[k.name]
+        dX += 1.01 * (eY[i] @ w.T + ez @ a.T) + n * F32 * (dY[i] @ w.T + zabs @ a.T)
+        dA.append(np.abs(x).T @ ez + (k.M + 8) * F32 * (np.abs(x).T @ zabs))
+        dB.append(k.c * (zi.T @ eY[i] + (k.M + 8) * F32 * (zi.T @ dY[i])))
+    dA, dB = np.hstack(dA), np.hstack(dB)
+    out16 = d if gdt is not None else F32
+    if got[0] is not None:
+        _close(got[0], dX0, dX + d * (np.abs(dX0) + dX) + TINY[k.name] + 1e-30, "dX")
+    _close(got[1], dA0, dA + out16 * (np.abs(dA0) + dA) + TINY[k.name] + 1e-30, "dA")
+    _close(got[2], dB0, dB + out16 * (np.abs(dB0) + dB) + TINY[k.name] + 1e-30, "dB")
+
+
+SHAPES = [(1, 64, 64, 8), (2, 1032, 320, 24), (5, 72, 128, 16), (16, 264, 192, 128), (16, 2056, 704, 40),
+          (17, 136, 64, 8), (40, 1032, 320, 24), (100, 4096, 1088, 16), (191, 256, 256, 128), (200, 264, 448, 16),
+          (300, 520, 704, 40), (257, 2056, 192, 72), (520, 96, 1344, 8)]
+
+
+@pytest.mark.parametrize("name", ["bf16", "f16"])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("M,K,F,r", SHAPES)
+def test_forward_and_backward(M, K, F, r, act, name):
+    import torch
+    say(f"gated M={M} K={K} F={F} r={r} {act} {name}")
+    k = Case(M, K, F, r, name)
+    H, Z, none = k.forward(act)
+    assert none is None
+    _check_forward(k, act, H, Z)
+    # what is kept changes no output; 8 bits keep what act8_encode makes of the 16
+    H16, Z16, gu = k.forward(act, "16")
+    H8, Z8, gu8 = k.forward(act, "8")
+    for h, z in ((H16, Z16), (H8, Z8)):
+        np.testing.assert_array_equal(host(h), host(H))
+        np.testing.assert_array_equal(host(z), host(Z))
+    same = qn.act8_encode(gu)
+    np.testing.assert_array_equal(host(gu8.codes), host(same.codes))
+    np.testing.assert_array_equal(host(gu8.absmax), host(same.absmax))
+    pair = host(gu).astype(np.float64)
+    got = k.backward(act, k.X, Z, gu)
+    _check_backward(k, act, k.x, Z, pair[:, :F], pair[:, F:], got, None)
+    # computed again: the same bits
+    for g, w in zip(k.backward(act, k.X, Z, None), got):
+        np.testing.assert_array_equal(host(g), host(w))
+    # from 8 bits: the bits of the decoded checkpoints
+    x8 = qn.act8_encode(k.X)
+    want = k.backward(act, qn.act8_decode(x8), Z, qn.act8_decode(gu8), need_dx=False, grad_dtype=k.X.dtype)
+    half = k.backward(act, x8, Z, gu8, need_dx=False, grad_dtype=k.X.dtype)
+    assert half[0] is None and half[1].dtype == k.X.dtype
+    for g, w in zip(half[1:], want[1:]):
+        np.testing.assert_array_equal(host(g), host(w))
+    torch.cuda.synchronize()
+
+
+def test_single_level_weights_and_no_z():
+    say("gated, single-level weights")
+    for M in (3, 40, 300):
+        k = Case(M, 264, 192, 16, "bf16", single=True)
+        H, Z, _ = k.forward("silu")
+        _check_forward(k, "silu", H, Z)
+        H2, none, _ = k.forward("silu", return_z=False)
+        assert none is None
+        np.testing.assert_array_equal(host(H2), host(H))
+
+
+@pytest.mark.parametrize("M", [3, 16, 70, 300])
+def test_rows_behind_the_last_stay(M):
+    import torch
+    say(f"gated canaries M={M}")
+    k = Case(M, 264, 320, 16, "bf16")
+    big = lambda cols, dt=torch.bfloat16: torch.full((M + 3, cols), 7, dtype=dt, device="cuda")
+    H, Z, gu, codes, am = big(k.F), big(2 * k.r), big(2 * k.F), big(2 * k.F, torch.int8), big(2 * k.F // 64)
+    k.forward("silu", H=H[:M], Z=Z[:M], saved=gu[:M])
+    k.forward("silu", H=H[:M], Z=Z[:M], saved=qn.Act8(codes[:M], am[:M]))
+    dX = big(k.K)
+    k.backward("silu", k.X, Z[:M], gu[:M], dX=dX[:M])
+    for t in (H, Z, gu, codes, am, dX):
+        assert (host(t[M:]) == 7).all()
+        assert not (host(t[:M]) == 7).all()
+
+
+def test_activation_extremes():
+    """Gates far outside the activations' bend: H = U G or 0, finite
+    gradients, no NaN from inf * 0."""
+    import torch
+    say("gated extremes")
+    K, F, r = 64, 64, 8
+    for M in (4, 64):
+        for act in ("silu", "gelu"):
+            for scale in (50.0, 3e4):
+                k = Case(M, K, F, r, "bf16")
+                k.X.mul_(scale)
+                k.x = host(k.X).astype(np.float64)
+                H, Z, gu = k.forward(act, "16")
+                pair = host(gu).astype(np.float64)
+                f = oo.act(act, pair[:, :F])[0] * pair[:, F:]
+                assert np.isfinite(host(H)).all()
+                assert np.max(np.abs(host(H) - f)) <= 0.05 * np.max(np.abs(f))
+                for t in k.backward(act, k.X, Z, gu):
+                    assert np.isfinite(host(t)).all()
+    # a NaN gate reaches its own row only
+    k = Case(40, K, F, r, "bf16")
+    k.X[7, 3] = float("nan")
+    H, Z, gu = k.forward("gelu", "16")
+    bad = np.isnan(host(H)).all(axis=1)
+    assert bad[7] and bad.sum() == 1
+    dX, _, _ = k.backward("gelu", k.X, Z, gu)
+    assert np.isnan(host(dX)[7]).all() and np.isfinite(np.delete(host(dX), 7, axis=0)).all()
+
+
+def test_captured_replayed_and_on_another_stream():
+    import torch
+    say("gated graph and stream")
+    for M in (2, 80, 600):
+        k = Case(M, 520, 256, 16, "bf16")
+        ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in qn.qlora_gated_workspace_bytes(M, 520, 256, 16)]
+        H, Z, saved = k.forward("silu", "8", workspace=ws[0])
+        outs = [torch.empty(M, 520, dtype=torch.bfloat16, device="cuda"), torch.empty(520, 32, device="cuda"),
+                torch.empty(16, 512, device="cuda")]
+
+        def step(stream=None):
+            k.forward("silu", H=H, Z=Z, saved=saved, workspace=ws[0], stream=stream)
+            k.backward("silu", k.X, Z, saved, dX=outs[0], dA=outs[1], dB=outs[2], workspace=ws[1], stream=stream)
+
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        step(side)
+        side.synchronize()
+        want = [host(t).copy() for t in (H, Z, *outs)]
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        for i in range(3):
+            for t in (H, Z, *outs):
+                t.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            for t, w in zip((H, Z, *outs), want):
+                np.testing.assert_array_equal(host(t), w)

@@ -79,3 +79,67 @@ def test_act8_wrappers_refuse_before_a_launch():
     kept = qn.Act8(torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4, 1, dtype=torch.bfloat16))
     with pytest.raises(ValueError):
         qn.act8_decode(kept)
+
+
+def test_gated_refusals():
+    L = qn.lib()
+    i64 = ctypes.c_int64
+    f, b = i64(), i64()
+    for shape in [(0, 64, 64, 8), (4, 12, 64, 8), (4, 64, 96, 8), (4, 64, 0, 8), (4, 64, 64, 4), (4, 64, 64, 136),
+                  (1 << 20, 64, 256, 8), (4, 1 << 15, 1 << 13, 8)]:
+        assert L.qlora_gated_workspace_bytes(*shape, ctypes.byref(f), ctypes.byref(b)) == qn.NF4_EINVAL, shape
+    assert L.qlora_gated_workspace_bytes(4, 64, 64, 8, ctypes.byref(f), ctypes.byref(b)) == qn.NF4_OK
+    states = (qn._State * 2)(*[qn._State(64 * 64, 0x1000, 0x2000, 0x3000, 0x4000)] * 2)
+    short = (qn._State * 2)(qn._State(64 * 64, 0x1000, 0x2000, 0x3000, 0x4000),
+                            qn._State(64 * 32, 0x1000, 0x2000, 0x3000, 0x4000))
+    #      dt act M  K   F   r  X      W       A      B      c  H      Z      GU    GU8   ws       bytes    stream
+    ok = [0, 0, 4, 64, 64, 8, 0x100, states, 0x200, 0x300, C, 0x400, 0x500, None, None, 0x10000, 1 << 30, None]
+    for change in [{0: 2}, {1: 2}, {1: -1}, {6: None}, {7: None}, {7: short}, {8: 0x208}, {11: None}, {12: 0x502},
+                   {13: 0x600, 14: _a8()}, {13: 0x608}, {14: _a8(codes=0x1004)}, {15: None}, {15: 0x10080}, {16: 0},
+                   {4: 96}, {5: 12}]:
+        args = list(ok)
+        for i, v in change.items():
+            args[i] = v
+        assert L.qlora_gated_fwd(*args) == qn.NF4_EINVAL, change
+    #      dt act grad M  K   F   r  dH     X      X8    Z      GU     GU8   W       A      B      c  dX    dA     dB     ws       bytes    stream
+    ok = [0, 0, 1, 4, 64, 64, 8, 0x100, 0x110, None, 0x120, 0x130, None, states, 0x200, 0x300, C, None, 0x400, 0x500, 0x10000, 1 << 30, None]
+    for change in [{0: 2}, {1: 2}, {2: 2}, {7: None}, {8: None}, {9: _a8()}, {10: None}, {12: _a8()}, {13: short},
+                   {8: None, 9: _a8(), 11: None}, {8: None, 9: _a8(absmax=None)}, {11: 0x132}, {17: 0x408}, {18: None},
+                   {19: 0x504}, {20: 0x10010}, {21: 0}]:
+        args = list(ok)
+        for i, v in change.items():
+            args[i] = v
+        assert L.qlora_gated_bwd(*args) == qn.NF4_EINVAL, change
+
+
+@pytest.mark.parametrize("name", ["silu", "gelu"])
+def test_gated_reference_gradients_match_differences(name):
+    rng = np.random.default_rng(4)
+    M, K, F, r, c, h = 3, 5, 4, 2, 0.7, 1e-5
+    X, Wg, Wu = rng.standard_normal((M, K)), rng.standard_normal((K, F)), rng.standard_normal((K, F))
+    A, B, dH = rng.standard_normal((K, 2 * r)), rng.standard_normal((r, 2 * F)), rng.standard_normal((M, F))
+    _, Z, G, U = oo.gated_forward(X, Wg, Wu, A, B, c, name)
+    grads = oo.gated_backward(dH, X, Z, G, U, Wg, Wu, A, B, c, name)
+    for v, g in zip((X, A, B), grads):
+        for i in np.ndindex(v.shape):
+            at, d = v[i], []
+            for s in (h, -h):
+                v[i] = at + s
+                d.append(np.sum(dH * oo.gated_forward(X, Wg, Wu, A, B, c, name)[0]))
+            v[i] = at
+            assert abs((d[0] - d[1]) / (2 * h) - g[i]) <= 1e-6 * (1 + abs(g[i]))
+
+
+def test_head_reference_gradient_matches_differences():
+    rng = np.random.default_rng(6)
+    M, K, V, h = 4, 5, 7, 1e-6
+    X, W, t, w = rng.standard_normal((M, K)), rng.standard_normal((V, K)), np.array([3, -100, 0, 6]), rng.random(M)
+    loss, lse, dX = oo.head_loss(X, W, t, w)
+    assert loss[1] == 0 and not dX[1].any() and np.isfinite(lse).all()
+    for i in np.ndindex(X.shape):
+        at, d = X[i], []
+        for s in (h, -h):
+            X[i] = at + s
+            d.append(np.sum(oo.head_loss(X, W, t, w)[0]))
+        X[i] = at
+        assert abs((d[0] - d[1]) / (2 * h) - dX[i]) <= 1e-7
