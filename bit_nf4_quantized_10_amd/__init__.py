@@ -22,6 +22,7 @@ KERNEL_IDS = {
     "quant_pass1": 0, "quant_mean": 1, "quant_pass2": 2, "dequant": 3, "lora_down": 4,
     "fwd_gemm": 5, "fwd_gemv": 6, "bwd_dz": 7, "bwd_dx": 8, "bwd_colsum": 9, "dequant_bf16": 10,
     "reduce": 11, "merge": 12, "sgd": 13, "act8_encode": 14, "act8_decode": 15, "gated_fwd": 16, "gated_dy": 17,
+    "head_logits": 18, "head_rows": 19, "head_dx": 20,
 }
 C_FUNCTIONS = [
     "nf4_sizes", "nf4_quantize", "nf4_dequantize", "qlora_workspace_bytes",
@@ -30,7 +31,8 @@ C_FUNCTIONS = [
     "qlora_grouped_fwd", "qlora_grouped_bwd", "qlora_linear_fwd_dt", "qlora_linear_bwd_dt", "qlora_sgd_step_dt",
     "qlora_linear_fwd_noalloc", "qlora_grouped_fwd_dt", "qlora_grouped_bwd_dt",
     "act8_encode", "act8_decode", "qlora_linear_bwd_ex",
-    "qlora_gated_workspace_bytes", "qlora_gated_fwd", "qlora_gated_bwd", "nf4_error_string",
+    "qlora_gated_workspace_bytes", "qlora_gated_fwd", "qlora_gated_bwd", "qlora_head_workspace_bytes", "qlora_head_loss",
+    "nf4_error_string",
 ]
 NF4_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 
@@ -102,6 +104,8 @@ def lib() -> ctypes.CDLL:
                                       vp, vp, vp, a8, vp, i64, vp]
         L.qlora_gated_bwd.argtypes = [ctypes.c_int] * 3 + [i64, i64, i64, i64, vp, vp, a8, vp, vp, a8, sp, vp, vp,
                                                            ctypes.c_float, vp, vp, vp, vp, i64, vp]
+        L.qlora_head_workspace_bytes.argtypes = [i64, i64, i64, ctypes.c_int, i64p]
+        L.qlora_head_loss.argtypes = [ctypes.c_int, i64, i64, i64, vp, vp, vp, vp, i64, vp, vp, vp, vp, i64, vp]
         L.nf4_error_string.argtypes = [ctypes.c_int]
         L.nf4_error_string.restype = ctypes.c_char_p
         for name in C_FUNCTIONS[:-1]:
@@ -705,6 +709,43 @@ def qlora_gated_bwd(dH, X, Z, saved, states, A, B, c: float, K: int, F: int, act
                                      gu, _ref(gu8), st, A.data_ptr(), B.data_ptr(), float(c), _ptr(dX), dA.data_ptr(),
                                      dB.data_ptr(), ws.data_ptr(), ws.numel(), s), "qlora_gated_bwd")
     return dX, dA, dB
+
+
+def qlora_head_workspace_bytes(M: int, K: int, V: int, need_dx: bool = True) -> int:
+    b = ctypes.c_int64()
+    _check(lib().qlora_head_workspace_bytes(M, K, V, int(need_dx), ctypes.byref(b)), "qlora_head_workspace_bytes")
+    return b.value
+
+
+def qlora_head_loss(X, W, targets, weights=None, need_dx: bool = True, ignore_index: int = -100, loss=None, lse=None,
+                    dX=None, workspace=None, stream=None):
+    """Softmax cross entropy of the logits X Wᵀ per token, and its gradient,
+    without keeping the logits: (loss (M, fp32), lse (M, fp32), dX (M x K) or
+    None).  X: M x K and the frozen head W: V x K, both bf16 or both fp16;
+    targets: M int64, ignore_index where a token carries no loss; weights: M
+    fp32 factors of the tokens' losses and gradients (None: 1; a mean over n
+    tokens is 1/n)."""
+    import torch
+    dt = _compute_dtype(X)
+    M, K = X.shape
+    V = W.shape[0]
+    _require_cuda(X, "X", dt)
+    _require_cuda(W, "W", dt)
+    _require_shape(W, "W", V, K)
+    _require_cuda(targets, "targets", torch.int64)
+    _require_shape(targets, "targets", M)
+    if weights is not None:
+        _require_cuda(weights, "weights", torch.float32)
+        _require_shape(weights, "weights", M)
+    with _on(X, stream, W, targets, weights, loss, lse, dX, workspace) as s:
+        loss = _out(loss, "loss", torch.float32, X.device, M)
+        lse = _out(lse, "lse", torch.float32, X.device, M)
+        dX = _out(dX, "dX", dt, X.device, M, K) if need_dx else None
+        ws = _workspace(workspace, qlora_head_workspace_bytes(M, K, V, need_dx), X.device)
+        _check(lib().qlora_head_loss(_COMPUTE[dt], M, K, V, X.data_ptr(), W.data_ptr(), targets.data_ptr(),
+                                     _ptr(weights), ignore_index, loss.data_ptr(), lse.data_ptr(), _ptr(dX),
+                                     ws.data_ptr(), ws.numel(), s), "qlora_head_loss")
+    return loss, lse, dX
 
 
 def qlora_timer_enable(kernel: str, enable: bool = True) -> None:

@@ -16,7 +16,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libqlora_nf4.so")
 SOURCES = ["quantize.hip", "gemm_big.hip", "skinny.hip", "gemv.hip", "layer.hip", "adapter.hip", "act8.hip",
-           "gated.hip", "api.cpp"]
+           "gated.hip", "head.hip", "api.cpp"]
 # the read-ceiling helper the benchmark times beside the memory-bound kernels
 PROBE_LIB = os.path.join(PKG, "libqlora_probe.so")
 PROBE_SOURCES = ["read_probe.hip"]

@@ -432,6 +432,32 @@ int qlora_gated_bwd(int compute_dtype, int act, int grad_dtype, int64_t M, int64
   return e == hipSuccess ? NF4_OK : NF4_EHIP;
 }
 
+static bool head_shape_ok(int64_t M, int64_t K, int64_t V) {
+  return M >= 1 && M <= (int64_t(1) << 20) && K >= 8 && K % 8 == 0 && K <= (int64_t(1) << 20) && V >= 1 &&
+         V <= (int64_t(1) << 24) && M * K < kMaxOperandElems;
+}
+
+int qlora_head_workspace_bytes(int64_t M, int64_t K, int64_t V, int need_dx, int64_t* bytes) {
+  if (!head_shape_ok(M, K, V)) return NF4_EINVAL;
+  if (bytes) *bytes = qn::head_workspace_bytes(M, K, V, need_dx != 0);
+  return NF4_OK;
+}
+
+int qlora_head_loss(int compute_dtype, int64_t M, int64_t K, int64_t V, const uint16_t* X, const uint16_t* W,
+                    const int64_t* targets, const float* weights, int64_t ignore_index, float* loss, float* lse,
+                    uint16_t* dX, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!dtype_ok(compute_dtype) || !head_shape_ok(M, K, V)) return NF4_EINVAL;
+  if (!X || !W || !targets || !loss || !workspace) return NF4_EINVAL;   // weights, lse and dX may be NULL
+  if (!aligned16(X) || !aligned16(W) || (dX && !aligned16(dX)) || (reinterpret_cast<uintptr_t>(targets) & 7u) ||
+      (reinterpret_cast<uintptr_t>(weights) & 3u) || (reinterpret_cast<uintptr_t>(loss) & 3u) ||
+      (reinterpret_cast<uintptr_t>(lse) & 3u) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return NF4_EINVAL;
+  if (workspace_bytes < qn::head_workspace_bytes(M, K, V, dX != nullptr)) return NF4_EINVAL;
+  hipError_t e = qn::launch_head_loss(M, K, V, X, W, targets, weights, ignore_index, loss, lse, dX, workspace,
+                                      static_cast<hipStream_t>(stream), compute_dtype);
+  return e == hipSuccess ? NF4_OK : NF4_EHIP;
+}
+
 int qlora_merge(int64_t K, int64_t N, int64_t r, const nf4_state_t* W, const void* A, const void* B, int ab_dtype,
                 float c, float* W_merged, void* stream) {
   if (K < 1 || N < 1 || r < 1 || r > 65536 || !state_ok(W) || W->numel != K * N) return NF4_EINVAL;

@@ -177,7 +177,7 @@ __device__ __forceinline__ void finish_gated_split(const Core& k, const GatedArg
   }
 }
 
-// The dense GEMM's loop (qlora_dense_kernel describes its stages) with the
+// The dense GEMM's loop (dense_loop) with the
 // gated epilogue.
 template <class T, bool kKTail, bool kSplit, bool kGelu, int kKeep>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void gated_dense_kernel(GatedArgs p) {
@@ -185,30 +185,8 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
   const BigArgs& a = p.g;
   typedef Dense<T, true, kKTail, true> Core;
   Core k(a, smem);
-  int64_t s_beg, s_end;
-  stage_range<kSplit>(a, k.red, kBK, s_beg, s_end);
   f32x16 acc[4][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-  const int64_t total = k.set_stages(s_beg, s_end, !kSplit || blockIdx.z == 0);
-#pragma unroll
-  for (int q = 0; q < 16; ++q) k.template copy_one<true>(0, 0, q);
-  __builtin_amdgcn_s_waitcnt(0);
-  __builtin_amdgcn_s_barrier();
-  typename Core::Frags F0, F1;
-  k.load_frags(0, 0, F0);
-#pragma unroll
-  for (int q = 0; q < 8; ++q) k.template copy_one<true>(1, 1, q);
-  int b = 0;
-  int64_t u = 0;
-  for (; u + 2 < k.n_main; ++u, b ^= 1) k.template stage<false>(u, b, F0, F1, acc);
-  for (; u < total; ++u, b ^= 1) k.template stage<true>(u, b, F0, F1, acc);
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
+  dense_loop<kSplit>(k, a, acc);
   if constexpr (kSplit) finish_gated_split(k, p, acc);
   else finish_gated<T, kGelu, kKeep>(k, p, acc);
 }

@@ -482,6 +482,43 @@ struct Dense {
   __device__ void compute(int, f32x16 (&)[4][4]) const {}
 };
 
+// The dense core's loop over this workgroup's stages (kSplit: blockIdx.z's
+// share of the reduction): clears and fills acc, and releases LDS.
+// Stage u (counted from the first of this workgroup's range; the LoRA
+// extension's stages follow the product's) lives in slot u & 1.  The
+// barrier of stage u, before its last substep, says: every wave has read
+// all of slot u & 1 (its last substep's fragments are in registers) and
+// stage u+1 has landed in the other slot.  Stage u+2's copies into slot
+// u & 1 follow it.  Copies past the end are masked or land in a slot that
+// is never read.
+template <bool kSplit, class Core>
+__device__ __forceinline__ void dense_loop(Core& k, const BigArgs& a, f32x16 (&acc)[4][4]) {
+  int64_t s_beg, s_end;
+  stage_range<kSplit>(a, k.red, kBK, s_beg, s_end);
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+  const int64_t total = k.set_stages(s_beg, s_end, !kSplit || blockIdx.z == 0);
+#pragma unroll
+  for (int q = 0; q < 16; ++q) k.template copy_one<true>(0, 0, q);
+  __builtin_amdgcn_s_waitcnt(0);
+  __builtin_amdgcn_s_barrier();
+  typename Core::Frags F0, F1;
+  k.load_frags(0, 0, F0);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) k.template copy_one<true>(1, 1, q);
+  int b = 0;
+  int64_t u = 0;
+  // stages whose copies (of u+1 and u+2) are all of the product, then the rest
+  for (; u + 2 < k.n_main; ++u, b ^= 1) k.template stage<false>(u, b, F0, F1, acc);
+  for (; u < total; ++u, b ^= 1) k.template stage<true>(u, b, F0, F1, acc);
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+}
+
 // LoRA extension: r more reduction steps over (Z, (c B)ᵀ) in the forward or
 // (dZ, A) in the backward; both operands are row-major with r contiguous
 // (M x r and cols x r), staged into the 64-wide LDS layout of the main loop.

@@ -1,0 +1,606 @@
+// Softmax cross entropy of the frozen output head, with its gradient, for
+// gfx950: logits s = X Wᵀ (M x V, never kept), per row
+//   loss = w (lse - s_t),  lse = log sum_v e^{s_v},  dX = w sum_v (p_v - [v = t]) W_v.
+//
+// One pass over the vocabulary in pieces of at most kPieceBytes of 16-bit
+// probabilities; 2 M K V operations for the loss and as many for dX.  Per piece:
+//   1. head_logits_kernel: the GEMM of X and the piece's rows of W.  Its
+//      epilogue turns a tile's logits into powers of two relative to an integer
+//      bound of their own row and 128 columns, P = 2^(s log2 e - ref), ref =
+//      ceil of the largest: P (16 bits, one rounding), ref and the sum of the
+//      unrounded P go to memory.  The target's own column is left out of all
+//      three; its logit is kept in fp32.
+//   2. head_rows_kernel: per row the running bound and sum over the pieces, and
+//      P times 2^(ref - bound): a power of two, so no second rounding.
+//   3. head_dx_kernel: the GEMM of P and the same rows of W, read in their
+//      stored order and transposed on the way out of LDS (ds_read_b64_tr_b16),
+//      added to the earlier pieces' fp32 sums times 2^(old bound - bound).
+// With l the sum without the target and u = log l + bound - s_t, the row's loss
+// is w softplus(u), 1 - p_t = sigmoid(u) =: g and
+//   dX = w g (sum_{v != t} P_v W_v / l - W_t),
+// so that neither the loss nor the target's part of dX suffers from
+// cancellation where the target is nearly certain.
+// Bound by the matrix cores; with few rows by the read of W.
+#include <hip/hip_ext.h>
+
+#include "gemm_core.hpp"
+
+namespace qn {
+
+namespace {
+
+constexpr float kLog2e = 1.44269504f, kLn2 = 0.69314718f;
+#ifndef QN_HEAD_PIECE_MB
+#define QN_HEAD_PIECE_MB 256
+#endif
+constexpr int64_t kPieceBytes = static_cast<int64_t>(QN_HEAD_PIECE_MB) << 20;
+
+// P is stored times 2^kShift: fp16 has few exponents, and its small values would
+// lose bits below 2^-14.
+template <class T>
+constexpr int head_shift() { return T::kDtype == F16::kDtype ? 14 : 0; }
+
+struct HeadArgs {
+  const int64_t* targets;
+  int64_t v0, nv, ldp;       // this piece's first vocabulary row, its rows, P's row stride
+  int64_t V, ignore;
+  uint16_t* P;               // M x ldp, or null: the loss alone
+  float2* stats;             // M x nh: (bound, sum) of each 128 columns
+  int64_t nh;
+  float* st;                 // M: the target's logit
+};
+
+template <class T, bool kKTail, bool kStore>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void head_logits_kernel(BigArgs a,
+                                                                                                         HeadArgs p) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  typedef Dense<T, true, kKTail> Core;
+  Core k(a, smem);
+  f32x16 acc[4][4];
+  dense_loop<false>(k, a, acc);
+  const int lane = k.lane, r32 = lane & 31, h = lane >> 5, wm = k.wave >> 1, wn = k.wave & 1;
+  const int64_t cbase = k.c0 + wn * 128;           // this wave's first column of the piece
+  const int64_t half = cbase >> 7;
+  const bool ragged = cbase + 128 > p.nv;          // the wave has columns past the piece
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t m = k.m0 + wm * 128 + 32 * i + r32;
+    const int64_t t = m < a.M ? p.targets[m] : -1;
+    const int64_t d = t - p.v0 - cbase;
+    // the target, if it is one of this wave's columns (an ignored row has none)
+    const bool here = t >= 0 && t < p.V && t != p.ignore && d >= 0 && d < 128;
+    if (ragged) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (cbase + 32 * j + 8 * (e >> 2) + 4 * h + (e & 3) >= p.nv) acc[i][j][e] = -__builtin_inff();
+    }
+    if (__any(here)) {
+      const int own = here ? static_cast<int>(d) - 4 * h : -1;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+          if (own == 32 * j + 8 * (e >> 2) + (e & 3)) {
+            p.st[m] = acc[i][j][e];
+            acc[i][j][e] = -__builtin_inff();
+          }
+    }
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) top = fmaxf(top, acc[i][j][e]);
+    top = fmaxf(top, __shfl_xor(top, 32, 64));
+    // nothing but masked columns: any bound serves, every P is 0
+    const float ref = top == -__builtin_inff() ? 0.0f : __builtin_ceilf(top * kLog2e);
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const float v = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], kLog2e, -ref));
+        sum += v;
+        acc[i][j][e] = v * static_cast<float>(1 << head_shift<T>());
+      }
+    sum += __shfl_xor(sum, 32, 64);
+    if (h == 0 && m < a.M && half < p.nh) p.stats[m * p.nh + half] = make_float2(ref, sum);
+  }
+  if constexpr (kStore) {
+    char* st = smem;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int R = wm * 128 + 32 * i + r32;
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int jj = 0; jj < 4; ++jj) {
+          const int q = wn * 16 + 4 * j + jj;
+          uint2 v;
+          v.x = T::pack2(acc[i][j][4 * jj], acc[i][j][4 * jj + 1]);
+          v.y = T::pack2(acc[i][j][4 * jj + 2], acc[i][j][4 * jj + 3]);
+          *reinterpret_cast<uint2*>(st + R * 512 + ((q ^ r32) << 4) + 8 * h) = v;
+        }
+    }
+    __syncthreads();
+    const int q = lane & 31;
+    const int64_t n = k.c0 + 8 * q;
+#pragma unroll 4
+    for (int u = 0; u < 32; ++u) {
+      const int R = k.wave * 64 + 2 * u + (lane >> 5);
+      const int64_t m = k.m0 + R;
+      const uint4 v = *reinterpret_cast<const uint4*>(st + R * 512 + ((q ^ (R & 31)) << 4));
+      if (m < a.M && n < p.ldp) *reinterpret_cast<uint4*>(p.P + m * p.ldp + n) = v;
+    }
+  }
+}
+
+struct RowArgs {
+  const float2* stats;
+  int64_t nh, ldp, M, V, ignore;
+  uint16_t* P;               // null: the loss alone
+  const float2* run_in;      // (bound, sum) of the earlier pieces; null for the first
+  float2* run_out;
+  const float* st;
+  const int64_t* targets;
+  const float* weights;      // null: 1
+  float* alpha;              // 2^(old bound - bound), for the earlier pieces' dX sums
+  float* loss;               // written with the last piece (else null)
+  float* lse;
+  float2* coef;              // last piece: (w g, 1 / l); (0, .) marks an ignored row, (NaN, .) a bad target
+};
+
+__device__ __forceinline__ float wg_max(float v, float* red) {
+  for (int s = 32; s >= 1; s >>= 1) v = fmaxf(v, __shfl_xor(v, s, 64));
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  __syncthreads();
+  return v;
+}
+__device__ __forceinline__ float wg_sum(float v, float* red) {
+  for (int s = 32; s >= 1; s >>= 1) v += __shfl_xor(v, s, 64);
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  v = (red[0] + red[1]) + (red[2] + red[3]);
+  __syncthreads();
+  return v;
+}
+
+// One row and a slice of its columns (blockIdx.y); every slice forms the row's
+// new bound and sum (the same bits), slice 0 writes them.
+template <class T>
+__global__ __launch_bounds__(256) void head_rows_kernel(RowArgs p) {
+  __shared__ float red[4];
+  const int64_t m = blockIdx.x;
+  const int t = threadIdx.x;
+  const float2* s = p.stats + m * p.nh;
+  float2 old = make_float2(-__builtin_inff(), 0.0f);
+  if (p.run_in != nullptr) old = p.run_in[m];
+  float top = old.x;
+  for (int64_t i = t; i < p.nh; i += 256) {
+    const float2 v = s[i];
+    // an empty group bounds nothing; a NaN sum must reach the row's
+    if (v.y != 0.0f) top = fmaxf(top, v.x);
+  }
+  top = wg_max(top, red);
+  if (top == -__builtin_inff()) top = 0.0f;   // nothing in the row so far
+  float sum = 0.0f;
+  for (int64_t i = t; i < p.nh; i += 256) {
+    const float2 v = s[i];
+    if (v.y != 0.0f) sum += v.y * __builtin_amdgcn_exp2f(v.x - top);
+  }
+  sum = wg_sum(sum, red);
+  const float back = old.y == 0.0f ? 0.0f : __builtin_amdgcn_exp2f(old.x - top);
+  sum += old.y == 0.0f ? 0.0f : old.y * back;
+  if (blockIdx.y == 0 && t == 0) {
+    p.run_out[m] = make_float2(sum == 0.0f ? -__builtin_inff() : top, sum);
+    if (p.alpha != nullptr) p.alpha[m] = back;
+    if (p.loss != nullptr) {
+      const int64_t target = p.targets[m];
+      const float others = sum == 0.0f ? -__builtin_inff() : (top + __builtin_log2f(sum)) * kLn2;
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      if (target == p.ignore) {
+        p.loss[m] = 0.0f;
+        p.lse[m] = others;
+        if (p.coef != nullptr) p.coef[m] = make_float2(0.0f, -1.0f);
+      } else if (target < 0 || target >= p.V) {
+        p.loss[m] = __builtin_nanf("");
+        p.lse[m] = others;
+        if (p.coef != nullptr) p.coef[m] = make_float2(__builtin_nanf(""), 1.0f);
+      } else {
+        const float w = p.weights != nullptr ? p.weights[m] : 1.0f;
+        const float u = others - p.st[m];
+        const float e = expf(-fabsf(u)), l1 = log1pf(e);
+        const float up = fmaxf(u, 0.0f) + l1;                 // softplus(u); -inf gives 0
+        const float g = (u >= 0.0f ? 1.0f : e) / (1.0f + e);  // sigmoid(u)
+        p.loss[m] = w * (u != u ? u : up);
+        p.lse[m] = p.st[m] + (u != u ? u : up);
+        if (p.coef != nullptr) p.coef[m] = make_float2(w * (u != u ? u : g), inv);
+      }
+    }
+  }
+  if (p.P == nullptr) return;
+  // 128 columns (16 chunks of 8) share a factor, an exact power of two
+  uint16_t* row = p.P + m * p.ldp;
+  const int64_t chunks = p.ldp / 8;
+  const int64_t step = static_cast<int64_t>(gridDim.y) * 256;
+  for (int64_t i = static_cast<int64_t>(blockIdx.y) * 256 + t; i < chunks; i += step) {
+    const float2 v = s[i >> 4];
+    if (v.x == top || v.y == 0.0f) continue;
+    const float f = __builtin_amdgcn_exp2f(v.x - top);
+    uint4 x = *reinterpret_cast<const uint4*>(row + 8 * i);
+    uint32_t* w = reinterpret_cast<uint32_t*>(&x);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) w[c] = T::pack2(T::widen(w[c] & 0xffffu) * f, T::widen(w[c] >> 16) * f);
+    *reinterpret_cast<uint4*>(row + 8 * i) = x;
+  }
+}
+
+// What becomes of a piece's product at rows m and columns of dX.
+struct DxArgs {
+  int64_t M, K, nv, ldp;
+  const uint16_t* P;
+  const uint16_t* Wp;        // the piece's rows of W, nv x K
+  float* part;               // splits x M x K partials (more than one split), else null
+  int64_t k_per;             // vocabulary rows per split
+  int64_t splits;
+  const float* prev;         // earlier pieces' sums M x K, or null
+  const float* alpha;
+  float* sum;                // this piece's sums (not the last piece), else null
+  const float2* coef;        // last piece
+  const uint16_t* W;         // V x K, for the target's row
+  const int64_t* targets;
+  uint16_t* dX;
+  float unshift;             // 2^-shift of P
+};
+
+// Four columns of row m: v = this piece's product.
+template <class T>
+__device__ __forceinline__ void dx_store4(const DxArgs& p, int64_t m, int64_t col, f32x4 v) {
+  v *= p.unshift;
+  if (p.prev != nullptr) {
+    const float al = p.alpha[m];
+    const f32x4 o = *reinterpret_cast<const f32x4*>(p.prev + m * p.K + col);
+    if (al != 0.0f) v += o * al;   // 0: nothing was summed before
+  }
+  if (p.sum != nullptr) {
+    *reinterpret_cast<f32x4*>(p.sum + m * p.K + col) = v;
+    return;
+  }
+  const float2 c = p.coef[m];
+  float r[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (c.x != c.x) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = c.x;
+  } else if (c.y >= 0.0f) {
+    const uint2 wt = *reinterpret_cast<const uint2*>(p.W + p.targets[m] * p.K + col);
+    const float t[4] = {T::widen(wt.x & 0xffffu), T::widen(wt.x >> 16), T::widen(wt.y & 0xffffu), T::widen(wt.y >> 16)};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = c.x * (__builtin_fmaf(v[e], c.y, -t[e]));
+  }
+  *reinterpret_cast<uint2*>(p.dX + m * p.K + col) = make_uint2(T::pack2(r[0], r[1]), T::pack2(r[2], r[3]));
+}
+
+// The sums over the splits of a piece, then the same.
+template <class T>
+__global__ __launch_bounds__(256) void head_sum_kernel(DxArgs p) {
+  const uint32_t per = static_cast<uint32_t>(p.K / 4), count = static_cast<uint32_t>(p.M) * per;
+  const int64_t plane = p.M * p.K;
+  for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < count; i += gridDim.x * 256) {
+    const int64_t m = i / per, at = static_cast<int64_t>(i) * 4;
+    f32x4 v = *reinterpret_cast<const f32x4*>(p.part + at);
+#pragma unroll 4
+    for (int64_t z = 1; z < p.splits; ++z) v += *reinterpret_cast<const f32x4*>(p.part + z * plane + at);
+    dx_store4<T>(p, m, at - m * p.K, v);
+  }
+}
+
+// P (M x nv) times the piece's rows of W (nv x K).  Dense's tile, slots and
+// stages (see there); the weight's half of a slot holds 64 vocabulary rows of
+// 256 columns (512 bytes; 16-byte chunk c of row v at c ^ 4 (v & 3), so that
+// the four rows a transposing read takes lie on different banks).
+template <class T>
+struct DenseTr {
+  const DxArgs& a;
+  char* smem;
+  int t, lane, wave;
+  int64_t m0, c0;
+  Rsrc r_act, r_w;
+  uint32_t act_voff[8], w_voff[8];
+  int act_lim[8], w_lim[8];     // copy valid while k0 < lim
+  int fA[4], fW[4];
+  int64_t s_beg;
+
+  __device__ DenseTr(const DxArgs& args, char* s) : a(args), smem(s) {
+    t = threadIdx.x;
+    lane = t & 63;
+    wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    tile_origin(m0, c0);
+    r_act = make_rsrc(a.P, a.M * a.ldp * 2);
+    r_w = make_rsrc(a.Wp, a.nv * a.K * 2);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int chunk = (lane & 7) ^ (lane >> 3) ^ j;
+      const int64_t m = m0 + wave * 64 + 8 * j + (lane >> 3);
+      act_voff[j] = m < a.M ? static_cast<uint32_t>((m * a.ldp + 8 * chunk) * 2) : kMasked;
+      act_lim[j] = static_cast<int>(a.ldp - 8 * chunk);
+      const int v = wave * 16 + 2 * j + (lane >> 5);
+      const int64_t col = c0 + 8 * ((lane & 31) ^ ((v & 3) << 2));
+      w_voff[j] = col < a.K ? static_cast<uint32_t>((v * a.K + col) * 2) : kMasked;
+      w_lim[j] = static_cast<int>(a.nv - v);
+    }
+    const int r32 = lane & 31, h = lane >> 5, wm = wave >> 1, wn = wave & 1;
+    const int G = lane >> 4, L = lane & 15;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      fA[i] = lds_off(wm * 128 + 32 * i + r32, h);
+      const int col = wn * 128 + 32 * i + 16 * (G & 1) + 4 * (L & 3);
+      fW[i] = kTileBytes + (8 * (G >> 1) + (L >> 2)) * 512 + (((col >> 3) ^ ((L >> 2) << 2)) << 4) + 2 * (col & 7);
+    }
+  }
+
+  __device__ void copy_one(int64_t u, int b, int q) const {
+    const int j = q >> 1;
+    const int64_t k0 = (s_beg + u) * kBK;
+    if ((q & 1) == 0) {
+      char* dst = smem + b * kDenseSlot + (wave * 64 + 8 * j) * 128;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r_act, (lds_ptr_t)(dst), 16, k0 < act_lim[j] ? act_voff[j] : kMasked,
+                                               static_cast<uint32_t>(k0 * 2), 0, 0);
+    } else {
+      char* dst = smem + b * kDenseSlot + kTileBytes + (wave * 16 + 2 * j) * 512;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(r_w, (lds_ptr_t)(dst), 16, k0 < w_lim[j] ? w_voff[j] : kMasked,
+                                               static_cast<uint32_t>(k0 * a.K * 2), 0, 0);
+    }
+  }
+
+  struct Frags {
+    typename T::v8 a[4], w[4];
+  };
+  __device__ void read_one(int b, int ks, int q, Frags& F) const {
+    const char* base = smem + b * kDenseSlot;
+    if ((q & 1) == 0) {
+      F.a[q >> 1] = *reinterpret_cast<const typename T::v8*>(base + (fA[q >> 1] ^ (ks << 5)));
+    } else {
+      typedef short v4i16 __attribute__((ext_vector_type(4)));
+      typedef __attribute__((address_space(3))) v4i16* lp;
+      const char* p = base + fW[q >> 1] + ks * 16 * 512;
+      const v4i16 both[2] = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(p)),
+                             __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(p + 4 * 512))};
+      F.w[q >> 1] = __builtin_bit_cast(typename T::v8, both);
+    }
+  }
+  __device__ void load_frags(int b, int ks, Frags& F) const {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) read_one(b, ks, q, F);
+  }
+  // Dense::sub_step and Dense::stage, over these copies and reads
+  __device__ void sub_step(const Frags& Fc, Frags& Fn, int bn, int ksn, int64_t cs, int cb, int q0, int nc,
+                           f32x16 (&acc)[4][4]) const {
+    const int sp = 16 / (nc > 0 ? nc : 1);
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int m = 4 * g + u;
+        acc[g][u] = T::mfma32(Fc.w[u], Fc.a[g], acc[g][u]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (m < 8) {
+          read_one(bn, ksn, m, Fn);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (nc > 0 && m % sp == (sp > 1 ? 1 : 0)) {
+          copy_one(cs, cb, q0 + m / sp);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+    }
+  }
+  __device__ void stage(int64_t u, int b, Frags& F0, Frags& F1, f32x16 (&acc)[4][4]) const {
+    sub_step(F0, F1, b, 1, u + 1, b ^ 1, 8, 8, acc);
+    sub_step(F1, F0, b, 2, 0, 0, 0, 0, acc);
+    sub_step(F0, F1, b, 3, 0, 0, 0, 0, acc);
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    sub_step(F1, F0, b ^ 1, 0, u + 2, b, 0, 8, acc);
+  }
+};
+
+template <class T>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void head_dx_kernel(DxArgs p) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  DenseTr<T> k(p, smem);
+  const int64_t all = (p.ldp + kBK - 1) / kBK;
+  int64_t end = all;
+  k.s_beg = 0;
+  if (p.part != nullptr) {
+    k.s_beg = static_cast<int64_t>(blockIdx.z) * (p.k_per / kBK);
+    end = k.s_beg + p.k_per / kBK < all ? k.s_beg + p.k_per / kBK : all;
+  }
+  const int64_t total = end - k.s_beg;
+  f32x16 acc[4][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+  // Copies past the split's end fetch the next split's data or nothing; they
+  // land in slots that are never read.
+#pragma unroll
+  for (int q = 0; q < 16; ++q) k.copy_one(0, 0, q);
+  __builtin_amdgcn_s_waitcnt(0);
+  __builtin_amdgcn_s_barrier();
+  typename DenseTr<T>::Frags F0, F1;
+  k.load_frags(0, 0, F0);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) k.copy_one(1, 1, q);
+  int b = 0;
+  for (int64_t u = 0; u < total; ++u, b ^= 1) k.stage(u, b, F0, F1, acc);
+  __builtin_amdgcn_s_waitcnt(0);
+  const int r32 = k.lane & 31, h = k.lane >> 5, wm = k.wave >> 1, wn = k.wave & 1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t m = k.m0 + wm * 128 + 32 * i + r32;
+    if (m >= p.M) continue;
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int jj = 0; jj < 4; ++jj) {
+        const int64_t col = k.c0 + wn * 128 + 32 * j + 8 * jj + 4 * h;
+        if (col >= p.K) continue;
+        const f32x4 v = {acc[i][j][4 * jj], acc[i][j][4 * jj + 1], acc[i][j][4 * jj + 2], acc[i][j][4 * jj + 3]};
+        if (p.part != nullptr) *reinterpret_cast<f32x4*>(p.part + (blockIdx.z * p.M + m) * p.K + col) = v;
+        else dx_store4<T>(p, m, col, v);
+      }
+  }
+}
+
+int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
+
+// Pieces of the vocabulary and splits of dX's reduction.
+struct HeadPlan {
+  int64_t pieces, rows;             // rows per piece, a multiple of 256
+  int64_t splits, k_per;
+  int64_t p_bytes, stats_bytes, row_bytes, sum_bytes, part_bytes;
+  int64_t total() const { return p_bytes + stats_bytes + 6 * row_bytes + sum_bytes + part_bytes; }
+};
+
+// A piece keeps its probabilities within kPieceBytes and its rows of W within
+// 2^29 elements (32-bit offsets).  dX's M x K tiles get up to 256 workgroups by
+// splitting the piece's rows, at least kMinStages 64-row stages each.
+HeadPlan head_plan(int64_t M, int64_t K, int64_t V, bool need_dx) {
+  HeadPlan h{};
+  int64_t most = (int64_t(1) << 29) / K;
+  if (need_dx && kPieceBytes / 2 / M < most) most = kPieceBytes / 2 / M;
+  most = most / 256 * 256;
+  if (most < 256) most = 256;
+  h.pieces = (V + most - 1) / most;
+  h.rows = ((V + h.pieces - 1) / h.pieces + 255) / 256 * 256;
+  h.pieces = (V + h.rows - 1) / h.rows;
+  h.stats_bytes = align256(M * (h.rows / 128) * 8);
+  h.row_bytes = align256(M * 8);
+  h.splits = 1;
+  h.k_per = h.rows;
+  if (!need_dx) return h;
+  const int64_t width = V < h.rows ? (V + 63) / 64 * 64 : h.rows;
+  h.p_bytes = align256(M * width * 2);
+  if (h.pieces > 1) h.sum_bytes = align256(M * K * 4);
+  constexpr int64_t kMinStages = 8;
+  const int64_t tiles = ((M + kBM - 1) / kBM) * ((K + kBN - 1) / kBN);
+  int64_t s = 256 / tiles, most_s = width / (kBK * kMinStages);
+  if (s > most_s) s = most_s;
+  if (s >= 2) {
+    h.k_per = ((width + s - 1) / s + kBK - 1) / kBK * kBK;
+    h.splits = (width + h.k_per - 1) / h.k_per;
+    if (h.splits < 2) h.splits = 1;
+    else h.part_bytes = align256(h.splits * M * K * 4);
+  }
+  return h;
+}
+
+template <class T, bool kKTail, bool kStore>
+hipError_t launch_logits_t(const BigArgs& a, const HeadArgs& p, hipStream_t stream, const Timer& tm) {
+  // raised once per process; the initialisation of a function-local static
+  // is thread-safe, so concurrent first calls do not race
+  static const hipError_t lds_limit =
+      hipFuncSetAttribute(reinterpret_cast<const void*>(&head_logits_kernel<T, kKTail, kStore>),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, kDenseLds);
+  if (lds_limit != hipSuccess) return lds_limit;
+  const dim3 grid(static_cast<unsigned>((p.nv + kBN - 1) / kBN), static_cast<unsigned>((a.M + kBM - 1) / kBM));
+  hipExtLaunchKernelGGL((head_logits_kernel<T, kKTail, kStore>), grid, dim3(kThreads), kDenseLds, stream, tm.start(),
+                        tm.end(), 0, a, p);
+  return hipGetLastError();
+}
+template <class T>
+hipError_t launch_logits(const BigArgs& a, const HeadArgs& p, hipStream_t stream) {
+  const Timer t(QK_HEAD_LOGITS, stream, true);
+  const bool tail = a.K % kBK != 0;
+  if (p.P != nullptr)
+    return tail ? launch_logits_t<T, true, true>(a, p, stream, t) : launch_logits_t<T, false, true>(a, p, stream, t);
+  return tail ? launch_logits_t<T, true, false>(a, p, stream, t) : launch_logits_t<T, false, false>(a, p, stream, t);
+}
+
+template <class T>
+hipError_t launch_dx(const DxArgs& p, hipStream_t stream) {
+  static const hipError_t lds_limit = hipFuncSetAttribute(reinterpret_cast<const void*>(&head_dx_kernel<T>),
+                                                          hipFuncAttributeMaxDynamicSharedMemorySize, kDenseLds);
+  if (lds_limit != hipSuccess) return lds_limit;
+  const unsigned zs = static_cast<unsigned>(p.part != nullptr ? p.splits : 1);
+  const dim3 grid(static_cast<unsigned>((p.K + kBN - 1) / kBN), static_cast<unsigned>((p.M + kBM - 1) / kBM), zs);
+  {
+    const Timer t(QK_HEAD_DX, stream, true);
+    hipExtLaunchKernelGGL(head_dx_kernel<T>, grid, dim3(kThreads), kDenseLds, stream, t.start(), t.end(), 0, p);
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.part == nullptr) return e;
+  int64_t blocks = (p.M * p.K / 4 + 255) / 256;
+  if (blocks > 8192) blocks = 8192;
+  Timer tm(QK_REDUCE, stream);
+  hipLaunchKernelGGL(head_sum_kernel<T>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, p);
+  tm.stop();
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t head_loss_t(int64_t M, int64_t K, int64_t V, const uint16_t* X, const uint16_t* W, const int64_t* targets,
+                       const float* weights, int64_t ignore, float* loss, float* lse, uint16_t* dX, void* ws,
+                       hipStream_t stream) {
+  const HeadPlan h = head_plan(M, K, V, dX != nullptr);
+  char* at = static_cast<char*>(ws);
+  auto take = [&](int64_t bytes) {
+    char* p = at;
+    at += bytes;
+    return p;
+  };
+  uint16_t* P = reinterpret_cast<uint16_t*>(take(h.p_bytes));
+  float2* stats = reinterpret_cast<float2*>(take(h.stats_bytes));
+  float2* run[2] = {reinterpret_cast<float2*>(take(h.row_bytes)), reinterpret_cast<float2*>(take(h.row_bytes))};
+  float* st = reinterpret_cast<float*>(take(h.row_bytes));
+  float* alpha = reinterpret_cast<float*>(take(h.row_bytes));
+  float2* coef = reinterpret_cast<float2*>(take(h.row_bytes));
+  float* lse_own = reinterpret_cast<float*>(take(h.row_bytes));
+  float* sums = reinterpret_cast<float*>(take(h.sum_bytes));
+  float* part = reinterpret_cast<float*>(take(h.part_bytes));
+  for (int64_t i = 0; i < h.pieces; ++i) {
+    const int64_t v0 = i * h.rows, nv = V - v0 < h.rows ? V - v0 : h.rows;
+    const bool last = i + 1 == h.pieces;
+    BigArgs g{X, K, NF4View{}, X, X, nullptr, M, K, nv, 0, W + v0 * K};
+    HeadArgs p{targets, v0, nv, (nv + 63) / 64 * 64, V, ignore, dX != nullptr ? P : nullptr, stats, (nv + 127) / 128, st};
+    hipError_t e = launch_logits<T>(g, p, stream);
+    if (e != hipSuccess) return e;
+    RowArgs r{stats, p.nh, p.ldp, M, V, ignore, p.P, i > 0 ? run[(i + 1) & 1] : nullptr, run[i & 1], st, targets, weights,
+              alpha, last ? loss : nullptr, lse != nullptr ? lse : lse_own, dX != nullptr ? coef : nullptr};
+    // slices of a row until about 2048 workgroups, at least 2048 columns each
+    int64_t slices = dX != nullptr ? (2048 + M - 1) / M : 1;
+    if (slices > (p.ldp + 2047) / 2048) slices = (p.ldp + 2047) / 2048;
+    {
+      Timer tm(QK_HEAD_ROWS, stream);
+      hipLaunchKernelGGL(head_rows_kernel<T>, dim3(static_cast<unsigned>(M), static_cast<unsigned>(slices)), dim3(256), 0,
+                         stream, r);
+      tm.stop();
+    }
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (dX == nullptr) continue;
+    DxArgs d{M, K, nv, p.ldp, P, W + v0 * K, h.splits > 1 ? part : nullptr, h.k_per, h.splits, i > 0 ? sums : nullptr, alpha,
+             last ? nullptr : sums, coef, W, targets, dX, 1.0f / static_cast<float>(1 << head_shift<T>())};
+    if (h.splits > 1) d.splits = (p.ldp + h.k_per - 1) / h.k_per;   // the last piece may be shorter
+    if ((e = launch_dx<T>(d, stream)) != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+int64_t head_workspace_bytes(int64_t M, int64_t K, int64_t V, bool need_dx) { return head_plan(M, K, V, need_dx).total(); }
+
+hipError_t launch_head_loss(int64_t M, int64_t K, int64_t V, const uint16_t* X, const uint16_t* W, const int64_t* targets,
+                            const float* weights, int64_t ignore, float* loss, float* lse, uint16_t* dX, void* ws,
+                            hipStream_t stream, int dtype) {
+  return dtype == kDtypeF16 ? head_loss_t<F16>(M, K, V, X, W, targets, weights, ignore, loss, lse, dX, ws, stream)
+                            : head_loss_t<Bf16>(M, K, V, X, W, targets, weights, ignore, loss, lse, dX, ws, stream);
+}
+
+}  // namespace qn

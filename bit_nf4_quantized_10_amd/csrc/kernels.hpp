@@ -223,6 +223,13 @@ hipError_t launch_gated_gemv(int64_t M, int64_t K, int64_t F, int64_t r, const u
                              const uint16_t* A, const uint16_t* B, float c, bool gelu, uint16_t* H, uint16_t* Z,
                              const GatedKeep& keep, void* ws, hipStream_t stream, int dtype);
 
+// The output head's cross entropy (head.hip): X M x K, W V x K, dX null: the
+// loss alone; lse may be null.
+int64_t head_workspace_bytes(int64_t M, int64_t K, int64_t V, bool need_dx);
+hipError_t launch_head_loss(int64_t M, int64_t K, int64_t V, const uint16_t* X, const uint16_t* W, const int64_t* targets,
+                            const float* weights, int64_t ignore, float* loss, float* lse, uint16_t* dX, void* ws,
+                            hipStream_t stream, int dtype);
+
 // Dequantize a K x N weight to the 16-bit compute type (dtype), either as
 // stored (K x N) or transposed (N x K).
 // out_ld: row stride of the untransposed output (0: N).

@@ -331,6 +331,28 @@ int qlora_gated_bwd(int compute_dtype, int act, int grad_dtype, int64_t M, int64
                     const act8_t* GU8, const nf4_state_t* W, const uint16_t* A, const uint16_t* B, float c,
                     uint16_t* dX, void* dA, void* dB, void* workspace, int64_t workspace_bytes, void* stream);
 
+/* Softmax cross entropy of a frozen output head, with the gradient of its
+ * input: for the logits s = X Wᵀ (M x V, never kept in memory) and each row m
+ *   lse_m  = log sum_v e^{s_mv},   loss_m = w_m (lse_m - s_mt),  t = targets[m],
+ *   dX_m   = w_m sum_v (p_mv - [v = t]) W_v,   p_mv = e^{s_mv - lse_m}.
+ * X: M x K and W: V x K (a row per vocabulary entry) of compute_dtype; targets:
+ * M int64; weights: M fp32, or NULL for 1 (a mean over n tokens is weight 1/n,
+ * an upstream gradient or loss scale a factor).  Outputs: loss and lse (may be
+ * NULL) M fp32, dX (NULL: the loss alone) M x K of compute_dtype.  A row whose
+ * target is ignore_index has loss 0 and dX 0, whatever it holds; one whose
+ * target is neither ignore_index nor in [0, V) has loss and dX NaN; both have
+ * their lse.  The vocabulary is processed in pieces whose 16-bit probabilities
+ * take at most 256 MiB of the workspace (or 256 columns of them, if those take
+ * more); logits and sums are fp32, loss and gradient come from one pass.
+ * Requirements: M >= 1, V >= 1, K % 8 == 0, 8 <= K <= 2^20, M <= 2^20, M * K
+ * below 2^29, V <= 2^24; X, W, dX 16-byte, targets 8-byte, the fp32 buffers
+ * 4-byte aligned; workspace 256-byte aligned and at least *bytes (need_dx:
+ * nonzero if dX will be given).  NF4_EINVAL otherwise. */
+int qlora_head_workspace_bytes(int64_t M, int64_t K, int64_t V, int need_dx, int64_t* bytes);
+int qlora_head_loss(int compute_dtype, int64_t M, int64_t K, int64_t V, const uint16_t* X, const uint16_t* W,
+                    const int64_t* targets, const float* weights, int64_t ignore_index, float* loss, float* lse,
+                    uint16_t* dX, void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Synchronise `stream`, then copy the device status word to *host_value.
  * Returns NF4_EHIP if the copy fails, else NF4_OK. */
 int nf4_status_read(const int32_t* status, int32_t* host_value, void* stream);
@@ -354,7 +376,10 @@ int nf4_status_read(const int32_t* status, int32_t* host_value, void* stream);
 #define QK_ACT8_DECODE  15  /* its 16-bit values                         */
 #define QK_GATED_FWD    16  /* gated block's GEMM with its activation    */
 #define QK_GATED_DY     17  /* dG and dU from dH                         */
-#define QK_NUM_KERNELS  18
+#define QK_HEAD_LOGITS  18  /* output head: logits to probabilities      */
+#define QK_HEAD_ROWS    19  /* output head: running sums, loss           */
+#define QK_HEAD_DX      20  /* output head: gradient product             */
+#define QK_NUM_KERNELS  21
 
 /* When enabled, the library records a pair of hipEvents on the launch
  * stream around every launch of kernel `kernel_id`.  qlora_timer_read

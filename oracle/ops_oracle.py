@@ -105,8 +105,16 @@ def head_loss(X, W, targets, weights=None, ignore_index: int = -100):
     e = np.exp(s - top)
     lse = np.log(e.sum(axis=1)) + top[:, 0]
     p = e / e.sum(axis=1, keepdims=True)
-    at = np.where(counted, t, 0)
-    loss = np.where(counted, w * (lse - s[np.arange(M), at]), 0.0)
-    p[np.arange(M), at] -= 1.0
+    at, row = np.where(counted, t, 0), np.arange(M)
+    # lse - s_t = log(1 + sum_{v != t} e^{s_v - s_t}) and p_t - 1 = -sum_{v != t} p_v:
+    # the differences themselves cancel to nothing where the target is nearly certain
+    with np.errstate(over="ignore"):
+        d = np.exp(s - s[row, at][:, None])
+    d[row, at] = 0.0
+    near = d.sum(axis=1)
+    nll = np.where(near < 1.0, np.log1p(np.minimum(near, 1.0)), lse - s[row, at])
+    loss = np.where(counted, w * nll, 0.0)
+    p[row, at] = 0.0
+    p[row, at] = -p.sum(axis=1)
     dX = np.where(counted[:, None], (p * w[:, None]) @ W, 0.0)
     return loss, lse, dX

@@ -1,0 +1,71 @@
+"""The operators as a training step uses them: gated front kept in 8 bits,
+down projection, head loss, and the way back from the checkpoints to an SGD
+step on both adapters - against the same step in 64 bits on the kept values."""
+import numpy as np
+import pytest
+
+import bit_nf4_quantized_10_amd as qn
+from oracle import ops_oracle as oo
+from tests.gpu_util import dev_f32, host, rel_err, say
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("M,K,F,r,V,name", [(40, 136, 192, 8, 500, "bf16"), (300, 264, 320, 16, 1003, "bf16"),
+                                            (300, 264, 320, 16, 1003, "f16"), (12, 72, 64, 8, 130, "f16")])
+def test_training_step(M, K, F, r, V, name):
+    import torch
+    say(f"training step M={M} K={K} F={F} V={V} {name}")
+    T = {"bf16": torch.bfloat16, "f16": torch.float16}[name]
+    rng = np.random.default_rng(M + V)
+    dev = lambda *s, std=1.0: (torch.from_numpy(rng.standard_normal(s).astype(np.float32)) * std).to(T).cuda()
+    Kd = 64 * (-(-K // 64))            # the down projection's output, a multiple of 64
+    c, lr = 0.5, 0.1
+    states, Ws = [], []
+    for shape in ((K, F), (K, F), (F, Kd)):
+        st, _ = qn.nf4_quantize(dev_f32(rng.standard_normal(shape) / np.sqrt(shape[0])))
+        states.append(st)
+        Ws.append(host(qn.nf4_dequantize(st, name)).reshape(shape).astype(np.float64))
+    X, A, B = dev(M, K), dev(K, 2 * r, std=1 / np.sqrt(K)), dev(r, 2 * F, std=0.2)
+    Ad, Bd, head = dev(F, r, std=1 / np.sqrt(F)), dev(r, Kd, std=0.2), dev(V, Kd, std=1 / np.sqrt(Kd))
+    t = torch.from_numpy(rng.integers(0, V, M)).cuda()
+    t[::5] = -100
+    n = int((t != -100).sum())
+    w = torch.full((M,), (64.0 if name == "f16" else 1.0) / n, device="cuda")
+
+    H, Z, gu = qn.qlora_gated_fwd(X, states[:2], A, B, c, K, F, save="8")
+    x8, h8 = qn.act8_encode(X), qn.act8_encode(H)
+    Y, Zd = qn.qlora_linear_fwd(H, states[2], Ad, Bd, c, F, Kd)
+    loss, lse, dY = qn.qlora_head_loss(Y, head, t, weights=w)
+    dH, dAd, dBd = qn.qlora_linear_bwd(dY, h8, Zd, states[2], Ad, Bd, c, F, Kd)
+    dX, dA, dB = qn.qlora_gated_bwd(dH, x8, Z, gu, states[:2], A, B, c, K, F)
+
+    f64 = lambda v: host(v).astype(np.float64)
+    # each operator on what it was given: no error is carried from one to the next
+    H0, Z0, _, _ = oo.gated_forward(f64(X), Ws[0], Ws[1], f64(A), f64(B), c, "silu")
+    loss0, lse0, dY0 = oo.head_loss(f64(Y), f64(head), host(t), f64(w))
+    hk = f64(qn.act8_decode(h8))
+    dZd = c * f64(dY) @ f64(Bd).T
+    kept = f64(qn.act8_decode(gu))
+    back = oo.gated_backward(f64(dH), f64(qn.act8_decode(x8)), f64(Z), kept[:, :F], kept[:, F:], Ws[0], Ws[1], f64(A),
+                             f64(B), c, "silu")
+    # every 16-bit rounding is below 2^-8 (bf16) of its value; at most three follow each other
+    tol = 3 * {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}[name] + 1e-5
+    for what, g, ref in (("H", H, H0), ("Z", Z, Z0), ("loss", loss, loss0), ("lse", lse, lse0), ("dY", dY, dY0),
+                         ("dH", dH, f64(dY) @ Ws[2].T + dZd @ f64(Ad).T), ("dAd", dAd, hk.T @ dZd),
+                         ("dBd", dBd, c * f64(Zd).T @ f64(dY)), ("dX", dX, back[0]), ("dA", dA, back[1]),
+                         ("dB", dB, back[2])):
+        err = rel_err(host(g), ref)
+        say(f"  {what} {err:.2e}")
+        assert err <= tol, what
+    # the step moves both adapters against their gradients
+    for a, b, da, db in ((A, B, dA, dB), (Ad, Bd, dAd, dBd)):
+        a0, b0 = a.clone(), b.clone()
+        if a is A:      # the pair's adapters side by side: one call over the whole matrices
+            qn.qlora_sgd_step(a, b[:, :F].contiguous(), da, db[:, :F].contiguous(), lr)
+            want = (a0.float() - lr * da).to(T)
+            np.testing.assert_array_equal(host(a), host(want))
+            continue
+        qn.qlora_sgd_step(a, b, da, db, lr)
+        np.testing.assert_array_equal(host(a), host((a0.float() - lr * da).to(T)))
+        np.testing.assert_array_equal(host(b), host((b0.float() - lr * db).to(T)))

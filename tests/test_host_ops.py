@@ -143,3 +143,28 @@ def test_head_reference_gradient_matches_differences():
             d.append(np.sum(oo.head_loss(X, W, t, w)[0]))
         X[i] = at
         assert abs((d[0] - d[1]) / (2 * h) - dX[i]) <= 1e-7
+
+
+def test_head_refusals():
+    L = qn.lib()
+    n = ctypes.c_int64()
+    for shape in [(0, 64, 10), (4, 12, 10), (4, 0, 10), (4, 64, 0), ((1 << 20) + 1, 64, 10), (1 << 20, 512, 10),
+                  (4, (1 << 20) + 8, 10), (4, 64, (1 << 24) + 1)]:
+        assert L.qlora_head_workspace_bytes(*shape, 1, ctypes.byref(n)) == qn.NF4_EINVAL, shape
+    assert L.qlora_head_workspace_bytes(4, 64, 10, 1, ctypes.byref(n)) == qn.NF4_OK
+    #     dt M  K   V   X      W      targets weights ignore loss   lse   dX     ws       bytes    stream
+    ok = [0, 4, 64, 10, 0x100, 0x200, 0x300, None, -100, 0x400, None, 0x500, 0x10000, 1 << 30, None]
+    for change in [{0: 2}, {1: 0}, {2: 12}, {3: 0}, {4: None}, {4: 0x108}, {5: None}, {6: None}, {6: 0x304}, {7: 0x302},
+                   {9: None}, {9: 0x402}, {10: 0x602}, {11: 0x508}, {12: None}, {12: 0x10010}, {13: 16}]:
+        args = list(ok)
+        for i, v in change.items():
+            args[i] = v
+        assert L.qlora_head_loss(*args) == qn.NF4_EINVAL, change
+
+
+def test_head_workspace_is_bounded_by_its_pieces():
+    small = qn.qlora_head_workspace_bytes(4096, 4096, 32000)
+    # twice the vocabulary costs no more probabilities, only the sums of the pieces
+    large = qn.qlora_head_workspace_bytes(4096, 4096, 256000)
+    assert small <= (256 << 20) + (32 << 20) and large <= small + 4096 * 4096 * 4 + (32 << 20)
+    assert qn.qlora_head_workspace_bytes(4096, 4096, 256000, need_dx=False) < 128 << 20
