@@ -13,8 +13,7 @@
 //   2. head_rows_kernel: per row the running bound and sum over the pieces, and
 //      P times 2^(ref - bound): a power of two, so no second rounding.
 //   3. head_dx_kernel: the GEMM of P and the same rows of W, read in their
-//      stored order and transposed on the way out of LDS (ds_read_b64_tr_b16),
-//      added to the earlier pieces' fp32 sums times 2^(old bound - bound).
+//      stored order and transposed on the way into LDS, added to the earlier pieces' fp32 sums times 2^(old bound - bound).
 // With l the sum without the target and u = log l + bound - s_t, the row's loss
 // is w softplus(u), 1 - p_t = sigmoid(u) =: g and
 //   dX = w g (sum_{v != t} P_v W_v / l - W_t),
@@ -297,26 +296,47 @@ __global__ __launch_bounds__(256) void head_sum_kernel(DxArgs p) {
   }
 }
 
-// P (M x nv) times the piece's rows of W (nv x K).  Dense's tile, slots and
-// stages (see there); the weight's half of a slot holds 64 vocabulary rows of
-// 256 columns (512 bytes; 16-byte chunk c of row v at c ^ 4 (v & 3), so that
-// the four rows a transposing read takes lie on different banks).
+// 8 x 8 transpose of 16-bit values: column c of the 8 rows `in`, as 16 bytes.
+__device__ __forceinline__ uint4 column8(const uint4 (&in)[8], int c) {
+  const uint32_t sel = (c & 1) ? 0x07060302u : 0x05040100u;
+  uint32_t d[4];
+#pragma unroll
+  for (int p = 0; p < 4; ++p) {
+    const uint4 &lo = in[2 * p], &hi = in[2 * p + 1];
+    const uint32_t l = (c >> 1) == 0 ? lo.x : ((c >> 1) == 1 ? lo.y : ((c >> 1) == 2 ? lo.z : lo.w));
+    const uint32_t h = (c >> 1) == 0 ? hi.x : ((c >> 1) == 1 ? hi.y : ((c >> 1) == 2 ? hi.z : hi.w));
+    d[p] = __builtin_amdgcn_perm(h, l, sel);
+  }
+  return make_uint4(d[0], d[1], d[2], d[3]);
+}
+
+// P (M x nv) times the piece's rows of W (nv x K): Dense's tile, slots and
+// fragment reads (see there), with the reduction running down the rows of W.
+// A stage's 64 rows x 256 columns of W come through registers: thread (vg, cg)
+// loads the 8 x 8 block of rows 8 vg .. and columns 8 cg .., turns it with byte
+// permutes and writes the columns as chunks of Dense's layout.  (Reading W from
+// LDS with transposing 8-byte loads instead moves half the bytes per cycle: it
+// made the loop LDS-bound, 2102 against 1007 us at 4096 x 4096 x 32000.)
+// Stage u: its first substep writes W of stage u+1 from the registers, its
+// second requests W of stage u+2; P of stage u+2 is copied straight to LDS in
+// the last one, after the barrier.
 template <class T>
 struct DenseTr {
   const DxArgs& a;
   char* smem;
-  int t, lane, wave;
+  int t, lane, wave, vg;
   int64_t m0, c0;
   Rsrc r_act, r_w;
-  uint32_t act_voff[8], w_voff[8];
-  int act_lim[8], w_lim[8];     // copy valid while k0 < lim
-  int fA[4], fW[4];
+  uint32_t act_voff[8], w_voff;
+  int act_lim[8];               // copy valid while k0 < lim
+  int fA[4], fW[4], wdst;
   int64_t s_beg;
 
   __device__ DenseTr(const DxArgs& args, char* s) : a(args), smem(s) {
     t = threadIdx.x;
     lane = t & 63;
     wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    vg = t >> 5;
     tile_origin(m0, c0);
     r_act = make_rsrc(a.P, a.M * a.ldp * 2);
     r_w = make_rsrc(a.Wp, a.nv * a.K * 2);
@@ -326,33 +346,40 @@ struct DenseTr {
       const int64_t m = m0 + wave * 64 + 8 * j + (lane >> 3);
       act_voff[j] = m < a.M ? static_cast<uint32_t>((m * a.ldp + 8 * chunk) * 2) : kMasked;
       act_lim[j] = static_cast<int>(a.ldp - 8 * chunk);
-      const int v = wave * 16 + 2 * j + (lane >> 5);
-      const int64_t col = c0 + 8 * ((lane & 31) ^ ((v & 3) << 2));
-      w_voff[j] = col < a.K ? static_cast<uint32_t>((v * a.K + col) * 2) : kMasked;
-      w_lim[j] = static_cast<int>(a.nv - v);
     }
+    const int cg = t & 31;
+    w_voff = c0 + 8 * cg < a.K ? static_cast<uint32_t>((8 * vg * a.K + c0 + 8 * cg) * 2) : kMasked;
+    wdst = kTileBytes + 8 * cg * 128 + (((vg ^ cg) & 7) << 4);   // column c: + 128 c, chunk bits ^ c
     const int r32 = lane & 31, h = lane >> 5, wm = wave >> 1, wn = wave & 1;
-    const int G = lane >> 4, L = lane & 15;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       fA[i] = lds_off(wm * 128 + 32 * i + r32, h);
-      const int col = wn * 128 + 32 * i + 16 * (G & 1) + 4 * (L & 3);
-      fW[i] = kTileBytes + (8 * (G >> 1) + (L >> 2)) * 512 + (((col >> 3) ^ ((L >> 2) << 2)) << 4) + 2 * (col & 7);
+      fW[i] = kTileBytes + lds_off(wn * 128 + 32 * i + r32, h);
     }
   }
 
-  __device__ void copy_one(int64_t u, int b, int q) const {
-    const int j = q >> 1;
+  // P rows wave*64 + 8j .. +7 of stage u into slot b
+  __device__ void copy_act(int64_t u, int b, int j) const {
     const int64_t k0 = (s_beg + u) * kBK;
-    if ((q & 1) == 0) {
-      char* dst = smem + b * kDenseSlot + (wave * 64 + 8 * j) * 128;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r_act, (lds_ptr_t)(dst), 16, k0 < act_lim[j] ? act_voff[j] : kMasked,
-                                               static_cast<uint32_t>(k0 * 2), 0, 0);
-    } else {
-      char* dst = smem + b * kDenseSlot + kTileBytes + (wave * 16 + 2 * j) * 512;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(r_w, (lds_ptr_t)(dst), 16, k0 < w_lim[j] ? w_voff[j] : kMasked,
-                                               static_cast<uint32_t>(k0 * a.K * 2), 0, 0);
-    }
+    char* dst = smem + b * kDenseSlot + (wave * 64 + 8 * j) * 128;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r_act, (lds_ptr_t)(dst), 16, k0 < act_lim[j] ? act_voff[j] : kMasked,
+                                             static_cast<uint32_t>(k0 * 2), 0, 0);
+  }
+  // row 8 vg + i of stage u (zeros past the piece)
+  __device__ uint4 load_w(int64_t u, int i) const {
+    const int64_t k0 = (s_beg + u) * kBK;
+    return ld128s(r_w, k0 + 8 * vg + i < a.nv ? w_voff : kMasked, static_cast<uint32_t>((k0 + i) * a.K * 2));
+  }
+  // Column c of the registers' block into slot b.  Written as an instruction:
+  // for a plain store the compiler first waits for every copy of P still in
+  // flight, since one could write the same LDS bytes (none does).  The writes
+  // are waited for before the barrier (lgkmcnt); waits the compiler sets for its
+  // own LDS reads count them as well and so only come out longer.
+  __device__ void store_w(const uint4 (&R)[8], int b, int c) const {
+    const uint4 v = column8(R, c);
+    const u32x4 d = {v.x, v.y, v.z, v.w};
+    const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem)) + b * kDenseSlot + ((wdst + 128 * c) ^ (c << 4));
+    asm volatile("ds_write_b128 %0, %1" ::"v"(at), "v"(d) : "memory");
   }
 
   struct Frags {
@@ -360,51 +387,43 @@ struct DenseTr {
   };
   __device__ void read_one(int b, int ks, int q, Frags& F) const {
     const char* base = smem + b * kDenseSlot;
-    if ((q & 1) == 0) {
+    if ((q & 1) == 0)
       F.a[q >> 1] = *reinterpret_cast<const typename T::v8*>(base + (fA[q >> 1] ^ (ks << 5)));
-    } else {
-      typedef short v4i16 __attribute__((ext_vector_type(4)));
-      typedef __attribute__((address_space(3))) v4i16* lp;
-      const char* p = base + fW[q >> 1] + ks * 16 * 512;
-      const v4i16 both[2] = {__builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(p)),
-                             __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(p + 4 * 512))};
-      F.w[q >> 1] = __builtin_bit_cast(typename T::v8, both);
-    }
+    else
+      F.w[q >> 1] = *reinterpret_cast<const typename T::v8*>(base + (fW[q >> 1] ^ (ks << 5)));
   }
   __device__ void load_frags(int b, int ks, Frags& F) const {
 #pragma unroll
     for (int q = 0; q < 8; ++q) read_one(b, ks, q, F);
   }
-  // Dense::sub_step and Dense::stage, over these copies and reads
-  __device__ void sub_step(const Frags& Fc, Frags& Fn, int bn, int ksn, int64_t cs, int cb, int q0, int nc,
-                           f32x16 (&acc)[4][4]) const {
-    const int sp = 16 / (nc > 0 ? nc : 1);
+  // 16 MFMAs from Fc; in their shadow the reads of substep ksn of slot bn and,
+  // after every second one, step g of `side`
+  template <class Side>
+  __device__ void sub_step(const Frags& Fc, Frags& Fn, int bn, int ksn, f32x16 (&acc)[4][4], Side side) const {
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int m = 4 * g + u;
-        acc[g][u] = T::mfma32(Fc.w[u], Fc.a[g], acc[g][u]);
+    for (int m = 0; m < 16; ++m) {
+      acc[m >> 2][m & 3] = T::mfma32(Fc.w[m & 3], Fc.a[m >> 2], acc[m >> 2][m & 3]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (m < 8) {
+        read_one(bn, ksn, m, Fn);
         __builtin_amdgcn_sched_barrier(0);
-        if (m < 8) {
-          read_one(bn, ksn, m, Fn);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        if (nc > 0 && m % sp == (sp > 1 ? 1 : 0)) {
-          copy_one(cs, cb, q0 + m / sp);
-          __builtin_amdgcn_sched_barrier(0);
-        }
+      }
+      if (m & 1) {
+        side(m >> 1);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
-  __device__ void stage(int64_t u, int b, Frags& F0, Frags& F1, f32x16 (&acc)[4][4]) const {
-    sub_step(F0, F1, b, 1, u + 1, b ^ 1, 8, 8, acc);
-    sub_step(F1, F0, b, 2, 0, 0, 0, 0, acc);
-    sub_step(F0, F1, b, 3, 0, 0, 0, 0, acc);
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+  __device__ void stage(int64_t u, int b, Frags& F0, Frags& F1, uint4 (&R)[8], f32x16 (&acc)[4][4]) const {
+    sub_step(F0, F1, b, 1, acc, [&](int g) { store_w(R, b ^ 1, g); });
+    sub_step(F1, F0, b, 2, acc, [&](int g) { R[g] = load_w(u + 2, g); });
+    sub_step(F0, F1, b, 3, acc, [](int) {});
+    // W of stage u+1 is written, P of stage u+1 has landed; W of stage u+2
+    // (8 loads, younger) may be in flight
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(8, 0));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    sub_step(F1, F0, b ^ 1, 0, u + 2, b, 0, 8, acc);
+    sub_step(F1, F0, b ^ 1, 0, acc, [&](int g) { copy_act(u + 2, b, g); });
   }
 };
 
@@ -427,18 +446,25 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-  // Copies past the split's end fetch the next split's data or nothing; they
+  // Loads past the split's end fetch the next split's data or nothing; they
   // land in slots that are never read.
+  uint4 R[8];
 #pragma unroll
-  for (int q = 0; q < 16; ++q) k.copy_one(0, 0, q);
-  __builtin_amdgcn_s_waitcnt(0);
+  for (int q = 0; q < 8; ++q) R[q] = k.load_w(0, q);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) k.copy_act(0, 0, q);
+#pragma unroll
+  for (int c = 0; c < 8; ++c) k.store_w(R, 0, c);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) R[q] = k.load_w(1, q);
+  __builtin_amdgcn_s_waitcnt(waitcnt_imm(8, 0));
   __builtin_amdgcn_s_barrier();
   typename DenseTr<T>::Frags F0, F1;
   k.load_frags(0, 0, F0);
 #pragma unroll
-  for (int q = 0; q < 8; ++q) k.copy_one(1, 1, q);
+  for (int q = 0; q < 8; ++q) k.copy_act(1, 1, q);
   int b = 0;
-  for (int64_t u = 0; u < total; ++u, b ^= 1) k.stage(u, b, F0, F1, acc);
+  for (int64_t u = 0; u < total; ++u, b ^= 1) k.stage(u, b, F0, F1, R, acc);
   __builtin_amdgcn_s_waitcnt(0);
   const int r32 = k.lane & 31, h = k.lane >> 5, wm = k.wave >> 1, wn = k.wave & 1;
 #pragma unroll
