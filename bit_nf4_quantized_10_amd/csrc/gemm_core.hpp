@@ -299,24 +299,25 @@ struct Big {
 
 // Dense core: both operands are 16-bit matrices with the reduction
 // contiguous (activations M x red and the dequantized weight, rows x red).
-// 64-element stages alternate between two LDS slots; a slot holds 256
-// activation rows and 256 weight rows of 128 bytes in the fused kernel's
-// layout (chunk c of row R at c ^ ((R ^ R >> 3) & 7)).  Copies are buffer
-// loads straight into LDS, each instruction 8 rows x 128 bytes, i.e. whole
-// cache lines: issuing the same bytes as 16 half-line rows per instruction
-// cost about 10% more time.  Stage s+2's 16 copies per wave go out in the
-// last substep of stage s and the first of stage s+1, one per two MFMAs (in
-// bursts they fill the TA command FIFO and stall the MFMA stream); the one
-// barrier per stage sits before the last substep, whose fragments are
-// already in registers.
+// 64-element stages go through three LDS slots of 256 activation rows and two
+// of 256 weight rows, 128 bytes a row in the fused kernel's layout (chunk c of
+// row R at c ^ ((R ^ R >> 3) & 7)): the whole 160 KB.  Copies are buffer loads
+// straight into LDS, each instruction 8 rows x 128 bytes, i.e. whole cache
+// lines: issuing the same bytes as 16 half-line rows per instruction cost about
+// 10% more time.  In stage u a wave copies its share of the activations of
+// stage u+2 during the first substep (they have 1.75 stages to land) and of its
+// weights during the last (0.75 of a stage), one copy per two MFMAs (in bursts
+// they fill the TA command FIFO and stall the MFMA stream); the one barrier per
+// stage sits before the last substep, whose fragments are already in registers,
+// and waits for all but the activations of stage u+2.
 // kGated: two weights of F columns each (rows 0 .. F-1 and F .. 2F-1 of the
 // stacked Ŵᵀ and (c B)ᵀ, a.N = 2F).  A tile takes 128 columns of the first and
 // the same 128 of the second, and each wave 64 of both, so a lane holds the
 // pair of values of an element (tiles j and j + 2).  The extension runs over
 // 4r: ext_a is M x 4r, [hi | lo] parts of the two weights' Z, and each weight's
 // rows meet only their own Z, in both parts.
-constexpr int kDenseSlot = 2 * kTileBytes;
-constexpr int kDenseLds = 2 * kDenseSlot;   // 128 KB
+constexpr int kDenseW = 3 * kTileBytes;     // the two weight slots follow the three activation slots
+constexpr int kDenseLds = 5 * kTileBytes;   // 160 KB
 
 template <class T, bool kForward, bool kKTail, bool kGated = false>
 struct Dense {
@@ -358,7 +359,7 @@ struct Dense {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       fA[i] = lds_off(wm * 128 + 32 * i + r32, h);
-      fW[i] = kTileBytes + lds_off((kGated ? (i >> 1) * 128 + wn * 64 + 32 * (i & 1) : wn * 128 + 32 * i) + r32, h);
+      fW[i] = kDenseW + lds_off((kGated ? (i >> 1) * 128 + wn * 64 + 32 * (i & 1) : wn * 128 + 32 * i) + r32, h);
     }
     lda = a.ext_a_ld ? a.ext_a_ld : a.r;
     int64_t zoff = 0;   // grouped forward: this tile's member's block of Z columns
@@ -386,26 +387,25 @@ struct Dense {
   __device__ char* sA(int) const { return smem; }
   __device__ char* sB(int) const { return smem + kTileBytes; }
 
-  // Copy q (0..15) of stage u (counted from s_beg) into slot b: the
-  // activation (even q) or weight (odd q) rows wave*64 + 8(q/2) .. +7.
-  // Past the reduction end and the extension: masked.  kMix: u may be an
-  // extension stage (else u < n_main, known to the caller).
-  template <bool kMix>
-  __device__ void copy_one(int64_t u, int b, int q) const {
-    const int j = q >> 1;
-    char* dst = smem + b * kDenseSlot + (q & 1) * kTileBytes + (wave * 64 + 8 * j) * 128;
+  // Copy of rows wave*64 + 8j .. +7 of stage u (counted from s_beg), of the
+  // activations (kW false) or the weight, to byte `slot` of LDS.  Past the
+  // reduction end and the extension: masked.  kMix: u may be an extension
+  // stage (else u < n_main, known to the caller).
+  template <bool kMix, bool kW>
+  __device__ void copy_one(int64_t u, int slot, int j) const {
+    char* dst = smem + slot + (wave * 64 + 8 * j) * 128;
     if (!kMix || u < n_main) {
       const int64_t k0 = (s_beg + u) * kBK;
       const uint32_t soff = static_cast<uint32_t>(k0 * 2);
       const bool ok = kKTail ? k0 < lim[j] : k0 < red;
-      if ((q & 1) == 0)
+      if (!kW)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r_act, (lds_ptr_t)(dst), 16, ok ? act_voff[j] : kMasked, soff, 0, 0);
       else
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r_w, (lds_ptr_t)(dst), 16, ok ? w_voff[j] : kMasked, soff, 0, 0);
     } else {
       const int row = wave * 64 + 8 * j + (lane >> 3);
       const int64_t e = (u - n_main) * kBK + 8 * ((lane & 7) ^ (lane >> 3) ^ j);
-      if ((q & 1) == 0) {
+      if (!kW) {
         const int64_t m = m0 + row;
         const uint32_t v = (m < a.M && e < r_ext) ? static_cast<uint32_t>((m * lda + e) * 2) : kMasked;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r_ea, (lds_ptr_t)(dst), 16, v, 0, 0, 0);
@@ -424,58 +424,52 @@ struct Dense {
     typename T::v8 a[4], w[4];
   };
   // Fragment q (activation q/2 for even q, weight q/2 for odd q) of
-  // substep ks of slot b: chunk 2ks + h of its row, i.e. the substep-0
-  // offset with bits 5-6 flipped by ks.
-  __device__ void read_one(int b, int ks, int q, Frags& F) const {
-    const char* base = smem + b * kDenseSlot;
+  // substep ks of the slots at bytes sa and sw: chunk 2ks + h of its row, i.e.
+  // the substep-0 offset with bits 5-6 flipped by ks (fW holds kDenseW).
+  __device__ void read_one(int sa, int sw, int ks, int q, Frags& F) const {
     if ((q & 1) == 0)
-      F.a[q >> 1] = *reinterpret_cast<const typename T::v8*>(base + (fA[q >> 1] ^ (ks << 5)));
+      F.a[q >> 1] = *reinterpret_cast<const typename T::v8*>(smem + sa + (fA[q >> 1] ^ (ks << 5)));
     else
-      F.w[q >> 1] = *reinterpret_cast<const typename T::v8*>(base + (fW[q >> 1] ^ (ks << 5)));
+      F.w[q >> 1] = *reinterpret_cast<const typename T::v8*>(smem + sw + (fW[q >> 1] ^ (ks << 5)));
   }
-  __device__ void load_frags(int b, int ks, Frags& F) const {
+  __device__ void load_frags(int sa, int sw, int ks, Frags& F) const {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) read_one(b, ks, q, F);
+    for (int q = 0; q < 8; ++q) read_one(sa, sw, ks, q, F);
   }
 
-  // 16 MFMAs from Fc; in their shadow the 8 reads of substep ksn of slot bn
-  // into Fn (within the first 8 MFMAs, so the last 8 cover their latency)
-  // and, when nc > 0, copies q0 .. q0+nc-1 of stage cs into slot cb, one
-  // per 16/nc MFMAs.  The order is pinned with scheduling barriers.
-  template <bool kMix>
-  __device__ void sub_step(const Frags& Fc, Frags& Fn, int bn, int ksn, int64_t cs, int cb, int q0, int nc,
-                           f32x16 (&acc)[4][4]) const {
-    const int sp = 16 / (nc > 0 ? nc : 1);
+  // 16 MFMAs from Fc; in their shadow the 8 reads of substep ksn of the slots
+  // sa and sw into Fn (within the first 8 MFMAs, so the last 8 cover their
+  // latency) and, after every second one, copy g of `side`.  The order is
+  // pinned with scheduling barriers.
+  template <class Side>
+  __device__ void sub_step(const Frags& Fc, Frags& Fn, int sa, int sw, int ksn, f32x16 (&acc)[4][4], Side side) const {
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int m = 4 * g + u;
-        acc[g][u] = T::mfma32(Fc.w[u], Fc.a[g], acc[g][u]);
+    for (int m = 0; m < 16; ++m) {
+      acc[m >> 2][m & 3] = T::mfma32(Fc.w[m & 3], Fc.a[m >> 2], acc[m >> 2][m & 3]);
+      __builtin_amdgcn_sched_barrier(0);
+      if (m < 8) {
+        read_one(sa, sw, ksn, m, Fn);
         __builtin_amdgcn_sched_barrier(0);
-        if (m < 8) {
-          read_one(bn, ksn, m, Fn);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        if (nc > 0 && m % sp == (sp > 1 ? 1 : 0)) {
-          copy_one<kMix>(cs, cb, q0 + m / sp);
-          __builtin_amdgcn_sched_barrier(0);
-        }
+      }
+      if (m & 1) {
+        side(m >> 1);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
   }
 
-  // Stage u from slot b, with the next stages' fragment reads and copies
-  // in its shadow (see qlora_dense_kernel).
+  // Stage u from activation slot sa and weight slot sw (bytes), the next stage's
+  // in sa1 and sw1; stage u+2 goes to sa2 and sw (see dense_loop).
   template <bool kMix>
-  __device__ void stage(int64_t u, int b, Frags& F0, Frags& F1, f32x16 (&acc)[4][4]) const {
-    sub_step<kMix>(F0, F1, b, 1, u + 1, b ^ 1, 8, 8, acc);
-    sub_step<kMix>(F1, F0, b, 2, 0, 0, 0, 0, acc);
-    sub_step<kMix>(F0, F1, b, 3, 0, 0, 0, 0, acc);
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+  __device__ void stage(int64_t u, int sa, int sa1, int sa2, int sw, int sw1, Frags& F0, Frags& F1,
+                        f32x16 (&acc)[4][4]) const {
+    sub_step(F0, F1, sa, sw, 1, acc, [&](int g) { copy_one<kMix, false>(u + 2, sa2, g); });
+    sub_step(F1, F0, sa, sw, 2, acc, [](int) {});
+    sub_step(F0, F1, sa, sw, 3, acc, [](int) {});
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(8, 0));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    sub_step<kMix>(F1, F0, b ^ 1, 0, u + 2, b, 0, 8, acc);
+    sub_step(F1, F0, sa1, sw1, 0, acc, [&](int g) { copy_one<kMix, true>(u + 2, kDenseW + sw, g); });
   }
 
   // finish() is called without the extension (it ran as the last stages).
@@ -485,12 +479,13 @@ struct Dense {
 // The dense core's loop over this workgroup's stages (kSplit: blockIdx.z's
 // share of the reduction): clears and fills acc, and releases LDS.
 // Stage u (counted from the first of this workgroup's range; the LoRA
-// extension's stages follow the product's) lives in slot u & 1.  The
-// barrier of stage u, before its last substep, says: every wave has read
-// all of slot u & 1 (its last substep's fragments are in registers) and
-// stage u+1 has landed in the other slot.  Stage u+2's copies into slot
-// u & 1 follow it.  Copies past the end are masked or land in a slot that
-// is never read.
+// extension's stages follow the product's) has its activations in slot u % 3
+// and its weights in slot u % 2.  The barrier of stage u, before its last
+// substep, says: every wave has read all of stage u (its last substep's
+// fragments are in registers) and stage u+1 has landed.  The weights of stage
+// u+2 follow it into slot u % 2; the activations of stage u+2 went into slot
+// (u - 1) % 3, free since the barrier before.  Copies past the end are masked
+// or land in a slot that is never read.
 template <bool kSplit, class Core>
 __device__ __forceinline__ void dense_loop(Core& k, const BigArgs& a, f32x16 (&acc)[4][4]) {
   int64_t s_beg, s_end;
@@ -503,18 +498,30 @@ __device__ __forceinline__ void dense_loop(Core& k, const BigArgs& a, f32x16 (&a
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
   const int64_t total = k.set_stages(s_beg, s_end, !kSplit || blockIdx.z == 0);
 #pragma unroll
-  for (int q = 0; q < 16; ++q) k.template copy_one<true>(0, 0, q);
-  __builtin_amdgcn_s_waitcnt(0);
+  for (int j = 0; j < 8; ++j) {
+    k.template copy_one<true, false>(0, 0, j);
+    k.template copy_one<true, true>(0, kDenseW, j);
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) k.template copy_one<true, false>(1, kTileBytes, j);
+  __builtin_amdgcn_s_waitcnt(waitcnt_imm(8, 0));
   __builtin_amdgcn_s_barrier();
   typename Core::Frags F0, F1;
-  k.load_frags(0, 0, F0);
+  k.load_frags(0, 0, 0, F0);
 #pragma unroll
-  for (int q = 0; q < 8; ++q) k.template copy_one<true>(1, 1, q);
-  int b = 0;
+  for (int j = 0; j < 8; ++j) k.template copy_one<true, true>(1, kDenseW + kTileBytes, j);
+  int sa = 0, sa1 = kTileBytes, sa2 = 2 * kTileBytes, sw = 0;
+  auto turn = [&] {
+    const int s = sa;
+    sa = sa1;
+    sa1 = sa2;
+    sa2 = s;
+    sw ^= kTileBytes;
+  };
   int64_t u = 0;
-  // stages whose copies (of u+1 and u+2) are all of the product, then the rest
-  for (; u + 2 < k.n_main; ++u, b ^= 1) k.template stage<false>(u, b, F0, F1, acc);
-  for (; u < total; ++u, b ^= 1) k.template stage<true>(u, b, F0, F1, acc);
+  // stages whose copies (of u+2) are all of the product, then the rest
+  for (; u + 2 < k.n_main; ++u, turn()) k.template stage<false>(u, sa, sa1, sa2, sw, sw ^ kTileBytes, F0, F1, acc);
+  for (; u < total; ++u, turn()) k.template stage<true>(u, sa, sa1, sa2, sw, sw ^ kTileBytes, F0, F1, acc);
   __builtin_amdgcn_s_waitcnt(0);
   __syncthreads();
 }

@@ -28,6 +28,10 @@ namespace qn {
 
 namespace {
 
+// The gradient product's two slots: 256 rows of P, then the 256 columns of W.
+constexpr int kDxSlot = 2 * kTileBytes;
+constexpr int kDxLds = 2 * kDxSlot;
+
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.69314718f;
 #ifndef QN_HEAD_PIECE_MB
 #define QN_HEAD_PIECE_MB 256
@@ -316,7 +320,7 @@ __device__ __forceinline__ uint4 column8(const uint4 (&in)[8], int c) {
 // loads the 8 x 8 block of rows 8 vg .. and columns 8 cg .., turns it with byte
 // permutes and writes the columns as chunks of Dense's layout.  (Reading W from
 // LDS with transposing 8-byte loads instead moves half the bytes per cycle: it
-// made the loop LDS-bound, 2102 against 1007 us at 4096 x 4096 x 32000.)
+// made the loop LDS-bound, 2102 against 960 us at 4096 x 4096 x 32000.)
 // Stage u: its first substep writes W of stage u+1 from the registers, its
 // second requests W of stage u+2; P of stage u+2 is copied straight to LDS in
 // the last one, after the barrier.
@@ -361,7 +365,7 @@ struct DenseTr {
   // P rows wave*64 + 8j .. +7 of stage u into slot b
   __device__ void copy_act(int64_t u, int b, int j) const {
     const int64_t k0 = (s_beg + u) * kBK;
-    char* dst = smem + b * kDenseSlot + (wave * 64 + 8 * j) * 128;
+    char* dst = smem + b * kDxSlot + (wave * 64 + 8 * j) * 128;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r_act, (lds_ptr_t)(dst), 16, k0 < act_lim[j] ? act_voff[j] : kMasked,
                                              static_cast<uint32_t>(k0 * 2), 0, 0);
   }
@@ -378,7 +382,7 @@ struct DenseTr {
   __device__ void store_w(const uint4 (&R)[8], int b, int c) const {
     const uint4 v = column8(R, c);
     const u32x4 d = {v.x, v.y, v.z, v.w};
-    const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem)) + b * kDenseSlot + ((wdst + 128 * c) ^ (c << 4));
+    const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem)) + b * kDxSlot + ((wdst + 128 * c) ^ (c << 4));
     asm volatile("ds_write_b128 %0, %1" ::"v"(at), "v"(d) : "memory");
   }
 
@@ -386,7 +390,7 @@ struct DenseTr {
     typename T::v8 a[4], w[4];
   };
   __device__ void read_one(int b, int ks, int q, Frags& F) const {
-    const char* base = smem + b * kDenseSlot;
+    const char* base = smem + b * kDxSlot;
     if ((q & 1) == 0)
       F.a[q >> 1] = *reinterpret_cast<const typename T::v8*>(base + (fA[q >> 1] ^ (ks << 5)));
     else
@@ -552,13 +556,13 @@ hipError_t launch_logits(const BigArgs& a, const HeadArgs& p, hipStream_t stream
 template <class T>
 hipError_t launch_dx(const DxArgs& p, hipStream_t stream) {
   static const hipError_t lds_limit = hipFuncSetAttribute(reinterpret_cast<const void*>(&head_dx_kernel<T>),
-                                                          hipFuncAttributeMaxDynamicSharedMemorySize, kDenseLds);
+                                                          hipFuncAttributeMaxDynamicSharedMemorySize, kDxLds);
   if (lds_limit != hipSuccess) return lds_limit;
   const unsigned zs = static_cast<unsigned>(p.part != nullptr ? p.splits : 1);
   const dim3 grid(static_cast<unsigned>((p.K + kBN - 1) / kBN), static_cast<unsigned>((p.M + kBM - 1) / kBM), zs);
   {
     const Timer t(QK_HEAD_DX, stream, true);
-    hipExtLaunchKernelGGL(head_dx_kernel<T>, grid, dim3(kThreads), kDenseLds, stream, t.start(), t.end(), 0, p);
+    hipExtLaunchKernelGGL(head_dx_kernel<T>, grid, dim3(kThreads), kDxLds, stream, t.start(), t.end(), 0, p);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.part == nullptr) return e;
