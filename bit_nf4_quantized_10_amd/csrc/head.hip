@@ -28,10 +28,6 @@ namespace qn {
 
 namespace {
 
-// The gradient product's two slots: 256 rows of P, then the 256 columns of W.
-constexpr int kDxSlot = 2 * kTileBytes;
-constexpr int kDxLds = 2 * kDxSlot;
-
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.69314718f;
 #ifndef QN_HEAD_PIECE_MB
 #define QN_HEAD_PIECE_MB 256
@@ -321,9 +317,9 @@ __device__ __forceinline__ uint4 column8(const uint4 (&in)[8], int c) {
 // permutes and writes the columns as chunks of Dense's layout.  (Reading W from
 // LDS with transposing 8-byte loads instead moves half the bytes per cycle: it
 // made the loop LDS-bound, 2102 against 960 us at 4096 x 4096 x 32000.)
-// Stage u: its first substep writes W of stage u+1 from the registers, its
-// second requests W of stage u+2; P of stage u+2 is copied straight to LDS in
-// the last one, after the barrier.
+// Stage u: its first substep writes W of stage u+1 from one of two register
+// sets, its second requests W of stage u+3 into that set, its third copies P of
+// stage u+2 straight into the third activation slot: 1.75 and 1.25 stages to land.
 template <class T>
 struct DenseTr {
   const DxArgs& a;
@@ -334,7 +330,7 @@ struct DenseTr {
   uint32_t act_voff[8], w_voff;
   int act_lim[8];               // copy valid while k0 < lim
   int fA[4], fW[4], wdst;
-  int64_t s_beg;
+  int64_t s_beg, w_end;
 
   __device__ DenseTr(const DxArgs& args, char* s) : a(args), smem(s) {
     t = threadIdx.x;
@@ -349,67 +345,72 @@ struct DenseTr {
       const int chunk = (lane & 7) ^ (lane >> 3) ^ j;
       const int64_t m = m0 + wave * 64 + 8 * j + (lane >> 3);
       act_voff[j] = m < a.M ? static_cast<uint32_t>((m * a.ldp + 8 * chunk) * 2) : kMasked;
-      act_lim[j] = static_cast<int>(a.ldp - 8 * chunk);
     }
     const int cg = t & 31;
     w_voff = c0 + 8 * cg < a.K ? static_cast<uint32_t>((8 * vg * a.K + c0 + 8 * cg) * 2) : kMasked;
-    wdst = kTileBytes + 8 * cg * 128 + (((vg ^ cg) & 7) << 4);   // column c: + 128 c, chunk bits ^ c
+    wdst = kDenseW + 8 * cg * 128 + (((vg ^ cg) & 7) << 4);   // column c: + 128 c, chunk bits ^ c
     const int r32 = lane & 31, h = lane >> 5, wm = wave >> 1, wn = wave & 1;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       fA[i] = lds_off(wm * 128 + 32 * i + r32, h);
-      fW[i] = kTileBytes + lds_off(wn * 128 + 32 * i + r32, h);
+      fW[i] = kDenseW + lds_off(wn * 128 + 32 * i + r32, h);
     }
   }
 
-  // P rows wave*64 + 8j .. +7 of stage u into slot b
-  __device__ void copy_act(int64_t u, int b, int j) const {
+  __device__ void limit(int64_t rows) {
+    w_end = rows < a.nv ? rows : a.nv;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int chunk = (lane & 7) ^ (lane >> 3) ^ j;
+      act_lim[j] = static_cast<int>((rows < a.ldp ? rows : a.ldp) - 8 * chunk);
+    }
+  }
+  // P rows wave*64 + 8j .. +7 of stage u to byte `slot` of LDS
+  __device__ void copy_act(int64_t u, int slot, int j) const {
     const int64_t k0 = (s_beg + u) * kBK;
-    char* dst = smem + b * kDxSlot + (wave * 64 + 8 * j) * 128;
+    char* dst = smem + slot + (wave * 64 + 8 * j) * 128;
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r_act, (lds_ptr_t)(dst), 16, k0 < act_lim[j] ? act_voff[j] : kMasked,
                                              static_cast<uint32_t>(k0 * 2), 0, 0);
   }
   // row 8 vg + i of stage u (zeros past the piece)
   __device__ uint4 load_w(int64_t u, int i) const {
     const int64_t k0 = (s_beg + u) * kBK;
-    return ld128s(r_w, k0 + 8 * vg + i < a.nv ? w_voff : kMasked, static_cast<uint32_t>((k0 + i) * a.K * 2));
+    return ld128s(r_w, k0 + 8 * vg + i < w_end ? w_voff : kMasked, static_cast<uint32_t>((k0 + i) * a.K * 2));
   }
-  // Column c of the registers' block into slot b.  Written as an instruction:
+  // Column c of the registers' block into weight slot sw (bytes).  Written as an instruction:
   // for a plain store the compiler first waits for every copy of P still in
   // flight, since one could write the same LDS bytes (none does).  The writes
   // are waited for before the barrier (lgkmcnt); waits the compiler sets for its
   // own LDS reads count them as well and so only come out longer.
-  __device__ void store_w(const uint4 (&R)[8], int b, int c) const {
+  __device__ void store_w(const uint4 (&R)[8], int sw, int c) const {
     const uint4 v = column8(R, c);
     const u32x4 d = {v.x, v.y, v.z, v.w};
-    const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem)) + b * kDxSlot + ((wdst + 128 * c) ^ (c << 4));
+    const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem)) + sw + ((wdst + 128 * c) ^ (c << 4));
     asm volatile("ds_write_b128 %0, %1" ::"v"(at), "v"(d) : "memory");
   }
 
   struct Frags {
     typename T::v8 a[4], w[4];
   };
-  __device__ void read_one(int b, int ks, int q, Frags& F) const {
-    const char* base = smem + b * kDxSlot;
+  __device__ void read_one(int sa, int sw, int ks, int q, Frags& F) const {
     if ((q & 1) == 0)
-      F.a[q >> 1] = *reinterpret_cast<const typename T::v8*>(base + (fA[q >> 1] ^ (ks << 5)));
+      F.a[q >> 1] = *reinterpret_cast<const typename T::v8*>(smem + sa + (fA[q >> 1] ^ (ks << 5)));
     else
-      F.w[q >> 1] = *reinterpret_cast<const typename T::v8*>(base + (fW[q >> 1] ^ (ks << 5)));
+      F.w[q >> 1] = *reinterpret_cast<const typename T::v8*>(smem + sw + (fW[q >> 1] ^ (ks << 5)));
   }
-  __device__ void load_frags(int b, int ks, Frags& F) const {
+  __device__ void load_frags(int sa, int sw, int ks, Frags& F) const {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) read_one(b, ks, q, F);
+    for (int q = 0; q < 8; ++q) read_one(sa, sw, ks, q, F);
   }
-  // 16 MFMAs from Fc; in their shadow the reads of substep ksn of slot bn and,
-  // after every second one, step g of `side`
+  // Dense::sub_step over these reads
   template <class Side>
-  __device__ void sub_step(const Frags& Fc, Frags& Fn, int bn, int ksn, f32x16 (&acc)[4][4], Side side) const {
+  __device__ void sub_step(const Frags& Fc, Frags& Fn, int sa, int sw, int ksn, f32x16 (&acc)[4][4], Side side) const {
 #pragma unroll
     for (int m = 0; m < 16; ++m) {
       acc[m >> 2][m & 3] = T::mfma32(Fc.w[m & 3], Fc.a[m >> 2], acc[m >> 2][m & 3]);
       __builtin_amdgcn_sched_barrier(0);
       if (m < 8) {
-        read_one(bn, ksn, m, Fn);
+        read_one(sa, sw, ksn, m, Fn);
         __builtin_amdgcn_sched_barrier(0);
       }
       if (m & 1) {
@@ -418,16 +419,18 @@ struct DenseTr {
       }
     }
   }
-  __device__ void stage(int64_t u, int b, Frags& F0, Frags& F1, uint4 (&R)[8], f32x16 (&acc)[4][4]) const {
-    sub_step(F0, F1, b, 1, acc, [&](int g) { store_w(R, b ^ 1, g); });
-    sub_step(F1, F0, b, 2, acc, [&](int g) { R[g] = load_w(u + 2, g); });
-    sub_step(F0, F1, b, 3, acc, [](int) {});
-    // W of stage u+1 is written, P of stage u+1 has landed; W of stage u+2
-    // (8 loads, younger) may be in flight
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(8, 0));
+  // R: the register set of stage u+1 (and u+3)
+  __device__ void stage(int64_t u, int sa, int sa1, int sa2, int sw, int sw1, Frags& F0, Frags& F1, uint4 (&R)[8],
+                        f32x16 (&acc)[4][4]) const {
+    sub_step(F0, F1, sa, sw, 1, acc, [&](int g) { store_w(R, sw1, g); });
+    sub_step(F1, F0, sa, sw, 2, acc, [&](int g) { R[g] = load_w(u + 3, g); });
+    sub_step(F0, F1, sa, sw, 3, acc, [&](int g) { copy_act(u + 2, sa2, g); });
+    // W of stage u+1 is written, P of stage u+1 has landed; W of stage u+3 and P
+    // of stage u+2 (8 loads each, younger) may be in flight
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(16, 0));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    sub_step(F1, F0, b ^ 1, 0, acc, [&](int g) { copy_act(u + 2, b, g); });
+    sub_step(F1, F0, sa1, sw1, 0, acc, [](int) {});
   }
 };
 
@@ -443,6 +446,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
     end = k.s_beg + p.k_per / kBK < all ? k.s_beg + p.k_per / kBK : all;
   }
   const int64_t total = end - k.s_beg;
+  k.limit(end * kBK);   // what lies past this split's rows reads as zeros
   f32x16 acc[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -450,25 +454,38 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-  // Loads past the split's end fetch the next split's data or nothing; they
-  // land in slots that are never read.
-  uint4 R[8];
+  uint4 Ra[8], Rb[8];
 #pragma unroll
-  for (int q = 0; q < 8; ++q) R[q] = k.load_w(0, q);
+  for (int q = 0; q < 8; ++q) Ra[q] = k.load_w(0, q);
 #pragma unroll
   for (int q = 0; q < 8; ++q) k.copy_act(0, 0, q);
 #pragma unroll
-  for (int c = 0; c < 8; ++c) k.store_w(R, 0, c);
+  for (int c = 0; c < 8; ++c) k.store_w(Ra, 0, c);
+  // in the order of the loop's own loads, whose waits the compiler counts
 #pragma unroll
-  for (int q = 0; q < 8; ++q) R[q] = k.load_w(1, q);
-  __builtin_amdgcn_s_waitcnt(waitcnt_imm(8, 0));
+  for (int q = 0; q < 8; ++q) Ra[q] = k.load_w(1, q);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) k.copy_act(1, kTileBytes, q);
+#pragma unroll
+  for (int q = 0; q < 8; ++q) Rb[q] = k.load_w(2, q);
+  __builtin_amdgcn_s_waitcnt(waitcnt_imm(24, 0));   // P and W of stage 0; the 24 loads since may be in flight
   __builtin_amdgcn_s_barrier();
   typename DenseTr<T>::Frags F0, F1;
-  k.load_frags(0, 0, F0);
-#pragma unroll
-  for (int q = 0; q < 8; ++q) k.copy_act(1, 1, q);
-  int b = 0;
-  for (int64_t u = 0; u < total; ++u, b ^= 1) k.stage(u, b, F0, F1, R, acc);
+  k.load_frags(0, 0, 0, F0);
+  int sa = 0, sa1 = kTileBytes, sa2 = 2 * kTileBytes;
+  auto turn = [&] {
+    const int s = sa;
+    sa = sa1;
+    sa1 = sa2;
+    sa2 = s;
+  };
+  // stages in pairs, one for each register set; an odd last one adds zeros
+  for (int64_t u = 0; u < total; u += 2) {
+    k.stage(u, sa, sa1, sa2, 0, kTileBytes, F0, F1, Ra, acc);
+    turn();
+    k.stage(u + 1, sa, sa1, sa2, kTileBytes, 0, F0, F1, Rb, acc);
+    turn();
+  }
   __builtin_amdgcn_s_waitcnt(0);
   const int r32 = k.lane & 31, h = k.lane >> 5, wm = k.wave >> 1, wn = k.wave & 1;
 #pragma unroll
@@ -556,13 +573,13 @@ hipError_t launch_logits(const BigArgs& a, const HeadArgs& p, hipStream_t stream
 template <class T>
 hipError_t launch_dx(const DxArgs& p, hipStream_t stream) {
   static const hipError_t lds_limit = hipFuncSetAttribute(reinterpret_cast<const void*>(&head_dx_kernel<T>),
-                                                          hipFuncAttributeMaxDynamicSharedMemorySize, kDxLds);
+                                                          hipFuncAttributeMaxDynamicSharedMemorySize, kDenseLds);
   if (lds_limit != hipSuccess) return lds_limit;
   const unsigned zs = static_cast<unsigned>(p.part != nullptr ? p.splits : 1);
   const dim3 grid(static_cast<unsigned>((p.K + kBN - 1) / kBN), static_cast<unsigned>((p.M + kBM - 1) / kBM), zs);
   {
     const Timer t(QK_HEAD_DX, stream, true);
-    hipExtLaunchKernelGGL(head_dx_kernel<T>, grid, dim3(kThreads), kDxLds, stream, t.start(), t.end(), 0, p);
+    hipExtLaunchKernelGGL(head_dx_kernel<T>, grid, dim3(kThreads), kDenseLds, stream, t.start(), t.end(), 0, p);
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.part == nullptr) return e;
