@@ -3,8 +3,8 @@
 // and the elementwise half of its backward.  (Up to 16 rows: gemv.hip.)
 //
 // Forward: one dense GEMM over both weights, dequantized beforehand and stacked
-// (2F x K).  A 256 x 256 tile of it takes 128 columns of each weight (Dense's
-// kGated), so the lane that holds G of an element also holds its U: the
+// (2F x K).  A 256 x 256 tile of it takes 128 columns of each weight (kPaired in
+// gemm16.hpp), so the lane that holds G of an element also holds its U: the
 // activation, the product, the 16-bit rounding and, where the backward wants
 // G and U kept in 8 bits, the checkpoint's encoding run on the accumulators,
 // and neither G nor U passes through memory to be combined.  Bound by the
@@ -20,175 +20,129 @@
 #include <hip/hip_ext.h>
 
 #include "gated.hpp"
-#include "gemm_core.hpp"
+#include "gemm16.hpp"
 
 namespace qn {
 
 namespace {
 
 struct GatedArgs {
-  BigArgs g;        // N = 2F, ext_a = [hi | lo] of c Z (M x 4r), ext_b = Bᵀ (2F x r), out = H (may be null)
+  G16Args g;        // act = X, w = [Ŵg | Ŵu]ᵀ (2F x K), ext_a = [hi | lo] of c Z (M x 4r), ext_b = Bᵀ (2F x r)
   GatedKeep keep;
+  uint16_t* H;      // null: not wanted (with kKeep16 only)
   int64_t F;
 };
 
 enum { kKeepNone = 0, kKeep16 = 1, kKeep8 = 2 };
 
-// 64 columns of one weight at one output row, held by lanes l and l ^ 32
-// (8 columns each step, 4 per lane): their checkpoint.  pairs[2 t], pairs[2 t + 1]:
-// the 16-bit values of the lane's t-th group of 4.  Returns the 4-byte codes.
-template <class T>
-__device__ __forceinline__ uint16_t encode_block(const uint32_t (&pairs)[16], uint32_t (&codes)[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) m = act8_max2(m, pairs[i] & 0x7fff7fffu);
-  m = act8_max2(m, __shfl_xor(m, 32, 64));
-  const Act8Scale s = act8_scale<T>(max(m & 0xffffu, m >> 16));
-#pragma unroll
-  for (int t = 0; t < 8; ++t) codes[t] = act8_codes4<T>(pairs[2 * t], pairs[2 * t + 1], s);
-  return s.kept;
-}
-
-// The tile's epilogue.  Lane l holds, for tiles (i, j) and (i, j + 2), row
-// 32i + l%32 and columns wn*64 + 32j + 8jj + 4(l/32) .. +3 of G and U.
+// The tile's epilogue.  A lane holds, of row 16 i + q and columns wn*64 + 16 j +
+// 4 g .. +3, G in acc[i][j] and U in acc[i][j + 4], j < 4.
 template <class T, bool kGelu, int kKeep, class Core>
-__device__ __forceinline__ void finish_gated(const Core& k, const GatedArgs& p, f32x16 (&acc)[4][4]) {
-  const BigArgs& a = p.g;
-  const int lane = k.lane, r32 = lane & 31, h = lane >> 5, wm = k.wave >> 1, wn = k.wave & 1;
-  const int64_t F = p.F;
+__device__ __forceinline__ void finish_gated(const Core& k, const GatedArgs& p, f32x4 (&acc)[8][8]) {
+  const int q = k.q, g = k.g, lane = k.lane;
+  const int64_t F = p.F, M = p.g.M;
   char* st = k.smem;
   if constexpr (kKeep == kKeep16) {
-    // [G | U] as 16-bit rows of 256 columns: chunk q < 16 of G, the others of U
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int R = wm * 128 + 32 * i + r32;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int jj = 0; jj < 4; ++jj) {
-          const int q = (j >> 1) * 16 + wn * 8 + 4 * (j & 1) + jj;
-          uint2 v;
-          v.x = T::pack2(acc[i][j][4 * jj], acc[i][j][4 * jj + 1]);
-          v.y = T::pack2(acc[i][j][4 * jj + 2], acc[i][j][4 * jj + 3]);
-          *reinterpret_cast<uint2*>(st + R * 512 + ((q ^ r32) << 4) + 8 * h) = v;
-        }
-    }
-    __syncthreads();
-    const int q = lane & 31;
-    const int64_t col = k.c0 + 8 * (q & 15);
-#pragma unroll 4
-    for (int u = 0; u < 32; ++u) {
-      const int R = k.wave * 64 + 2 * u + (lane >> 5);
-      const int64_t m = k.m0 + R;
-      const uint4 v = *reinterpret_cast<const uint4*>(st + R * 512 + ((q ^ (R & 31)) << 4));
-      if (m < a.M && col < F)
+    // [G | U]: 16-byte groups 0 .. 15 of a tile row are G's, the others U's
+    k.store_rows16(acc, [&](int R, int c, const uint4& v) {
+      const int64_t m = k.m0 + R, col = k.c0 + 8 * (c & 15);
+      if (m < M && col < F)
         __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v),
-                                    reinterpret_cast<u32x4*>(p.keep.gu + m * 2 * F + (q >> 4) * F + col));
-    }
-    if (a.out == nullptr) return;
+                                    reinterpret_cast<u32x4*>(p.keep.gu + m * 2 * F + (c >> 4) * F + col));
+    });
+    if (p.H == nullptr) return;
     __syncthreads();
   }
+  char* s8 = st + 256 * 256;   // codes as byte rows of 256 columns (128 of G, 128 of U), after the H tile
   if constexpr (kKeep == kKeep8) {
-    // codes as byte rows of 256 columns (128 of G, 128 of U), after the H tile
-    char* s8 = st + 256 * 256;
-    const int64_t nb = F / 64, blk = k.c0 / 64 + wn;
+    // A block of 64 columns of a row is the wave's 64 of one weight: 16 values in
+    // each of the four lanes q, q + 16, q + 32, q + 48.
+    const int64_t nb = F / 64, blk = k.c0 / 64 + k.wn;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int R = wm * 128 + 32 * i + r32;
+    for (int i = 0; i < 8; ++i) {
+      const int R = k.wm * 128 + 16 * i + q;
       const int64_t m = k.m0 + R;
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
-        uint32_t pairs[16], codes[8];
+        uint32_t pair[8], top = 0;
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          const f32x16& v = acc[i][2 * w + (t >> 2)];
-          const int e = 4 * (t & 3);
-          pairs[2 * t] = T::pack2(v[e], v[e + 1]);
-          pairs[2 * t + 1] = T::pack2(v[e + 2], v[e + 3]);
+        for (int j = 0; j < 4; ++j) {
+          const f32x4& v = acc[i][4 * w + j];
+          pair[2 * j] = T::pack2(v[0], v[1]);
+          pair[2 * j + 1] = T::pack2(v[2], v[3]);
+          top = act8_max2(top, act8_max2(pair[2 * j] & 0x7fff7fffu, pair[2 * j + 1] & 0x7fff7fffu));
         }
-        const uint16_t kept = encode_block<T>(pairs, codes);
-        if (h == 0 && m < a.M && blk < nb) p.keep.absmax[m * 2 * nb + w * nb + blk] = kept;
+        top = act8_max2(top, __shfl_xor(top, 16, 64));
+        top = act8_max2(top, __shfl_xor(top, 32, 64));
+        const Act8Scale s = act8_scale<T>(max(top & 0xffffu, top >> 16));
+        if (g == 0 && m < M && blk < nb) p.keep.absmax[m * 2 * nb + w * nb + blk] = s.kept;
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-          const int byte = w * 128 + wn * 64 + 32 * (t >> 2) + 8 * (t & 3) + 4 * h;
-          *reinterpret_cast<uint32_t*>(s8 + R * 256 + ((((byte >> 4) ^ R) & 15) << 4) + (byte & 15)) = codes[t];
-        }
+        for (int j = 0; j < 4; ++j)
+          *reinterpret_cast<uint32_t*>(s8 + R * 256 + (((w * 8 + k.wn * 4 + j) ^ q) << 4) + 4 * g) =
+              act8_codes4<T>(pair[2 * j], pair[2 * j + 1], s);
       }
     }
   }
   // H as 16-bit rows of 128 columns
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int R = wm * 128 + 32 * i + r32;
+  for (int i = 0; i < 8; ++i) {
+    const int R = k.wm * 128 + 16 * i + q;
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 4; ++j) {
+      float v[4];
 #pragma unroll
-      for (int jj = 0; jj < 4; ++jj) {
-        const int q = wn * 8 + 4 * j + jj;
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = act_of<kGelu>(acc[i][j][4 * jj + e]) * acc[i][j + 2][4 * jj + e];
-        *reinterpret_cast<uint2*>(st + R * 256 + (((q ^ R) & 15) << 4) + 8 * h) =
-            make_uint2(T::pack2(v[0], v[1]), T::pack2(v[2], v[3]));
-      }
+      for (int e = 0; e < 4; ++e) v[e] = act_of<kGelu>(acc[i][j][e]) * acc[i][j + 4][e];
+      *reinterpret_cast<uint2*>(st + R * 256 + (((k.wn * 8 + 2 * j + (g >> 1)) ^ q) << 4) + 8 * (g & 1)) =
+          make_uint2(T::pack2(v[0], v[1]), T::pack2(v[2], v[3]));
+    }
   }
   __syncthreads();
-  const int q = lane & 15;
-  const int64_t col = k.c0 + 8 * q;
+  const int c = lane & 15;
+  const int64_t col = k.c0 + 8 * c;
 #pragma unroll 4
   for (int u = 0; u < 16; ++u) {
     const int R = k.wave * 64 + 4 * u + (lane >> 4);
     const int64_t m = k.m0 + R;
-    const uint4 v = *reinterpret_cast<const uint4*>(st + R * 256 + (((q ^ R) & 15) << 4));
-    if (m < a.M && col < F)
-      __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4*>(a.out + m * F + col));
+    const uint4 v = *reinterpret_cast<const uint4*>(st + R * 256 + (((c ^ R) & 15) << 4));
+    if (m < M && col < F)
+      __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4*>(p.H + m * F + col));
     if constexpr (kKeep == kKeep8) {
-      const uint4 c8 = *reinterpret_cast<const uint4*>(st + 256 * 256 + R * 256 + (((q ^ R) & 15) << 4));
-      const int64_t c = k.c0 + 16 * (q & 7);   // chunks 0 .. 7 are G's, 8 .. 15 U's
-      if (m < a.M && c < F)
+      const uint4 c8 = *reinterpret_cast<const uint4*>(s8 + R * 256 + (((c ^ R) & 15) << 4));
+      const int64_t at = k.c0 + 16 * (c & 7);   // groups 0 .. 7 are G's, 8 .. 15 U's
+      if (m < M && at < F)
         __builtin_nontemporal_store(__builtin_bit_cast(u32x4, c8),
-                                    reinterpret_cast<u32x4*>(p.keep.codes + m * 2 * F + (q >> 3) * F + c));
+                                    reinterpret_cast<u32x4*>(p.keep.codes + m * 2 * F + (c >> 3) * F + at));
     }
   }
 }
 
-// The split's fp32 tile: columns c of G at c, of U at F + c of an M x 2F matrix.
-template <class Core>
-__device__ __forceinline__ void finish_gated_split(const Core& k, const GatedArgs& p, f32x16 (&acc)[4][4]) {
-  const BigArgs& a = p.g;
-  const int lane = k.lane, r32 = lane & 31, h = lane >> 5, wm = k.wave >> 1, wn = k.wave & 1;
-  const int64_t cols = 2 * p.F;
-  const Rsrc rp = make_rsrc(a.part + (static_cast<int64_t>(blockIdx.z) * a.M + k.m0) * cols + k.c0,
-                            ((a.M - k.m0) * cols - k.c0) * 4);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int row = wm * 128 + 32 * i + r32;
-    const bool row_ok = k.m0 + row < a.M;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int jj = 0; jj < 4; ++jj) {
-        const int col = wn * 64 + 32 * (j & 1) + 8 * jj + 4 * h;
-        const uint32_t voff = (row_ok && k.c0 + col < p.F)
-                                  ? static_cast<uint32_t>((row * cols + (j >> 1) * p.F + col) * 4) : kMasked;
-        const f32x4 v = {acc[i][j][4 * jj], acc[i][j][4 * jj + 1], acc[i][j][4 * jj + 2], acc[i][j][4 * jj + 3]};
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), rp, voff, 0, 0);
-      }
-  }
-}
-
-// The dense GEMM's loop (dense_loop) with the
-// gated epilogue.
-template <class T, bool kKTail, bool kSplit, bool kGelu, int kKeep>
+template <class T, bool kSplit, bool kGelu, int kKeep>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void gated_dense_kernel(GatedArgs p) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  const BigArgs& a = p.g;
-  typedef Dense<T, true, kKTail, true> Core;
-  Core k(a, smem);
-  f32x16 acc[4][4];
-  dense_loop<kSplit>(k, a, acc);
-  if constexpr (kSplit) finish_gated_split(k, p, acc);
+  Core16<T, kPaired> k(p.g, smem);
+  f32x4 acc[8][8];
+  k.template run<kSplit>(acc);
+  if constexpr (kSplit) k.store_part(acc, 2 * p.F);
   else finish_gated<T, kGelu, kKeep>(k, p, acc);
+}
+
+// dX = dY Ŵᵀ + dZ Aᵀ.
+template <class T, bool kSplit>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void gated_dx_kernel(G16Args p,
+                                                                                                      uint16_t* dX) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  Core16<T, kRows> k(p, smem);
+  f32x4 acc[8][8];
+  k.template run<kSplit>(acc);
+  if constexpr (kSplit) {
+    k.store_part(acc, p.wrows);
+  } else {
+    k.store_rows16(acc, [&](int R, int c, const uint4& v) {
+      const int64_t m = k.m0 + R, col = k.c0 + 8 * c;
+      if (m < p.M && col < p.wrows)
+        __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v), reinterpret_cast<u32x4*>(dX + m * p.wrows + col));
+    });
+  }
 }
 
 // After a split GEMM: G and U as the sums of the partials in split order, then
@@ -270,32 +224,42 @@ unsigned ew_grid(int64_t chunks) {
   return static_cast<unsigned>(b < 4096 ? b : 4096);
 }
 
-template <class T, bool kKTail, bool kSplit, bool kGelu, int kKeep>
+template <class T, bool kSplit, bool kGelu, int kKeep>
 hipError_t launch_gated_t(const GatedArgs& p, hipStream_t stream, const Timer& tm) {
   // raised once per process; the initialisation of a function-local static
   // is thread-safe, so concurrent first calls do not race
   static const hipError_t lds_limit =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(&gated_dense_kernel<T, kKTail, kSplit, kGelu, kKeep>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, kDenseLds);
+      hipFuncSetAttribute(reinterpret_cast<const void*>(&gated_dense_kernel<T, kSplit, kGelu, kKeep>),
+                          hipFuncAttributeMaxDynamicSharedMemorySize, kG16Lds);
   if (lds_limit != hipSuccess) return lds_limit;
-  const unsigned zs = kSplit ? static_cast<unsigned>((p.g.K + p.g.k_per - 1) / p.g.k_per) : 1u;
+  const unsigned zs = kSplit ? static_cast<unsigned>((p.g.red + p.g.k_per - 1) / p.g.k_per) : 1u;
   const dim3 grid(static_cast<unsigned>((p.F + 127) / 128), static_cast<unsigned>((p.g.M + kBM - 1) / kBM), zs);
-  hipExtLaunchKernelGGL((gated_dense_kernel<T, kKTail, kSplit, kGelu, kKeep>), grid, dim3(kThreads), kDenseLds, stream,
-                        tm.start(), tm.end(), 0, p);
+  hipExtLaunchKernelGGL((gated_dense_kernel<T, kSplit, kGelu, kKeep>), grid, dim3(kThreads), kG16Lds, stream, tm.start(),
+                        tm.end(), 0, p);
   return hipGetLastError();
 }
-template <class T, bool kKTail>
+template <class T>
 hipError_t launch_gated_k(const GatedArgs& p, bool gelu, hipStream_t stream, const Timer& tm) {
-  if (p.g.part != nullptr) return launch_gated_t<T, kKTail, true, false, kKeepNone>(p, stream, tm);
+  if (p.g.part != nullptr) return launch_gated_t<T, true, false, kKeepNone>(p, stream, tm);
   const int keep = p.keep.gu != nullptr ? kKeep16 : (p.keep.codes != nullptr ? kKeep8 : kKeepNone);
   if (gelu) {
-    if (keep == kKeep16) return launch_gated_t<T, kKTail, false, true, kKeep16>(p, stream, tm);
-    if (keep == kKeep8) return launch_gated_t<T, kKTail, false, true, kKeep8>(p, stream, tm);
-    return launch_gated_t<T, kKTail, false, true, kKeepNone>(p, stream, tm);
+    if (keep == kKeep16) return launch_gated_t<T, false, true, kKeep16>(p, stream, tm);
+    if (keep == kKeep8) return launch_gated_t<T, false, true, kKeep8>(p, stream, tm);
+    return launch_gated_t<T, false, true, kKeepNone>(p, stream, tm);
   }
-  if (keep == kKeep16) return launch_gated_t<T, kKTail, false, false, kKeep16>(p, stream, tm);
-  if (keep == kKeep8) return launch_gated_t<T, kKTail, false, false, kKeep8>(p, stream, tm);
-  return launch_gated_t<T, kKTail, false, false, kKeepNone>(p, stream, tm);
+  if (keep == kKeep16) return launch_gated_t<T, false, false, kKeep16>(p, stream, tm);
+  if (keep == kKeep8) return launch_gated_t<T, false, false, kKeep8>(p, stream, tm);
+  return launch_gated_t<T, false, false, kKeepNone>(p, stream, tm);
+}
+template <class T, bool kSplit>
+hipError_t launch_gated_dx_t(const G16Args& p, uint16_t* dX, hipStream_t stream, const Timer& tm) {
+  static const hipError_t lds_limit = hipFuncSetAttribute(reinterpret_cast<const void*>(&gated_dx_kernel<T, kSplit>),
+                                                          hipFuncAttributeMaxDynamicSharedMemorySize, kG16Lds);
+  if (lds_limit != hipSuccess) return lds_limit;
+  const unsigned zs = kSplit ? static_cast<unsigned>((p.red + p.k_per - 1) / p.k_per) : 1u;
+  const dim3 grid(static_cast<unsigned>((p.wrows + kBN - 1) / kBN), static_cast<unsigned>((p.M + kBM - 1) / kBM), zs);
+  hipExtLaunchKernelGGL((gated_dx_kernel<T, kSplit>), grid, dim3(kThreads), kG16Lds, stream, tm.start(), tm.end(), 0, p, dX);
+  return hipGetLastError();
 }
 
 }  // namespace
@@ -305,23 +269,19 @@ hipError_t launch_gated_dense(int64_t M, int64_t K, int64_t F, int64_t r, const 
                               const uint16_t* Zext, const uint16_t* Bt, bool gelu, uint16_t* H, const GatedKeep& keep,
                               hipStream_t stream, int dtype, void* split_ws) {
   GatedArgs p{};
-  p.g = BigArgs{X, K, NF4View{}, Zext, Bt, H, M, K, 2 * F, r, WhatT};
-  p.g.ext_a_ld = 4 * r;
+  p.g = G16Args{X, K, WhatT, M, 2 * F, K, Zext, 4 * r, Bt, r, nullptr, 0};
   p.keep = keep;
+  p.H = H;
   p.F = F;
   const SplitPlan sp = plan_split(M, 2 * F, K);
   if (sp.splits >= 2) {
     p.g.part = static_cast<float*>(split_ws);
     p.g.k_per = sp.k_per;
   }
-  const bool tail = K % kBK != 0;
   hipError_t e;
   {
     const Timer t(QK_GATED_FWD, stream, true);
-    if (dtype == kDtypeF16)
-      e = tail ? launch_gated_k<F16, true>(p, gelu, stream, t) : launch_gated_k<F16, false>(p, gelu, stream, t);
-    else
-      e = tail ? launch_gated_k<Bf16, true>(p, gelu, stream, t) : launch_gated_k<Bf16, false>(p, gelu, stream, t);
+    e = dtype == kDtypeF16 ? launch_gated_k<F16>(p, gelu, stream, t) : launch_gated_k<Bf16>(p, gelu, stream, t);
   }
   if (e != hipSuccess || sp.splits < 2) return e;
   auto* sum = dtype == kDtypeF16 ? (gelu ? gated_sum_kernel<F16, true> : gated_sum_kernel<F16, false>)
@@ -330,6 +290,27 @@ hipError_t launch_gated_dense(int64_t M, int64_t K, int64_t F, int64_t r, const 
   hipLaunchKernelGGL(sum, dim3(ew_grid(M * F / 8)), dim3(256), 0, stream, p.g.part, sp.splits, M, F, H, keep);
   tm.stop();
   return hipGetLastError();
+}
+
+hipError_t launch_gated_dx(int64_t M, int64_t K, int64_t red, int64_t rt, const uint16_t* dY, const uint16_t* What,
+                           const uint16_t* dZ, const uint16_t* A, uint16_t* dX, hipStream_t stream, int dtype,
+                           void* split_ws) {
+  G16Args p{dY, red, What, M, K, red, dZ, rt, A, rt, nullptr, 0};
+  const SplitPlan sp = plan_split(M, K, red);
+  if (sp.splits >= 2) {
+    p.part = static_cast<float*>(split_ws);
+    p.k_per = sp.k_per;
+  }
+  hipError_t e;
+  {
+    const Timer t(QK_BWD_DX, stream, true);
+    if (dtype == kDtypeF16)
+      e = p.part != nullptr ? launch_gated_dx_t<F16, true>(p, dX, stream, t) : launch_gated_dx_t<F16, false>(p, dX, stream, t);
+    else
+      e = p.part != nullptr ? launch_gated_dx_t<Bf16, true>(p, dX, stream, t) : launch_gated_dx_t<Bf16, false>(p, dX, stream, t);
+  }
+  if (e != hipSuccess || sp.splits < 2) return e;
+  return launch_split_sum(p.part, sp.splits, M * K, dX, stream, dtype);
 }
 
 hipError_t launch_gated_dy(int64_t M, int64_t F, const uint16_t* dH, const GatedKeep& kept, bool gelu, uint16_t* dY,

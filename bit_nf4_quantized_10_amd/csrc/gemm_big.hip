@@ -212,18 +212,7 @@ void attach_split(BigArgs& a, int64_t cols, int64_t red, void* part_ws) {
 hipError_t split_sum(const BigArgs& a, int64_t cols, hipStream_t stream, int dtype) {
   if (a.part == nullptr) return hipGetLastError();
   const int64_t red = cols == a.N ? a.K : a.N;
-  const int64_t splits = (red + a.k_per - 1) / a.k_per, count = a.M * cols;
-  int64_t blocks = (count / 8 + 255) / 256;
-  if (blocks > 4096) blocks = 4096;
-  Timer tm(QK_REDUCE, stream);
-  if (dtype == F16::kDtype)
-    hipLaunchKernelGGL(split_sum_kernel<F16>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, a.part,
-                       splits, count, a.out);
-  else
-    hipLaunchKernelGGL(split_sum_kernel<Bf16>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, a.part,
-                       splits, count, a.out);
-  tm.stop();
-  return hipGetLastError();
+  return launch_split_sum(a.part, (red + a.k_per - 1) / a.k_per, a.M * cols, a.out, stream, dtype);
 }
 
 #ifndef QN_SPLIT_TARGET
@@ -255,6 +244,21 @@ SplitPlan plan_split(int64_t M, int64_t cols, int64_t red) {
   const int64_t splits = (red + per - 1) / per;
   if (splits < 2) return SplitPlan{1, red, 0};
   return SplitPlan{splits, per, (splits * M * cols * 4 + 255) / 256 * 256};
+}
+
+hipError_t launch_split_sum(const float* part, int64_t splits, int64_t count, uint16_t* out, hipStream_t stream,
+                            int dtype) {
+  int64_t blocks = (count / 8 + 255) / 256;
+  if (blocks > 4096) blocks = 4096;
+  Timer tm(QK_REDUCE, stream);
+  if (dtype == F16::kDtype)
+    hipLaunchKernelGGL(split_sum_kernel<F16>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, part, splits,
+                       count, out);
+  else
+    hipLaunchKernelGGL(split_sum_kernel<Bf16>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream, part, splits,
+                       count, out);
+  tm.stop();
+  return hipGetLastError();
 }
 
 hipError_t launch_fwd_dense(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t* X, const uint16_t* WhatT,

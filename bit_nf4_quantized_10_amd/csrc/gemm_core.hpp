@@ -310,18 +310,11 @@ struct Big {
 // they fill the TA command FIFO and stall the MFMA stream); the one barrier per
 // stage sits before the last substep, whose fragments are already in registers,
 // and waits for all but the activations of stage u+2.
-// kGated: two weights of F columns each (rows 0 .. F-1 and F .. 2F-1 of the
-// stacked Ŵᵀ and (c B)ᵀ, a.N = 2F).  A tile takes 128 columns of the first and
-// the same 128 of the second, and each wave 64 of both, so a lane holds the
-// pair of values of an element (tiles j and j + 2).  The extension runs over
-// 4r: ext_a is M x 4r, [hi | lo] parts of the two weights' Z, and each weight's
-// rows meet only their own Z, in both parts.
 constexpr int kDenseW = 3 * kTileBytes;     // the two weight slots follow the three activation slots
 constexpr int kDenseLds = 5 * kTileBytes;   // 160 KB
 
-template <class T, bool kForward, bool kKTail, bool kGated = false>
+template <class T, bool kForward, bool kKTail>
 struct Dense {
-  static constexpr int kCols = kGated ? kBN / 2 : kBN;   // output columns a tile advances by
   const BigArgs& a;
   char* smem;
   int t, lane, wave;
@@ -339,7 +332,7 @@ struct Dense {
     t = threadIdx.x;
     lane = t & 63;
     wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    tile_origin<kCols>(m0, c0);
+    tile_origin(m0, c0);
     red = kForward ? a.K : a.N;
     const int64_t wrows = kForward ? a.N : a.K;
     cols = wrows;
@@ -350,7 +343,7 @@ struct Dense {
       // row = wave*64 + 8j + lane/8, whose swizzle is (lane/8) ^ j
       const int chunk = (lane & 7) ^ (lane >> 3) ^ j;
       const int row = wave * 64 + 8 * j + (lane >> 3);
-      const int64_t m = m0 + row, n = weight_row(row);
+      const int64_t m = m0 + row, n = c0 + row;
       act_voff[j] = m < a.M ? static_cast<uint32_t>((m * red + 8 * chunk) * 2) : kMasked;
       w_voff[j] = n < wrows ? static_cast<uint32_t>((n * red + 8 * chunk) * 2) : kMasked;
       lim[j] = static_cast<int>(red - 8 * chunk);
@@ -359,7 +352,7 @@ struct Dense {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       fA[i] = lds_off(wm * 128 + 32 * i + r32, h);
-      fW[i] = kDenseW + lds_off((kGated ? (i >> 1) * 128 + wn * 64 + 32 * (i & 1) : wn * 128 + 32 * i) + r32, h);
+      fW[i] = kDenseW + lds_off(wn * 128 + 32 * i + r32, h);
     }
     lda = a.ext_a_ld ? a.ext_a_ld : a.r;
     int64_t zoff = 0;   // grouped forward: this tile's member's block of Z columns
@@ -368,18 +361,11 @@ struct Dense {
     r_ea = make_rsrc(a.ext_a + zoff, (a.M * lda - zoff) * 2);
     r_eb = make_rsrc(a.ext_b, cols * a.r * 2);
   }
-  // Row of the stacked weight that the tile's weight row `row` (0 .. 255)
-  // takes; past its end (masked) where there is none.
-  __device__ int64_t weight_row(int row) const {
-    if (!kGated) return c0 + row;
-    const int64_t half = cols >> 1, col = c0 + (row & 127);
-    return col < half ? (row < 128 ? col : half + col) : cols;
-  }
   // this workgroup's stages (with_ext: it also adds the LoRA extension)
   __device__ int64_t set_stages(int64_t beg, int64_t end, bool with_ext) {
     s_beg = beg;
     n_main = end - beg;
-    r_ext = with_ext ? (kGated ? 4 * a.r : a.r) : 0;
+    r_ext = with_ext ? a.r : 0;
     return n_main + (r_ext + kBK - 1) / kBK;
   }
 
@@ -410,11 +396,8 @@ struct Dense {
         const uint32_t v = (m < a.M && e < r_ext) ? static_cast<uint32_t>((m * lda + e) * 2) : kMasked;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r_ea, (lds_ptr_t)(dst), 16, v, 0, 0, 0);
       } else {
-        const int64_t n = weight_row(row);
-        int64_t own = e;   // within this row's own r
-        if (kGated) own = (e >= 2 * a.r ? e - 2 * a.r : e) - (row < 128 ? 0 : a.r);
-        const uint32_t v = (n < cols && e < r_ext && (!kGated || (own >= 0 && own < a.r)))
-                               ? static_cast<uint32_t>((n * a.r + own) * 2) : kMasked;
+        const int64_t n = c0 + row;
+        const uint32_t v = (n < cols && e < r_ext) ? static_cast<uint32_t>((n * a.r + e) * 2) : kMasked;
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r_eb, (lds_ptr_t)(dst), 16, v, 0, 0, 0);
       }
     }

@@ -22,7 +22,7 @@
 // Bound by the matrix cores; with few rows by the read of W.
 #include <hip/hip_ext.h>
 
-#include "gemm_core.hpp"
+#include "gemm16.hpp"
 
 namespace qn {
 
@@ -49,89 +49,74 @@ struct HeadArgs {
   float* st;                 // M: the target's logit
 };
 
-template <class T, bool kKTail, bool kStore>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void head_logits_kernel(BigArgs a,
+template <class T, bool kStore>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void head_logits_kernel(G16Args a,
                                                                                                          HeadArgs p) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  typedef Dense<T, true, kKTail> Core;
-  Core k(a, smem);
-  f32x16 acc[4][4];
-  dense_loop<false>(k, a, acc);
-  const int lane = k.lane, r32 = lane & 31, h = lane >> 5, wm = k.wave >> 1, wn = k.wave & 1;
-  const int64_t cbase = k.c0 + wn * 128;           // this wave's first column of the piece
+  Core16<T, kRows> k(a, smem);
+  f32x4 acc[8][8];
+  k.template run<false>(acc);
+  // a row's 128 columns of this wave: 32 in each of the four lanes q, q + 16, q + 32, q + 48
+  const int64_t cbase = k.c0 + k.wn * 128;         // this wave's first column of the piece
   const int64_t half = cbase >> 7;
   const bool ragged = cbase + 128 > p.nv;          // the wave has columns past the piece
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t m = k.m0 + wm * 128 + 32 * i + r32;
+  for (int i = 0; i < 8; ++i) {
+    const int64_t m = k.m0 + k.wm * 128 + 16 * i + k.q;
     const int64_t t = m < a.M ? p.targets[m] : -1;
     const int64_t d = t - p.v0 - cbase;
     // the target, if it is one of this wave's columns (an ignored row has none)
     const bool here = t >= 0 && t < p.V && t != p.ignore && d >= 0 && d < 128;
-    if (ragged) {
+    float v[32];
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (cbase + 32 * j + 8 * (e >> 2) + 4 * h + (e & 3) >= p.nv) acc[i][j][e] = -__builtin_inff();
-    }
+      for (int e = 0; e < 4; ++e) {
+        v[4 * j + e] = acc[i][j][e];
+        if (ragged && cbase + 16 * j + 4 * k.g + e >= p.nv) v[4 * j + e] = -__builtin_inff();
+      }
     if (__any(here)) {
-      const int own = here ? static_cast<int>(d) - 4 * h : -1;
+      const int own = here ? static_cast<int>(d) - 4 * k.g : -1;   // 16 j + e where it is this lane's
+      float s = 0.0f;
+      bool mine = false;
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 8; ++j)
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          if (own == 32 * j + 8 * (e >> 2) + (e & 3)) {
-            p.st[m] = acc[i][j][e];
-            acc[i][j][e] = -__builtin_inff();
-          }
+        for (int e = 0; e < 4; ++e) {
+          const bool at = own == 16 * j + e;
+          s = at ? v[4 * j + e] : s;
+          v[4 * j + e] = at ? -__builtin_inff() : v[4 * j + e];
+          mine = mine || at;
+        }
+      if (mine) p.st[m] = s;
     }
-    float top = -__builtin_inff();
+    float top = v[0];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) top = fmaxf(top, acc[i][j][e]);
+    for (int x = 1; x < 32; ++x) top = fmaxf(top, v[x]);
+    top = fmaxf(top, __shfl_xor(top, 16, 64));
     top = fmaxf(top, __shfl_xor(top, 32, 64));
     // nothing but masked columns: any bound serves, every P is 0
     const float ref = top == -__builtin_inff() ? 0.0f : __builtin_ceilf(top * kLog2e);
     float sum = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float v = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][e], kLog2e, -ref));
-        sum += v;
-        acc[i][j][e] = v * static_cast<float>(1 << head_shift<T>());
-      }
+    for (int x = 0; x < 32; ++x) {
+      v[x] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[x], kLog2e, -ref));
+      sum += v[x];
+      v[x] *= static_cast<float>(1 << head_shift<T>());
+    }
+    sum += __shfl_xor(sum, 16, 64);
     sum += __shfl_xor(sum, 32, 64);
-    if (h == 0 && m < a.M && half < p.nh) p.stats[m * p.nh + half] = make_float2(ref, sum);
+    if (k.g == 0 && m < a.M && half < p.nh) p.stats[m * p.nh + half] = make_float2(ref, sum);
+    if constexpr (kStore) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) k.put16(i, j, v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    }
   }
   if constexpr (kStore) {
-    char* st = smem;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int R = wm * 128 + 32 * i + r32;
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int jj = 0; jj < 4; ++jj) {
-          const int q = wn * 16 + 4 * j + jj;
-          uint2 v;
-          v.x = T::pack2(acc[i][j][4 * jj], acc[i][j][4 * jj + 1]);
-          v.y = T::pack2(acc[i][j][4 * jj + 2], acc[i][j][4 * jj + 3]);
-          *reinterpret_cast<uint2*>(st + R * 512 + ((q ^ r32) << 4) + 8 * h) = v;
-        }
-    }
-    __syncthreads();
-    const int q = lane & 31;
-    const int64_t n = k.c0 + 8 * q;
-#pragma unroll 4
-    for (int u = 0; u < 32; ++u) {
-      const int R = k.wave * 64 + 2 * u + (lane >> 5);
-      const int64_t m = k.m0 + R;
-      const uint4 v = *reinterpret_cast<const uint4*>(st + R * 512 + ((q ^ (R & 31)) << 4));
-      if (m < a.M && n < p.ldp) *reinterpret_cast<uint4*>(p.P + m * p.ldp + n) = v;
-    }
+    k.flush16([&](int R, int c, const uint4& x) {
+      const int64_t m = k.m0 + R, n = k.c0 + 8 * c;
+      if (m < a.M && n < p.ldp) *reinterpret_cast<uint4*>(p.P + m * p.ldp + n) = x;
+    });
   }
 }
 
@@ -239,11 +224,8 @@ __global__ __launch_bounds__(256) void head_rows_kernel(RowArgs p) {
 
 // What becomes of a piece's product at rows m and columns of dX.
 struct DxArgs {
-  int64_t M, K, nv, ldp;
-  const uint16_t* P;
-  const uint16_t* Wp;        // the piece's rows of W, nv x K
-  float* part;               // splits x M x K partials (more than one split), else null
-  int64_t k_per;             // vocabulary rows per split
+  int64_t M, K;
+  const float* part;         // splits x M x K partials of a split product, else null
   int64_t splits;
   const float* prev;         // earlier pieces' sums M x K, or null
   const float* alpha;
@@ -296,212 +278,26 @@ __global__ __launch_bounds__(256) void head_sum_kernel(DxArgs p) {
   }
 }
 
-// 8 x 8 transpose of 16-bit values: column c of the 8 rows `in`, as 16 bytes.
-__device__ __forceinline__ uint4 column8(const uint4 (&in)[8], int c) {
-  const uint32_t sel = (c & 1) ? 0x07060302u : 0x05040100u;
-  uint32_t d[4];
-#pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const uint4 &lo = in[2 * p], &hi = in[2 * p + 1];
-    const uint32_t l = (c >> 1) == 0 ? lo.x : ((c >> 1) == 1 ? lo.y : ((c >> 1) == 2 ? lo.z : lo.w));
-    const uint32_t h = (c >> 1) == 0 ? hi.x : ((c >> 1) == 1 ? hi.y : ((c >> 1) == 2 ? hi.z : hi.w));
-    d[p] = __builtin_amdgcn_perm(h, l, sel);
-  }
-  return make_uint4(d[0], d[1], d[2], d[3]);
-}
-
-// P (M x nv) times the piece's rows of W (nv x K): Dense's tile, slots and
-// fragment reads (see there), with the reduction running down the rows of W.
-// A stage's 64 rows x 256 columns of W come through registers: thread (vg, cg)
-// loads the 8 x 8 block of rows 8 vg .. and columns 8 cg .., turns it with byte
-// permutes and writes the columns as chunks of Dense's layout.  (Reading W from
-// LDS with transposing 8-byte loads instead moves half the bytes per cycle: it
-// made the loop LDS-bound, 2102 against 960 us at 4096 x 4096 x 32000.)
-// Stage u: its first substep writes W of stage u+1 from one of two register
-// sets, its second requests W of stage u+3 into that set, its third copies P of
-// stage u+2 straight into the third activation slot: 1.75 and 1.25 stages to land.
-template <class T>
-struct DenseTr {
-  const DxArgs& a;
-  char* smem;
-  int t, lane, wave, vg;
-  int64_t m0, c0;
-  Rsrc r_act, r_w;
-  uint32_t act_voff[8], w_voff;
-  int act_lim[8];               // copy valid while k0 < lim
-  int fA[4], fW[4], wdst;
-  int64_t s_beg, w_end;
-
-  __device__ DenseTr(const DxArgs& args, char* s) : a(args), smem(s) {
-    t = threadIdx.x;
-    lane = t & 63;
-    wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    vg = t >> 5;
-    tile_origin(m0, c0);
-    r_act = make_rsrc(a.P, a.M * a.ldp * 2);
-    r_w = make_rsrc(a.Wp, a.nv * a.K * 2);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int chunk = (lane & 7) ^ (lane >> 3) ^ j;
-      const int64_t m = m0 + wave * 64 + 8 * j + (lane >> 3);
-      act_voff[j] = m < a.M ? static_cast<uint32_t>((m * a.ldp + 8 * chunk) * 2) : kMasked;
-    }
-    const int cg = t & 31;
-    w_voff = c0 + 8 * cg < a.K ? static_cast<uint32_t>((8 * vg * a.K + c0 + 8 * cg) * 2) : kMasked;
-    wdst = kDenseW + 8 * cg * 128 + (((vg ^ cg) & 7) << 4);   // column c: + 128 c, chunk bits ^ c
-    const int r32 = lane & 31, h = lane >> 5, wm = wave >> 1, wn = wave & 1;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      fA[i] = lds_off(wm * 128 + 32 * i + r32, h);
-      fW[i] = kDenseW + lds_off(wn * 128 + 32 * i + r32, h);
-    }
-  }
-
-  __device__ void limit(int64_t rows) {
-    w_end = rows < a.nv ? rows : a.nv;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int chunk = (lane & 7) ^ (lane >> 3) ^ j;
-      act_lim[j] = static_cast<int>((rows < a.ldp ? rows : a.ldp) - 8 * chunk);
-    }
-  }
-  // P rows wave*64 + 8j .. +7 of stage u to byte `slot` of LDS
-  __device__ void copy_act(int64_t u, int slot, int j) const {
-    const int64_t k0 = (s_beg + u) * kBK;
-    char* dst = smem + slot + (wave * 64 + 8 * j) * 128;
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(r_act, (lds_ptr_t)(dst), 16, k0 < act_lim[j] ? act_voff[j] : kMasked,
-                                             static_cast<uint32_t>(k0 * 2), 0, 0);
-  }
-  // row 8 vg + i of stage u (zeros past the piece)
-  __device__ uint4 load_w(int64_t u, int i) const {
-    const int64_t k0 = (s_beg + u) * kBK;
-    return ld128s(r_w, k0 + 8 * vg + i < w_end ? w_voff : kMasked, static_cast<uint32_t>((k0 + i) * a.K * 2));
-  }
-  // Column c of the registers' block into weight slot sw (bytes).  Written as an instruction:
-  // for a plain store the compiler first waits for every copy of P still in
-  // flight, since one could write the same LDS bytes (none does).  The writes
-  // are waited for before the barrier (lgkmcnt); waits the compiler sets for its
-  // own LDS reads count them as well and so only come out longer.
-  __device__ void store_w(const uint4 (&R)[8], int sw, int c) const {
-    const uint4 v = column8(R, c);
-    const u32x4 d = {v.x, v.y, v.z, v.w};
-    const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem)) + sw + ((wdst + 128 * c) ^ (c << 4));
-    asm volatile("ds_write_b128 %0, %1" ::"v"(at), "v"(d) : "memory");
-  }
-
-  struct Frags {
-    typename T::v8 a[4], w[4];
-  };
-  __device__ void read_one(int sa, int sw, int ks, int q, Frags& F) const {
-    if ((q & 1) == 0)
-      F.a[q >> 1] = *reinterpret_cast<const typename T::v8*>(smem + sa + (fA[q >> 1] ^ (ks << 5)));
-    else
-      F.w[q >> 1] = *reinterpret_cast<const typename T::v8*>(smem + sw + (fW[q >> 1] ^ (ks << 5)));
-  }
-  __device__ void load_frags(int sa, int sw, int ks, Frags& F) const {
-#pragma unroll
-    for (int q = 0; q < 8; ++q) read_one(sa, sw, ks, q, F);
-  }
-  // Dense::sub_step over these reads
-  template <class Side>
-  __device__ void sub_step(const Frags& Fc, Frags& Fn, int sa, int sw, int ksn, f32x16 (&acc)[4][4], Side side) const {
-#pragma unroll
-    for (int m = 0; m < 16; ++m) {
-      acc[m >> 2][m & 3] = T::mfma32(Fc.w[m & 3], Fc.a[m >> 2], acc[m >> 2][m & 3]);
-      __builtin_amdgcn_sched_barrier(0);
-      if (m < 8) {
-        read_one(sa, sw, ksn, m, Fn);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      if (m & 1) {
-        side(m >> 1);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    }
-  }
-  // R: the register set of stage u+1 (and u+3)
-  __device__ void stage(int64_t u, int sa, int sa1, int sa2, int sw, int sw1, Frags& F0, Frags& F1, uint4 (&R)[8],
-                        f32x16 (&acc)[4][4]) const {
-    sub_step(F0, F1, sa, sw, 1, acc, [&](int g) { store_w(R, sw1, g); });
-    sub_step(F1, F0, sa, sw, 2, acc, [&](int g) { R[g] = load_w(u + 3, g); });
-    sub_step(F0, F1, sa, sw, 3, acc, [&](int g) { copy_act(u + 2, sa2, g); });
-    // W of stage u+1 is written, P of stage u+1 has landed; W of stage u+3 and P
-    // of stage u+2 (8 loads each, younger) may be in flight
-    __builtin_amdgcn_s_waitcnt(waitcnt_imm(16, 0));
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    sub_step(F1, F0, sa1, sw1, 0, acc, [](int) {});
-  }
-};
-
-template <class T>
-__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void head_dx_kernel(DxArgs p) {
+// P (M x nv) times the piece's rows of W (nv x K).
+template <class T, bool kSplit>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void head_dx_kernel(G16Args a, DxArgs p) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
-  DenseTr<T> k(p, smem);
-  const int64_t all = (p.ldp + kBK - 1) / kBK;
-  int64_t end = all;
-  k.s_beg = 0;
-  if (p.part != nullptr) {
-    k.s_beg = static_cast<int64_t>(blockIdx.z) * (p.k_per / kBK);
-    end = k.s_beg + p.k_per / kBK < all ? k.s_beg + p.k_per / kBK : all;
+  Core16<T, kTurned> k(a, smem);
+  f32x4 acc[8][8];
+  k.template run<kSplit>(acc);
+  if constexpr (kSplit) {
+    k.store_part(acc, p.K);
+    return;
   }
-  const int64_t total = end - k.s_beg;
-  k.limit(end * kBK);   // what lies past this split's rows reads as zeros
-  f32x16 acc[4][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-  uint4 Ra[8], Rb[8];
-#pragma unroll
-  for (int q = 0; q < 8; ++q) Ra[q] = k.load_w(0, q);
-#pragma unroll
-  for (int q = 0; q < 8; ++q) k.copy_act(0, 0, q);
-#pragma unroll
-  for (int c = 0; c < 8; ++c) k.store_w(Ra, 0, c);
-  // in the order of the loop's own loads, whose waits the compiler counts
-#pragma unroll
-  for (int q = 0; q < 8; ++q) Ra[q] = k.load_w(1, q);
-#pragma unroll
-  for (int q = 0; q < 8; ++q) k.copy_act(1, kTileBytes, q);
-#pragma unroll
-  for (int q = 0; q < 8; ++q) Rb[q] = k.load_w(2, q);
-  __builtin_amdgcn_s_waitcnt(waitcnt_imm(24, 0));   // P and W of stage 0; the 24 loads since may be in flight
-  __builtin_amdgcn_s_barrier();
-  typename DenseTr<T>::Frags F0, F1;
-  k.load_frags(0, 0, 0, F0);
-  int sa = 0, sa1 = kTileBytes, sa2 = 2 * kTileBytes;
-  auto turn = [&] {
-    const int s = sa;
-    sa = sa1;
-    sa1 = sa2;
-    sa2 = s;
-  };
-  // stages in pairs, one for each register set; an odd last one adds zeros
-  for (int64_t u = 0; u < total; u += 2) {
-    k.stage(u, sa, sa1, sa2, 0, kTileBytes, F0, F1, Ra, acc);
-    turn();
-    k.stage(u + 1, sa, sa1, sa2, kTileBytes, 0, F0, F1, Rb, acc);
-    turn();
-  }
-  __builtin_amdgcn_s_waitcnt(0);
-  const int r32 = k.lane & 31, h = k.lane >> 5, wm = k.wave >> 1, wn = k.wave & 1;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t m = k.m0 + wm * 128 + 32 * i + r32;
+  for (int i = 0; i < 8; ++i) {
+    const int64_t m = k.m0 + k.wm * 128 + 16 * i + k.q;
     if (m >= p.M) continue;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int jj = 0; jj < 4; ++jj) {
-        const int64_t col = k.c0 + wn * 128 + 32 * j + 8 * jj + 4 * h;
-        if (col >= p.K) continue;
-        const f32x4 v = {acc[i][j][4 * jj], acc[i][j][4 * jj + 1], acc[i][j][4 * jj + 2], acc[i][j][4 * jj + 3]};
-        if (p.part != nullptr) *reinterpret_cast<f32x4*>(p.part + (blockIdx.z * p.M + m) * p.K + col) = v;
-        else dx_store4<T>(p, m, col, v);
-      }
+    for (int j = 0; j < 8; ++j) {
+      const int64_t col = k.c0 + k.wn * 128 + 16 * j + 4 * k.g;
+      if (col < p.K) dx_store4<T>(p, m, col, acc[i][j]);
+    }
   }
 }
 
@@ -548,40 +344,33 @@ HeadPlan head_plan(int64_t M, int64_t K, int64_t V, bool need_dx) {
   return h;
 }
 
-template <class T, bool kKTail, bool kStore>
-hipError_t launch_logits_t(const BigArgs& a, const HeadArgs& p, hipStream_t stream, const Timer& tm) {
+template <class T, bool kStore>
+hipError_t launch_logits_t(const G16Args& a, const HeadArgs& p, hipStream_t stream) {
   // raised once per process; the initialisation of a function-local static
   // is thread-safe, so concurrent first calls do not race
-  static const hipError_t lds_limit =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(&head_logits_kernel<T, kKTail, kStore>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, kDenseLds);
+  static const hipError_t lds_limit = hipFuncSetAttribute(reinterpret_cast<const void*>(&head_logits_kernel<T, kStore>),
+                                                          hipFuncAttributeMaxDynamicSharedMemorySize, kG16Lds);
   if (lds_limit != hipSuccess) return lds_limit;
+  const Timer t(QK_HEAD_LOGITS, stream, true);
   const dim3 grid(static_cast<unsigned>((p.nv + kBN - 1) / kBN), static_cast<unsigned>((a.M + kBM - 1) / kBM));
-  hipExtLaunchKernelGGL((head_logits_kernel<T, kKTail, kStore>), grid, dim3(kThreads), kDenseLds, stream, tm.start(),
-                        tm.end(), 0, a, p);
+  hipExtLaunchKernelGGL((head_logits_kernel<T, kStore>), grid, dim3(kThreads), kG16Lds, stream, t.start(), t.end(), 0, a, p);
+  return hipGetLastError();
+}
+
+template <class T, bool kSplit>
+hipError_t launch_dx_t(const G16Args& a, const DxArgs& p, hipStream_t stream) {
+  static const hipError_t lds_limit = hipFuncSetAttribute(reinterpret_cast<const void*>(&head_dx_kernel<T, kSplit>),
+                                                          hipFuncAttributeMaxDynamicSharedMemorySize, kG16Lds);
+  if (lds_limit != hipSuccess) return lds_limit;
+  const unsigned zs = static_cast<unsigned>(kSplit ? p.splits : 1);
+  const dim3 grid(static_cast<unsigned>((p.K + kBN - 1) / kBN), static_cast<unsigned>((p.M + kBM - 1) / kBM), zs);
+  const Timer t(QK_HEAD_DX, stream, true);
+  hipExtLaunchKernelGGL((head_dx_kernel<T, kSplit>), grid, dim3(kThreads), kG16Lds, stream, t.start(), t.end(), 0, a, p);
   return hipGetLastError();
 }
 template <class T>
-hipError_t launch_logits(const BigArgs& a, const HeadArgs& p, hipStream_t stream) {
-  const Timer t(QK_HEAD_LOGITS, stream, true);
-  const bool tail = a.K % kBK != 0;
-  if (p.P != nullptr)
-    return tail ? launch_logits_t<T, true, true>(a, p, stream, t) : launch_logits_t<T, false, true>(a, p, stream, t);
-  return tail ? launch_logits_t<T, true, false>(a, p, stream, t) : launch_logits_t<T, false, false>(a, p, stream, t);
-}
-
-template <class T>
-hipError_t launch_dx(const DxArgs& p, hipStream_t stream) {
-  static const hipError_t lds_limit = hipFuncSetAttribute(reinterpret_cast<const void*>(&head_dx_kernel<T>),
-                                                          hipFuncAttributeMaxDynamicSharedMemorySize, kDenseLds);
-  if (lds_limit != hipSuccess) return lds_limit;
-  const unsigned zs = static_cast<unsigned>(p.part != nullptr ? p.splits : 1);
-  const dim3 grid(static_cast<unsigned>((p.K + kBN - 1) / kBN), static_cast<unsigned>((p.M + kBM - 1) / kBM), zs);
-  {
-    const Timer t(QK_HEAD_DX, stream, true);
-    hipExtLaunchKernelGGL(head_dx_kernel<T>, grid, dim3(kThreads), kDenseLds, stream, t.start(), t.end(), 0, p);
-  }
-  hipError_t e = hipGetLastError();
+hipError_t launch_dx(const G16Args& a, const DxArgs& p, hipStream_t stream) {
+  const hipError_t e = p.part != nullptr ? launch_dx_t<T, true>(a, p, stream) : launch_dx_t<T, false>(a, p, stream);
   if (e != hipSuccess || p.part == nullptr) return e;
   int64_t blocks = (p.M * p.K / 4 + 255) / 256;
   if (blocks > 8192) blocks = 8192;
@@ -614,9 +403,9 @@ hipError_t head_loss_t(int64_t M, int64_t K, int64_t V, const uint16_t* X, const
   for (int64_t i = 0; i < h.pieces; ++i) {
     const int64_t v0 = i * h.rows, nv = V - v0 < h.rows ? V - v0 : h.rows;
     const bool last = i + 1 == h.pieces;
-    BigArgs g{X, K, NF4View{}, X, X, nullptr, M, K, nv, 0, W + v0 * K};
+    const G16Args g{X, K, W + v0 * K, M, nv, K, nullptr, 0, nullptr, 0, nullptr, 0};
     HeadArgs p{targets, v0, nv, (nv + 63) / 64 * 64, V, ignore, dX != nullptr ? P : nullptr, stats, (nv + 127) / 128, st};
-    hipError_t e = launch_logits<T>(g, p, stream);
+    hipError_t e = dX != nullptr ? launch_logits_t<T, true>(g, p, stream) : launch_logits_t<T, false>(g, p, stream);
     if (e != hipSuccess) return e;
     RowArgs r{stats, p.nh, p.ldp, M, V, ignore, p.P, i > 0 ? run[(i + 1) & 1] : nullptr, run[i & 1], st, targets, weights,
               alpha, last ? loss : nullptr, lse != nullptr ? lse : lse_own, dX != nullptr ? coef : nullptr};
@@ -631,10 +420,13 @@ hipError_t head_loss_t(int64_t M, int64_t K, int64_t V, const uint16_t* X, const
     }
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (dX == nullptr) continue;
-    DxArgs d{M, K, nv, p.ldp, P, W + v0 * K, h.splits > 1 ? part : nullptr, h.k_per, h.splits, i > 0 ? sums : nullptr, alpha,
-             last ? nullptr : sums, coef, W, targets, dX, 1.0f / static_cast<float>(1 << head_shift<T>())};
-    if (h.splits > 1) d.splits = (p.ldp + h.k_per - 1) / h.k_per;   // the last piece may be shorter
-    if ((e = launch_dx<T>(d, stream)) != hipSuccess) return e;
+    // the last piece may be shorter and need fewer splits
+    const int64_t splits = (nv + h.k_per - 1) / h.k_per;
+    const bool split = h.splits > 1;
+    const G16Args w{P, p.ldp, W + v0 * K, M, K, nv, nullptr, 0, nullptr, 0, split ? part : nullptr, h.k_per};
+    const DxArgs d{M, K, w.part, splits, i > 0 ? sums : nullptr, alpha, last ? nullptr : sums, coef, W, targets, dX,
+                   1.0f / static_cast<float>(1 << head_shift<T>())};
+    if ((e = launch_dx<T>(w, d, stream)) != hipSuccess) return e;
   }
   return hipSuccess;
 }

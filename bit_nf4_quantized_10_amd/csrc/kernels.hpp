@@ -81,8 +81,7 @@ hipError_t launch_merge(int64_t K, int64_t N, int64_t r, NF4View W, const void* 
 hipError_t launch_sgd(int64_t K, int64_t N, int64_t r, uint16_t* A, uint16_t* B, const float* dA, const float* dB,
                       float lr, float* A_master, float* B_master, hipStream_t stream, int dtype = 0);
 
-// Grouped linears sharing X (see layer.hip).  dZ_lo (scratch, M x g r): dA is
-// formed from dZ before its rounding to 16 bits.
+// Grouped linears sharing X (see layer.hip).
 int64_t grouped_fwd_workspace_bytes(int64_t M, int64_t K, int g, const int64_t* Ns, int64_t r);
 int64_t grouped_bwd_workspace_bytes(int64_t M, int64_t K, int g, const int64_t* Ns, int64_t r);
 hipError_t launch_grouped_fwd(int64_t M, int64_t K, int g, const int64_t* Ns, int64_t r, const uint16_t* X,
@@ -90,9 +89,8 @@ hipError_t launch_grouped_fwd(int64_t M, int64_t K, int g, const int64_t* Ns, in
                               uint16_t* Z, void* ws, hipStream_t stream, int dtype = kDtypeBf16);
 hipError_t launch_grouped_bwd(int64_t M, int64_t K, int g, const int64_t* Ns, int64_t r, const uint16_t* G,
                               const uint16_t* X, const uint16_t* Z, const NF4View* W, const uint16_t* A,
-                              const uint16_t* B, float c, uint16_t* dX, void* dA, void* dB, void* ws,
-                              hipStream_t stream, int dtype = kDtypeBf16, bool grad16 = false, Act8View x8 = {},
-                              uint16_t* dZ_lo = nullptr);
+                              const uint16_t* B, float c, uint16_t* dX, float* dA, float* dB, void* ws,
+                              hipStream_t stream, int dtype = kDtypeBf16);
 
 // Workspace needs (bytes) of the layer kernels; the C ABI adds them up.
 int64_t fwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t r);
@@ -130,6 +128,8 @@ GroupPlan plan_grouped(int64_t M, int64_t K, int g, const int64_t* Ns, int64_t r
 hipError_t launch_dz_grouped(int64_t M, int g, const int64_t* Ns, int64_t Ntot, int64_t r, const uint16_t* G,
                              const uint16_t* B, float c, uint16_t* dZ, const GroupPlan& gp, void* part_ws,
                              hipStream_t stream, int dtype = 0, RdJob* defer = nullptr, uint16_t* dZ_lo = nullptr);
+// dZ_lo (M x g r, or null): what dZ's rounding to 16 bits left out (launch_dz_grouped
+// writes it); dA is then formed from both.
 hipError_t launch_colsums_grouped(int64_t M, int64_t K, int g, const int64_t* Ns, int64_t Ntot, int64_t r,
                                   const uint16_t* X, const uint16_t* G, const uint16_t* Z, const uint16_t* dZ, float c,
                                   void* dA, void* dB, const GroupPlan& gp, void* da_ws, void* db_ws,
@@ -167,6 +167,10 @@ struct SplitPlan {
   int64_t splits, k_per, part_bytes;
 };
 SplitPlan plan_split(int64_t M, int64_t cols, int64_t red);
+// out = the 16-bit rounding of the sum of `splits` fp32 planes of count
+// elements (count % 8 == 0) in order.
+hipError_t launch_split_sum(const float* part, int64_t splits, int64_t count, uint16_t* out, hipStream_t stream,
+                            int dtype);
 
 // The GEMMs below split their reduction per plan_split when split_ws (at
 // least part_bytes, 16-byte aligned) is given, then sum the partials in
@@ -212,6 +216,10 @@ hipError_t launch_gated_bwd(int64_t M, int64_t K, int64_t F, int64_t r, const ui
 hipError_t launch_gated_dense(int64_t M, int64_t K, int64_t F, int64_t r, const uint16_t* X, const uint16_t* WhatT,
                               const uint16_t* Zext, const uint16_t* Bt, bool gelu, uint16_t* H, const GatedKeep& keep,
                               hipStream_t stream, int dtype, void* split_ws);
+// dX = dY Ŵᵀ + dZ Aᵀ: dY M x red, What K x red, dZ M x rt, A K x rt.
+hipError_t launch_gated_dx(int64_t M, int64_t K, int64_t red, int64_t rt, const uint16_t* dY, const uint16_t* What,
+                           const uint16_t* dZ, const uint16_t* A, uint16_t* dX, hipStream_t stream, int dtype,
+                           void* split_ws);
 hipError_t launch_gated_dy(int64_t M, int64_t F, const uint16_t* dH, const GatedKeep& kept, bool gelu, uint16_t* dY,
                            hipStream_t stream, int dtype);
 // Up to 16 rows: split-K partials of both weights and of Z, then their sums.

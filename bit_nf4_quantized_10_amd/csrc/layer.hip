@@ -188,8 +188,8 @@ hipError_t launch_grouped_fwd(int64_t M, int64_t K, int g, const int64_t* Ns, in
 
 hipError_t launch_grouped_bwd(int64_t M, int64_t K, int g, const int64_t* Ns, int64_t r, const uint16_t* G,
                               const uint16_t* X, const uint16_t* Z, const NF4View* W, const uint16_t* A,
-                              const uint16_t* B, float c, uint16_t* dX, void* dA, void* dB, void* ws,
-                              hipStream_t stream, int dtype, bool grad16, Act8View x8, uint16_t* dZ_lo) {
+                              const uint16_t* B, float c, uint16_t* dX, float* dA, float* dB, void* ws,
+                              hipStream_t stream, int dtype) {
   const GroupPlan gp = plan_grouped(M, K, g, Ns, r);
   int64_t Ntot = 0;
   for (int i = 0; i < g; ++i) Ntot += Ns[i];
@@ -201,7 +201,7 @@ hipError_t launch_grouped_bwd(int64_t M, int64_t K, int g, const int64_t* Ns, in
   // with dX wanted, member i's dZ sum rides along in member i's dequantize launch
   RdJob jz[kMaxGroupMembers];
   hipError_t e = launch_dz_grouped(M, g, Ns, Ntot, r, G, B, c, dz16, gp, base, stream, dtype,
-                                   dX != nullptr ? jz : nullptr, dZ_lo);
+                                   dX != nullptr ? jz : nullptr);
   if (e != hipSuccess) return e;
   if (dX != nullptr) {
     int64_t off = 0;
@@ -212,8 +212,8 @@ hipError_t launch_grouped_bwd(int64_t M, int64_t K, int g, const int64_t* Ns, in
       off += Ns[i];
     }
   }
-  if ((e = launch_colsums_grouped(M, K, g, Ns, Ntot, r, X, G, Z, dz16, c, dA, dB, gp, da_ws, db_ws, stream, dtype,
-                                  grad16, x8, dZ_lo)) != hipSuccess)
+  if ((e = launch_colsums_grouped(M, K, g, Ns, Ntot, r, X, G, Z, dz16, c, dA, dB, gp, da_ws, db_ws, stream, dtype)) !=
+      hipSuccess)
     return e;
   if (dX == nullptr) return hipGetLastError();
   return launch_dx_dense(M, K, Ntot, g * r, G, wd, dz16, A, dX, stream, dtype,
@@ -304,8 +304,27 @@ hipError_t launch_gated_bwd(int64_t M, int64_t K, int64_t F, int64_t r, const ui
       return e;
   }
   if ((e = launch_gated_dy(M, F, dH, from, gelu, dY, stream, dtype)) != hipSuccess) return e;
+  // the backward of the grouped linear of G and U (launch_grouped_bwd), with dA
+  // from dZ before its rounding and dX by the core of this block's forward
   const int64_t Ns[2] = {F, F};
-  return launch_grouped_bwd(M, K, 2, Ns, r, dY, X, Z, W, A, B, c, dX, dA, dB, rest, stream, dtype, grad16, x8, dZ_lo);
+  const GroupPlan gp = plan_grouped(M, K, 2, Ns, r);
+  uint16_t* dz16 = reinterpret_cast<uint16_t*>(rest + gp.dz_part);
+  char* da_ws = rest + gp.dz_part + align256(M * 2 * r * 2);
+  char* db_ws = da_ws + gp.da_part;
+  uint16_t* wd = reinterpret_cast<uint16_t*>(db_ws + gp.db_part_total);
+  RdJob jz[2];
+  if ((e = launch_dz_grouped(M, 2, Ns, 2 * F, r, dY, B, c, dz16, gp, rest, stream, dtype, dX != nullptr ? jz : nullptr,
+                             dZ_lo)) != hipSuccess)
+    return e;
+  for (int i = 0; dX != nullptr && i < 2; ++i)
+    if ((e = launch_dequant_bf16(W[i], K, F, false, wd + i * F, stream, 2 * F, dtype, nullptr, &jz[i])) != hipSuccess)
+      return e;
+  if ((e = launch_colsums_grouped(M, K, 2, Ns, 2 * F, r, X, dY, Z, dz16, c, dA, dB, gp, da_ws, db_ws, stream, dtype,
+                                  grad16, x8, dZ_lo)) != hipSuccess)
+    return e;
+  if (dX == nullptr) return hipGetLastError();
+  return launch_gated_dx(M, K, 2 * F, 2 * r, dY, wd, dz16, A, dX, stream, dtype,
+                         reinterpret_cast<char*>(wd) + align256(K * 2 * F * 2));
 }
 
 }  // namespace qn
