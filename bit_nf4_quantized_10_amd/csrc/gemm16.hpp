@@ -59,18 +59,14 @@ struct G16Args {
 constexpr int kG16W = 3 * kTileBytes;      // the weight slots follow the activation slots
 constexpr int kG16Lds = 5 * kTileBytes;
 
-// 8 x 8 transpose of 16-bit values: column c of the 8 rows `in`, as 16 bytes.
-__device__ __forceinline__ uint4 column8(const uint4 (&in)[8], int c) {
-  const uint32_t sel = (c & 1) ? 0x07060302u : 0x05040100u;
-  uint32_t d[4];
-#pragma unroll
-  for (int p = 0; p < 4; ++p) {
-    const uint4 &lo = in[2 * p], &hi = in[2 * p + 1];
-    const uint32_t l = (c >> 1) == 0 ? lo.x : ((c >> 1) == 1 ? lo.y : ((c >> 1) == 2 ? lo.z : lo.w));
-    const uint32_t h = (c >> 1) == 0 ? hi.x : ((c >> 1) == 1 ? hi.y : ((c >> 1) == 2 ? hi.z : hi.w));
-    d[p] = __builtin_amdgcn_perm(h, l, sel);
-  }
-  return make_uint4(d[0], d[1], d[2], d[3]);
+// Rows 2p and 2p + 1 of column c of the 8 x 8 block of 16-bit values `in` (one
+// uint4 a row).
+__device__ __forceinline__ uint32_t column2(const uint4 (&in)[8], int c, int p) {
+  const uint4 &lo = in[2 * p], &hi = in[2 * p + 1];
+  const int w = c >> 1;
+  const uint32_t l = w == 0 ? lo.x : (w == 1 ? lo.y : (w == 2 ? lo.z : lo.w));
+  const uint32_t h = w == 0 ? hi.x : (w == 1 ? hi.y : (w == 2 ? hi.z : hi.w));
+  return __builtin_amdgcn_perm(h, l, (c & 1) ? 0x07060302u : 0x05040100u);
 }
 
 template <class T, int kW>
@@ -150,46 +146,48 @@ struct Core16 {
   __device__ __forceinline__ void aim(int64_t u) {
     so = static_cast<uint32_t>((s_beg + u) * (kBK * 2));
     if (u < n_full) return;
-    if (u < n_main) {
-      // (selects, not a return from some lanes: the descriptors must stay uniform)
-      const bool past = (s_beg + u) * kBK + chunk8 >= a.red;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        av[j] = past ? kMasked : av[j];
-        wv[j] = past ? kMasked : wv[j];
-      }
-      return;
-    }
-    so = 0;
+    // One assignment per offset, whichever case holds (stores that the compiler
+    // merges from two branches would keep the arrays in memory), and descriptors
+    // that change in uniform control flow only.
+    const bool tail = u < n_main;
+    const bool past = (s_beg + u) * kBK + chunk8 >= a.red;
     const int64_t e = (u - n_main) * kBK + chunk8;
-    r_act = r_ea;
-    if (kW != kTurned) r_w = r_eb;
+    if (!tail) {
+      so = 0;
+      r_act = r_ea;
+      if (kW != kTurned) r_w = r_eb;
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int row = wave * 64 + 8 * j + (lane >> 3);
       const int64_t m = m0 + row;
-      av[j] = m < a.M && e < r_ext ? static_cast<uint32_t>((m * a.ext_a_ld + e) * 2) : kMasked;
+      const uint32_t ea = m < a.M && e < r_ext ? static_cast<uint32_t>((m * a.ext_a_ld + e) * 2) : kMasked;
+      av[j] = tail ? (past ? kMasked : av[j]) : ea;
       if (kW == kTurned) continue;
       const int64_t n = weight_row(row);
       int64_t own = e;   // within this row's own r
       if (kW == kPaired) own = (e >= 2 * a.r ? e - 2 * a.r : e) - (row < 128 ? 0 : a.r);
-      wv[j] = n < a.wrows && e < r_ext && own >= 0 && own < a.r ? static_cast<uint32_t>((n * a.r + own) * 2) : kMasked;
+      const uint32_t eb =
+          n < a.wrows && e < r_ext && own >= 0 && own < a.r ? static_cast<uint32_t>((n * a.r + own) * 2) : kMasked;
+      wv[j] = tail ? (past ? kMasked : wv[j]) : eb;
     }
   }
   // kTurned: row 8 vg + i of stage u (zeros past this workgroup's rows)
   __device__ uint4 load_w(int64_t u, int i) const {
     return ld128s(r_w, w_block, static_cast<uint32_t>(((s_beg + u) * kBK + i) * a.wrows * 2));
   }
-  // kTurned: column c of the registers' block to weight slot `slot`.  Written as
+  // kTurned: writes column c of the registers' block to weight slot `slot`.  As
   // an instruction: for a plain store the compiler first waits for every copy
   // still in flight, since one could write the same LDS bytes (none does).  The
   // writes are waited for before the barrier (lgkmcnt); waits the compiler sets
   // for its own LDS reads count them as well and so only come out longer.
-  __device__ void store_w(const uint4 (&R)[8], int slot, int c) const {
-    const uint4 v = column8(R, c);
-    const u32x4 d = {v.x, v.y, v.z, v.w};
-    const uint32_t at = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem)) + slot + ((wdst + 128 * c) ^ (c << 4));
+  __device__ void put_w(uint32_t d0, uint32_t d1, uint32_t d2, uint32_t d3, int slot, int c) const {
+    const u32x4 d = {d0, d1, d2, d3};
+    const uint32_t at = (wdst ^ (c << 4)) + (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(smem)) + slot + 128 * c);
     asm volatile("ds_write_b128 %0, %1" ::"v"(at), "v"(d) : "memory");
+  }
+  __device__ void store_w(const uint4 (&R)[8], int slot, int c) const {
+    put_w(column2(R, c, 0), column2(R, c, 1), column2(R, c, 2), column2(R, c, 3), slot, c);
   }
 
   // Addresses of a half's fragments.
@@ -230,8 +228,10 @@ struct Core16 {
       for (int j = 0; j < 8; ++j) {
         acc[i][j] = T::mfma16(Fc.w[j], Fc.a[i], acc[i][j]);
         __builtin_amdgcn_sched_barrier(0);
-        if ((j & 1) && i < 4) {
-          read(p, 4 * i + (j >> 1), Fn);
+        // kTurned: three of eight, which leaves its other work the gaps between
+        const int x = kW == kTurned ? (j < 6 ? 3 * i + (j >> 1) : 16) : 4 * i + (j >> 1);
+        if ((j & 1) && x < 16) {
+          read(p, x, Fn);
           __builtin_amdgcn_sched_barrier(0);
         }
         side(i, j);
@@ -266,31 +266,36 @@ struct Core16 {
       }
     });
   }
-  // kTurned: the first half copies the activations of stage u+2 and, in its
-  // second part, writes the weights of stage u+1 from R to sw1; the second half
-  // requests the weights of stage u+2 into R.
+  // kTurned: the first half writes the weights of stage u+1 from R to sw1, two
+  // columns per eight MFMAs, then requests those of stage u+2 into R and copies
+  // the activations of stage u+2.
   __device__ __forceinline__ void stage_turned(int64_t u, int sa, int sa1, int sa2, int sw, int sw1, Frags& F0, Frags& F1,
                                                uint4 (&R)[8], f32x4 (&acc)[8][8]) {
     aim(u + 2);
+    uint32_t d[4];
     half(F0, F1, place(sa, sw, 1), acc, [&](int i, int j) {
-      if ((j & 3) == 2 && i < 4) {
-        copy_a(sa2, 2 * i + (j >> 2));
-        __builtin_amdgcn_sched_barrier(0);
+      if (i < 4) {
+        const int c = 2 * i + (j >> 2);
+        if ((j & 3) == 0) {
+          d[0] = column2(R, c, 0);
+          d[1] = column2(R, c, 1);
+        } else if ((j & 3) == 1) {
+          d[2] = column2(R, c, 2);
+          d[3] = column2(R, c, 3);
+        } else if ((j & 3) == 2) {
+          put_w(d[0], d[1], d[2], d[3], sw1, c);
+        }
+      } else {
+        const int x = 2 * (i - 4) + (j >> 2);
+        if ((j & 3) == 0) R[x] = load_w(u + 2, x);
+        else if ((j & 3) == 2) copy_a(sa2, x);
       }
-      if ((j & 3) == 0 && i >= 4) {
-        store_w(R, sw1, 2 * (i - 4) + (j >> 2));
-        __builtin_amdgcn_sched_barrier(0);
-      }
+      if ((j & 3) != 3) __builtin_amdgcn_sched_barrier(0);
     });
     // the weights of stage u+1 are written, its activations have landed; the
-    // activations of stage u+2 may be in flight
-    meet<8>();
-    half(F1, F0, place(sa1, sw1, 0), acc, [&](int i, int j) {
-      if ((j & 3) == 2 && i < 4) {
-        R[2 * i + (j >> 2)] = load_w(u + 2, 2 * i + (j >> 2));
-        __builtin_amdgcn_sched_barrier(0);
-      }
-    });
+    // weights and the activations of stage u+2 may be in flight
+    meet<16>();
+    half(F1, F0, place(sa1, sw1, 0), acc, [](int, int) {});
   }
 
   // The whole reduction (kSplit: blockIdx.z's share): clears and fills acc and
@@ -337,9 +342,10 @@ struct Core16 {
       for (int c = 0; c < 8; ++c) store_w(R, 0, c);
       aim(1);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) copy_a(kTileBytes, j);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) R[i] = load_w(1, i);
+      for (int j = 0; j < 8; ++j) {   // in the order of the loop's own loads, whose waits the compiler counts
+        R[j] = load_w(1, j);
+        copy_a(kTileBytes, j);
+      }
       __builtin_amdgcn_s_waitcnt(waitcnt_imm(16, 0));   // stage 0; the 16 loads since may be in flight
       __builtin_amdgcn_s_barrier();
       const Place p = place(0, 0, 0);
