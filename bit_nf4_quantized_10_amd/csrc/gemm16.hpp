@@ -228,8 +228,8 @@ struct Core16 {
       for (int j = 0; j < 8; ++j) {
         acc[i][j] = T::mfma16(Fc.w[j], Fc.a[i], acc[i][j]);
         __builtin_amdgcn_sched_barrier(0);
-        // kTurned: three of eight, which leaves its other work the gaps between
-        const int x = kW == kTurned ? (j < 6 ? 3 * i + (j >> 1) : 16) : 4 * i + (j >> 1);
+        // kTurned: after its other work
+        const int x = kW == kTurned ? (i >= 2 && j < 6 ? 3 * (i - 2) + (j >> 1) : 16) : 4 * i + (j >> 1);
         if ((j & 1) && x < 16) {
           read(p, x, Fn);
           __builtin_amdgcn_sched_barrier(0);
@@ -266,31 +266,30 @@ struct Core16 {
       }
     });
   }
-  // kTurned: the first half writes the weights of stage u+1 from R to sw1, two
-  // columns per eight MFMAs, then requests those of stage u+2 into R and copies
-  // the activations of stage u+2.
+  // kTurned: the first half writes the weights of stage u+1 from R to sw1 during
+  // its first 16 MFMAs, requests those of stage u+2 into R (most of a stage ahead
+  // of their use) and copies the activations of stage u+2.
   __device__ __forceinline__ void stage_turned(int64_t u, int sa, int sa1, int sa2, int sw, int sw1, Frags& F0, Frags& F1,
                                                uint4 (&R)[8], f32x4 (&acc)[8][8]) {
     aim(u + 2);
     uint32_t d[4];
     half(F0, F1, place(sa, sw, 1), acc, [&](int i, int j) {
-      if (i < 4) {
-        const int c = 2 * i + (j >> 2);
-        if ((j & 3) == 0) {
-          d[0] = column2(R, c, 0);
-          d[1] = column2(R, c, 1);
-        } else if ((j & 3) == 1) {
-          d[2] = column2(R, c, 2);
-          d[3] = column2(R, c, 3);
-        } else if ((j & 3) == 2) {
+      if (i < 2) {
+        const int c = 4 * i + (j >> 1);
+        if ((j & 1) == 0) {
+#pragma unroll
+          for (int p = 0; p < 4; ++p) d[p] = column2(R, c, p);
+        } else {
           put_w(d[0], d[1], d[2], d[3], sw1, c);
         }
-      } else {
-        const int x = 2 * (i - 4) + (j >> 2);
-        if ((j & 3) == 0) R[x] = load_w(u + 2, x);
-        else if ((j & 3) == 2) copy_a(sa2, x);
+        __builtin_amdgcn_sched_barrier(0);
+      } else if (i < 4 && (j & 1) == 0) {
+        R[4 * (i - 2) + (j >> 1)] = load_w(u + 2, 4 * (i - 2) + (j >> 1));
+        __builtin_amdgcn_sched_barrier(0);
+      } else if (i >= 4 && (j & 3) == 2) {
+        copy_a(sa2, 2 * (i - 4) + (j >> 2));
+        __builtin_amdgcn_sched_barrier(0);
       }
-      if ((j & 3) != 3) __builtin_amdgcn_sched_barrier(0);
     });
     // the weights of stage u+1 are written, its activations have landed; the
     // weights and the activations of stage u+2 may be in flight
@@ -342,10 +341,9 @@ struct Core16 {
       for (int c = 0; c < 8; ++c) store_w(R, 0, c);
       aim(1);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {   // in the order of the loop's own loads, whose waits the compiler counts
-        R[j] = load_w(1, j);
-        copy_a(kTileBytes, j);
-      }
+      for (int i = 0; i < 8; ++i) R[i] = load_w(1, i);   // in the order of the loop's own loads, whose waits the compiler counts
+#pragma unroll
+      for (int j = 0; j < 8; ++j) copy_a(kTileBytes, j);
       __builtin_amdgcn_s_waitcnt(waitcnt_imm(16, 0));   // stage 0; the 16 loads since may be in flight
       __builtin_amdgcn_s_barrier();
       const Place p = place(0, 0, 0);
