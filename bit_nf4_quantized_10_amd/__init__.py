@@ -7,7 +7,6 @@ not built, every call raises.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 from dataclasses import dataclass
@@ -138,27 +137,37 @@ def _require_cuda(t, name: str, dtype=None) -> None:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
 
 
-@contextlib.contextmanager
-def _on(t, stream=None, *others):
+class _on:
     """The scope in which a call on tensor t allocates and launches: t's
     device current and, where one is given, `stream` current, so that outputs
     and workspaces belong to the stream that the kernels run on.  Yields that
     stream's handle.  The other tensors must be on the same device."""
-    import torch
-    for o in others:
-        if o is not None and o.device != t.device:
-            raise ValueError(f"tensors on {t.device} and {o.device}")
-    if stream is None:
-        if t.device.index == torch.cuda.current_device():
-            yield torch.cuda.current_stream().cuda_stream
-        else:
-            with torch.cuda.device(t.device):
-                yield torch.cuda.current_stream().cuda_stream
-        return
-    if stream.device != t.device:
-        raise ValueError(f"tensors on {t.device}, stream on {stream.device}")
-    with torch.cuda.stream(stream):
-        yield stream.cuda_stream
+    __slots__ = ("device", "stream", "scope")
+
+    def __init__(self, t, stream=None, *others):
+        self.device = d = t.device
+        for o in others:
+            if o is not None and o.device != d:
+                raise ValueError(f"tensors on {d} and {o.device}")
+        if stream is not None and stream.device != d:
+            raise ValueError(f"tensors on {d}, stream on {stream.device}")
+        self.stream = stream
+        self.scope = None
+
+    def __enter__(self):
+        import torch
+        if self.stream is not None:
+            self.scope = torch.cuda.stream(self.stream)
+        elif self.device.index != torch._C._cuda_getDevice():
+            self.scope = torch.cuda.device(self.device)
+        if self.scope is not None:
+            self.scope.__enter__()
+        # the handle of torch.cuda.current_stream(), without making a Stream of it
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
+
+    def __exit__(self, *e):
+        if self.scope is not None:
+            self.scope.__exit__(*e)
 
 
 def _require_shape(t, name: str, *shape) -> None:
@@ -212,6 +221,8 @@ def _require_matrix(t, name: str) -> int:
     _compute_dtype(t)
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
+    if t.dim() == 2 and t.is_contiguous():
+        return t.shape[1]
     if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} must be a matrix with contiguous rows")
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
@@ -239,17 +250,17 @@ def act8_decode(kept: Act8, out=None, stream=None):
     import torch
     kept.check("kept")
     M, K = kept.shape
+    ld = K
     if out is not None:
         if out.dtype != kept.dtype:
             raise ValueError(f"out must be {kept.dtype}, got {out.dtype}")
-        _require_matrix(out, "out")
+        ld = _require_matrix(out, "out")
         _require_shape(out, "out", M, K)
     with _on(kept.codes, stream, out) as s:
         if out is None:
             out = torch.empty(M, K, dtype=kept.dtype, device=kept.device)
         st = kept.c_struct()
-        _check(lib().act8_decode(_COMPUTE[kept.dtype], M, K, ctypes.byref(st), out.data_ptr(),
-                                 _require_matrix(out, "out"), s), "act8_decode")
+        _check(lib().act8_decode(_COMPUTE[kept.dtype], M, K, ctypes.byref(st), out.data_ptr(), ld, s), "act8_decode")
     return out
 
 
@@ -403,22 +414,25 @@ def qlora_grouped_bwd(G, X, Z, states, A, B, c: float, K: int, Ns, need_dx: bool
 NF4_AB_BF16, NF4_AB_F32, NF4_AB_F16 = 0, 1, 2
 
 
-class _ComputeMap:
+class _ComputeMap(dict):
     """torch dtype -> NF4_COMPUTE_* code (torch is imported lazily)."""
 
-    def __getitem__(self, dt):
+    def __missing__(self, dt):
         import torch
-        return {torch.bfloat16: NF4_COMPUTE_BF16, torch.float16: NF4_COMPUTE_F16}[dt]
+        self.update({torch.bfloat16: NF4_COMPUTE_BF16, torch.float16: NF4_COMPUTE_F16})
+        return dict.__getitem__(self, dt)
 
 
 _COMPUTE = _ComputeMap()
 
 
 def _compute_dtype(X):
-    import torch
-    if X.dtype not in (torch.bfloat16, torch.float16):
-        raise ValueError(f"the compute type is bf16 or fp16, got {X.dtype}")
-    return X.dtype
+    dt = X.dtype
+    if dt not in _COMPUTE:
+        import torch
+        if dt not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"the compute type is bf16 or fp16, got {dt}")
+    return dt
 
 
 def qlora_merge(state: NF4State, A, B, c: float, K: int, N: int, out=None, stream=None):

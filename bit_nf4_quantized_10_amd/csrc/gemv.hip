@@ -517,11 +517,14 @@ hipError_t launch_gemv(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_
   return hipGetLastError();
 }
 
+#ifndef QN_GV2_WAVES
+#define QN_GV2_WAVES 2752
+#endif
 // The gated block's two weights share a launch: twice the strips, so half the
 // row ranges of one weight's plan.
 GatedGemvPlan plan_gated_gemv(int64_t M, int64_t K, int64_t F, int64_t r) {
   const int64_t pairs = 2 * cdiv(F, 2 * kGvCols);
-  const int64_t groups = cdiv(QN_GV_WAVES, pairs * kGvWaves);
+  const int64_t groups = cdiv(QN_GV2_WAVES, pairs * kGvWaves);
   const int64_t rpw = round_up(cdiv(K, groups * 2), 64), splits = cdiv(K, 2 * rpw);
   return GatedGemvPlan{rpw, splits, round_up(splits * M * 2 * F * 4, 256), round_up(splits * M * 2 * r * 4, 256)};
 }
