@@ -82,14 +82,14 @@ __device__ __forceinline__ void transpose8x8_bf16(const uint4 (&in)[8], uint4 (&
   }
 }
 
-// Split-K partial of Z = X A for M <= 16 over rows [split * 4 rpw, +4 rpw),
+// Split-K partial of Z = X A for rows row0 .. row0 + 15 over rows [split * 4 rpw, +4 rpw),
 // each wave over the rows its GEMV counterpart streams.  A is read row-major
 // (8 rows of 8 columns per lane, transposed in registers), X rows feed the
 // MFMA as the 16-row operand; lane (q, g) accumulates columns j0 + 8q .. +7.
 // The four waves are added in LDS in a fixed order: (w0 + w2) + (w1 + w3).
 // zpart[split][m][j], fp32.  red: 16 KB of LDS.
 template <class T>
-__device__ void gemv_zpart(const uint16_t* __restrict__ X, int64_t M, int64_t K, int64_t rpw,
+__device__ void gemv_zpart(const uint16_t* __restrict__ X, int64_t M, int64_t row0, int64_t K, int64_t rpw,
                            const uint16_t* __restrict__ A, int64_t r, float* __restrict__ zpart, int64_t split,
                            float* red) {
   const int t = threadIdx.x, lane = t & 63, q = lane & 15, g = lane >> 4;
@@ -104,7 +104,8 @@ __device__ void gemv_zpart(const uint16_t* __restrict__ X, int64_t M, int64_t K,
     for (int i = 0; i < 8; ++i) acc[i] = f32x4{0, 0, 0, 0};
     for (int64_t kb = kw0; kb < kend; kb += 32) {
       const int64_t k = kb + 8 * g;
-      const uint4 xv = ld_b128(rx, (q < M && k < kend) ? static_cast<uint32_t>((q * K + k) * 2) : kMasked);
+      const uint4 xv =
+          ld_b128(rx, (row0 + q < M && k < kend) ? static_cast<uint32_t>(((row0 + q) * K + k) * 2) : kMasked);
       uint4 rows8[8], cols8[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -140,7 +141,7 @@ __device__ void gemv_zpart(const uint16_t* __restrict__ X, int64_t M, int64_t K,
     if (wave == 0 && j < r) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int64_t m = 4 * g + e;
+        const int64_t m = row0 + 4 * g + e;
         if (m >= M) continue;
         float v[8];
 #pragma unroll
@@ -153,9 +154,10 @@ __device__ void gemv_zpart(const uint16_t* __restrict__ X, int64_t M, int64_t K,
   }
 }
 
+template <int R>
 struct GvStep {
   uint4 c[2];   // 16 code bytes of one row per load (row order of the LDS stage)
-  uint4 x;      // activation fragment X[q][k + 8g .. k + 8g + 7]
+  uint4 x[R];   // activation fragments X[16 rt + q][k + 8g .. k + 8g + 7]
   int q;        // second-level code of the table this lane builds
   float s2;
 };
@@ -171,21 +173,25 @@ struct GvStep {
 // the 4 waves (fixed order).
 // kTwo: two weights of N columns each (the gated block's), `pairs` strip pairs
 // of the first, then of the second; the partials are M x 2N, side by side.
-template <class T, bool kTwo>
-__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3, 3))) void gemv_kernel(const uint16_t* __restrict__ X, int64_t M, NF4View W_, int64_t K,
-                                                   int64_t N, int64_t rpw, int64_t pairs, float* __restrict__ part,
-                                                   const uint16_t* __restrict__ A, int64_t r,
-                                                   float* __restrict__ zpart, NF4View W2) {
+// R > 1 (kTwo only): a workgroup multiplies each decoded fragment with R tiles
+// of 16 rows; blocks of 16 R rows are a third factor of the grid.
+template <class T, bool kTwo, int R>
+__device__ __forceinline__ void gemv_body(const uint16_t* __restrict__ X, int64_t M, NF4View W_, int64_t K, int64_t N,
+                                          int64_t rpw, int64_t pairs, float* __restrict__ part,
+                                          const uint16_t* __restrict__ A, int64_t r, float* __restrict__ zpart,
+                                          NF4View W2) {
   __shared__ float q2t[256];
   __shared__ __attribute__((aligned(16))) char lds[kGvWaves * kGvWaveLds];
   const int t = threadIdx.x, lane = t & 63, q = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(t >> 6);
   const int64_t splits = (K + 2 * rpw - 1) / (2 * rpw);
   const int64_t row_pairs = kTwo ? 2 * pairs : pairs;
-  const int64_t gv = row_pairs * splits;
+  const int64_t row_blocks = R > 1 ? (M + 16 * R - 1) / (16 * R) : 1;
+  const int64_t gv = row_pairs * splits * row_blocks;
   if (blockIdx.x >= gv) {
-    // the last `splits` workgroups: Z partials over the same row ranges
-    gemv_zpart<T>(X, M, K, rpw / 2, A, r, zpart, blockIdx.x - gv, reinterpret_cast<float*>(lds));
+    // the last workgroups: Z partials over the same row ranges, 16 rows each
+    const int64_t z = blockIdx.x - gv;
+    gemv_zpart<T>(X, M, z / splits * 16, K, rpw / 2, A, r, zpart, z % splits, reinterpret_cast<float*>(lds));
     return;
   }
   q2t[t] = q2_value(t - 128);
@@ -195,10 +201,13 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3, 3))) voi
   // whose L2 then fetches the lines of int8 scale codes they share once.
   const int64_t per = gv / 8, rem = gv % 8, xcd = blockIdx.x % 8;
   const int64_t L = xcd * per + min(xcd, rem) + blockIdx.x / 8;
-  const int64_t split = L / row_pairs;
-  const bool second = kTwo && L % row_pairs >= pairs;
+  // (row blocks of one strip and row range are neighbours: they decode the same codes)
+  const int64_t rb = R > 1 ? L % row_blocks : 0, Ls = R > 1 ? L / row_blocks : L;
+  const int64_t row0 = rb * 16 * R;
+  const int64_t split = Ls / row_pairs;
+  const bool second = kTwo && Ls % row_pairs >= pairs;
   const NF4View W = second ? W2 : W_;
-  const int64_t n0 = (2 * (L % row_pairs - (second ? pairs : 0)) + (wave & 1)) * kGvCols;
+  const int64_t n0 = (2 * (Ls % row_pairs - (second ? pairs : 0)) + (wave & 1)) * kGvCols;
   const int64_t kw0 = (split * 2 + (wave >> 1)) * rpw;
   const int64_t kend = min(K, kw0 + rpw);   // this wave's rows; nothing past them is fetched
   const int64_t rows = kend > kw0 ? kend - kw0 : 0;
@@ -230,48 +239,60 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3, 3))) voi
   const int64_t tcol = n0 + 64 * tblk;
   const uint32_t voff_q = tcol < N ? static_cast<uint32_t>((trow * N + tcol) >> 6) : kMasked;
   char* my_tab = tabs + gv_pos(trow) * 64 + 32 * tblk;
-  const uint32_t voff_x = q < M ? static_cast<uint32_t>((q * K + kw0 + 8 * g) * 2) : kMasked;
+  uint32_t voff_x[R];
+#pragma unroll
+  for (int rt = 0; rt < R; ++rt) {
+    const int64_t m = row0 + 16 * rt + q;
+    voff_x[rt] = m < M ? static_cast<uint32_t>((m * K + kw0 + 8 * g) * 2) : kMasked;
+  }
 
-  auto load = [&](GvStep& S, int64_t kk) {
+  auto load = [&](GvStep<R>& S, int64_t kk) {
     // offsets past this wave's rows (or masked) are out of the descriptor: zeros
     const uint32_t sw = static_cast<uint32_t>((kk * N) >> 1);
 #pragma unroll
     for (int j = 0; j < 2; ++j) S.c[j] = ld_b128(rc, voff_c[j] + sw);
     // zero activations past this wave's rows (their codes read as 0, a finite weight)
-    S.x = ld_b128(rx, (kw0 + kk + 8 * g < kend) ? voff_x + static_cast<uint32_t>(kk * 2) : kMasked);
+#pragma unroll
+    for (int rt = 0; rt < R; ++rt)
+      S.x[rt] = ld_b128(rx, (kw0 + kk + 8 * g < kend) ? voff_x[rt] + static_cast<uint32_t>(kk * 2) : kMasked);
     const int64_t kt = kw0 + kk + trow;
     const bool ok = kt < kend && tcol < N;
     S.q = ld_i8(rq, ok ? voff_q + static_cast<uint32_t>((kk * N) >> 6) : kMasked);
     S.s2 = ld_f32(rs, ok ? static_cast<uint32_t>(((kt * N + tcol) >> s_shift) * 4) : kMasked);
   };
 
-  f32x4 acc[8];
+  f32x4 acc[R][8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = f32x4{0, 0, 0, 0};
+  for (int rt = 0; rt < R; ++rt)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc[rt][i] = f32x4{0, 0, 0, 0};
   __syncthreads();  // q2t
-  // kGvDepth steps of loads in flight per wave: set u holds step D j + u and
+  // kDepth steps of loads in flight per wave: set u holds step D j + u and
   // is refilled with step D (j+1) + u as soon as it has been staged.  Each
   // wave's stage and tables are its own, so no workgroup barrier is needed
   // (LDS operations of one wave complete in order).
-  GvStep R[kGvDepth];
+  constexpr int kDepth = R > 2 ? 2 : kGvDepth;   // four activation fragments a step leave registers for two
+  GvStep<R> S[kDepth];
 #pragma unroll
-  for (int u = 0; u < kGvDepth; ++u) load(R[u], 32 * u);
+  for (int u = 0; u < kDepth; ++u) load(S[u], 32 * u);
   // lookups of row 8g + i go to tbase + 256 i + 2 code
   const uint32_t tbase = static_cast<uint32_t>(reinterpret_cast<uintptr_t>(tabs + g * 64 + 32 * (q >> 3)));
-  for (int64_t kk = 0; kk < rpw; kk += 32 * kGvDepth) {
+  for (int64_t kk = 0; kk < rpw; kk += 32 * kDepth) {
 #pragma unroll
-    for (int u = 0; u < kGvDepth; ++u) {
+    for (int u = 0; u < kDepth; ++u) {
       const int64_t ks = kk + 32 * u;
       if (ks >= rpw) break;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) *reinterpret_cast<uint4*>(stage + j * 1024 + lane * 16) = R[u].c[j];
+      for (int j = 0; j < 2; ++j) *reinterpret_cast<uint4*>(stage + j * 1024 + lane * 16) = S[u].c[j];
       write_block_table<T>(reinterpret_cast<uint16_t*>(my_tab),
-                           single ? R[u].s2 : __fadd_rn(__fmul_rn(q2t[R[u].q + 128], R[u].s2), off));
-      const typename T::v8 xf = __builtin_bit_cast(typename T::v8, R[u].x);
+                           single ? S[u].s2 : __fadd_rn(__fmul_rn(q2t[S[u].q + 128], S[u].s2), off));
+      typename T::v8 xf[R];
+#pragma unroll
+      for (int rt = 0; rt < R; ++rt) xf[rt] = __builtin_bit_cast(typename T::v8, S[u].x[rt]);
       uint32_t w[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) w[i] = *reinterpret_cast<const uint32_t*>(stage + (4 * i + g) * 64 + 4 * q);
-      load(R[u], ks + 32 * kGvDepth);   // past the k-range: masked, reads zeros
+      load(S[u], ks + 32 * kDepth);   // past the k-range: masked, reads zeros
       // doubled codes: byte b of ev = 2 * code of column 2b, of od = 2 * code
       // of column 2b + 1
       uint32_t ev[8], od[8];
@@ -291,7 +312,9 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3, 3))) voi
           const uint32_t hi = lds_u16(a1 + (2 * p + 1) * 256);
           fw[p] = perm(hi, lo, 0x05040100u);
         }
-        acc[tile] = T::mfma16(xf, __builtin_bit_cast(typename T::v8, make_uint4(fw[0], fw[1], fw[2], fw[3])), acc[tile]);
+        const typename T::v8 wf = __builtin_bit_cast(typename T::v8, make_uint4(fw[0], fw[1], fw[2], fw[3]));
+#pragma unroll
+        for (int rt = 0; rt < R; ++rt) acc[rt][tile] = T::mfma16(xf[rt], wf, acc[rt][tile]);
       }
     }
   }
@@ -300,29 +323,47 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3, 3))) voi
   // lane holds Y[m = 4g+e][n0 + 8q + tile]; the two row ranges of a strip
   // are added in a fixed order: wave w (w < 2) + wave w + 2
   float* red = reinterpret_cast<float*>(lds);   // 2 waves x 32 floats x 64 lanes = 16 KB
-  if (wave >= 2) {
 #pragma unroll
-    for (int tile = 0; tile < 8; ++tile)
+  for (int rt = 0; rt < R; ++rt) {
+    if (rt > 0) __syncthreads();
+    if (wave >= 2) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) red[((wave - 2) * 32 + tile * 4 + e) * 64 + lane] = acc[tile][e];
-  }
-  __syncthreads();
-  if (wave < 2) {
-    const int64_t ldn = kTwo ? 2 * N : N;
-    float* out = part + split * M * ldn + (second ? N : 0);
-    const int64_t n = n0 + 8 * q;
+      for (int tile = 0; tile < 8; ++tile)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int64_t m = 4 * g + e;
-      float v[8];
+        for (int e = 0; e < 4; ++e) red[((wave - 2) * 32 + tile * 4 + e) * 64 + lane] = acc[rt][tile][e];
+    }
+    __syncthreads();
+    if (wave < 2) {
+      const int64_t ldn = kTwo ? 2 * N : N;
+      float* out = part + split * M * ldn + (second ? N : 0);
+      const int64_t n = n0 + 8 * q;
 #pragma unroll
-      for (int tile = 0; tile < 8; ++tile) v[tile] = acc[tile][e] + red[(wave * 32 + tile * 4 + e) * 64 + lane];
-      if (m < M && n < N) {
-        *reinterpret_cast<float4*>(out + m * ldn + n) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4*>(out + m * ldn + n + 4) = make_float4(v[4], v[5], v[6], v[7]);
+      for (int e = 0; e < 4; ++e) {
+        const int64_t m = row0 + 16 * rt + 4 * g + e;
+        float v[8];
+#pragma unroll
+        for (int tile = 0; tile < 8; ++tile) v[tile] = acc[rt][tile][e] + red[(wave * 32 + tile * 4 + e) * 64 + lane];
+        if (m < M && n < N) {
+          *reinterpret_cast<float4*>(out + m * ldn + n) = make_float4(v[0], v[1], v[2], v[3]);
+          *reinterpret_cast<float4*>(out + m * ldn + n + 4) = make_float4(v[4], v[5], v[6], v[7]);
+        }
       }
     }
   }
+}
+
+// Waves per SIMD: three where the registers of one row tile allow it, two above.
+template <class T, bool kTwo>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(3, 3))) void gemv_kernel(
+    const uint16_t* __restrict__ X, int64_t M, NF4View W, int64_t K, int64_t N, int64_t rpw, int64_t pairs,
+    float* __restrict__ part, const uint16_t* __restrict__ A, int64_t r, float* __restrict__ zpart, NF4View W2) {
+  gemv_body<T, kTwo, 1>(X, M, W, K, N, rpw, pairs, part, A, r, zpart, W2);
+}
+template <class T, int R>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) void gemv_rows_kernel(
+    const uint16_t* __restrict__ X, int64_t M, NF4View W, int64_t K, int64_t N, int64_t rpw, int64_t pairs,
+    float* __restrict__ part, const uint16_t* __restrict__ A, int64_t r, float* __restrict__ zpart, NF4View W2) {
+  gemv_body<T, true, R>(X, M, W, K, N, rpw, pairs, part, A, r, zpart, W2);
 }
 
 // Y = sum_s part[s] + c Z B for M <= 16.  Workgroup (4 waves) = 512
@@ -365,18 +406,22 @@ __global__ __launch_bounds__(256) void gemv_finish_kernel(const float* __restric
                                                           GatedKeep keep) {
   __shared__ __attribute__((aligned(16))) uint16_t zl[16 * 256];   // Z, M x r (M <= 16, r <= 256)
   const int t = threadIdx.x, lane = t & 63, q = lane & 15, g = lane >> 4, wave = t >> 6;
-  const int e = blockIdx.y;
+  // kTwo: row tile of 16 rows (blockIdx.y / 4) and its row phase
+  const int e = kTwo ? blockIdx.y & 3 : blockIdx.y;
+  const int64_t row0 = kTwo ? static_cast<int64_t>(blockIdx.y >> 2) * 16 : 0;
+  const int64_t Mt = kTwo ? (M - row0 < 16 ? M - row0 : 16) : M;   // rows of this tile
   const int member = kTwo ? wave >> 1 : 0;
   const int64_t ncol = kTwo ? static_cast<int64_t>(blockIdx.x) * (kFinCols / 2) + 128 * (wave & 1) + 8 * q
                             : static_cast<int64_t>(blockIdx.x) * kFinCols + 128 * wave + 8 * q;
   const bool n_ok = ncol < N;
   const int64_t ldn = kTwo ? 2 * N : N, n = ncol + member * N;
   const int64_t rt = kTwo ? 2 * r : r;   // Z's row length
-  const int64_t m = 4 * g + e;
+  const int64_t m = row0 + 4 * g + e;
   const bool out_ok = m < M && n_ok;
-  const int64_t MR = M * rt;
+  const int64_t MR = Mt * rt;            // Z's elements of this tile, from zrow on
   const Rsrc rb = make_rsrc(B, r * ldn * 2);
-  const Rsrc rzp = make_rsrc(zpart, static_cast<int64_t>(splits) * MR * 4);
+  const int64_t zrow = row0 * rt, zplane = M * rt;
+  const Rsrc rzp = make_rsrc(zpart, static_cast<int64_t>(splits) * zplane * 4);
   const Rsrc rp = make_rsrc(part, static_cast<int64_t>(splits) * M * ldn * 4);
   auto load_b = [&](int64_t j0, uint4 (&rows8)[8]) {
     const int64_t jb = j0 + 8 * g;
@@ -397,13 +442,13 @@ __global__ __launch_bounds__(256) void gemv_finish_kernel(const float* __restric
   auto load_z = [&](int s0, int64_t idx, uint4 (&za)[8]) {
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-      za[k] = ld_b128(rzp, (idx < MR && s0 + k < splits) ? static_cast<uint32_t>(((s0 + k) * MR + idx) * 4) : kMasked);
+      za[k] = ld_b128(rzp, (idx < MR && s0 + k < splits) ? static_cast<uint32_t>(((s0 + k) * zplane + zrow + idx) * 4) : kMasked);
   };
   auto store_z = [&](int64_t idx, const float (&zs)[4]) {
     if (idx >= MR) return;
     const uint2 zv = make_uint2(T::pack2(zs[0], zs[1]), T::pack2(zs[2], zs[3]));
     *reinterpret_cast<uint2*>(zl + idx) = zv;
-    if (blockIdx.x == 0 && e == 0) *reinterpret_cast<uint2*>(Z + idx) = zv;
+    if (blockIdx.x == 0 && e == 0) *reinterpret_cast<uint2*>(Z + zrow + idx) = zv;
   };
   uint4 pa[8], pb[8], b0[8], b1[8], za[8];
   load_part(0, pa, pb);
@@ -433,7 +478,7 @@ __global__ __launch_bounds__(256) void gemv_finish_kernel(const float* __restric
   for (int i = 0; i < 8; ++i) accl[i] = f32x4{0, 0, 0, 0};
   auto lora_step = [&](int64_t j0, const uint4 (&rows8)[8]) {
     const int64_t jb = j0 + 8 * g;
-    const uint4 zv = (q < M && jb < r) ? *reinterpret_cast<const uint4*>(zl + q * rt + member * r + jb) : make_uint4(0, 0, 0, 0);
+    const uint4 zv = (q < Mt && jb < r) ? *reinterpret_cast<const uint4*>(zl + q * rt + member * r + jb) : make_uint4(0, 0, 0, 0);
     uint4 cols8[8];
     transpose8x8_bf16(rows8, cols8);
 #pragma unroll
@@ -520,11 +565,17 @@ hipError_t launch_gemv(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_
 #ifndef QN_GV2_WAVES
 #define QN_GV2_WAVES 2752
 #endif
+#ifndef QN_GVR_WAVES
+#define QN_GVR_WAVES 2048
+#endif
 // The gated block's two weights share a launch: twice the strips, so half the
-// row ranges of one weight's plan.
+// row ranges of one weight's plan; and blocks of 16 R rows.
+static int gated_row_tiles(int64_t M) { return M <= 16 ? 1 : (M <= 32 ? 2 : 4); }
+
 GatedGemvPlan plan_gated_gemv(int64_t M, int64_t K, int64_t F, int64_t r) {
-  const int64_t pairs = 2 * cdiv(F, 2 * kGvCols);
-  const int64_t groups = cdiv(QN_GV2_WAVES, pairs * kGvWaves);
+  const int R = gated_row_tiles(M);
+  const int64_t units = 2 * cdiv(F, 2 * kGvCols) * cdiv(M, 16 * R);
+  const int64_t groups = cdiv(R == 1 ? QN_GV2_WAVES : QN_GVR_WAVES, units * kGvWaves);
   const int64_t rpw = round_up(cdiv(K, groups * 2), 64), splits = cdiv(K, 2 * rpw);
   return GatedGemvPlan{rpw, splits, round_up(splits * M * 2 * F * 4, 256), round_up(splits * M * 2 * r * 4, 256)};
 }
@@ -533,16 +584,20 @@ hipError_t launch_gated_gemv(int64_t M, int64_t K, int64_t F, int64_t r, const u
                              const uint16_t* A, const uint16_t* B, float c, bool gelu, uint16_t* H, uint16_t* Z,
                              const GatedKeep& keep, void* ws, hipStream_t stream, int dtype) {
   const GatedGemvPlan p = plan_gated_gemv(M, K, F, r);
-  const int64_t pairs = cdiv(F, 2 * kGvCols);
+  const int R = gated_row_tiles(M);
+  const int64_t pairs = cdiv(F, 2 * kGvCols), tiles = cdiv(M, 16);
   float* part = static_cast<float*>(ws);
   float* zpart = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part);
+  auto* k = dtype == kDtypeF16 ? (R == 1 ? gemv_kernel<F16, true> : (R == 2 ? gemv_rows_kernel<F16, 2> : gemv_rows_kernel<F16, 4>))
+                               : (R == 1 ? gemv_kernel<Bf16, true> : (R == 2 ? gemv_rows_kernel<Bf16, 2> : gemv_rows_kernel<Bf16, 4>));
   Timer tm(QK_FWD_GEMV, stream);
-  hipLaunchKernelGGL((dtype == kDtypeF16 ? gemv_kernel<F16, true> : gemv_kernel<Bf16, true>),
-                     dim3(static_cast<unsigned>((2 * pairs + 1) * p.splits)), dim3(kGvWaves * 64), 0, stream, X, M,
-                     W[0], K, F, p.rows_per_wave, pairs, part, A, 2 * r, zpart, W[1]);
+  hipLaunchKernelGGL(k, dim3(static_cast<unsigned>((2 * pairs * cdiv(M, 16 * R) + tiles) * p.splits)),
+                     dim3(kGvWaves * 64), 0, stream, X, M, W[0], K, F, p.rows_per_wave, pairs, part, A, 2 * r, zpart,
+                     W[1]);
   tm.stop();
   Timer te(QK_REDUCE, stream);
-  const unsigned phases = static_cast<unsigned>(M < 4 ? M : 4);   // rows 4g + e, e < phases
+  // rows 4g + e, e < phases, of each tile
+  const unsigned phases = static_cast<unsigned>(M < 4 ? M : 4 * tiles);
   auto* fin = dtype == kDtypeF16 ? (gelu ? gemv_finish_kernel<F16, true, true> : gemv_finish_kernel<F16, true, false>)
                                  : (gelu ? gemv_finish_kernel<Bf16, true, true> : gemv_finish_kernel<Bf16, true, false>);
   hipLaunchKernelGGL(fin, dim3(static_cast<unsigned>(cdiv(F, kFinCols / 2)), phases), dim3(256), 0, stream,

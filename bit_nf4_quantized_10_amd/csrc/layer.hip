@@ -221,12 +221,17 @@ hipError_t launch_grouped_bwd(int64_t M, int64_t K, int g, const int64_t* Ns, in
 }
 
 // --------------------------------------------------- gated feed-forward front
+// Up to this many rows the packed weights are decoded inside the product.
+#ifndef QN_GATED_GEMV_M
+#define QN_GATED_GEMV_M 128
+#endif
+constexpr int64_t kGatedGemvM = QN_GATED_GEMV_M;
 // The forward is a grouped linear of two members whose last kernel combines
 // them (gated.hip; up to 16 rows: gemv.hip).  The backward turns dH into the
 // grouped linear's dY = [dG | dU] and runs that linear's backward.
 int64_t gated_fwd_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t r) {
   const int64_t z = align256(M * 2 * r * 2);
-  if (M <= 16) {
+  if (M <= kGatedGemvM) {
     const GatedGemvPlan p = plan_gated_gemv(M, K, F, r);
     return p.part + p.zpart + z;
   }
@@ -282,7 +287,7 @@ hipError_t launch_gated_fwd(int64_t M, int64_t K, int64_t F, int64_t r, const ui
                             const GatedKeep& keep, void* ws, hipStream_t stream, int dtype) {
   if (Z == nullptr)
     Z = reinterpret_cast<uint16_t*>(static_cast<char*>(ws) + gated_fwd_workspace_bytes(M, K, F, r) - align256(M * 2 * r * 2));
-  if (M <= 16) return launch_gated_gemv(M, K, F, r, X, W, A, B, c, gelu, H, Z, keep, ws, stream, dtype);
+  if (M <= kGatedGemvM) return launch_gated_gemv(M, K, F, r, X, W, A, B, c, gelu, H, Z, keep, ws, stream, dtype);
   return gated_fwd(M, K, F, r, X, W, A, B, c, gelu, H, Z, keep, ws, stream, dtype);
 }
 

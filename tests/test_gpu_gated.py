@@ -106,7 +106,8 @@ def _check_backward(k, act, x, Z, G, U, got, gdt):
 
 
 SHAPES = [(1, 64, 64, 8), (2, 1032, 320, 24), (5, 72, 128, 16), (16, 264, 192, 128), (16, 2056, 704, 40),
-          (17, 136, 64, 8), (40, 1032, 320, 24), (100, 4096, 1088, 16), (191, 256, 256, 128), (200, 264, 448, 16),
+          (17, 136, 64, 8), (32, 520, 192, 128), (33, 264, 448, 8), (40, 1032, 320, 24), (64, 2056, 64, 40),
+          (65, 72, 320, 16), (100, 4096, 1088, 16), (128, 520, 576, 24), (129, 520, 576, 24), (191, 256, 256, 128), (200, 264, 448, 16),
           (300, 520, 704, 40), (257, 2056, 192, 72), (520, 96, 1344, 8)]
 
 
@@ -156,7 +157,7 @@ def test_single_level_weights_and_no_z():
         np.testing.assert_array_equal(host(H2), host(H))
 
 
-@pytest.mark.parametrize("M", [3, 16, 70, 300])
+@pytest.mark.parametrize("M", [3, 16, 27, 70, 125, 300])
 def test_rows_behind_the_last_stay(M):
     import torch
     say(f"gated canaries M={M}")
@@ -204,7 +205,7 @@ def test_activation_extremes():
 def test_captured_replayed_and_on_another_stream():
     import torch
     say("gated graph and stream")
-    for M in (2, 80, 600):
+    for M in (2, 30, 80, 600):
         k = Case(M, 520, 256, 16, "bf16")
         ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in qn.qlora_gated_workspace_bytes(M, 520, 256, 16)]
         H, Z, saved = k.forward("silu", "8", workspace=ws[0])
