@@ -565,18 +565,40 @@ hipError_t launch_gemv(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_
 #ifndef QN_GV2_WAVES
 #define QN_GV2_WAVES 2752
 #endif
-#ifndef QN_GVR_WAVES
-#define QN_GVR_WAVES 2048
-#endif
 // The gated block's two weights share a launch: twice the strips, so half the
 // row ranges of one weight's plan; and blocks of 16 R rows.
 static int gated_row_tiles(int64_t M) { return M <= 16 ? 1 : (M <= 32 ? 2 : 4); }
 
+// One row tile: about QN_GV2_WAVES waves, which fill the device once (three
+// workgroups a CU).  More: the device holds kRowsSlots workgroups at a time (two
+// a CU, by registers), and the split is the one with the least estimated time:
+// full rounds of workgroups, each kRowsStart us and kRowsStep us per 32-row
+// step, then the partials' way through memory.  (Measured at 4096 x 11008, 100
+// rows: two row ranges, 358 workgroups in one round, 62 us; three, 537 in two
+// rounds, 80 us; at 8192 x 22016, 128 rows: 1.6 us a step.)
+constexpr int64_t kRowsSlots = 512;
+constexpr double kRowsStart = 4.0, kRowsStep = 1.6, kRowsBytesPerUs = 5e6;
 GatedGemvPlan plan_gated_gemv(int64_t M, int64_t K, int64_t F, int64_t r) {
   const int R = gated_row_tiles(M);
   const int64_t units = 2 * cdiv(F, 2 * kGvCols) * cdiv(M, 16 * R);
-  const int64_t groups = cdiv(R == 1 ? QN_GV2_WAVES : QN_GVR_WAVES, units * kGvWaves);
-  const int64_t rpw = round_up(cdiv(K, groups * 2), 64), splits = cdiv(K, 2 * rpw);
+  int64_t rpw = round_up(cdiv(K, cdiv(QN_GV2_WAVES, units * kGvWaves) * 2), 64);
+  if (R > 1) {
+    double best = 0.0;
+    int64_t last = 0;
+    for (int64_t s = 1; s <= 32; ++s) {
+      const int64_t rows = round_up(cdiv(K, 2 * s), 64), splits = cdiv(K, 2 * rows);
+      if (rows == last) continue;
+      last = rows;
+      const int64_t rounds = cdiv((units + cdiv(M, 16)) * splits, kRowsSlots);
+      const double us = static_cast<double>(rounds) * (kRowsStart + kRowsStep * static_cast<double>(rows / 32)) +
+                        static_cast<double>(splits * M * 2 * F) * 8.0 / kRowsBytesPerUs;
+      if (s == 1 || us < best) {
+        best = us;
+        rpw = rows;
+      }
+    }
+  }
+  const int64_t splits = cdiv(K, 2 * rpw);
   return GatedGemvPlan{rpw, splits, round_up(splits * M * 2 * F * 4, 256), round_up(splits * M * 2 * r * 4, 256)};
 }
 
