@@ -1,6 +1,6 @@
-// The gated feed-forward front of the layer for more than 16 rows, on gfx950:
+// The gated feed-forward front of the layer for more than 256 rows, on gfx950:
 //   [Zg | Zu] = X A,  G = X Ŵg + c Zg Bg,  U = X Ŵu + c Zu Bu,  H = act(G) * U
-// and the elementwise half of its backward.  (Up to 16 rows: gemv.hip.)
+// and the elementwise half of its backward.  (Up to 256 rows: gemv.hip.)
 //
 // Forward: one dense GEMM over both weights, dequantized beforehand and stacked
 // (2F x K).  A 256 x 256 tile of it takes 128 columns of each weight (kPaired in

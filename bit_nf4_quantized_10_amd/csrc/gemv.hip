@@ -1,4 +1,4 @@
-// Small-M forward (M <= 16) for gfx950: Y = X Ŵ + c Z B as a dequant-GEMV
+// Small-M forward (M <= 16; the gated block M <= 256) for gfx950: Y = X Ŵ + c Z B as a dequant-GEMV
 // (page "QLoRA：冻结的 4-bit 权重怎样参与一次微调", section "量化基座与可训练支路怎样相加";
 // the decode is the one of section "Double Quantization 压缩的是 Scale").
 //
@@ -17,6 +17,15 @@
 // past the wave's range read as zeros and meet zero activations).  The two
 // row ranges of a strip are added in LDS in a fixed order; the split-K
 // partials and the LoRA term are added by gemv_finish_kernel.
+//
+// The gated block's forward for up to 256 rows is the same walk over two weights
+// in one launch, its finish forming H = act(G) * U.  Above 16 rows a decoded
+// fragment feeds the MFMAs of two or four 16-row tiles (gemv_rows_kernel): the
+// lookups, not the matrix cores, are what a step costs, so more rows a step are
+// nearly free.  Measured, whole forward, 4096 x 11008: 1 row 33 us, 16 44, 32
+// 46, 64 51, 128 75, 256 132; 8192 x 22016: 69, 86, 111, 143, 231, 393.
+// Bound by the lookups (LDS reads and byte adds per weight, once per 64 rows):
+// at 16 rows of 8192 x 22016 the codes and scales, 186 MB, arrive at 2.2 TB/s.
 #include "common.hpp"
 #include "gated.hpp"
 #include "kernels.hpp"
@@ -366,7 +375,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2, 2))) voi
   gemv_body<T, true, R>(X, M, W, K, N, rpw, pairs, part, A, r, zpart, W2);
 }
 
-// Y = sum_s part[s] + c Z B for M <= 16.  Workgroup (4 waves) = 512
+// Y = sum_s part[s] + c Z B for M <= 16 (kTwo: any M, 16-row tiles).  Workgroup (4 waves) = 512
 // columns and row phase e (blockIdx.y); lane (q, g) of wave w owns columns
 // n0 + 128w + 8q .. +7 and row 4g + e.  A workgroup requests at its start
 // the first 8 split partials of its outputs, the first 64 rows of B and the
@@ -404,7 +413,7 @@ __global__ __launch_bounds__(256) void gemv_finish_kernel(const float* __restric
                                                           uint16_t* __restrict__ Z, const uint16_t* __restrict__ B,
                                                           int64_t r, float c, uint16_t* __restrict__ Y,
                                                           GatedKeep keep) {
-  __shared__ __attribute__((aligned(16))) uint16_t zl[16 * 256];   // Z, M x r (M <= 16, r <= 256)
+  __shared__ __attribute__((aligned(16))) uint16_t zl[16 * 256];   // Z of 16 rows, 16 x rt (rt <= 256)
   const int t = threadIdx.x, lane = t & 63, q = lane & 15, g = lane >> 4, wave = t >> 6;
   // kTwo: row tile of 16 rows (blockIdx.y / 4) and its row phase
   const int e = kTwo ? blockIdx.y & 3 : blockIdx.y;
@@ -588,6 +597,7 @@ GatedGemvPlan plan_gated_gemv(int64_t M, int64_t K, int64_t F, int64_t r) {
     for (int64_t s = 1; s <= 32; ++s) {
       const int64_t rows = round_up(cdiv(K, 2 * s), 64), splits = cdiv(K, 2 * rows);
       if (rows == last) continue;
+      if (splits * M * 2 * F * 4 > INT32_MAX) break;   // the finish addresses them with 31-bit offsets; one range always fits
       last = rows;
       const int64_t rounds = cdiv((units + cdiv(M, 16)) * splits, kRowsSlots);
       const double us = static_cast<double>(rounds) * (kRowsStart + kRowsStep * static_cast<double>(rows / 32)) +

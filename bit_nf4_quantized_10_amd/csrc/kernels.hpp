@@ -199,7 +199,7 @@ hipError_t launch_dx_dense(int64_t M, int64_t K, int64_t N, int64_t r, const uin
                            const uint16_t* dZ, const uint16_t* A, uint16_t* dX, hipStream_t stream, int dtype = 0,
                            void* split_ws = nullptr);
 
-// The gated feed-forward front (gated.hip; up to 16 rows gemv.hip): W[0], W[1]
+// The gated feed-forward front (gated.hip; up to 256 rows gemv.hip): W[0], W[1]
 // the K x F weights, A K x 2r, B r x 2F, H M x F (null in launch_gated_dense:
 // not wanted), Z M x 2r.
 struct GatedKeep;
@@ -222,7 +222,7 @@ hipError_t launch_gated_dx(int64_t M, int64_t K, int64_t red, int64_t rt, const 
                            void* split_ws);
 hipError_t launch_gated_dy(int64_t M, int64_t F, const uint16_t* dH, const GatedKeep& kept, bool gelu, uint16_t* dY,
                            hipStream_t stream, int dtype);
-// Up to 16 rows: split-K partials of both weights and of Z, then their sums.
+// Up to 256 rows: split-K partials of both weights and of Z, then their sums.
 struct GatedGemvPlan {
   int64_t rows_per_wave, splits, part, zpart;
 };

@@ -223,15 +223,15 @@ hipError_t launch_grouped_bwd(int64_t M, int64_t K, int g, const int64_t* Ns, in
 // --------------------------------------------------- gated feed-forward front
 // Up to this many rows the packed weights are decoded inside the product; above,
 // both are dequantized first and one dense GEMM follows.  Whole forward, decoded
-// against dense: 4096 x 11008 at 192 rows 106 and 136 us, at 256 122 and 136, at
-// 320 144 and 138; 8192 x 22016 at 192 344 and 451, at 256 424 and 428, at 384
-// 640 and 546.
+// against dense: 4096 x 11008 at 192 rows 106 and 136 us, at 256 132 and 136 to
+// 140, at 320 144 and 138; 8192 x 22016 at 192 333 and 451, at 256 393 and 428,
+// at 384 640 and 546; 1024 x 2816 at 256 43, dense at 257 47.
 #ifndef QN_GATED_GEMV_M
 #define QN_GATED_GEMV_M 256
 #endif
 constexpr int64_t kGatedGemvM = QN_GATED_GEMV_M;
 // The forward is a grouped linear of two members whose last kernel combines
-// them (gated.hip; up to 16 rows: gemv.hip).  The backward turns dH into the
+// them (gated.hip; up to kGatedGemvM rows: gemv.hip).  The backward turns dH into the
 // grouped linear's dY = [dG | dU] and runs that linear's backward.
 int64_t gated_fwd_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t r) {
   const int64_t z = align256(M * 2 * r * 2);

@@ -307,10 +307,11 @@ int qlora_linear_bwd_ex(int compute_dtype, int grad_dtype, int64_t M, int64_t K,
  * makes of GU).  At most one of the two is given; with neither, nothing is
  * kept.  Requirements: F % 64 == 0, K % 8 == 0, r % 8 == 0, r <= 128, and
  * qlora_linear_fwd's on (M, K, 2F, 2r); all pointers 16-byte aligned
- * (GU8->absmax 2-byte); workspace 256-byte aligned, at least fwd_bytes.  M <= 16
- * reads the packed weights once, as a dequant-GEMV; above, both weights are
- * dequantized into the workspace and multiplied by one GEMM whose epilogue is
- * the activation. */
+ * (GU8->absmax 2-byte); workspace 256-byte aligned, at least fwd_bytes.  M <= 256
+ * decodes the packed weights inside the product (each code read once per 64
+ * rows, 16 where M <= 16, 32 where M <= 32); above, both weights are dequantized
+ * into the workspace and multiplied by one GEMM whose epilogue is the
+ * activation. */
 #define NF4_ACT_SILU 0   /* g / (1 + e^-g)                                                 */
 #define NF4_ACT_GELU 1   /* the tanh form 0.5 g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3)))   */
 int qlora_gated_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t r, int64_t* fwd_bytes, int64_t* bwd_bytes);
