@@ -6,12 +6,13 @@
 // probabilities; 2 M K V operations for the loss and as many for dX.  Per piece:
 //   1. head_logits_kernel: the GEMM of X and the piece's rows of W.  Its
 //      epilogue turns a tile's logits into powers of two relative to an integer
-//      bound of their own row and 128 columns, P = 2^(s log2 e - ref), ref =
-//      ceil of the largest: P (16 bits, one rounding), ref and the sum of the
-//      unrounded P go to memory.  The target's own column is left out of all
+//      bound of their own row and 128 columns, P = 2^(s log2 e - ref), ref = 0 or
+//      the ceil of the largest (head_ref): P (16 bits, one rounding), ref and the
+//      sum of the unrounded P go to memory.  The target's own column is left out of all
 //      three; its logit is kept in fp32.
 //   2. head_rows_kernel: per row the running bound and sum over the pieces, and
-//      P times 2^(ref - bound): a power of two, so no second rounding.
+//      P times 2^(ref - bound) where they differ: a power of two, so no second
+//      rounding.
 //   3. head_dx_kernel: the GEMM of P and the same rows of W, read in their
 //      stored order and turned in registers on the way into LDS, added to the
 //      earlier pieces' fp32 sums times 2^(old bound - bound).
@@ -42,6 +43,18 @@ constexpr int64_t kPieceBytes = static_cast<int64_t>(QN_HEAD_PIECE_MB) << 20;
 // lose bits below 2^-14.
 template <class T>
 constexpr int head_shift() { return T::kDtype == F16::kDtype ? 14 : 0; }
+
+// The bound of a row's 128 columns with largest logit `top`.  bf16 has fp32's
+// exponents, so within 2^-64 .. 2^40 the logits stand as they are (bound 0): a
+// row whose groups all do, as a language model's, needs no common bound made for
+// it afterwards.  A group's terms below 2^-126 are then 2^-62 of its largest.
+template <class T>
+__device__ __forceinline__ float head_ref(float top) {
+  // nothing but masked columns: any bound serves, every P is 0
+  if (top == -__builtin_inff()) return 0.0f;
+  const float e = __builtin_ceilf(top * kLog2e);
+  return T::kDtype == Bf16::kDtype && e >= -64.0f && e <= 40.0f ? 0.0f : e;
+}
 
 struct HeadArgs {
   const int64_t* targets;
@@ -99,8 +112,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
     for (int x = 1; x < 32; ++x) top = fmaxf(top, v[x]);
     top = fmaxf(top, __shfl_xor(top, 16, 64));
     top = fmaxf(top, __shfl_xor(top, 32, 64));
-    // nothing but masked columns: any bound serves, every P is 0
-    const float ref = top == -__builtin_inff() ? 0.0f : __builtin_ceilf(top * kLog2e);
+    const float ref = head_ref<T>(top);
     float sum = 0.0f;
 #pragma unroll
     for (int x = 0; x < 32; ++x) {
@@ -122,6 +134,70 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
       if (m < a.M && n < p.ldp) *reinterpret_cast<uint4*>(p.P + m * p.ldp + n) = x;
     });
   }
+}
+
+// The same with the reduction split: fp32 partials of the tiles, M x ldp a split.
+template <class T>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void head_part_kernel(G16Args a,
+                                                                                                       int64_t ldp) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  Core16<T, kRows> k(a, smem);
+  f32x4 acc[8][8];
+  k.template run<true>(acc);
+  k.store_part(acc, ldp);
+}
+
+// Their sums in split order, and the epilogue of head_logits_kernel: 32 lanes
+// take a row's 128 columns, four each.  Up to kJoin splits are requested at once.
+template <class T, bool kStore>
+__global__ __launch_bounds__(256) void head_join_kernel(const float* __restrict__ part, int64_t splits, int64_t M,
+                                                        HeadArgs p) {
+  constexpr int kJoin = 8;
+  const int lane = threadIdx.x & 31;
+  const int64_t unit = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const bool live = unit < M * p.nh;
+  const int64_t m = live ? unit / p.nh : 0, half = live ? unit - m * p.nh : 0;
+  const int64_t col = half * 128 + 4 * lane, plane = M * p.ldp;
+  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+  const bool stored = live && col < p.ldp;
+  if (stored) {
+    const float* from = part + m * p.ldp + col;
+    for (int64_t z = 0; z < splits; z += kJoin) {
+      f32x4 x[kJoin];
+#pragma unroll
+      for (int i = 0; i < kJoin; ++i)
+        x[i] = z + i < splits ? *reinterpret_cast<const f32x4*>(from + (z + i) * plane) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < kJoin; ++i) v += x[i];
+    }
+  }
+  const int64_t t = live ? p.targets[m] : -1;
+  const bool wanted = t >= 0 && t < p.V && t != p.ignore;
+  float top = -__builtin_inff();
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (wanted && stored && col + e == t - p.v0) {
+      p.st[m] = v[e];
+      v[e] = -__builtin_inff();
+    }
+    if (col + e >= p.nv) v[e] = -__builtin_inff();
+    top = fmaxf(top, v[e]);
+  }
+#pragma unroll
+  for (int s = 16; s >= 1; s >>= 1) top = fmaxf(top, __shfl_xor(top, s, 64));
+  const float ref = head_ref<T>(top);
+  float sum = 0.0f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[e] = __builtin_amdgcn_exp2f(__builtin_fmaf(v[e], kLog2e, -ref));
+    sum += v[e];
+    v[e] *= static_cast<float>(1 << head_shift<T>());
+  }
+#pragma unroll
+  for (int s = 16; s >= 1; s >>= 1) sum += __shfl_xor(sum, s, 64);
+  if (live && lane == 0) p.stats[m * p.nh + half] = make_float2(ref, sum);
+  if (kStore && stored)
+    *reinterpret_cast<uint2*>(p.P + m * p.ldp + col) = make_uint2(T::pack2(v[0], v[1]), T::pack2(v[2], v[3]));
 }
 
 struct RowArgs {
@@ -166,13 +242,17 @@ __global__ __launch_bounds__(256) void head_rows_kernel(RowArgs p) {
   const float2* s = p.stats + m * p.nh;
   float2 old = make_float2(-__builtin_inff(), 0.0f);
   if (p.run_in != nullptr) old = p.run_in[m];
-  float top = old.x;
+  float top = old.x, low = __builtin_inff();
   for (int64_t i = t; i < p.nh; i += 256) {
     const float2 v = s[i];
     // an empty group bounds nothing; a NaN sum must reach the row's
-    if (v.y != 0.0f) top = fmaxf(top, v.x);
+    if (v.y != 0.0f) {
+      top = fmaxf(top, v.x);
+      low = fminf(low, v.x);
+    }
   }
   top = wg_max(top, red);
+  low = -wg_max(-low, red);
   if (top == -__builtin_inff()) top = 0.0f;   // nothing in the row so far
   float sum = 0.0f;
   for (int64_t i = t; i < p.nh; i += 256) {
@@ -209,7 +289,7 @@ __global__ __launch_bounds__(256) void head_rows_kernel(RowArgs p) {
       }
     }
   }
-  if (p.P == nullptr) return;
+  if (p.P == nullptr || low >= top) return;   // (one bound, or nothing)
   // 128 columns (16 chunks of 8) share a factor, an exact power of two
   uint16_t* row = p.P + m * p.ldp;
   const int64_t chunks = p.ldp / 8;
@@ -311,7 +391,8 @@ int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 struct HeadPlan {
   int64_t pieces, rows;             // rows per piece, a multiple of 256
   int64_t splits, k_per;
-  int64_t p_bytes, stats_bytes, row_bytes, sum_bytes, part_bytes;
+  SplitPlan logits;                 // of their reduction, for a whole piece
+  int64_t p_bytes, stats_bytes, row_bytes, sum_bytes, part_bytes;   // part: the logits' or dX's, one after the other
   int64_t total() const { return p_bytes + stats_bytes + 6 * row_bytes + sum_bytes + part_bytes; }
 };
 
@@ -331,8 +412,10 @@ HeadPlan head_plan(int64_t M, int64_t K, int64_t V, bool need_dx) {
   h.row_bytes = align256(M * 8);
   h.splits = 1;
   h.k_per = h.rows;
-  if (!need_dx) return h;
   const int64_t width = V < h.rows ? (V + 63) / 64 * 64 : h.rows;
+  h.logits = plan_split(M, width, K);
+  h.part_bytes = h.logits.part_bytes;
+  if (!need_dx) return h;
   h.p_bytes = align256(M * width * 2);
   if (h.pieces > 1) h.sum_bytes = align256(M * K * 4);
   constexpr int64_t kMinStages = 8;
@@ -343,7 +426,7 @@ HeadPlan head_plan(int64_t M, int64_t K, int64_t V, bool need_dx) {
     h.k_per = ((width + s - 1) / s + kBK - 1) / kBK * kBK;
     h.splits = (width + h.k_per - 1) / h.k_per;
     if (h.splits < 2) h.splits = 1;
-    else h.part_bytes = align256(h.splits * M * K * 4);
+    else if (align256(h.splits * M * K * 4) > h.part_bytes) h.part_bytes = align256(h.splits * M * K * 4);
   }
   return h;
 }
@@ -358,6 +441,30 @@ hipError_t launch_logits_t(const G16Args& a, const HeadArgs& p, hipStream_t stre
   const Timer t(QK_HEAD_LOGITS, stream, true);
   const dim3 grid(static_cast<unsigned>((p.nv + kBN - 1) / kBN), static_cast<unsigned>((a.M + kBM - 1) / kBM));
   hipExtLaunchKernelGGL((head_logits_kernel<T, kStore>), grid, dim3(kThreads), kG16Lds, stream, t.start(), t.end(), 0, a, p);
+  return hipGetLastError();
+}
+
+template <class T>
+hipError_t launch_logits_split(const G16Args& a, const HeadArgs& p, hipStream_t stream) {
+  static const hipError_t lds_limit = hipFuncSetAttribute(reinterpret_cast<const void*>(&head_part_kernel<T>),
+                                                          hipFuncAttributeMaxDynamicSharedMemorySize, kG16Lds);
+  if (lds_limit != hipSuccess) return lds_limit;
+  const int64_t splits = (a.red + a.k_per - 1) / a.k_per;
+  const dim3 grid(static_cast<unsigned>((p.nv + kBN - 1) / kBN), static_cast<unsigned>((a.M + kBM - 1) / kBM),
+                  static_cast<unsigned>(splits));
+  {
+    const Timer t(QK_HEAD_LOGITS, stream, true);
+    hipExtLaunchKernelGGL((head_part_kernel<T>), grid, dim3(kThreads), kG16Lds, stream, t.start(), t.end(), 0, a, p.ldp);
+  }
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const dim3 units(static_cast<unsigned>((a.M * p.nh + 7) / 8));
+  Timer tm(QK_REDUCE, stream);
+  if (p.P != nullptr)
+    hipLaunchKernelGGL((head_join_kernel<T, true>), units, dim3(256), 0, stream, a.part, splits, a.M, p);
+  else
+    hipLaunchKernelGGL((head_join_kernel<T, false>), units, dim3(256), 0, stream, a.part, splits, a.M, p);
+  tm.stop();
   return hipGetLastError();
 }
 
@@ -407,9 +514,12 @@ hipError_t head_loss_t(int64_t M, int64_t K, int64_t V, const uint16_t* X, const
   for (int64_t i = 0; i < h.pieces; ++i) {
     const int64_t v0 = i * h.rows, nv = V - v0 < h.rows ? V - v0 : h.rows;
     const bool last = i + 1 == h.pieces;
-    const G16Args g{X, K, W + v0 * K, M, nv, K, nullptr, 0, nullptr, 0, nullptr, 0};
+    const bool logits_split = h.logits.splits > 1;
+    const G16Args g{X, K, W + v0 * K, M, nv, K, nullptr, 0, nullptr, 0, logits_split ? part : nullptr, h.logits.k_per};
     HeadArgs p{targets, v0, nv, (nv + 63) / 64 * 64, V, ignore, dX != nullptr ? P : nullptr, stats, (nv + 127) / 128, st};
-    hipError_t e = dX != nullptr ? launch_logits_t<T, true>(g, p, stream) : launch_logits_t<T, false>(g, p, stream);
+    hipError_t e = logits_split    ? launch_logits_split<T>(g, p, stream)
+                   : dX != nullptr ? launch_logits_t<T, true>(g, p, stream)
+                                   : launch_logits_t<T, false>(g, p, stream);
     if (e != hipSuccess) return e;
     RowArgs r{stats, p.nh, p.ldp, M, V, ignore, p.P, i > 0 ? run[(i + 1) & 1] : nullptr, run[i & 1], st, targets, weights,
               alpha, last ? loss : nullptr, lse != nullptr ? lse : lse_own, dX != nullptr ? coef : nullptr};

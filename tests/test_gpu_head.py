@@ -210,3 +210,50 @@ def test_rows_behind_the_last_stay_and_calls_repeat():
         torch.cuda.synchronize()
         for o, h in zip(outs, want):
             np.testing.assert_array_equal(host(o), h)
+
+
+@pytest.mark.parametrize("name", ["bf16", "f16"])
+@pytest.mark.parametrize("K", [64, 1032])
+def test_rows_of_very_different_groups(K, name):
+    """Vocabulary groups of 128 whose logits reach from a fraction to hundreds:
+    bounds of one row's groups on both sides of where bf16 takes them as 0."""
+    say(f"head groups K={K} {name}")
+    M, V = 37, 1000
+    rng = np.random.default_rng(K)
+    gain = np.array([1.0, 0.05, 12.0, 40.0, 0.0, 3.0, 25.0, 1.0])[np.arange(V) // 128]
+    W = rng.standard_normal((V, K)) / np.sqrt(K) * gain[:, None]
+    # rows 0 .. 18: the large groups far below (every product negative)
+    X = rng.standard_normal((M, K))
+    W[256:512] = -np.abs(W[256:512])
+    X[:19] = np.abs(X[:19])
+    W, X = _dev(W, name), _dev(X, name)
+    import torch
+    t = torch.from_numpy(rng.integers(0, V, size=M)).cuda()
+    t[3] = -100
+    _compare(X, W, t, None, qn.qlora_head_loss(X, W, t), name)
+
+
+def test_masks_of_a_split_reduction():
+    """Few tiles and a long K: the logits come from partial sums."""
+    import torch
+    say("head masks, split")
+    M, K, V = 40, 2056, 700
+    X, W, t, w = _case(M, K, V, "bf16", 8)
+    t[:] = torch.arange(M, device="cuda") % V
+    want = [host(v).copy() for v in qn.qlora_head_loss(X, W, t, weights=w)]
+    X2, t2 = X.clone(), t.clone()
+    X2[0] = float("nan")
+    t2[0], t2[1], t2[2] = -100, V, -7
+    loss, lse, dX = (host(v) for v in qn.qlora_head_loss(X2, W, t2, weights=w))
+    assert loss[0] == 0 and not dX[0].any()
+    for r in (1, 2):
+        assert np.isnan(loss[r]) and np.isnan(dX[r]).all()
+        np.testing.assert_allclose(lse[r], want[1][r], rtol=1e-6)
+    for g, h in zip((loss, lse, dX), want):
+        np.testing.assert_array_equal(g[3:], h[3:])
+    # the last columns of the last group, and a piece of one column
+    t2[:] = V - 1
+    _compare(X, W, t2, None, qn.qlora_head_loss(X, W, t2), "bf16")
+    one = torch.zeros(M, dtype=torch.int64, device="cuda")
+    loss, lse, dX = (host(v) for v in qn.qlora_head_loss(X, W[:1], one))
+    assert not loss.any() and not dX.any()
