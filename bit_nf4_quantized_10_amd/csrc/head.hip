@@ -321,31 +321,45 @@ struct DxArgs {
   float unshift;             // 2^-shift of P
 };
 
-// Four columns of row m: v = this piece's product.
-template <class T>
-__device__ __forceinline__ void dx_store4(const DxArgs& p, int64_t m, int64_t col, f32x4 v) {
-  v *= p.unshift;
+// Columns col + 16 j .. + 3, j < N, of row m: v[j] = this piece's product.  All
+// loads of the row are requested before the first is used (one after the other,
+// each waits for memory behind the stores of the last).
+template <class T, int N>
+__device__ __forceinline__ void dx_store(const DxArgs& p, int64_t m, int64_t col, f32x4 (&v)[N]) {
+#pragma unroll
+  for (int j = 0; j < N; ++j) v[j] *= p.unshift;
   if (p.prev != nullptr) {
     const float al = p.alpha[m];
-    const f32x4 o = *reinterpret_cast<const f32x4*>(p.prev + m * p.K + col);
-    if (al != 0.0f) v += o * al;   // 0: nothing was summed before
+    f32x4 o[N];
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      o[j] = col + 16 * j < p.K ? *reinterpret_cast<const f32x4*>(p.prev + m * p.K + col + 16 * j) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (al != 0.0f) v[j] += o[j] * al;   // 0: nothing was summed before
   }
   if (p.sum != nullptr) {
-    *reinterpret_cast<f32x4*>(p.sum + m * p.K + col) = v;
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (col + 16 * j < p.K) *reinterpret_cast<f32x4*>(p.sum + m * p.K + col + 16 * j) = v[j];
     return;
   }
   const float2 c = p.coef[m];
-  float r[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (c.x != c.x) {
+  const bool counts = c.x == c.x && c.y >= 0.0f;
+  uint2 wt[N];
+  const uint16_t* from = p.W + (counts ? p.targets[m] : 0) * p.K + col;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) r[e] = c.x;
-  } else if (c.y >= 0.0f) {
-    const uint2 wt = *reinterpret_cast<const uint2*>(p.W + p.targets[m] * p.K + col);
-    const float t[4] = {T::widen(wt.x & 0xffffu), T::widen(wt.x >> 16), T::widen(wt.y & 0xffffu), T::widen(wt.y >> 16)};
+  for (int j = 0; j < N; ++j)
+    wt[j] = counts && col + 16 * j < p.K ? *reinterpret_cast<const uint2*>(from + 16 * j) : make_uint2(0, 0);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) r[e] = c.x * (__builtin_fmaf(v[e], c.y, -t[e]));
+  for (int j = 0; j < N; ++j) {
+    const float t[4] = {T::widen(wt[j].x & 0xffffu), T::widen(wt[j].x >> 16), T::widen(wt[j].y & 0xffffu), T::widen(wt[j].y >> 16)};
+    float r[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) r[e] = counts ? c.x * (__builtin_fmaf(v[j][e], c.y, -t[e])) : (c.x != c.x ? c.x : 0.0f);
+    if (col + 16 * j < p.K)
+      *reinterpret_cast<uint2*>(p.dX + m * p.K + col + 16 * j) = make_uint2(T::pack2(r[0], r[1]), T::pack2(r[2], r[3]));
   }
-  *reinterpret_cast<uint2*>(p.dX + m * p.K + col) = make_uint2(T::pack2(r[0], r[1]), T::pack2(r[2], r[3]));
 }
 
 // The sums over the splits of a piece, then the same.
@@ -358,7 +372,8 @@ __global__ __launch_bounds__(256) void head_sum_kernel(DxArgs p) {
     f32x4 v = *reinterpret_cast<const f32x4*>(p.part + at);
 #pragma unroll 4
     for (int64_t z = 1; z < p.splits; ++z) v += *reinterpret_cast<const f32x4*>(p.part + z * plane + at);
-    dx_store4<T>(p, m, at - m * p.K, v);
+    f32x4 one[1] = {v};
+    dx_store<T, 1>(p, m, at - m * p.K, one);
   }
 }
 
@@ -376,12 +391,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int64_t m = k.m0 + k.wm * 128 + 16 * i + k.q;
-    if (m >= p.M) continue;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int64_t col = k.c0 + k.wn * 128 + 16 * j + 4 * k.g;
-      if (col < p.K) dx_store4<T>(p, m, col, acc[i][j]);
-    }
+    if (m < p.M) dx_store<T, 8>(p, m, k.c0 + k.wn * 128 + 4 * k.g, acc[i]);
   }
 }
 
