@@ -266,10 +266,10 @@ hipError_t launch_gated_dx_t(const G16Args& p, uint16_t* dX, hipStream_t stream,
 
 // The GEMM and, after a split one, the sums.  WhatT: 2F x K, Zext: M x 4r, Bt: 2F x r.
 hipError_t launch_gated_dense(int64_t M, int64_t K, int64_t F, int64_t r, const uint16_t* X, const uint16_t* WhatT,
-                              const uint16_t* Zext, const uint16_t* Bt, bool gelu, uint16_t* H, const GatedKeep& keep,
+                              int64_t w_ld, const uint16_t* Zext, const uint16_t* Bt, bool gelu, uint16_t* H, const GatedKeep& keep,
                               hipStream_t stream, int dtype, void* split_ws) {
   GatedArgs p{};
-  p.g = G16Args{X, K, WhatT, M, 2 * F, K, Zext, 4 * r, Bt, r, nullptr, 0};
+  p.g = G16Args{X, K, WhatT, w_ld, M, 2 * F, K, Zext, 4 * r, Bt, r, nullptr, 0};
   p.keep = keep;
   p.H = H;
   p.F = F;
@@ -295,7 +295,7 @@ hipError_t launch_gated_dense(int64_t M, int64_t K, int64_t F, int64_t r, const 
 hipError_t launch_gated_dx(int64_t M, int64_t K, int64_t red, int64_t rt, const uint16_t* dY, const uint16_t* What,
                            const uint16_t* dZ, const uint16_t* A, uint16_t* dX, hipStream_t stream, int dtype,
                            void* split_ws) {
-  G16Args p{dY, red, What, M, K, red, dZ, rt, A, rt, nullptr, 0};
+  G16Args p{dY, red, What, red, M, K, red, dZ, rt, A, rt, nullptr, 0};
   const SplitPlan sp = plan_split(M, K, red);
   if (sp.splits >= 2) {
     p.part = static_cast<float*>(split_ws);

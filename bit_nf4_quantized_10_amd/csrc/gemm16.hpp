@@ -42,6 +42,7 @@ struct G16Args {
   const uint16_t* act;     // M x red, row stride act_ld
   int64_t act_ld;
   const uint16_t* w;
+  int64_t w_ld;            // kRows, kPaired: w's row stride
   int64_t M, wrows, red;
   // Adapter term, as more stages after the product's: kRows: ext_a (M x r) times
   // ext_b (wrows x r)ᵀ.  kPaired: ext_a is M x 4r, [hi | lo] parts of the two
@@ -102,7 +103,7 @@ struct Core16 {
     wn = wave & 1;
     tile_origin<kCols>(m0, c0);
     r_act = make_rsrc(a.act, ((a.M - 1) * a.act_ld + (a.red + 7) / 8 * 8) * 2);   // whole chunks
-    if (kW != kTurned) r_w = make_rsrc(a.w, a.wrows * a.red * 2);   // kTurned: see run()
+    if (kW != kTurned) r_w = make_rsrc(a.w, a.wrows * a.w_ld * 2);   // kTurned: see run()
     r_ea = make_rsrc(a.ext_a, a.r ? a.M * a.ext_a_ld * 2 : 0);
     r_eb = make_rsrc(a.ext_b, a.wrows * a.r * 2);
     chunk8 = 8 * ((lane & 7) ^ (lane >> 3));
@@ -111,7 +112,7 @@ struct Core16 {
       const int row = wave * 64 + 8 * j + (lane >> 3);
       const int64_t m = m0 + row, n = weight_row(row);
       av[j] = m < a.M ? static_cast<uint32_t>((m * a.act_ld + chunk8) * 2) : kMasked;
-      wv[j] = kW != kTurned && n < a.wrows ? static_cast<uint32_t>((n * a.red + chunk8) * 2) : kMasked;
+      wv[j] = kW != kTurned && n < a.wrows ? static_cast<uint32_t>((n * a.w_ld + chunk8) * 2) : kMasked;
     }
     pA = (wm * 128 + q) * 128 + ((g ^ (q & 7)) << 4);
     const int wrow = (kW == kPaired ? wn * 64 : wn * 128) + q;

@@ -525,7 +525,7 @@ hipError_t head_loss_t(int64_t M, int64_t K, int64_t V, const uint16_t* X, const
     const int64_t v0 = i * h.rows, nv = V - v0 < h.rows ? V - v0 : h.rows;
     const bool last = i + 1 == h.pieces;
     const bool logits_split = h.logits.splits > 1;
-    const G16Args g{X, K, W + v0 * K, M, nv, K, nullptr, 0, nullptr, 0, logits_split ? part : nullptr, h.logits.k_per};
+    const G16Args g{X, K, W + v0 * K, K, M, nv, K, nullptr, 0, nullptr, 0, logits_split ? part : nullptr, h.logits.k_per};
     HeadArgs p{targets, v0, nv, (nv + 63) / 64 * 64, V, ignore, dX != nullptr ? P : nullptr, stats, (nv + 127) / 128, st};
     hipError_t e = logits_split    ? launch_logits_split<T>(g, p, stream)
                    : dX != nullptr ? launch_logits_t<T, true>(g, p, stream)
@@ -547,7 +547,7 @@ hipError_t head_loss_t(int64_t M, int64_t K, int64_t V, const uint16_t* X, const
     // the last piece may be shorter and need fewer splits
     const int64_t splits = (nv + h.k_per - 1) / h.k_per;
     const bool split = h.splits > 1;
-    const G16Args w{P, p.ldp, W + v0 * K, M, K, nv, nullptr, 0, nullptr, 0, split ? part : nullptr, h.k_per};
+    const G16Args w{P, p.ldp, W + v0 * K, K, M, K, nv, nullptr, 0, nullptr, 0, split ? part : nullptr, h.k_per};
     const DxArgs d{M, K, w.part, splits, i > 0 ? sums : nullptr, alpha, last ? nullptr : sums, coef, W, targets, dX,
                    1.0f / static_cast<float>(1 << head_shift<T>())};
     if ((e = launch_dx<T>(w, d, stream)) != hipSuccess) return e;

@@ -213,8 +213,9 @@ hipError_t launch_gated_bwd(int64_t M, int64_t K, int64_t F, int64_t r, const ui
                             Act8View x8, const uint16_t* Z, const GatedKeep& kept, const NF4View* W, const uint16_t* A,
                             const uint16_t* B, float c, bool gelu, uint16_t* dX, void* dA, void* dB, void* ws,
                             hipStream_t stream, int dtype, bool grad16);
+// w_ld: row stride of WhatT.
 hipError_t launch_gated_dense(int64_t M, int64_t K, int64_t F, int64_t r, const uint16_t* X, const uint16_t* WhatT,
-                              const uint16_t* Zext, const uint16_t* Bt, bool gelu, uint16_t* H, const GatedKeep& keep,
+                              int64_t w_ld, const uint16_t* Zext, const uint16_t* Bt, bool gelu, uint16_t* H, const GatedKeep& keep,
                               hipStream_t stream, int dtype, void* split_ws);
 // dX = dY Ŵᵀ + dZ Aᵀ: dY M x red, What K x red, dZ M x rt, A K x rt.
 hipError_t launch_gated_dx(int64_t M, int64_t K, int64_t red, int64_t rt, const uint16_t* dY, const uint16_t* What,
@@ -240,7 +241,7 @@ hipError_t launch_head_loss(int64_t M, int64_t K, int64_t V, const uint16_t* X, 
 
 // Dequantize a K x N weight to the 16-bit compute type (dtype), either as
 // stored (K x N) or transposed (N x K).
-// out_ld: row stride of the untransposed output (0: N).
+// out_ld: row stride of the output (0: N, transposed K).
 // Side jobs run as extra workgroups of the same launch: side_t (two
 // transposes, transposed output only), side_r (one split sum, untransposed
 // output only).

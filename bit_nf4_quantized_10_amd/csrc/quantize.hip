@@ -485,7 +485,7 @@ constexpr int kTPad = 66;  // bf16 per LDS row (64 k + 2): 132-byte rows
 // instead, one 32 x 32 tile per workgroup.
 template <class T>
 __global__ __launch_bounds__(256) void nf4_dequant_t_kernel(NF4View W, int64_t K, int64_t N,
-                                                            uint16_t* __restrict__ out, TJob t0, TJob t1) {
+                                                            uint16_t* __restrict__ out, int64_t ld, TJob t0, TJob t1) {
   __shared__ float s_lut[16];
   __shared__ __attribute__((aligned(16))) uint16_t tile[128 * kTPad];
   const int64_t ky = (K + 63) / 64;
@@ -536,7 +536,7 @@ __global__ __launch_bounds__(256) void nf4_dequant_t_kernel(NF4View W, int64_t K
     const int64_t n = n0 + nn, k = k0 + 8 * c;
     if (n < N && k < K) {
       const uint32_t* src = reinterpret_cast<const uint32_t*>(tile + nn * kTPad + 8 * c);
-      *reinterpret_cast<uint4*>(out + n * K + k) = make_uint4(src[0], src[1], src[2], src[3]);
+      *reinterpret_cast<uint4*>(out + n * ld + k) = make_uint4(src[0], src[1], src[2], src[3]);
     }
   }
 }
@@ -630,7 +630,7 @@ hipError_t launch_dequant_bf16(NF4View W, int64_t K, int64_t N, bool transposed,
   Timer t(QK_DEQUANT_BF16, stream);
   dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(ky + side_rows));
   hipLaunchKernelGGL(dtype == kDtypeF16 ? nf4_dequant_t_kernel<F16> : nf4_dequant_t_kernel<Bf16>, grid, dim3(256), 0,
-                     stream, W, K, N, out, t0, t1);
+                     stream, W, K, N, out, out_ld != 0 ? out_ld : K, t0, t1);
   t.stop();
   return hipGetLastError();
 }
