@@ -122,7 +122,7 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
   Core16<T, kPaired> k(p.g, smem);
   f32x4 acc[8][8];
   k.template run<kSplit>(acc);
-  if constexpr (kSplit) k.store_part(acc, 2 * p.F);
+  if constexpr (kSplit) k.store_part(acc, 2 * (p.F - p.g.first));
   else finish_gated<T, kGelu, kKeep>(k, p, acc);
 }
 
@@ -145,13 +145,14 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
   }
 }
 
-// After a split GEMM: G and U as the sums of the partials in split order, then
-// the epilogue's work.  count: M F / 8 chunks.
+// After a split GEMM of the columns from `first` on: G and U as the sums of the
+// partials in split order, then the epilogue's work.
 template <class T, bool kGelu>
 __global__ __launch_bounds__(256) void gated_sum_kernel(const float* __restrict__ part, int64_t splits, int64_t M,
-                                                        int64_t F, uint16_t* H, GatedKeep keep) {
-  const uint32_t per = static_cast<uint32_t>(F / 8), count = static_cast<uint32_t>(M) * per;
-  const int64_t plane = M * 2 * F;
+                                                        int64_t F, int64_t first, uint16_t* H, GatedKeep keep) {
+  const int64_t Fs = F - first;
+  const uint32_t per = static_cast<uint32_t>(Fs / 8), count = static_cast<uint32_t>(M) * per;
+  const int64_t plane = M * 2 * Fs;
   for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < count; i += gridDim.x * 256) {
     const uint32_t m = i / per;
     const int64_t col = static_cast<int64_t>(i - m * per) * 8;
@@ -160,15 +161,15 @@ __global__ __launch_bounds__(256) void gated_sum_kernel(const float* __restrict_
     for (int k = 0; k < 4; ++k) s[k] = f32x4{0, 0, 0, 0};
 #pragma unroll 4
     for (int64_t z = 0; z < splits; ++z) {
-      const float* pg = part + z * plane + m * 2 * F + col;
+      const float* pg = part + z * plane + m * 2 * Fs + col;
       s[0] += *reinterpret_cast<const f32x4*>(pg);
       s[1] += *reinterpret_cast<const f32x4*>(pg + 4);
-      s[2] += *reinterpret_cast<const f32x4*>(pg + F);
-      s[3] += *reinterpret_cast<const f32x4*>(pg + F + 4);
+      s[2] += *reinterpret_cast<const f32x4*>(pg + Fs);
+      s[3] += *reinterpret_cast<const f32x4*>(pg + Fs + 4);
     }
     const float g[8] = {s[0][0], s[0][1], s[0][2], s[0][3], s[1][0], s[1][1], s[1][2], s[1][3]};
     const float u[8] = {s[2][0], s[2][1], s[2][2], s[2][3], s[3][0], s[3][1], s[3][2], s[3][3]};
-    gated_store8<T, kGelu>(g, u, m, col, F, H, keep);
+    gated_store8<T, kGelu>(g, u, m, first + col, F, H, keep);
   }
 }
 
@@ -225,7 +226,7 @@ unsigned ew_grid(int64_t chunks) {
 }
 
 template <class T, bool kSplit, bool kGelu, int kKeep>
-hipError_t launch_gated_t(const GatedArgs& p, hipStream_t stream, const Timer& tm) {
+hipError_t launch_gated_t(const GatedArgs& p, int64_t cols, hipStream_t stream, const Timer& tm) {
   // raised once per process; the initialisation of a function-local static
   // is thread-safe, so concurrent first calls do not race
   static const hipError_t lds_limit =
@@ -233,23 +234,23 @@ hipError_t launch_gated_t(const GatedArgs& p, hipStream_t stream, const Timer& t
                           hipFuncAttributeMaxDynamicSharedMemorySize, kG16Lds);
   if (lds_limit != hipSuccess) return lds_limit;
   const unsigned zs = kSplit ? static_cast<unsigned>((p.g.red + p.g.k_per - 1) / p.g.k_per) : 1u;
-  const dim3 grid(static_cast<unsigned>((p.F + 127) / 128), static_cast<unsigned>((p.g.M + kBM - 1) / kBM), zs);
+  const dim3 grid(static_cast<unsigned>((cols + 127) / 128), static_cast<unsigned>((p.g.M + kBM - 1) / kBM), zs);
   hipExtLaunchKernelGGL((gated_dense_kernel<T, kSplit, kGelu, kKeep>), grid, dim3(kThreads), kG16Lds, stream, tm.start(),
                         tm.end(), 0, p);
   return hipGetLastError();
 }
 template <class T>
-hipError_t launch_gated_k(const GatedArgs& p, bool gelu, hipStream_t stream, const Timer& tm) {
-  if (p.g.part != nullptr) return launch_gated_t<T, true, false, kKeepNone>(p, stream, tm);
+hipError_t launch_gated_k(const GatedArgs& p, int64_t cols, bool gelu, hipStream_t stream, const Timer& tm) {
+  if (p.g.part != nullptr) return launch_gated_t<T, true, false, kKeepNone>(p, cols, stream, tm);
   const int keep = p.keep.gu != nullptr ? kKeep16 : (p.keep.codes != nullptr ? kKeep8 : kKeepNone);
   if (gelu) {
-    if (keep == kKeep16) return launch_gated_t<T, false, true, kKeep16>(p, stream, tm);
-    if (keep == kKeep8) return launch_gated_t<T, false, true, kKeep8>(p, stream, tm);
-    return launch_gated_t<T, false, true, kKeepNone>(p, stream, tm);
+    if (keep == kKeep16) return launch_gated_t<T, false, true, kKeep16>(p, cols, stream, tm);
+    if (keep == kKeep8) return launch_gated_t<T, false, true, kKeep8>(p, cols, stream, tm);
+    return launch_gated_t<T, false, true, kKeepNone>(p, cols, stream, tm);
   }
-  if (keep == kKeep16) return launch_gated_t<T, false, false, kKeep16>(p, stream, tm);
-  if (keep == kKeep8) return launch_gated_t<T, false, false, kKeep8>(p, stream, tm);
-  return launch_gated_t<T, false, false, kKeepNone>(p, stream, tm);
+  if (keep == kKeep16) return launch_gated_t<T, false, false, kKeep16>(p, cols, stream, tm);
+  if (keep == kKeep8) return launch_gated_t<T, false, false, kKeep8>(p, cols, stream, tm);
+  return launch_gated_t<T, false, false, kKeepNone>(p, cols, stream, tm);
 }
 template <class T, bool kSplit>
 hipError_t launch_gated_dx_t(const G16Args& p, uint16_t* dX, hipStream_t stream, const Timer& tm) {
@@ -264,6 +265,52 @@ hipError_t launch_gated_dx_t(const G16Args& p, uint16_t* dX, hipStream_t stream,
 
 }  // namespace
 
+// The split of a Core16 product of M x cols outputs: the one of least estimated
+// time, where a CU takes kStageUs for a 64-element stage and kTileUs besides them
+// for a tile, tiles run in rounds of 256, and partials go through memory twice at
+// kBytesPerUs, added by one more launch.  (The dense kernels' plan_split fills the
+// device at most once and bounds the partials to 32 MiB: it left dX of 770 rows,
+// K 5568, F 19520, 88 tiles of 610 stages, whole, 705 us;
+// split it brings that training step from 1857 to 1490 us with the forward's.)
+SplitPlan plan_split16(int64_t M, int64_t cols, int64_t red) {
+  constexpr double kStageUs = 1.4, kTileUs = 5.0, kBytesPerUs = 5e6, kLaunchUs = 4.0, kAddUs = 0.1;
+  // (32-bit: a call's host time goes into these divisions)
+  const uint32_t tiles = static_cast<uint32_t>(((M + kBM - 1) / kBM) * ((cols + kBN - 1) / kBN));
+  const uint32_t stages = static_cast<uint32_t>((red + kBK - 1) / kBK);
+  const int64_t plane = M * cols * 4;
+  SplitPlan best{1, red, 0};
+  if (tiles >= 256) return best;
+  double least = kStageUs * stages + kTileUs;
+  for (uint32_t s = 2; 4 * s <= stages && s <= 64 && s * tiles <= 1024; ++s) {
+    const uint32_t per = (stages + s - 1) / s, splits = (stages + per - 1) / per;
+    if (splits * plane > (int64_t(1) << 28)) break;
+    const double us = ((tiles * splits + 255) / 256) * (kStageUs * per + kTileUs) +
+                      static_cast<double>(splits * plane) * (2.0 / kBytesPerUs) + kLaunchUs + kAddUs * splits;
+    if (us >= least) continue;
+    least = us;
+    best = SplitPlan{splits, static_cast<int64_t>(per) * kBK, (splits * plane + 255) / 256 * 256};
+  }
+  return best;
+}
+
+// Fewer than 256 tiles: plan_split16's, of all columns (first = 0).  More: the
+// tiles run in rounds of 256, one a CU, and a last round of few leaves most CUs
+// idle; there the column tiles past the full rounds are split alone, where the
+// estimate (as plan_split16's) says so.  After two full rounds it does not pay:
+// the others then run at the power limit, and what idle CUs leave goes to them.
+// Whole forward product, split and not: 375 rows, K 7064, F 19072 (298 tiles)
+// 256 and 350 us; 4096 rows, K 4096, F 11008 (1376 tiles, 5 rounds and 96) 657 and
+// 651; 2048 rows, K 8192, F 22016 (as many) 1168 and 1157.
+GatedSplit plan_gated_split(int64_t M, int64_t K, int64_t F) {
+  constexpr int64_t kTailRounds = 2;
+  const int64_t mt = (M + kBM - 1) / kBM, nt = (F + 127) / 128;
+  const int64_t full = mt * nt / 256, n1 = full * 256 / mt;   // column tiles of the full rounds
+  if (full > kTailRounds || n1 >= nt) return GatedSplit{F, 1, K, 0};
+  const SplitPlan sp = plan_split16(M, 2 * (F - 128 * n1), K);
+  if (sp.splits < 2) return GatedSplit{F, 1, K, 0};
+  return GatedSplit{128 * n1, sp.splits, sp.k_per, sp.part_bytes};
+}
+
 // The GEMM and, after a split one, the sums.  WhatT: 2F x K, Zext: M x 4r, Bt: 2F x r.
 hipError_t launch_gated_dense(int64_t M, int64_t K, int64_t F, int64_t r, const uint16_t* X, const uint16_t* WhatT,
                               int64_t w_ld, const uint16_t* Zext, const uint16_t* Bt, bool gelu, uint16_t* H, const GatedKeep& keep,
@@ -273,21 +320,27 @@ hipError_t launch_gated_dense(int64_t M, int64_t K, int64_t F, int64_t r, const 
   p.keep = keep;
   p.H = H;
   p.F = F;
-  const SplitPlan sp = plan_split(M, 2 * F, K);
-  if (sp.splits >= 2) {
-    p.g.part = static_cast<float*>(split_ws);
-    p.g.k_per = sp.k_per;
-  }
-  hipError_t e;
-  {
+  const GatedSplit sp = plan_gated_split(M, K, F);
+  hipError_t e = hipSuccess;
+  if (sp.first > 0) {
     const Timer t(QK_GATED_FWD, stream, true);
-    e = dtype == kDtypeF16 ? launch_gated_k<F16>(p, gelu, stream, t) : launch_gated_k<Bf16>(p, gelu, stream, t);
+    e = dtype == kDtypeF16 ? launch_gated_k<F16>(p, sp.first, gelu, stream, t) : launch_gated_k<Bf16>(p, sp.first, gelu, stream, t);
   }
   if (e != hipSuccess || sp.splits < 2) return e;
+  p.g.part = static_cast<float*>(split_ws);
+  p.g.k_per = sp.k_per;
+  p.g.first = sp.first;
+  {
+    const Timer t(QK_GATED_FWD, stream, true);
+    e = dtype == kDtypeF16 ? launch_gated_k<F16>(p, F - sp.first, gelu, stream, t)
+                           : launch_gated_k<Bf16>(p, F - sp.first, gelu, stream, t);
+  }
+  if (e != hipSuccess) return e;
   auto* sum = dtype == kDtypeF16 ? (gelu ? gated_sum_kernel<F16, true> : gated_sum_kernel<F16, false>)
                                  : (gelu ? gated_sum_kernel<Bf16, true> : gated_sum_kernel<Bf16, false>);
   Timer tm(QK_REDUCE, stream);
-  hipLaunchKernelGGL(sum, dim3(ew_grid(M * F / 8)), dim3(256), 0, stream, p.g.part, sp.splits, M, F, H, keep);
+  hipLaunchKernelGGL(sum, dim3(ew_grid(M * (F - sp.first) / 8)), dim3(256), 0, stream, p.g.part, sp.splits, M, F, sp.first,
+                     H, keep);
   tm.stop();
   return hipGetLastError();
 }
@@ -296,7 +349,7 @@ hipError_t launch_gated_dx(int64_t M, int64_t K, int64_t red, int64_t rt, const 
                            const uint16_t* dZ, const uint16_t* A, uint16_t* dX, hipStream_t stream, int dtype,
                            void* split_ws) {
   G16Args p{dY, red, What, red, M, K, red, dZ, rt, A, rt, nullptr, 0};
-  const SplitPlan sp = plan_split(M, K, red);
+  const SplitPlan sp = plan_split16(M, K, red);
   if (sp.splits >= 2) {
     p.part = static_cast<float*>(split_ws);
     p.k_per = sp.k_per;

@@ -55,6 +55,7 @@ struct G16Args {
   // (z+1) k_per); only z = 0 adds the adapter term.
   float* part;
   int64_t k_per;
+  int64_t first = 0;       // column of the launch's first tile (a multiple of kCols)
 };
 
 constexpr int kG16W = 3 * kTileBytes;      // the weight slots follow the activation slots
@@ -102,6 +103,7 @@ struct Core16 {
     wm = wave >> 1;
     wn = wave & 1;
     tile_origin<kCols>(m0, c0);
+    c0 += a.first;
     r_act = make_rsrc(a.act, ((a.M - 1) * a.act_ld + (a.red + 7) / 8 * 8) * 2);   // whole chunks
     if (kW != kTurned) r_w = make_rsrc(a.w, a.wrows * a.w_ld * 2);   // kTurned: see run()
     r_ea = make_rsrc(a.ext_a, a.r ? a.M * a.ext_a_ld * 2 : 0);
@@ -408,9 +410,10 @@ struct Core16 {
       for (int j = 0; j < 8; ++j) put16(i, j, acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
     flush16(store8);
   }
-  // The split's fp32 tile into part + z M cols; store column of (i, j) as run()
-  // says (kPaired: G at c, U at cols / 2 + c).
+  // The split's fp32 tile into part + z M cols; store column of (i, j), counted
+  // from a.first, as run() says (kPaired: G at c, U at cols / 2 + c).
   __device__ __forceinline__ void store_part(const f32x4 (&acc)[8][8], int64_t cols) const {
+    const int64_t c0 = this->c0 - a.first;
     const Rsrc rp = make_rsrc(a.part + (static_cast<int64_t>(blockIdx.z) * a.M + m0) * cols + c0,
                               ((a.M - m0) * cols - c0) * 4);
     const int64_t last = kW == kPaired ? cols / 2 : cols;

@@ -370,7 +370,7 @@ __global__ __launch_bounds__(256) void head_sum_kernel(DxArgs p) {
   for (uint32_t i = blockIdx.x * 256 + threadIdx.x; i < count; i += gridDim.x * 256) {
     const int64_t m = i / per, at = static_cast<int64_t>(i) * 4;
     f32x4 v = *reinterpret_cast<const f32x4*>(p.part + at);
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t z = 1; z < p.splits; ++z) v += *reinterpret_cast<const f32x4*>(p.part + z * plane + at);
     f32x4 one[1] = {v};
     dx_store<T, 1>(p, m, at - m * p.K, one);
@@ -407,8 +407,8 @@ struct HeadPlan {
 };
 
 // A piece keeps its probabilities within kPieceBytes and its rows of W within
-// 2^29 elements (32-bit offsets).  dX's M x K tiles get up to 256 workgroups by
-// splitting the piece's rows, at least kMinStages 64-row stages each.
+// 2^29 elements (32-bit offsets).  Few tiles' reductions are split: the logits'
+// over K, dX's over the piece's rows.
 HeadPlan head_plan(int64_t M, int64_t K, int64_t V, bool need_dx) {
   HeadPlan h{};
   int64_t most = (int64_t(1) << 29) / K;
@@ -423,21 +423,15 @@ HeadPlan head_plan(int64_t M, int64_t K, int64_t V, bool need_dx) {
   h.splits = 1;
   h.k_per = h.rows;
   const int64_t width = V < h.rows ? (V + 63) / 64 * 64 : h.rows;
-  h.logits = plan_split(M, width, K);
+  h.logits = plan_split16(M, width, K);
   h.part_bytes = h.logits.part_bytes;
   if (!need_dx) return h;
   h.p_bytes = align256(M * width * 2);
   if (h.pieces > 1) h.sum_bytes = align256(M * K * 4);
-  constexpr int64_t kMinStages = 8;
-  const int64_t tiles = ((M + kBM - 1) / kBM) * ((K + kBN - 1) / kBN);
-  int64_t s = 256 / tiles, most_s = width / (kBK * kMinStages);
-  if (s > most_s) s = most_s;
-  if (s >= 2) {
-    h.k_per = ((width + s - 1) / s + kBK - 1) / kBK * kBK;
-    h.splits = (width + h.k_per - 1) / h.k_per;
-    if (h.splits < 2) h.splits = 1;
-    else if (align256(h.splits * M * K * 4) > h.part_bytes) h.part_bytes = align256(h.splits * M * K * 4);
-  }
+  const SplitPlan dx = plan_split16(M, K, width);
+  h.splits = dx.splits;
+  h.k_per = dx.k_per;
+  if (dx.part_bytes > h.part_bytes) h.part_bytes = dx.part_bytes;
   return h;
 }
 

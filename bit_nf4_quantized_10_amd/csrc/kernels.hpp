@@ -213,6 +213,12 @@ hipError_t launch_gated_bwd(int64_t M, int64_t K, int64_t F, int64_t r, const ui
                             Act8View x8, const uint16_t* Z, const GatedKeep& kept, const NF4View* W, const uint16_t* A,
                             const uint16_t* B, float c, bool gelu, uint16_t* dX, void* dA, void* dB, void* ws,
                             hipStream_t stream, int dtype, bool grad16);
+SplitPlan plan_split16(int64_t M, int64_t cols, int64_t red);
+// Columns of the split (from `first` on; first = F and one split: none) and its parts.
+struct GatedSplit {
+  int64_t first, splits, k_per, part_bytes;
+};
+GatedSplit plan_gated_split(int64_t M, int64_t K, int64_t F);
 // w_ld: row stride of WhatT.
 hipError_t launch_gated_dense(int64_t M, int64_t K, int64_t F, int64_t r, const uint16_t* X, const uint16_t* WhatT,
                               int64_t w_ld, const uint16_t* Zext, const uint16_t* Bt, bool gelu, uint16_t* H, const GatedKeep& keep,

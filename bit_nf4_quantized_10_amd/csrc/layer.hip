@@ -245,13 +245,14 @@ int64_t gated_fwd_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t r) {
     return p.part + p.zpart + z;
   }
   const SkinnyPlan zp = plan_skinny(M, K, 2 * F, 2 * r);
-  return zp.at_bytes + zp.z_part + align256(2 * F * r * 2) + align256(2 * F * gated_w_ld(K) * 2) + plan_split(M, 2 * F, K).part_bytes +
+  return zp.at_bytes + zp.z_part + align256(2 * F * r * 2) + align256(2 * F * gated_w_ld(K) * 2) + plan_gated_split(M, K, F).part_bytes +
          align256(M * 4 * r * 2) + z;
 }
 
 int64_t gated_bwd_workspace_bytes(int64_t M, int64_t K, int64_t F, int64_t r) {
   const int64_t Ns[2] = {F, F};
-  const int64_t grouped = grouped_bwd_workspace_bytes(M, K, 2, Ns, r);
+  const int64_t grouped = grouped_bwd_workspace_bytes(M, K, 2, Ns, r) - plan_split(M, K, 2 * F).part_bytes +
+                          plan_split16(M, K, 2 * F).part_bytes;
   // G and U computed again: the forward's scratch and the kept pair
   const int64_t again = gated_fwd_workspace_bytes(M, K, F, r) + align256(M * 2 * F * 2);
   return align256(M * 2 * F * 2) + align256(M * 2 * r * 2) + (grouped > again ? grouped : again);

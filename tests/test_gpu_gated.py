@@ -231,3 +231,21 @@ def test_captured_replayed_and_on_another_stream():
             torch.cuda.synchronize()
             for t, w in zip((H, Z, *outs), want):
                 np.testing.assert_array_equal(host(t), w)
+
+
+@pytest.mark.parametrize("M,F,act,name", [(300, 16704, "silu", "bf16"), (700, 11072, "gelu", "f16")])
+def test_last_round_of_tiles_split(M, F, act, name):
+    """A little more than 256 tiles: the last columns are summed from partials."""
+    say(f"gated, last round M={M} F={F} {act} {name}")
+    k = Case(M, 1544, F, 8, name)
+    H, Z, _ = k.forward(act)
+    _check_forward(k, act, H, Z)
+    for save in ("16", "8"):
+        H2, Z2, kept = k.forward(act, save)
+        np.testing.assert_array_equal(host(H2), host(H))
+        np.testing.assert_array_equal(host(Z2), host(Z))
+        if save == "16":
+            pair = qn.act8_encode(kept)
+        else:
+            np.testing.assert_array_equal(host(kept.codes), host(pair.codes))
+            np.testing.assert_array_equal(host(kept.absmax), host(pair.absmax))
