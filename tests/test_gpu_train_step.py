@@ -69,3 +69,37 @@ def test_training_step(M, K, F, r, V, name):
         qn.qlora_sgd_step(a, b, da, db, lr)
         np.testing.assert_array_equal(host(a), host((a0.float() - lr * da).to(T)))
         np.testing.assert_array_equal(host(b), host((b0.float() - lr * db).to(T)))
+
+
+def test_wrappers_refuse_shapes_and_types():
+    import torch
+    say("refusals")
+    b, K, F, r = torch.bfloat16, 64, 128, 8
+    z = lambda *s, t=b: torch.zeros(*s, dtype=t, device="cuda")
+    states = [qn.nf4_quantize(z(K * F, t=torch.float32) + 1)[0] for _ in range(2)]
+    X, A, B, dH, Z = z(4, K), z(K, 2 * r), z(r, 2 * F), z(4, F), z(4, 2 * r)
+    ok = dict(c=1.0, K=K, F=F)
+    qn.qlora_gated_fwd(X, states, A, B, **ok)
+    for args, kw in (((X[:, :32], states, A, B), {}), ((X, states, A[:32], B), {}), ((X, states, A, B[:, :F]), {}),
+                     ((X, states, A, B), {"H": z(4, K)}), ((X, states, A, B), {"Z": z(4, r)}),
+                     ((X, states, A, B), {"saved": z(4, F)}), ((X, states, A, B), {"saved": z(4, 2 * F, t=torch.float16)}),
+                     ((X, states, A, B.half()), {}), ((X, states, A, B), {"H": z(F, 4).T}),
+                     ((X, states, A, B), {"H": torch.zeros(4, F, dtype=b)})):
+        with pytest.raises(ValueError):
+            qn.qlora_gated_fwd(*args, **ok, **kw)
+    kept = qn.act8_encode(X)
+    for args, kw in (((dH[:3], X, Z, None), {}), ((dH, kept, Z, None), {}), ((dH, X, Z[:, :r], None), {}),
+                     ((dH, X, Z, None), {"grad_dtype": torch.float16}), ((dH, X, Z, None), {"dA": z(K, 2 * r)}),
+                     ((dH, X, Z, None), {"dX": z(K, 4)})):
+        with pytest.raises(ValueError):
+            qn.qlora_gated_bwd(*args, states, A, B, **ok, **kw)
+    with pytest.raises(RuntimeError):                       # a workspace that is too small
+        qn.qlora_gated_fwd(X, states, A, B, **ok, workspace=z(256, t=torch.uint8))
+    W, t = z(30, K), z(4, t=torch.int64)
+    qn.qlora_head_loss(X, W, t)
+    for args, kw in (((X, W[:, :32], t), {}), ((X, W, t[:3]), {}), ((X, W, t.int()), {}), ((X, W.half(), t), {}),
+                     ((X, W, t), {"weights": z(4)}), ((X, W, t), {"loss": z(3, t=torch.float32)}),
+                     ((X, W, t), {"dX": z(4, K, t=torch.float32)}), ((X, W, t.cpu()), {})):
+        with pytest.raises(ValueError):
+            qn.qlora_head_loss(*args, **kw)
+    torch.cuda.synchronize()

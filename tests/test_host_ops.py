@@ -168,3 +168,51 @@ def test_head_workspace_is_bounded_by_its_pieces():
     large = qn.qlora_head_workspace_bytes(4096, 4096, 256000)
     assert small <= (256 << 20) + (32 << 20) and large <= small + 4096 * 4096 * 4 + (32 << 20)
     assert qn.qlora_head_workspace_bytes(4096, 4096, 256000, need_dx=False) < 128 << 20
+
+
+def test_gated_and_head_wrappers_refuse_before_a_launch():
+    torch = pytest.importorskip("torch")
+    b = torch.bfloat16
+    X, A, B, dH = (torch.zeros(*s, dtype=b) for s in ((4, 64), (64, 16), (8, 128), (4, 64)))
+    state = qn.NF4State(64 * 64, *[torch.zeros(1)] * 4)
+    for kw in ({"act": "relu"}, {"save": "4"}, {"save": 8}):
+        with pytest.raises(ValueError, match="one of|save"):
+            qn.qlora_gated_fwd(X, [state] * 2, A, B, C, 64, 64, **kw)
+    with pytest.raises(ValueError, match="two states"):
+        qn.qlora_gated_fwd(X, [state], A, B, C, 64, 64)
+    with pytest.raises(ValueError, match="2r"):
+        qn.qlora_gated_fwd(X, [state] * 2, A[:, :15], B, C, 64, 64)
+    with pytest.raises(ValueError, match="compute type"):
+        qn.qlora_gated_fwd(X.float(), [state] * 2, A, B, C, 64, 64)
+    with pytest.raises(ValueError):                    # not device tensors
+        qn.qlora_gated_fwd(X, [state] * 2, A, B, C, 64, 64)
+    with pytest.raises(ValueError):
+        qn.qlora_gated_bwd(dH, X, A, None, [state] * 2, A, B, C, 64, 64)
+    t = torch.zeros(4, dtype=torch.int64)
+    with pytest.raises(ValueError):
+        qn.qlora_head_loss(X, torch.zeros(9, 64, dtype=b), t)
+    with pytest.raises(ValueError, match="compute type"):
+        qn.qlora_head_loss(X.float(), torch.zeros(9, 64), t)
+    assert qn._grad_code(None, b) == (torch.float32, qn.NF4_AB_F32)
+    assert qn._grad_code(b, b) == (b, qn.NF4_AB_BF16)
+    with pytest.raises(ValueError, match="grad_dtype"):
+        qn._grad_code(torch.float16, b)
+
+
+def test_workspaces_over_the_whole_range():
+    """Every size the calls take has a workspace size that is counted in whole,
+    positive 64-bit bytes, also where the split partials are largest."""
+    for M in (1, 16, 17, 64, 256, 257, 700, 4096, 1 << 20):
+        for K in (8, 72, 520, 4096, 1 << 16, 1 << 20):
+            if M * K >= 1 << 29:
+                continue
+            for V in (1, 300, 70000, 1 << 24):
+                for need in (False, True):
+                    n = qn.qlora_head_workspace_bytes(M, K, V, need)
+                    # probabilities, sums of a piece, partials and a few values a row
+                    assert 0 < n < max(256 << 20, M * 512) + M * K * 4 + (256 << 20) + M * 64 + (1 << 20) + M * V // 8 + 256 * M, (M, K, V)
+            for F in (64, 704, 22016, 1 << 20):
+                if K * 2 * F >= 1 << 29 or M * 2 * F >= 1 << 29 or 16 * F >= 1 << 29:
+                    continue
+                fwd, bwd = qn.qlora_gated_workspace_bytes(M, K, F, 8)
+                assert 0 < fwd < 1 << 33 and 0 < bwd < 1 << 34, (M, K, F)
