@@ -97,8 +97,10 @@ __device__ __forceinline__ void transpose8x8_bf16(const uint4 (&in)[8], uint4 (&
 // MFMA as the 16-row operand; lane (q, g) accumulates columns j0 + 8q .. +7.
 // The four waves are added in LDS in a fixed order: (w0 + w2) + (w1 + w3).
 // zpart[split][m][j], fp32.  red: 16 KB of LDS.
+// Inlined by force: as a function it reaches `red` through flat loads, which wait
+// for the stores before them (7 us more a call at 8192 x 22016, 1 to 4 rows).
 template <class T>
-__device__ void gemv_zpart(const uint16_t* __restrict__ X, int64_t M, int64_t row0, int64_t K, int64_t rpw,
+__device__ __forceinline__ void gemv_zpart(const uint16_t* __restrict__ X, int64_t M, int64_t row0, int64_t K, int64_t rpw,
                            const uint16_t* __restrict__ A, int64_t r, float* __restrict__ zpart, int64_t split,
                            float* red) {
   const int t = threadIdx.x, lane = t & 63, q = lane & 15, g = lane >> 4;
