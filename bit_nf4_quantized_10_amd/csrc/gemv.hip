@@ -22,8 +22,8 @@
 // in one launch, its finish forming H = act(G) * U.  Above 16 rows a decoded
 // fragment feeds the MFMAs of two or four 16-row tiles (gemv_rows_kernel): the
 // lookups, not the matrix cores, are what a step costs, so more rows a step are
-// nearly free.  Measured, whole forward, 4096 x 11008: 1 row 33 us, 16 44, 32
-// 46, 64 51, 128 75, 256 132; 8192 x 22016: 69, 86, 111, 143, 231, 393.
+// nearly free.  Measured, whole forward, 4096 x 11008: 1 row 24 us, 16 27, 32
+// 32, 64 44, 128 74, 256 131; 8192 x 22016: 69, 83, 101, 142, 230, 391.
 // Bound by the lookups (LDS reads and byte adds per weight, once per 64 rows):
 // at 16 rows of 8192 x 22016 the codes and scales, 186 MB, arrive at 2.2 TB/s.
 #include "common.hpp"

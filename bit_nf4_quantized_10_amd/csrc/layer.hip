@@ -223,9 +223,10 @@ hipError_t launch_grouped_bwd(int64_t M, int64_t K, int g, const int64_t* Ns, in
 // --------------------------------------------------- gated feed-forward front
 // Up to this many rows the packed weights are decoded inside the product; above,
 // both are dequantized first and one dense GEMM follows.  Whole forward, decoded
-// against dense: 4096 x 11008 at 192 rows 106 and 136 us, at 256 132 and 136 to
-// 140, at 320 144 and 138; 8192 x 22016 at 192 333 and 451, at 256 393 and 428,
-// at 384 640 and 546; 1024 x 2816 at 256 43, dense at 257 47.
+// against dense: 4096 x 11008 at 192 rows 103 and 117 us, at 256 131 and 124;
+// 8192 x 22016 at 192 331 and 431, at 256 391 and 436; 1024 x 2816 at 256 29 and
+// 47; 1000 x 16000 at 192 69 and 66, at 256 81 and 67; 6000 x 2048 at 256 44 and
+// 66; 8192 x 22016 at 384 640 and 546.
 #ifndef QN_GATED_GEMV_M
 #define QN_GATED_GEMV_M 256
 #endif
