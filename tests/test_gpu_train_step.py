@@ -103,3 +103,52 @@ def test_wrappers_refuse_shapes_and_types():
         with pytest.raises(ValueError):
             qn.qlora_head_loss(*args, **kw)
     torch.cuda.synchronize()
+
+
+def test_split_products_captured_and_on_two_streams():
+    """Products whose reductions are split, in two graphs that share no
+    workspace and on two streams at once: the bits of the eager calls."""
+    import torch
+    say("split products, captured")
+    b = torch.bfloat16
+    gen = torch.Generator("cuda").manual_seed(9)
+    n = lambda *s, std=1.0: (torch.randn(*s, generator=gen, device="cuda") * std).to(b)
+    M, K, F, r = 300, 1544, 16704, 8
+    states = [qn.nf4_quantize(torch.randn(K * F, generator=gen, device="cuda") * 0.05)[0] for _ in range(2)]
+    X, A, B, dH = n(M, K), n(K, 2 * r, std=0.1), n(r, 2 * F, std=0.1), n(M, F)
+    Y, W = n(40, 2056), n(700, 2056, std=0.02)
+    t = torch.arange(40, device="cuda") * 17
+    wide = n(30, K)
+
+    def block():
+        H, Z, kept = qn.qlora_gated_fwd(X, states, A, B, 0.5, K, F, save="8")
+        return [H, Z, kept.codes, kept.absmax, *qn.qlora_gated_bwd(dH, X, Z, kept, states, A, B, 0.5, K, F)]
+
+    def loss():
+        few = qn.qlora_gated_fwd(wide, states, A, B, 0.5, K, F)
+        return [*qn.qlora_head_loss(Y, W, t), *few[:2]]
+
+    want = [[host(v).copy() for v in f()] for f in (block, loss)]
+    graphs = []
+    side = torch.cuda.Stream()
+    for f in (block, loss):
+        g = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g):
+            out = f()
+        graphs.append((g, out))
+    for _ in range(3):
+        for v in graphs[0][1] + graphs[1][1]:
+            v.zero_()
+        block()                                     # eager work between the replays
+        torch.cuda.synchronize()
+        graphs[0][0].replay()
+        with torch.cuda.stream(side):
+            graphs[1][0].replay()
+            again = loss()
+        torch.cuda.synchronize()
+        for (_, out), w in zip(graphs, want):
+            for o, v in zip(out, w):
+                np.testing.assert_array_equal(host(o), v)
+        for o, v in zip(again, want[1]):
+            np.testing.assert_array_equal(host(o), v)
