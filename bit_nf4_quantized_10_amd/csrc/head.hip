@@ -90,21 +90,23 @@ __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         v[4 * j + e] = acc[i][j][e];
-        if (ragged && cbase + 16 * j + 4 * k.g + e >= p.nv) v[4 * j + e] = -__builtin_inff();
+        asm("" : "+v"(v[4 * j + e]));   // (values that the branches below change would stay accumulators)
       }
-    if (__any(here)) {
-      const int own = here ? static_cast<int>(d) - 4 * k.g : -1;   // 16 j + e where it is this lane's
+    if (ragged) {
+      const int left = static_cast<int>(p.nv - cbase) - 4 * k.g;
+#pragma unroll
+      for (int x = 0; x < 32; ++x) v[x] = 16 * (x >> 2) + (x & 3) < left ? v[x] : -__builtin_inff();
+    }
+    // column 16 j + 4 g + e of a row is value 4 j + e of its lane g
+    const bool mine = here && ((d >> 2) & 3) == k.g;
+    if (__any(mine)) {
+      const int own = mine ? static_cast<int>((d >> 4) * 4 + (d & 3)) : -1;
       float s = 0.0f;
-      bool mine = false;
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool at = own == 16 * j + e;
-          s = at ? v[4 * j + e] : s;
-          v[4 * j + e] = at ? -__builtin_inff() : v[4 * j + e];
-          mine = mine || at;
-        }
+      for (int x = 0; x < 32; ++x) {
+        s = own == x ? v[x] : s;
+        v[x] = own == x ? -__builtin_inff() : v[x];
+      }
       if (mine) p.st[m] = s;
     }
     float top = v[0];
