@@ -22,9 +22,9 @@
 // so that neither the loss nor the target's part of dX suffers from
 // cancellation where the target is nearly certain.
 // Bound by the matrix cores; with few rows by the read of W.  Measured at 4096
-// rows of 4096 columns and 32000 entries: 1816 us (1.18 PFLOP/s), of it the
-// logits 840 to 906, the gradient product 880 to 940, the rows 90 (the one pass
-// over P: 5 %).
+// rows of 4096 columns and 32000 entries: 1670 us (1.29 PFLOP/s), of it the
+// logits 804 to 870, the gradient product 840 to 925, the rows 12 (90 where the
+// groups' bounds differ and P is rescaled).
 #include <hip/hip_ext.h>
 
 #include "gemm16.hpp"
