@@ -87,12 +87,12 @@ struct Core16 {
   int64_t m0, c0;
   Rsrc r_act, r_w, r_ea, r_eb;
   uint32_t av[8], wv[8];       // copies: row wave*64 + 8j + lane/8, chunk (lane & 7) ^ (lane >> 3)
+                               // (kTurned: wv[i] is row i of this thread's 8 x 8 block)
   int chunk8;                  // 8 * that chunk
   int pA, pW;                  // LDS bytes of fragment 0 at half 0
-  uint32_t w_block;            // kTurned: this thread's 8 x 8 block
-  int wdst;
+  int wdst;                    // kTurned: where the turned block goes
   int64_t s_beg, n_main, n_full, r_ext;
-  uint32_t so;                 // scalar byte offset of the next copies
+  uint32_t so, so_w;           // scalar byte offsets of the next copies and, kTurned, weight loads
 
   __device__ Core16(const G16Args& args, char* s) : a(args), smem(s) {
     t = threadIdx.x;
@@ -105,7 +105,7 @@ struct Core16 {
     tile_origin<kCols>(m0, c0);
     c0 += a.first;
     r_act = make_rsrc(a.act, ((a.M - 1) * a.act_ld + (a.red + 7) / 8 * 8) * 2);   // whole chunks
-    if (kW != kTurned) r_w = make_rsrc(a.w, a.wrows * a.w_ld * 2);   // kTurned: see run()
+    r_w = make_rsrc(a.w, (kW == kTurned ? a.red * a.wrows : a.wrows * a.w_ld) * 2);
     r_ea = make_rsrc(a.ext_a, a.r ? a.M * a.ext_a_ld * 2 : 0);
     r_eb = make_rsrc(a.ext_b, a.wrows * a.r * 2);
     chunk8 = 8 * ((lane & 7) ^ (lane >> 3));
@@ -114,14 +114,16 @@ struct Core16 {
       const int row = wave * 64 + 8 * j + (lane >> 3);
       const int64_t m = m0 + row, n = weight_row(row);
       av[j] = m < a.M ? static_cast<uint32_t>((m * a.act_ld + chunk8) * 2) : kMasked;
-      wv[j] = kW != kTurned && n < a.wrows ? static_cast<uint32_t>((n * a.w_ld + chunk8) * 2) : kMasked;
+      if (kW != kTurned) wv[j] = n < a.wrows ? static_cast<uint32_t>((n * a.w_ld + chunk8) * 2) : kMasked;
     }
     pA = (wm * 128 + q) * 128 + ((g ^ (q & 7)) << 4);
     const int wrow = (kW == kPaired ? wn * 64 : wn * 128) + q;
     pW = kG16W + wrow * 128 + ((g ^ wswz(wrow)) << 4);
     if (kW == kTurned) {
       const int vg = t >> 5, cg = t & 31;
-      w_block = c0 + 8 * cg < a.wrows ? static_cast<uint32_t>((8 * vg * a.wrows + c0 + 8 * cg) * 2) : kMasked;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        wv[i] = c0 + 8 * cg < a.wrows ? static_cast<uint32_t>(((8 * vg + i) * a.wrows + c0 + 8 * cg) * 2) : kMasked;
       wdst = kG16W + 8 * cg * 128 + (((vg ^ cg) & 7) << 4);   // column c: + 128 c, chunk bits ^ c
     }
   }
@@ -145,9 +147,12 @@ struct Core16 {
   }
   // Points the copies at stage u (counted from s_beg; called for every stage in
   // turn).  Past the product's whole stages: the chunks past the reduction's end
-  // are masked, then come the adapter's stages, then nothing.
+  // are masked, then come the adapter's stages, then nothing.  Every mask is in the
+  // lane's own offset and no scalar offset passes its operand's end, since a
+  // buffer's range check need not count the scalar part.
   __device__ __forceinline__ void aim(int64_t u) {
     so = static_cast<uint32_t>((s_beg + u) * (kBK * 2));
+    if (kW == kTurned) so_w = static_cast<uint32_t>(s_beg + u) * static_cast<uint32_t>(a.wrows * (kBK * 2));
     if (u < n_full) return;
     // One assignment per offset, whichever case holds (stores that the compiler
     // merges from two branches would keep the arrays in memory), and descriptors
@@ -157,6 +162,7 @@ struct Core16 {
     const int64_t e = (u - n_main) * kBK + chunk8;
     if (!tail) {
       so = 0;
+      so_w = 0;
       r_act = r_ea;
       if (kW != kTurned) r_w = r_eb;
     }
@@ -166,7 +172,10 @@ struct Core16 {
       const int64_t m = m0 + row;
       const uint32_t ea = m < a.M && e < r_ext ? static_cast<uint32_t>((m * a.ext_a_ld + e) * 2) : kMasked;
       av[j] = tail ? (past ? kMasked : av[j]) : ea;
-      if (kW == kTurned) continue;
+      if (kW == kTurned) {
+        wv[j] = tail && (s_beg + u) * kBK + 8 * (t >> 5) + j < a.red ? wv[j] : kMasked;
+        continue;
+      }
       const int64_t n = weight_row(row);
       int64_t own = e;   // within this row's own r
       if (kW == kPaired) own = (e >= 2 * a.r ? e - 2 * a.r : e) - (row < 128 ? 0 : a.r);
@@ -175,10 +184,9 @@ struct Core16 {
       wv[j] = tail ? (past ? kMasked : wv[j]) : eb;
     }
   }
-  // kTurned: row 8 vg + i of stage u (zeros past this workgroup's rows)
-  __device__ uint4 load_w(int64_t u, int i) const {
-    return ld128s(r_w, w_block, static_cast<uint32_t>(((s_beg + u) * kBK + i) * a.wrows * 2));
-  }
+  // kTurned: row 8 vg + i of the stage aim() was last called for (zeros past this
+  // workgroup's rows)
+  __device__ uint4 load_w(int i) const { return ld128s(r_w, wv[i], so_w); }
   // kTurned: writes column c of the registers' block to weight slot `slot`.  As
   // an instruction: for a plain store the compiler first waits for every copy
   // still in flight, since one could write the same LDS bytes (none does).  The
@@ -287,7 +295,7 @@ struct Core16 {
         }
         __builtin_amdgcn_sched_barrier(0);
       } else if (i < 4 && (j & 1) == 0) {
-        R[4 * (i - 2) + (j >> 1)] = load_w(u + 2, 4 * (i - 2) + (j >> 1));
+        R[4 * (i - 2) + (j >> 1)] = load_w(4 * (i - 2) + (j >> 1));
         __builtin_amdgcn_sched_barrier(0);
       } else if (i >= 4 && (j & 3) == 2) {
         copy_a(sa2, 2 * (i - 4) + (j >> 2));
@@ -331,20 +339,17 @@ struct Core16 {
       sw ^= kTileBytes;
     };
     if constexpr (kW == kTurned) {
-      // rows past this workgroup's share lie past the descriptor's end and read as zeros
-      const int64_t rows = end * kBK < a.red ? end * kBK : a.red;
-      r_w = make_rsrc(a.w, rows * a.wrows * 2);
       uint4 R[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) R[i] = load_w(0, i);
       aim(0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) R[i] = load_w(i);
 #pragma unroll
       for (int j = 0; j < 8; ++j) copy_a(0, j);
 #pragma unroll
       for (int c = 0; c < 8; ++c) store_w(R, 0, c);
       aim(1);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) R[i] = load_w(1, i);   // in the order of the loop's own loads, whose waits the compiler counts
+      for (int i = 0; i < 8; ++i) R[i] = load_w(i);   // in the order of the loop's own loads, whose waits the compiler counts
 #pragma unroll
       for (int j = 0; j < 8; ++j) copy_a(kTileBytes, j);
       __builtin_amdgcn_s_waitcnt(waitcnt_imm(16, 0));   // stage 0; the 16 loads since may be in flight
