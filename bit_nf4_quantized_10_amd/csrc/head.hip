@@ -281,12 +281,14 @@ __global__ __launch_bounds__(256) void head_rows_kernel(RowArgs p) {
         if (p.coef != nullptr) p.coef[m] = make_float2(__builtin_nanf(""), 1.0f);
       } else {
         const float w = p.weights != nullptr ? p.weights[m] : 1.0f;
-        const float u = others - p.st[m];
+        // a target logit of +inf: lse - s_t is inf - inf, a NaN, as any overflow's
+        const float s = p.st[m], inf = __builtin_inff();
+        const float u = s == inf ? __builtin_nanf("") : others - s;
         const float e = expf(-fabsf(u)), l1 = log1pf(e);
         const float up = fmaxf(u, 0.0f) + l1;                 // softplus(u); -inf gives 0
         const float g = (u >= 0.0f ? 1.0f : e) / (1.0f + e);  // sigmoid(u)
         p.loss[m] = w * (u != u ? u : up);
-        p.lse[m] = p.st[m] + (u != u ? u : up);
+        p.lse[m] = fabsf(s) != inf ? s + (u != u ? u : up) : (s < 0.0f || others != others ? others : s);
         if (p.coef != nullptr) p.coef[m] = make_float2(w * (u != u ? u : g), inv);
       }
     }

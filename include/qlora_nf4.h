@@ -342,7 +342,9 @@ int qlora_gated_bwd(int compute_dtype, int act, int grad_dtype, int64_t M, int64
  * NULL) M fp32, dX (NULL: the loss alone) M x K of compute_dtype.  A row whose
  * target is ignore_index has loss 0 and dX 0, whatever it holds; one whose
  * target is neither ignore_index nor in [0, V) has loss and dX NaN; both have
- * their lse.  The vocabulary is processed in pieces whose 16-bit probabilities
+ * their lse.  A NaN or +inf among a counted row's logits makes its loss and dX
+ * NaN (its lse NaN, or +inf where the target's alone is +inf); a target logit of
+ * -inf makes the loss +inf, beside the lse of the others.  The vocabulary is processed in pieces whose 16-bit probabilities
  * take at most 256 MiB of the workspace (or 256 columns of them, if those take
  * more); logits and sums are fp32, loss and gradient come from one pass.
  * Requirements: M >= 1, V >= 1, K % 8 == 0, 8 <= K <= 2^20, M <= 2^20, M * K

@@ -102,17 +102,20 @@ def head_loss(X, W, targets, weights=None, ignore_index: int = -100):
     w = np.where(counted, w, 0.0)
     s = X @ W.T
     top = s.max(axis=1, keepdims=True)
-    e = np.exp(s - top)
-    lse = np.log(e.sum(axis=1)) + top[:, 0]
+    with np.errstate(invalid="ignore"):
+        e = np.exp(s - top)
+    lse = np.where(np.isposinf(top[:, 0]), np.inf, np.log(e.sum(axis=1)) + top[:, 0])
     p = e / e.sum(axis=1, keepdims=True)
     at, row = np.where(counted, t, 0), np.arange(M)
     # lse - s_t = log(1 + sum_{v != t} e^{s_v - s_t}) and p_t - 1 = -sum_{v != t} p_v:
     # the differences themselves cancel to nothing where the target is nearly certain
-    with np.errstate(over="ignore"):
+    with np.errstate(over="ignore", invalid="ignore"):
         d = np.exp(s - s[row, at][:, None])
     d[row, at] = 0.0
-    near = d.sum(axis=1)
-    nll = np.where(near < 1.0, np.log1p(np.minimum(near, 1.0)), lse - s[row, at])
+    # (an infinite s_t: the difference as it stands, NaN for +inf and inf for -inf)
+    near = np.where(np.isinf(s[row, at]), np.inf, d.sum(axis=1))
+    with np.errstate(invalid="ignore"):
+        nll = np.where(near < 1.0, np.log1p(np.minimum(near, 1.0)), lse - s[row, at])
     loss = np.where(counted, w * nll, 0.0)
     p[row, at] = 0.0
     p[row, at] = -p.sum(axis=1)

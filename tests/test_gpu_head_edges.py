@@ -27,3 +27,39 @@ def test_nothing_behind_the_inputs_is_used(M, K, V):
         np.testing.assert_array_equal(host(g), v)
     rows = np.arange(min(M, 60))
     _compare(X, W, t, w, got, "bf16", rows)
+
+
+@pytest.mark.parametrize("name", ["bf16", "f16"])
+@pytest.mark.parametrize("K,V", [(136, 700), (2056, 700)])
+def test_infinite_logits(K, V, name):
+    """One entry of the head is +inf: its logit is +inf or -inf by the sign that a
+    row has there.  Short K whole, long K summed from partials."""
+    say(f"head, infinite logits K={K} {name}")
+    M, v, col = 40, 5, 3
+    X, W, t, _ = _case(M, K, V, name, 21)
+    t[:] = (t.abs() * 7 + 11) % V
+    t[t == v] = v + 1
+    t[0:4] = v
+    sign = np.where(np.arange(M) % 2 == 0, 1.0, -1.0)
+    X[:, col] = X[:, col].abs().clamp(min=0.5)
+    X[1::2, col] *= -1
+    W[v, col] = float("inf")
+    got = [host(g).astype(np.float64) for g in qn.qlora_head_loss(X, W, t)]
+    alone = [host(g).astype(np.float64) for g in qn.qlora_head_loss(X, W, t, need_dx=False)[:2]]
+    x, w64, tt = host(X).astype(np.float64), host(W).astype(np.float64), host(t)
+    s = x @ np.delete(w64, v, axis=0).T
+    top = s.max(axis=1)
+    rest = np.log(np.exp(s - top[:, None]).sum(axis=1)) + top          # without the infinite one
+    target = np.where(tt == v, sign * np.inf, (x * np.where(np.isinf(w64), 0, w64)[tt]).sum(axis=1))
+    up, hit = sign > 0, tt == v
+    tol = (K + 40) * 2.0 ** -24 * (np.abs(x) @ np.abs(np.delete(w64, v, axis=0)).T).max(axis=1) + 1e-5
+    for loss, lse in (got[:2], alone):
+        assert np.isnan(loss[up]).all() and not np.isfinite(lse[up]).any()
+        assert np.isposinf(lse[up & hit]).all()
+        assert np.isposinf(loss[~up & hit]).all()
+        assert (np.abs(lse - rest)[~up] <= tol[~up]).all()
+        fine = ~up & ~hit
+        assert (np.abs(loss[fine] - (rest - target)[fine]) <= 2 * tol[fine]).all()
+    assert np.isnan(got[2][up]).all()
+    others = np.delete(got[2], col, axis=1)
+    assert np.isfinite(others[~up]).all()

@@ -1,0 +1,16 @@
+"""References of the operators around the NF4 layer at infinite values, and
+refusals and workspace sizes at the ends of their ranges.  No GPU work is issued."""
+import numpy as np
+
+from oracle import ops_oracle as oo
+
+
+def test_head_reference_with_infinite_logits():
+    X = np.array([[1.0, 2.0], [-1.0, 2.0], [1.0, 0.5], [-1.0, 1.0]])
+    W = np.array([[np.inf, 0.0], [1.0, 1.0], [0.0, -1.0]])
+    # logits: row 0 (inf, 3, -2), row 1 (-inf, 1, -2), row 2 (inf, 1.5, -0.5), row 3 (-inf, 0, -1)
+    with np.errstate(invalid="ignore"):
+        loss, lse, dX = oo.head_loss(X, W, np.array([0, 0, 1, 1]))
+    assert np.isnan(loss[0]) and np.isposinf(lse[0]) and np.isposinf(loss[1]) and np.isposinf(loss[2])
+    np.testing.assert_allclose(lse[[1, 3]], [1 + np.log1p(np.exp(-3.0)), np.log1p(np.exp(-1.0))], rtol=1e-12)
+    np.testing.assert_allclose(loss[3], np.log1p(np.exp(-1.0)), rtol=1e-12)
