@@ -23,7 +23,8 @@ __device__ __forceinline__ float sigmoid_of(float y) {
 // Both activations are g sigmoid(y): silu with y = g, gelu (its tanh form
 // 0.5 g (1 + tanh(y / 2))) with y = 2 sqrt(2 / pi) (g + 0.044715 g^3).
 // The derivative is s + g s (1 - s) y'.  Past |g| = 1000 the sigmoid is 0 or 1
-// in fp32, so g is clamped there before the cube: no infinity meets a zero.
+// in fp32, so g is clamped there before the cube, and -inf (what fp16 keeps of a
+// G below -65504) is taken as the lowest finite number: no infinity meets a zero.
 constexpr float kGelu0 = 1.5957691216f, kGelu1 = 0.044715f;
 __device__ __forceinline__ float clamp_g(float g) {
   return __builtin_fabsf(g) > 1000.0f ? __builtin_copysignf(1000.0f, g) : g;   // a NaN stays one
@@ -32,9 +33,10 @@ __device__ __forceinline__ float gelu_y(float g) {
   const float x = clamp_g(g);
   return kGelu0 * x * __builtin_fmaf(kGelu1 * x, x, 1.0f);
 }
+__device__ __forceinline__ float above_inf(float g) { return g == -__builtin_inff() ? -3.40282347e38f : g; }
 template <bool kGelu>
 __device__ __forceinline__ float act_of(float g) {
-  return g * sigmoid_of(kGelu ? gelu_y(g) : g);
+  return above_inf(g) * sigmoid_of(kGelu ? gelu_y(g) : g);
 }
 // f = act(g), df = act'(g)
 template <bool kGelu>
@@ -42,7 +44,7 @@ __device__ __forceinline__ void act_grad_of(float g, float& f, float& df) {
   const float s = sigmoid_of(kGelu ? gelu_y(g) : g);
   const float x = clamp_g(g);
   const float dy = kGelu ? kGelu0 * __builtin_fmaf(3.0f * kGelu1 * x, x, 1.0f) : 1.0f;
-  f = g * s;
+  f = above_inf(g) * s;
   df = __builtin_fmaf(x * s * (1.0f - s), dy, s);
 }
 

@@ -305,7 +305,10 @@ int qlora_linear_bwd_ex(int compute_dtype, int grad_dtype, int64_t M, int64_t K,
  * side by side ([G | U], M x 2F): rounded to 16 bits in GU, or that rounding
  * as an 8-bit checkpoint in GU8 (act8_t with cols = 2F: the bits act8_encode
  * makes of GU).  At most one of the two is given; with neither, nothing is
- * kept.  Requirements: F % 64 == 0, K % 8 == 0, r % 8 == 0, r <= 128, and
+ * kept.  A G or U past the 16-bit type's range (fp16: 65504) is kept as an
+ * infinity: for G = -inf the backward has act = act' = 0, as for the value
+ * itself; G = +inf or an infinite U make dU or dG infinite or NaN; in 8 bits the
+ * block of 64 columns is kept as NaN.  Requirements: F % 64 == 0, K % 8 == 0, r % 8 == 0, r <= 128, and
  * qlora_linear_fwd's on (M, K, 2F, 2r); all pointers 16-byte aligned
  * (GU8->absmax 2-byte); workspace 256-byte aligned, at least fwd_bytes.  M <= 256
  * decodes the packed weights inside the product (each code read once per 64
