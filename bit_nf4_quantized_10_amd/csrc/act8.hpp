@@ -83,7 +83,8 @@ template <class T>
 __device__ __forceinline__ float act8_step(uint32_t kept) {
   return __fdiv_rn(T::widen(kept), 127.0f);
 }
-// Four codes (one per byte) -> four 16-bit values.
+// Four codes (one per byte) -> four 16-bit values.  (In fp16 the product may be
+// rounded once, in its conversion, or twice: no code and magnitude tell them apart.)
 template <class T>
 __device__ __forceinline__ uint2 act8_values4(uint32_t q, float step) {
   float v[4];

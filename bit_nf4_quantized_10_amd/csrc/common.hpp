@@ -113,6 +113,10 @@ typedef __attribute__((address_space(3))) void* lds_ptr_t;
 // where BF16 is not wanted).  Each tag gives the MFMA operand vector, the
 // 16x16x32 and 32x32x16 MFMAs with fp32 accumulation, the fp32 -> 16-bit
 // round-to-nearest-even packing of two values, and the widening to fp32.
+// settle(x) is x, kept as the fp32 number that it was rounded to: the compiler
+// otherwise folds a product into its conversion to fp16 (v_fma_mixlo_f16), which
+// rounds once, where a value defined as RNE_16(fl32(a b)) rounds twice - one fp16
+// step apart in about one NF4 weight of 13000 (21 of 267264 normal ones).
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 
@@ -120,6 +124,7 @@ struct Bf16 {
   typedef bf16x8 v8;
   static constexpr int kDtype = 0;
   __device__ static __forceinline__ uint32_t pack2(float lo, float hi) { return pack_bf16x2(lo, hi); }
+  __device__ static __forceinline__ float settle(float x) { return x; }
   __device__ static __forceinline__ float widen(uint32_t bits16) { return bf16_bits_to_f32(bits16); }
   __device__ static __forceinline__ f32x4 mfma16(const v8& a, const v8& b, const f32x4& c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
@@ -135,6 +140,10 @@ struct F16 {
   __device__ static __forceinline__ uint32_t pack2(float lo, float hi) {
     f16x2 v = {static_cast<_Float16>(lo), static_cast<_Float16>(hi)};
     return __builtin_bit_cast(uint32_t, v);
+  }
+  __device__ static __forceinline__ float settle(float x) {
+    asm("" : "+v"(x));
+    return x;
   }
   __device__ static __forceinline__ float widen(uint32_t bits16) {
     return static_cast<float>(__builtin_bit_cast(_Float16, static_cast<uint16_t>(bits16)));
@@ -153,7 +162,7 @@ template <class T = Bf16>
 __device__ __forceinline__ void write_block_table(uint16_t* tab, float ahat) {
   uint32_t w[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) w[j] = T::pack2(__fmul_rn(kNF4[2 * j], ahat), __fmul_rn(kNF4[2 * j + 1], ahat));
+  for (int j = 0; j < 8; ++j) w[j] = T::pack2(T::settle(__fmul_rn(kNF4[2 * j], ahat)), T::settle(__fmul_rn(kNF4[2 * j + 1], ahat)));
   reinterpret_cast<uint4*>(tab)[0] = make_uint4(w[0], w[1], w[2], w[3]);
   reinterpret_cast<uint4*>(tab)[1] = make_uint4(w[4], w[5], w[6], w[7]);
 }

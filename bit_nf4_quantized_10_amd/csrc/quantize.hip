@@ -383,10 +383,10 @@ template <class O>
 __device__ __forceinline__ void dq_store(void* out, int64_t e0, const float v[8]) {
   if constexpr (!std::is_same<O, float>::value) {
     uint4 pk;
-    pk.x = O::pack2(v[0], v[1]);
-    pk.y = O::pack2(v[2], v[3]);
-    pk.z = O::pack2(v[4], v[5]);
-    pk.w = O::pack2(v[6], v[7]);
+    pk.x = O::pack2(O::settle(v[0]), O::settle(v[1]));
+    pk.y = O::pack2(O::settle(v[2]), O::settle(v[3]));
+    pk.z = O::pack2(O::settle(v[4]), O::settle(v[5]));
+    pk.w = O::pack2(O::settle(v[6]), O::settle(v[7]));
     *reinterpret_cast<uint4*>(static_cast<uint16_t*>(out) + e0) = pk;
   } else {
     float* o = static_cast<float*>(out) + e0;
@@ -460,7 +460,7 @@ __global__ __launch_bounds__(kQuantThreads) void nf4_dequant_kernel(NF4View W, i
     for (int i = 0; i < 8; ++i) {
       const int64_t e = words * 8 + i;
       if (e >= P) break;
-      if constexpr (!std::is_same<O, float>::value) static_cast<uint16_t*>(out)[e] = static_cast<uint16_t>(O::pack2(v[i], 0.0f) & 0xffffu);
+      if constexpr (!std::is_same<O, float>::value) static_cast<uint16_t*>(out)[e] = static_cast<uint16_t>(O::pack2(O::settle(v[i]), 0.0f) & 0xffffu);
       else static_cast<float*>(out)[e] = v[i];
     }
   }
@@ -526,7 +526,7 @@ __global__ __launch_bounds__(256) void nf4_dequant_t_kernel(NF4View W, int64_t K
       float v[8];
       decode8(w[c], ahat, s_lut, v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) tile[(32 * part + 8 * c + e) * kTPad + kk] = static_cast<uint16_t>(T::pack2(v[e], 0.0f));
+      for (int e = 0; e < 8; ++e) tile[(32 * part + 8 * c + e) * kTPad + kk] = static_cast<uint16_t>(T::pack2(T::settle(v[e]), 0.0f));
     }
   }
   __syncthreads();

@@ -106,7 +106,7 @@ __device__ __forceinline__ void reduce_block(const RdJob& J, int64_t blk) {
       for (int u = 0; u < 8; ++u) s += v[u];
     }
     for (; k < J.splits; ++k) s += J.part[k * count + i];
-    s *= J.scale;
+    s = F16::settle(s * J.scale);   // every output is a rounding of this fp32 number
     const int64_t o = J.transpose ? (i % J.cols) * J.out_ld + i / J.cols : (i / J.cols) * J.out_ld + i % J.cols;
     if (J.out_f32) J.out_f32[o] = s;
     if (J.out_bf16) J.out_bf16[o] = half_of(s, J.f16);

@@ -14,3 +14,14 @@ def test_head_reference_with_infinite_logits():
     assert np.isnan(loss[0]) and np.isposinf(lse[0]) and np.isposinf(loss[1]) and np.isposinf(loss[2])
     np.testing.assert_allclose(lse[[1, 3]], [1 + np.log1p(np.exp(-3.0)), np.log1p(np.exp(-1.0))], rtol=1e-12)
     np.testing.assert_allclose(loss[3], np.log1p(np.exp(-1.0)), rtol=1e-12)
+
+
+def test_fp16_checkpoints_round_alike_once_and_twice():
+    """RNE_16(fl32(q step)) = RNE_16(q step) for every fp16 magnitude and code, so a
+    kernel may convert the product directly."""
+    a = np.arange(1, 0x7C00, dtype=np.uint16).view(np.float16).astype(np.float32)
+    step = (a / np.float32(127)).astype(np.float64)
+    for q in range(1, 128):
+        p = q * step          # exact: 7 and 24 bits
+        with np.errstate(over="ignore"):
+            np.testing.assert_array_equal(p.astype(np.float32).astype(np.float16), p.astype(np.float16))
