@@ -408,7 +408,11 @@ __device__ __forceinline__ void fin_add8(float (&s)[8], const uint4 (&a)[8], con
 // kTwo (the gated block; N = F columns per weight, r per member, Z M x 2r): a
 // workgroup owns 256 columns, waves 0 and 1 of G, waves 2 and 3 of U; the U
 // waves hand their values over in LDS and the G waves store Y = act(G) * U and
-// what is kept of G and U.
+// what is kept of G and U.  There Z enters the product in two 16-bit parts, its
+// rounding (which is the Z written out) and the rounded rest, within 2^-16 of it
+// together: G and U then carry none of Z's rounding, which would move many of their
+// 8-bit codes, as above 256 rows.  (One more MFMA a fragment: 0.1 to 0.3 us of the
+// 26 of a call at 16 rows, 4096 x 11008, and as much of the 62 at 8192 x 22016.)
 template <class T, bool kTwo, bool kGelu>
 __global__ __launch_bounds__(256) void gemv_finish_kernel(const float* __restrict__ part, int splits, int64_t M,
                                                           int64_t N, const float* __restrict__ zpart,
@@ -416,6 +420,7 @@ __global__ __launch_bounds__(256) void gemv_finish_kernel(const float* __restric
                                                           int64_t r, float c, uint16_t* __restrict__ Y,
                                                           GatedKeep keep) {
   __shared__ __attribute__((aligned(16))) uint16_t zl[16 * 256];   // Z of 16 rows, 16 x rt (rt <= 256)
+  __shared__ __attribute__((aligned(16))) uint16_t zr[kTwo ? 16 * 256 : 8];   // kTwo: the rest of its rounding
   const int t = threadIdx.x, lane = t & 63, q = lane & 15, g = lane >> 4, wave = t >> 6;
   // kTwo: row tile of 16 rows (blockIdx.y / 4) and its row phase
   const int e = kTwo ? blockIdx.y & 3 : blockIdx.y;
@@ -459,6 +464,16 @@ __global__ __launch_bounds__(256) void gemv_finish_kernel(const float* __restric
     if (idx >= MR) return;
     const uint2 zv = make_uint2(T::pack2(zs[0], zs[1]), T::pack2(zs[2], zs[3]));
     *reinterpret_cast<uint2*>(zl + idx) = zv;
+    if constexpr (kTwo) {
+      const uint32_t hi[4] = {zv.x & 0xffffu, zv.x >> 16, zv.y & 0xffffu, zv.y >> 16};
+      float rest[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float d = zs[k] - T::widen(hi[k]);
+        rest[k] = __builtin_fabsf(d) < __builtin_inff() ? d : 0.0f;   // an infinite rounding has no rest
+      }
+      *reinterpret_cast<uint2*>(zr + idx) = make_uint2(T::pack2(rest[0], rest[1]), T::pack2(rest[2], rest[3]));
+    }
     if (blockIdx.x == 0 && e == 0) *reinterpret_cast<uint2*>(Z + zrow + idx) = zv;
   };
   uint4 pa[8], pb[8], b0[8], b1[8], za[8];
@@ -489,12 +504,20 @@ __global__ __launch_bounds__(256) void gemv_finish_kernel(const float* __restric
   for (int i = 0; i < 8; ++i) accl[i] = f32x4{0, 0, 0, 0};
   auto lora_step = [&](int64_t j0, const uint4 (&rows8)[8]) {
     const int64_t jb = j0 + 8 * g;
-    const uint4 zv = (q < Mt && jb < r) ? *reinterpret_cast<const uint4*>(zl + q * rt + member * r + jb) : make_uint4(0, 0, 0, 0);
+    const int64_t zat = q * rt + member * r + jb;
+    const bool z_ok = q < Mt && jb < r;
+    const uint4 zv = z_ok ? *reinterpret_cast<const uint4*>(zl + zat) : make_uint4(0, 0, 0, 0);
     uint4 cols8[8];
     transpose8x8_bf16(rows8, cols8);
 #pragma unroll
     for (int tc = 0; tc < 8; ++tc)
       accl[tc] = T::mfma16(__builtin_bit_cast(typename T::v8, zv), __builtin_bit_cast(typename T::v8, cols8[tc]), accl[tc]);
+    if constexpr (kTwo) {
+      const uint4 zd = z_ok ? *reinterpret_cast<const uint4*>(zr + zat) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int tc = 0; tc < 8; ++tc)
+        accl[tc] = T::mfma16(__builtin_bit_cast(typename T::v8, zd), __builtin_bit_cast(typename T::v8, cols8[tc]), accl[tc]);
+    }
   };
   lora_step(0, b0);
   if (r > 32) lora_step(32, b1);
