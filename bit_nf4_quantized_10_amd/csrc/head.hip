@@ -410,13 +410,16 @@ struct HeadPlan {
   int64_t total() const { return p_bytes + stats_bytes + 6 * row_bytes + sum_bytes + part_bytes; }
 };
 
-// A piece keeps its probabilities within kPieceBytes and its rows of W within
-// 2^29 elements (32-bit offsets).  Few tiles' reductions are split: the logits'
-// over K, dX's over the piece's rows.
+// A piece keeps its probabilities within kPieceBytes, its bounds and sums within
+// kStatsBytes (which without dX is what M limits a piece by) and its rows of W
+// within 2^29 elements (32-bit offsets).  Few tiles' reductions are split: the
+// logits' over K, dX's over the piece's rows.
+constexpr int64_t kStatsBytes = int64_t(64) << 20;
 HeadPlan head_plan(int64_t M, int64_t K, int64_t V, bool need_dx) {
   HeadPlan h{};
   int64_t most = (int64_t(1) << 29) / K;
   if (need_dx && kPieceBytes / 2 / M < most) most = kPieceBytes / 2 / M;
+  if (kStatsBytes / 8 / M * 128 < most) most = kStatsBytes / 8 / M * 128;
   most = most / 256 * 256;
   if (most < 256) most = 256;
   h.pieces = (V + most - 1) / most;

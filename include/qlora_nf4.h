@@ -348,8 +348,8 @@ int qlora_gated_bwd(int compute_dtype, int act, int grad_dtype, int64_t M, int64
  * their lse.  A NaN or +inf among a counted row's logits makes its loss and dX
  * NaN (its lse NaN, or +inf where the target's alone is +inf); a target logit of
  * -inf makes the loss +inf, beside the lse of the others.  The vocabulary is processed in pieces whose 16-bit probabilities
- * take at most 256 MiB of the workspace (or 256 columns of them, if those take
- * more); logits and sums are fp32, loss and gradient come from one pass.
+ * take at most 256 MiB of the workspace and whose bounds and sums (a pair per row
+ * and 128 columns) 64 MiB (or 256 columns of either, if those take more); logits and sums are fp32, loss and gradient come from one pass.
  * Requirements: M >= 1, V >= 1, K % 8 == 0, 8 <= K <= 2^20, M <= 2^20, M * K
  * below 2^29, V <= 2^24; X, W, dX 16-byte, targets 8-byte, the fp32 buffers
  * 4-byte aligned; workspace 256-byte aligned and at least *bytes (need_dx:

@@ -63,3 +63,16 @@ def test_infinite_logits(K, V, name):
     assert np.isnan(got[2][up]).all()
     others = np.delete(got[2], col, axis=1)
     assert np.isfinite(others[~up]).all()
+
+
+@pytest.mark.parametrize("M,K,V,name", [(40000, 16, 40007, "bf16"), (5003, 72, 300001, "f16")])
+def test_loss_alone_in_pieces(M, K, V, name):
+    """Many tokens: the bounds and sums of a piece end at 64 MiB, here two of them."""
+    import torch
+    say(f"head, loss alone in pieces M={M} V={V} {name}")
+    X, W, t, w = _case(M, K, V, name, 12, lean=8.0)
+    edge = np.concatenate((np.arange(0, V, V // 40), [V - 1]))
+    t[:len(edge)] = torch.from_numpy(edge).cuda()
+    got = qn.qlora_head_loss(X, W, t, weights=w, need_dx=False)
+    _compare(X, W, t, w, got, name, np.arange(len(edge) + 20))
+    _compare(X, W, t, w, got, name, np.arange(M - 40, M))

@@ -2,6 +2,7 @@
 refusals and workspace sizes at the ends of their ranges.  No GPU work is issued."""
 import numpy as np
 
+import bit_nf4_quantized_10_amd as qn
 from oracle import ops_oracle as oo
 
 
@@ -25,3 +26,16 @@ def test_fp16_checkpoints_round_alike_once_and_twice():
         p = q * step          # exact: 7 and 24 bits
         with np.errstate(over="ignore"):
             np.testing.assert_array_equal(p.astype(np.float32).astype(np.float16), p.astype(np.float16))
+
+
+def test_head_workspace_of_the_loss_alone():
+    """Without the gradient nothing of size M x V is kept: bounds and sums of a piece
+    (64 MiB, or a pair for each row and 128 of 256 columns), partials, a few values a row."""
+    for M in (1, 333, 4096, 5003, 131072, 1 << 20):
+        for K in (8, 256, 4096):
+            if M * K >= 1 << 29:
+                continue
+            for V in (1, 50257, 128256, 1 << 24):
+                n = qn.qlora_head_workspace_bytes(M, K, V, need_dx=False)
+                assert n <= max(64 << 20, M * 16) + (256 << 20) + 64 * M + 4096, (M, K, V, n)
+                assert n <= qn.qlora_head_workspace_bytes(M, K, V), (M, K, V)
