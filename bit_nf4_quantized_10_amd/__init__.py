@@ -546,6 +546,12 @@ def qlora_linear_bwd(G, X, Z, state: NF4State, A, B, c: float, K: int, N: int, n
     for t, n in ((G, "G"), (X, "X"), (Z, "Z"), (A, "A"), (B, "B")):
         if t is not None or n != "Z":
             _require_cuda(t, n, dt)
+    for t, n, odt, count in ((dX if need_dx else None, "dX", dt, M * K), (dA, "dA", torch.float32, K * r),
+                             (dB, "dB", torch.float32, r * N)):
+        if t is not None:
+            _require_cuda(t, n, odt)
+            if t.numel() < count:
+                raise ValueError(f"{n} must hold {count} elements, got {t.numel()}")
     if need_dx and dX is None:
         dX = torch.empty(M, K, dtype=dt, device=X.device)
     if dA is None:

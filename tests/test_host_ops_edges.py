@@ -1,6 +1,7 @@
 """References of the operators around the NF4 layer at infinite values, and
 refusals and workspace sizes at the ends of their ranges.  No GPU work is issued."""
 import numpy as np
+import pytest
 
 import bit_nf4_quantized_10_amd as qn
 from oracle import ops_oracle as oo
@@ -39,3 +40,26 @@ def test_head_workspace_of_the_loss_alone():
                 n = qn.qlora_head_workspace_bytes(M, K, V, need_dx=False)
                 assert n <= max(64 << 20, M * 16) + (256 << 20) + 64 * M + 4096, (M, K, V, n)
                 assert n <= qn.qlora_head_workspace_bytes(M, K, V), (M, K, V)
+
+
+def _host_tensors_pass(monkeypatch):
+    """The wrappers' other checks on host tensors: no launch is reached."""
+    def check(t, name, dtype=None):
+        if not t.is_contiguous() or (dtype is not None and t.dtype != dtype):
+            raise ValueError(name)
+    monkeypatch.setattr(qn, "_require_cuda", check)
+
+
+def test_linear_backward_refuses_gradients_of_another_type_or_size(monkeypatch):
+    """dA and dB are fp32 unless grad_dtype says otherwise: a 16-bit tensor would be
+    written past its end."""
+    torch = pytest.importorskip("torch")
+    _host_tensors_pass(monkeypatch)
+    b, M, K, N, r = torch.bfloat16, 4, 64, 128, 8
+    z = lambda *s, t=b: torch.zeros(*s, dtype=t)
+    state = qn.NF4State(K * N, *[torch.zeros(1)] * 4)
+    f = torch.float32
+    for kw in ({"dA": z(K, r)}, {"dB": z(r, N)}, {"dA": z(K, r - 1, t=f)}, {"dB": z(r, N // 2, t=f)}, {"dX": z(M, K, t=f)},
+               {"dX": z(M - 1, K)}, {"dA": z(K, r), "grad_dtype": f}, {"dA": z(2 * K, r, t=f)[::2]}):
+        with pytest.raises(ValueError, match="dA|dB|dX"):
+            qn.qlora_linear_bwd(z(M, N), z(M, K), z(M, r), state, z(K, r), z(r, N), 1.0, K, N, **kw)
