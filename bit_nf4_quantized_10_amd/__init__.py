@@ -284,6 +284,22 @@ class NF4State:
         return _State(self.numel, self.codes.data_ptr(), _ptr(self.qabsmax), _ptr(self.absmax2),
                       _ptr(self.offset), _ptr(self.absmax))
 
+    def check(self, name: str, device) -> None:
+        """Raises where a tensor is not what numel weights need, on `device`."""
+        n1 = (self.numel + 63) // 64
+        _require_part(self.codes, name, "codes", "torch.uint8", (self.numel + 1) // 2, device)
+        if self.absmax is None:
+            _require_part(self.qabsmax, name, "qabsmax", "torch.int8", n1, device)
+            _require_part(self.absmax2, name, "absmax2", "torch.float32", (n1 + 255) // 256, device)
+            _require_part(self.offset, name, "offset", "torch.float32", 1, device)
+        else:
+            _require_part(self.absmax, name, "absmax", "torch.float32", n1, device)
+
+
+def _require_part(t, name: str, part: str, dtype: str, count: int, device) -> None:
+    if t is None or t.device != device or str(t.dtype) != dtype or t.numel() < count or not t.is_contiguous():
+        raise ValueError(f"{name}.{part} must be {count} contiguous {dtype} on {device}")
+
 
 def nf4_sizes(numel: int) -> dict:
     out = [ctypes.c_int64() for _ in range(4)]
@@ -591,7 +607,11 @@ def _out(t, name: str, dtype, device, *shape):
 
 def _workspace(workspace, need: int, device):
     import torch
-    return torch.empty(max(need, 256), dtype=torch.uint8, device=device) if workspace is None else workspace
+    if workspace is None:
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=device)
+    if workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous uint8")
+    return workspace
 
 
 def _kept_or_dense(X, M: int, K: int, name: str):
@@ -621,7 +641,8 @@ def _linear_bwd_ex(G, X, Z, state, A, B, c, K, N, need_dx, dX, dA, dB, workspace
         raise ValueError("Z is required where X is kept in 8 bits")
     xp, x8 = _kept_or_dense(X, M, K, "X")
     gdt, gcode = _grad_code(grad_dtype, dt)
-    with _on(G, stream, X, Z, A, B, state.codes, dX, dA, dB, workspace) as s:
+    state.check("state", G.device)
+    with _on(G, stream, X, Z, A, B, dX, dA, dB, workspace) as s:
         dX = _out(dX, "dX", dt, G.device, M, K) if need_dx else None
         dA = _out(dA, "dA", gdt, G.device, K, r)
         dB = _out(dB, "dB", gdt, G.device, r, N)
@@ -659,6 +680,8 @@ def _gated_args(X, states, A, B, K: int, F: int, act: str):
     _require_cuda(B, "B", dt)
     _require_shape(A, "A", K, r2)
     _require_shape(B, "B", r2 // 2, 2 * F)
+    for i, state in enumerate(states):
+        state.check(f"states[{i}]", A.device)
     return M, r2 // 2, dt, (_State * 2)(*[s.c_struct() for s in states]), _ACTS[act]
 
 
@@ -687,7 +710,7 @@ def qlora_gated_fwd(X, states, A, B, c: float, K: int, F: int, act: str = "silu"
     _require_cuda(X, "X", dt)
     _require_shape(X, "X", M, K)
     import torch
-    with _on(X, stream, A, B, states[0].codes, states[1].codes, H, Z, saved, workspace) as s:
+    with _on(X, stream, A, B, H, Z, saved, workspace) as s:
         H = _out(H, "H", dt, X.device, M, F)
         if Z is not None or return_z:
             Z = _out(Z, "Z", dt, X.device, M, 2 * r)
@@ -720,7 +743,7 @@ def qlora_gated_bwd(dH, X, Z, saved, states, A, B, c: float, K: int, F: int, act
     xp, x8 = _kept_or_dense(X, M, K, "X")
     gu, gu8 = _gated_kept(saved, M, F, dt)
     gdt, gcode = _grad_code(grad_dtype, dt)
-    with _on(dH, stream, X, Z, saved, A, B, states[0].codes, states[1].codes, dX, dA, dB, workspace) as s:
+    with _on(dH, stream, X, Z, saved, A, B, dX, dA, dB, workspace) as s:
         dX = _out(dX, "dX", dt, dH.device, M, K) if need_dx else None
         dA = _out(dA, "dA", gdt, dH.device, K, 2 * r)
         dB = _out(dB, "dB", gdt, dH.device, r, 2 * F)

@@ -63,3 +63,43 @@ def test_linear_backward_refuses_gradients_of_another_type_or_size(monkeypatch):
                {"dX": z(M - 1, K)}, {"dA": z(K, r), "grad_dtype": f}, {"dA": z(2 * K, r, t=f)[::2]}):
         with pytest.raises(ValueError, match="dA|dB|dX"):
             qn.qlora_linear_bwd(z(M, N), z(M, K), z(M, r), state, z(K, r), z(r, N), 1.0, K, N, **kw)
+
+
+def _state(torch, K, N, single=False, **change):
+    P = K * N
+    n1, n2 = P // 64, (P // 64 + 255) // 256
+    z = torch.zeros
+    parts = {"codes": z(P // 2, dtype=torch.uint8), "qabsmax": z(n1, dtype=torch.int8), "absmax2": z(n2),
+             "offset": z(1), "absmax": None}
+    if single:
+        parts |= {"qabsmax": None, "absmax2": None, "offset": None, "absmax": z(n1)}
+    return qn.NF4State(P, **(parts | change))
+
+
+def test_calls_refuse_states_that_are_not_their_weights(monkeypatch):
+    """A tensor of a state that is too short, of another type, strided, missing or on
+    another device would be read past its end."""
+    torch = pytest.importorskip("torch")
+    _host_tensors_pass(monkeypatch)
+    b, M, K, F, r = torch.bfloat16, 4, 192, 128, 8
+    z = lambda *s, t=b: torch.zeros(*s, dtype=t)
+    X, A, B, dH, Z = z(M, K), z(K, 2 * r), z(r, 2 * F), z(M, F), z(M, 2 * r)
+    good = _state(torch, K, F)
+    n1 = K * F // 64
+    assert good.check("x", X.device) is None and _state(torch, K, F, single=True).check("x", X.device) is None
+    bad = [{"codes": z(K * F // 2 - 1, t=torch.uint8)}, {"codes": z(K * F // 2, t=torch.int8)}, {"qabsmax": None},
+           {"qabsmax": z(n1 - 1, t=torch.int8)}, {"qabsmax": z(n1)}, {"absmax2": z(1)}, {"absmax2": z(4, t=torch.float32)[::2]},
+           {"offset": z(0, t=torch.float32)}, {"offset": None}, {"absmax": z(n1 - 1, t=torch.float32)}, {"absmax": z(n1)},
+           {"offset": torch.empty(1, device="meta")}]
+    for change in bad:
+        wrong = _state(torch, K, F, **change)
+        for states in ([wrong, good], [good, wrong]):
+            with pytest.raises(ValueError, match=r"states\[[01]\]"):
+                qn.qlora_gated_fwd(X, states, A, B, 1.0, K, F)
+            with pytest.raises(ValueError, match=r"states\[[01]\]"):
+                qn.qlora_gated_bwd(dH, X, Z, None, states, A, B, 1.0, K, F)
+        with pytest.raises(ValueError, match="state"):
+            qn.qlora_linear_bwd(z(M, F), X, z(M, r), wrong, z(K, r), z(r, F), 1.0, K, F, grad_dtype=b)
+    for ws in (z(1 << 20), z(1 << 20, t=torch.uint8)[::2], z(1, t=torch.uint8).expand(1 << 20)):
+        with pytest.raises(ValueError, match="workspace"):
+            qn._workspace(ws, 256, X.device)
