@@ -31,8 +31,8 @@
 // chunks are masked, so tails add exact zeros.
 //
 // qlora_dense_kernel (M >= 192) reads a weight dequantized beforehand to bf16
-// (bit-identical to the fused decode) and streams both operands through two
-// LDS slots of 64-element stages, whole cache lines per copy (see Dense).
+// (bit-identical to the fused decode) and streams 64-element stages through three
+// LDS slots of activations and two of weights, whole cache lines per copy (see Dense).
 //
 // Every global load is a raw buffer load, so masked lanes need no branches:
 // a lane whose row, column or reduction index lies outside its operand

@@ -20,12 +20,17 @@
 //
 // The gated block's forward for up to 256 rows is the same walk over two weights
 // in one launch, its finish forming H = act(G) * U.  Above 16 rows a decoded
-// fragment feeds the MFMAs of two or four 16-row tiles (gemv_rows_kernel): the
-// lookups, not the matrix cores, are what a step costs, so more rows a step are
-// nearly free.  Measured, whole forward, 4096 x 11008: 1 row 24 us, 16 27, 32
+// fragment feeds the MFMAs of two or four 16-row tiles (gemv_rows_kernel): a step's
+// decode is then shared, and the matrix cores have room (4 to 13 % busy).
+// Measured, whole forward, 4096 x 11008: 1 row 24 us, 16 27, 32
 // 32, 64 44, 128 74, 256 131; 8192 x 22016: 69, 83, 101, 142, 230, 391.
-// Bound by the lookups (LDS reads and byte adds per weight, once per 64 rows):
-// at 16 rows of 8192 x 22016 the codes and scales, 186 MB, arrive at 2.2 TB/s.
+// No unit is saturated.  One row of 8192 x 22016 (62 us; the codes and scales, 186
+// MB, read once at 3.0 TB/s): the waves issue 39 % of their time, wait for loads 25 %
+// and hold a ready instruction 37 %, of it 22 % an LDS one; VALU 42 % busy, LDS 21 %
+// and 12 % more in bank conflicts.  16 rows of 4096 x 11008, eight steps a wave: the
+// CUs hold waves for 59 % of the launch, start and end being the rest, VALU 27 %.
+// 100 rows of it: 72 %, 42 % of the waves' time waiting for loads (344 of 512
+// workgroups that fit, each weight decoded once per 64 rows).
 #include "common.hpp"
 #include "gated.hpp"
 #include "kernels.hpp"

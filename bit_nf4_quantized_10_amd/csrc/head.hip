@@ -9,10 +9,13 @@
 //      bound of their own row and 128 columns, P = 2^(s log2 e - ref), ref = 0 or
 //      the ceil of the largest (head_ref): P (16 bits, one rounding), ref and the
 //      sum of the unrounded P go to memory.  The target's own column is left out of all
-//      three; its logit is kept in fp32.
+//      three; its logit is kept in fp32.  (P is an operand of the next product's
+//      MFMAs, hence 16 bits; each term of dX carries that one rounding, the loss
+//      and lse none.)
 //   2. head_rows_kernel: per row the running bound and sum over the pieces, and
 //      P times 2^(ref - bound) where they differ: a power of two, so no second
-//      rounding.
+//      rounding - but for fp16 values that fall below 2^-28 of the row's bound,
+//      which become subnormal and are off by at most 2^-39 of it.
 //   3. head_dx_kernel: the GEMM of P and the same rows of W, read in their
 //      stored order and turned in registers on the way into LDS, added to the
 //      earlier pieces' fp32 sums times 2^(old bound - bound).
@@ -22,9 +25,10 @@
 // so that neither the loss nor the target's part of dX suffers from
 // cancellation where the target is nearly certain.
 // Bound by the matrix cores; with few rows by the read of W.  Measured at 4096
-// rows of 4096 columns and 32000 entries: 1670 us (1.29 PFLOP/s), of it the
-// logits 804 to 870, the gradient product 840 to 925, the rows 12 (90 where the
-// groups' bounds differ and P is rescaled).
+// rows of 4096 columns and 32000 entries: 1665 us (1.29 PFLOP/s), of it the
+// logits 798 to 870 (MFMA pipes 66 % busy at 1.78 GHz), the gradient product 840 to
+// 928 (58 % at 1.84 GHz), the rows 12 (90 where the groups' bounds differ and P is
+// rescaled).
 #include <hip/hip_ext.h>
 
 #include "gemm16.hpp"

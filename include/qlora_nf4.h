@@ -289,7 +289,8 @@ int act8_decode(int dtype, int64_t rows, int64_t cols, const act8_t* in, uint16_
  * bits and never decoded to memory; Z must then be given (it was computed from
  * the input before it was kept).  grad_dtype: NF4_AB_F32, or NF4_AB_BF16 /
  * NF4_AB_F16 matching compute_dtype; dA and dB are of that type (the fp32 sum
- * rounded once).  Workspace, requirements and the rest as qlora_linear_bwd. */
+ * rounded once).  dZ is rounded to 16 bits on its way into dA and dX, as in
+ * qlora_linear_bwd, whose bits these are for a 16-bit X.  Workspace, requirements and the rest as qlora_linear_bwd. */
 int qlora_linear_bwd_ex(int compute_dtype, int grad_dtype, int64_t M, int64_t K, int64_t N, int64_t r,
                         const uint16_t* G, const uint16_t* X, const act8_t* X8, const uint16_t* Z,
                         const nf4_state_t* W, const uint16_t* A, const uint16_t* B, float c, uint16_t* dX, void* dA,
