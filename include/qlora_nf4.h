@@ -278,7 +278,8 @@ typedef struct act8 {
  * with row stride ld (elements), or decode into such a matrix.  rows >= 1,
  * cols >= 8, cols % 8 == 0, ld >= cols, ld % 8 == 0, rows * ld and 8 rows
  * below 2^29, X 16-byte aligned; NF4_EINVAL otherwise.  Columns cols .. ld-1
- * are neither read nor written.  One launch, no workspace. */
+ * are neither read nor written; X overlaps neither codes nor magnitudes.  One
+ * launch, no workspace. */
 int act8_encode(int dtype, int64_t rows, int64_t cols, const uint16_t* X, int64_t ld, const act8_t* out, void* stream);
 int act8_decode(int dtype, int64_t rows, int64_t cols, const act8_t* in, uint16_t* X, int64_t ld, void* stream);
 
@@ -309,9 +310,11 @@ int qlora_linear_bwd_ex(int compute_dtype, int grad_dtype, int64_t M, int64_t K,
  * kept.  A G or U past the 16-bit type's range (fp16: 65504) is kept as an
  * infinity: for G = -inf the backward has act = act' = 0, as for the value
  * itself; G = +inf or an infinite U make dU or dG infinite or NaN; in 8 bits the
- * block of 64 columns is kept as NaN.  Requirements: F % 64 == 0, K % 8 == 0, r % 8 == 0, r <= 128, and
- * qlora_linear_fwd's on (M, K, 2F, 2r); all pointers 16-byte aligned
- * (GU8->absmax 2-byte); workspace 256-byte aligned, at least fwd_bytes.  M <= 256
+ * block of 64 columns is kept as NaN.  Outputs overlap neither the inputs nor each
+ * other (so in all calls below).  Requirements: F % 64 == 0, K % 8 == 0,
+ * r % 8 == 0, r <= 128, and qlora_linear_fwd's on (M, K, 2F, 2r); all pointers
+ * 16-byte aligned (GU8->absmax 2-byte); workspace 256-byte aligned, at least
+ * fwd_bytes.  M <= 256
  * decodes the packed weights inside the product (each code read once per 64
  * rows, 16 where M <= 16, 32 where M <= 32); above, both weights are dequantized
  * into the workspace and multiplied by one GEMM whose epilogue is the
