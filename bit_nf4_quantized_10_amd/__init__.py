@@ -21,7 +21,7 @@ KERNEL_IDS = {
     "quant_pass1": 0, "quant_mean": 1, "quant_pass2": 2, "dequant": 3, "lora_down": 4,
     "fwd_gemm": 5, "fwd_gemv": 6, "bwd_dz": 7, "bwd_dx": 8, "bwd_colsum": 9, "dequant_bf16": 10,
     "reduce": 11, "merge": 12, "sgd": 13, "act8_encode": 14, "act8_decode": 15, "gated_fwd": 16, "gated_dy": 17,
-    "head_logits": 18, "head_rows": 19, "head_dx": 20,
+    "head_logits": 18, "head_rows": 19, "head_dx": 20, "mx_quant": 21, "mx_dequant": 22, "mx_gemm": 23,
 }
 C_FUNCTIONS = [
     "nf4_sizes", "nf4_quantize", "nf4_dequantize", "qlora_workspace_bytes",
@@ -31,6 +31,8 @@ C_FUNCTIONS = [
     "qlora_linear_fwd_noalloc", "qlora_grouped_fwd_dt", "qlora_grouped_bwd_dt",
     "act8_encode", "act8_decode", "qlora_linear_bwd_ex",
     "qlora_gated_workspace_bytes", "qlora_gated_fwd", "qlora_gated_bwd", "qlora_head_workspace_bytes", "qlora_head_loss",
+    "mxfp4_sizes", "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_matmul_workspace_bytes", "mxfp4_matmul",
+    "qlora_mx_workspace_bytes", "qlora_mx_linear_fwd", "qlora_mx_linear_bwd",
     "nf4_error_string",
 ]
 NF4_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
@@ -49,6 +51,11 @@ class _State(ctypes.Structure):
 
 class _Act8(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("absmax", ctypes.c_void_p)]
+
+
+class _Mx(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("codes", ctypes.c_void_p),
+                ("scales", ctypes.c_void_p)]
 
 
 _lib = None
@@ -105,6 +112,17 @@ def lib() -> ctypes.CDLL:
                                                            ctypes.c_float, vp, vp, vp, vp, i64, vp]
         L.qlora_head_workspace_bytes.argtypes = [i64, i64, i64, ctypes.c_int, i64p]
         L.qlora_head_loss.argtypes = [ctypes.c_int, i64, i64, i64, vp, vp, vp, vp, i64, vp, vp, vp, vp, i64, vp]
+        mx = ctypes.POINTER(_Mx)
+        L.mxfp4_sizes.argtypes = [i64, i64, i64p, i64p]
+        L.mxfp4_quantize.argtypes = [ctypes.c_int, ctypes.c_int, vp, i64, mx, vp]
+        L.mxfp4_dequantize.argtypes = [ctypes.c_int, ctypes.c_int, mx, vp, i64, vp]
+        L.mxfp4_matmul_workspace_bytes.argtypes = [i64, i64, i64, i64p]
+        L.mxfp4_matmul.argtypes = [ctypes.c_int, mx, mx, vp, vp, i64, vp]
+        L.qlora_mx_workspace_bytes.argtypes = L.qlora_workspace_bytes.argtypes
+        L.qlora_mx_linear_fwd.argtypes = [ctypes.c_int, i64, i64, i64, i64, vp, mx, vp, vp, ctypes.c_float, vp, vp, vp,
+                                          i64, vp]
+        L.qlora_mx_linear_bwd.argtypes = [ctypes.c_int, ctypes.c_int, i64, i64, i64, i64, vp, vp, a8, vp, mx, vp, vp,
+                                          ctypes.c_float, vp, vp, vp, vp, i64, vp]
         L.nf4_error_string.argtypes = [ctypes.c_int]
         L.nf4_error_string.restype = ctypes.c_char_p
         for name in C_FUNCTIONS[:-1]:
@@ -789,6 +807,194 @@ def qlora_head_loss(X, W, targets, weights=None, need_dx: bool = True, ignore_in
                                      _ptr(weights), ignore_index, loss.data_ptr(), lse.data_ptr(), _ptr(dX),
                                      ws.data_ptr(), ws.numel(), s), "qlora_head_loss")
     return loss, lse, dX
+
+
+@dataclass
+class MXFP4:
+    """A rows x cols matrix in microscaled 4-bit floating point (device tensors):
+    two codes a byte, the first in the low half, and a power of two per row and
+    block of 32 columns, in the order of the products' operands.  Made by
+    mxfp4_quantize."""
+    rows: int
+    cols: int
+    codes: "torch.Tensor"     # uint8, rows * 16 ceil(cols / 32)
+    scales: "torch.Tensor"    # uint8, 256 ceil(rows / 16) ceil(cols / 512)
+
+    @property
+    def shape(self):
+        return self.rows, self.cols
+
+    @property
+    def device(self):
+        return self.codes.device
+
+    def c_struct(self) -> _Mx:
+        return _Mx(self.rows, self.cols, self.codes.data_ptr(), self.scales.data_ptr())
+
+    def check(self, name: str, device=None) -> None:
+        """Raises where a tensor is not what the matrix needs, on `device`."""
+        device = self.codes.device if device is None else device
+        if device.type != "cuda":
+            raise ValueError(f"{name} must be on a device")
+        codes, scales = mxfp4_sizes(self.rows, self.cols)
+        _require_part(self.codes, name, "codes", "torch.uint8", codes, device)
+        _require_part(self.scales, name, "scales", "torch.uint8", scales, device)
+
+
+def mxfp4_sizes(rows: int, cols: int) -> tuple[int, int]:
+    """Bytes of the codes and of the scales of a rows x cols matrix."""
+    c, s = ctypes.c_int64(), ctypes.c_int64()
+    _check(lib().mxfp4_sizes(rows, cols, ctypes.byref(c), ctypes.byref(s)), "mxfp4_sizes")
+    return c.value, s.value
+
+
+def empty_mxfp4(rows: int, cols: int, device="cuda") -> MXFP4:
+    import torch
+    c, s = mxfp4_sizes(rows, cols)
+    return MXFP4(rows, cols, torch.empty(c, dtype=torch.uint8, device=device),
+                 torch.empty(s, dtype=torch.uint8, device=device))
+
+
+def _element_code(dtype) -> int:
+    """NF4_OUT_* code of a torch dtype."""
+    import torch
+    code = {torch.float32: NF4_OUT_F32, torch.bfloat16: NF4_OUT_BF16, torch.float16: NF4_OUT_F16}.get(dtype)
+    if code is None:
+        raise ValueError(f"the element type is fp32, bf16 or fp16, got {dtype}")
+    return code
+
+
+def _row_stride(t, name: str) -> int:
+    """A device matrix with contiguous rows; returns its row stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a device tensor")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a matrix with contiguous rows")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def mxfp4_quantize(X, transpose: bool = False, out: MXFP4 | None = None, stream=None) -> MXFP4:
+    """Keep the fp32, bf16 or fp16 matrix X (rows may be strided by a multiple of 8
+    elements) in MXFP4, blocks along its rows; with transpose, Xᵀ, blocks along
+    X's columns (a K x N weight as the N rows of K that the products take)."""
+    code = _element_code(X.dtype)
+    ld = _row_stride(X, "X")
+    rows, cols = (X.shape[1], X.shape[0]) if transpose else X.shape
+    if out is not None:
+        out.check("out", X.device)
+        if out.shape != (rows, cols):
+            raise ValueError(f"out must be {rows} x {cols}, got {out.shape}")
+    with _on(X, stream) as s:
+        if out is None:
+            out = empty_mxfp4(rows, cols, X.device)
+        st = out.c_struct()
+        _check(lib().mxfp4_quantize(code, int(transpose), X.data_ptr(), ld, ctypes.byref(st), s), "mxfp4_quantize")
+    return out
+
+
+def mxfp4_dequantize(kept: MXFP4, dtype=None, transpose: bool = False, out=None, stream=None):
+    """The values that `kept` stands for as fp32 (the default), bf16 or fp16;
+    with transpose as a cols x rows matrix."""
+    import torch
+    kept.check("kept")
+    shape = (kept.cols, kept.rows) if transpose else (kept.rows, kept.cols)
+    if out is not None:
+        if dtype not in (None, out.dtype):
+            raise ValueError(f"out must be {dtype}, got {out.dtype}")
+        _require_shape(out, "out", *shape)
+        ld = _row_stride(out, "out")
+    with _on(kept.codes, stream, out) as s:
+        if out is None:
+            out = torch.empty(*shape, dtype=torch.float32 if dtype is None else dtype, device=kept.device)
+            ld = shape[1]
+        st = kept.c_struct()
+        _check(lib().mxfp4_dequantize(_element_code(out.dtype), int(transpose), ctypes.byref(st), out.data_ptr(), ld, s),
+               "mxfp4_dequantize")
+    return out
+
+
+def mxfp4_matmul_workspace_bytes(M: int, N: int, K: int) -> int:
+    b = ctypes.c_int64()
+    _check(lib().mxfp4_matmul_workspace_bytes(M, N, K, ctypes.byref(b)), "mxfp4_matmul_workspace_bytes")
+    return b.value
+
+
+def mxfp4_matmul(P: MXFP4, Q: MXFP4, dtype=None, out=None, workspace=None, stream=None):
+    """P Qᵀ (M x K times N x K) as fp32 (the default), bf16 or fp16, summed in fp32."""
+    import torch
+    P.check("P")
+    Q.check("Q", P.device)
+    if P.cols != Q.cols:
+        raise ValueError(f"P and Q must have as many columns, got {P.cols} and {Q.cols}")
+    dtype = (torch.float32 if out is None else out.dtype) if dtype is None else dtype
+    code = _element_code(dtype)
+    with _on(P.codes, stream, out, workspace) as s:
+        out = _out(out, "out", dtype, P.device, P.rows, Q.rows)
+        ws = _workspace(workspace, mxfp4_matmul_workspace_bytes(P.rows, Q.rows, P.cols), P.device)
+        p, q = P.c_struct(), Q.c_struct()
+        _check(lib().mxfp4_matmul(code, ctypes.byref(p), ctypes.byref(q), out.data_ptr(), ws.data_ptr(), ws.numel(), s),
+               "mxfp4_matmul")
+    return out
+
+
+def qlora_mx_workspace_bytes(M: int, K: int, N: int, r: int) -> tuple[int, int]:
+    f, b = ctypes.c_int64(), ctypes.c_int64()
+    _check(lib().qlora_mx_workspace_bytes(M, K, N, r, ctypes.byref(f), ctypes.byref(b)), "qlora_mx_workspace_bytes")
+    return f.value, b.value
+
+
+def qlora_mx_linear_fwd(X, W: MXFP4, A, B, c: float, Y=None, Z=None, workspace=None, stream=None,
+                        return_z: bool = True):
+    """Y = Q(X) Wᵀ + c Z B, Z = X A, for a frozen weight W (N x K) in MXFP4; Q(X) is
+    what MXFP4 keeps of X's rows.  X: M x K, A: K x r, B: r x N, all bf16 or all
+    fp16.  Returns (Y, Z); with return_z=False and no Z given, (Y, None)."""
+    dt = _compute_dtype(X)
+    M, (N, K), r = X.shape[0], W.shape, A.shape[1]
+    for t, n, shape in ((X, "X", (M, K)), (A, "A", (K, r)), (B, "B", (r, N))):
+        _require_cuda(t, n, dt)
+        _require_shape(t, n, *shape)
+    W.check("W", X.device)
+    with _on(X, stream, A, B, Y, Z, workspace) as s:
+        Y = _out(Y, "Y", dt, X.device, M, N)
+        if Z is not None or return_z:
+            Z = _out(Z, "Z", dt, X.device, M, r)
+        ws = _workspace(workspace, qlora_mx_workspace_bytes(M, K, N, r)[0], X.device)
+        st = W.c_struct()
+        _check(lib().qlora_mx_linear_fwd(_COMPUTE[dt], M, K, N, r, X.data_ptr(), ctypes.byref(st), A.data_ptr(),
+                                         B.data_ptr(), float(c), Y.data_ptr(), _ptr(Z), ws.data_ptr(), ws.numel(), s),
+               "qlora_mx_linear_fwd")
+    return Y, Z
+
+
+def qlora_mx_linear_bwd(G, X, Z, W: MXFP4, A, B, c: float, need_dx: bool = True, grad_dtype=None, dX=None, dA=None,
+                        dB=None, workspace=None, stream=None):
+    """Backward of qlora_mx_linear_fwd with the derivative of Q taken as one:
+    dZ = c G Bᵀ, dA = Xᵀ dZ, dB = c Zᵀ G, dX = G W + dZ Aᵀ.  Returns (dX or None,
+    dA, dB).  X may be an Act8.  grad_dtype: of dA and dB, float32 (the default) or
+    G's dtype."""
+    dt = _compute_dtype(G)
+    M, (N, K), r = G.shape[0], W.shape, A.shape[1]
+    for t, n, shape in ((G, "G", (M, N)), (Z, "Z", (M, r)), (A, "A", (K, r)), (B, "B", (r, N))):
+        _require_cuda(t, n, dt)
+        _require_shape(t, n, *shape)
+    if X.dtype != dt:
+        raise ValueError(f"X must be of {dt}, got {X.dtype}")
+    if not isinstance(X, Act8):
+        _require_cuda(X, "X", dt)
+    xp, x8 = _kept_or_dense(X, M, K, "X")
+    gdt, gcode = _grad_code(grad_dtype, dt)
+    W.check("W", G.device)
+    with _on(G, stream, X, Z, A, B, dX, dA, dB, workspace) as s:
+        dX = _out(dX, "dX", dt, G.device, M, K) if need_dx else None
+        dA = _out(dA, "dA", gdt, G.device, K, r)
+        dB = _out(dB, "dB", gdt, G.device, r, N)
+        ws = _workspace(workspace, qlora_mx_workspace_bytes(M, K, N, r)[1], G.device)
+        st = W.c_struct()
+        _check(lib().qlora_mx_linear_bwd(_COMPUTE[dt], gcode, M, K, N, r, G.data_ptr(), xp, _ref(x8), Z.data_ptr(),
+                                         ctypes.byref(st), A.data_ptr(), B.data_ptr(), float(c), _ptr(dX),
+                                         dA.data_ptr(), dB.data_ptr(), ws.data_ptr(), ws.numel(), s),
+               "qlora_mx_linear_bwd")
+    return dX, dA, dB
 
 
 def qlora_timer_enable(kernel: str, enable: bool = True) -> None:

@@ -9,6 +9,7 @@
 #include "../../include/qlora_nf4.h"
 #include "gated.hpp"
 #include "kernels.hpp"
+#include "mxfp4.hpp"
 
 namespace {
 
@@ -39,11 +40,14 @@ bool dtype_ok(int d) { return d == NF4_COMPUTE_BF16 || d == NF4_COMPUTE_F16; }
 // 2 GiB, keeps all real offsets below 2^31.
 constexpr int64_t kMaxOperandElems = int64_t(1) << 29;
 
-bool layer_shape_ok(int64_t M, int64_t K, int64_t N, int64_t r) {
-  return M >= 1 && K >= 1 && N >= 1 && r >= 1 && N % NF4_BLOCK1 == 0 && K % 8 == 0 && r % 8 == 0 &&
+bool layer_sizes_ok(int64_t M, int64_t K, int64_t N, int64_t r) {
+  return M >= 1 && K >= 1 && N >= 1 && r >= 1 && N % 8 == 0 && K % 8 == 0 && r % 8 == 0 &&
          r <= 256 && M <= (int64_t(1) << 20) && K <= (int64_t(1) << 24) && N <= (int64_t(1) << 24) &&
          M * K < kMaxOperandElems && M * N < kMaxOperandElems && K * N < kMaxOperandElems &&
          K * r < kMaxOperandElems && r * N < kMaxOperandElems;
+}
+bool layer_shape_ok(int64_t M, int64_t K, int64_t N, int64_t r) {
+  return N % NF4_BLOCK1 == 0 && layer_sizes_ok(M, K, N, r);
 }
 
 // ---------------------------------------------------------------- timers
@@ -455,6 +459,105 @@ int qlora_head_loss(int compute_dtype, int64_t M, int64_t K, int64_t V, const ui
   if (workspace_bytes < qn::head_workspace_bytes(M, K, V, dX != nullptr)) return NF4_EINVAL;
   hipError_t e = qn::launch_head_loss(M, K, V, X, W, targets, weights, ignore_index, loss, lse, dX, workspace,
                                       static_cast<hipStream_t>(stream), compute_dtype);
+  return e == hipSuccess ? NF4_OK : NF4_EHIP;
+}
+
+static bool out_type_ok(int t) { return t == NF4_OUT_F32 || t == NF4_OUT_BF16 || t == NF4_OUT_F16; }
+
+static bool mx_shape_ok(int64_t rows, int64_t cols) {
+  return rows >= 1 && cols >= 8 && cols % 8 == 0 && rows < kMaxOperandElems && cols < kMaxOperandElems &&
+         rows * cols < kMaxOperandElems;
+}
+static bool mx_ok(const mxfp4_t* m) {
+  return m != nullptr && mx_shape_ok(m->rows, m->cols) && m->codes != nullptr && m->scales != nullptr &&
+         aligned16(m->codes) && aligned16(m->scales);
+}
+static qn::MxView mx_view(const mxfp4_t* m) { return qn::MxView{m->codes, m->scales, m->rows, m->cols}; }
+
+static bool mx_dense_ok(int type, int transposed, const mxfp4_t* m, const void* X, int64_t ld) {
+  if (!out_type_ok(type) || !mx_ok(m) || X == nullptr || !aligned16(X)) return false;
+  if (transposed != 0 && m->rows % 8 != 0) return false;
+  const int64_t n = transposed != 0 ? m->cols : m->rows, len = transposed != 0 ? m->rows : m->cols;
+  return ld >= len && ld % 8 == 0 && ld < kMaxOperandElems && n * ld < kMaxOperandElems;
+}
+
+int mxfp4_sizes(int64_t rows, int64_t cols, int64_t* code_bytes, int64_t* scale_bytes) {
+  if (!mx_shape_ok(rows, cols)) return NF4_EINVAL;
+  if (code_bytes) *code_bytes = qn::mx_code_bytes(rows, cols);
+  if (scale_bytes) *scale_bytes = qn::mx_scale_bytes(rows, cols);
+  return NF4_OK;
+}
+
+int mxfp4_quantize(int type, int transposed, const void* X, int64_t ld, const mxfp4_t* out, void* stream) {
+  if (!mx_dense_ok(type, transposed, out, X, ld)) return NF4_EINVAL;
+  hipError_t e = qn::launch_mx_quantize(type, transposed != 0, X, ld, mx_view(out), static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? NF4_OK : NF4_EHIP;
+}
+
+int mxfp4_dequantize(int type, int transposed, const mxfp4_t* in, void* X, int64_t ld, void* stream) {
+  if (!mx_dense_ok(type, transposed, in, X, ld)) return NF4_EINVAL;
+  hipError_t e = qn::launch_mx_dequantize(type, transposed != 0, mx_view(in), X, ld, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? NF4_OK : NF4_EHIP;
+}
+
+static bool mx_product_ok(int64_t M, int64_t N, int64_t K) {
+  return mx_shape_ok(M, K) && mx_shape_ok(N, K) && N % 8 == 0 && M <= (int64_t(1) << 20) && N <= (int64_t(1) << 24) &&
+         M * N < kMaxOperandElems;
+}
+
+int mxfp4_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t* bytes) {
+  if (!mx_product_ok(M, N, K)) return NF4_EINVAL;
+  if (bytes) *bytes = qn::mx_matmul_workspace_bytes(M, N, K);
+  return NF4_OK;
+}
+
+int mxfp4_matmul(int out_type, const mxfp4_t* P, const mxfp4_t* Q, void* C, void* workspace, int64_t workspace_bytes,
+                 void* stream) {
+  if (!out_type_ok(out_type) || !mx_ok(P) || !mx_ok(Q) || P->cols != Q->cols) return NF4_EINVAL;
+  if (!mx_product_ok(P->rows, Q->rows, P->cols)) return NF4_EINVAL;
+  if (!C || !aligned16(C) || !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0) return NF4_EINVAL;
+  if (workspace_bytes < qn::mx_matmul_workspace_bytes(P->rows, Q->rows, P->cols)) return NF4_EINVAL;
+  hipError_t e = qn::launch_mx_matmul(mx_view(P), mx_view(Q), out_type, C, workspace, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? NF4_OK : NF4_EHIP;
+}
+
+int qlora_mx_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t r, int64_t* fwd_bytes, int64_t* bwd_bytes) {
+  if (!layer_sizes_ok(M, K, N, r)) return NF4_EINVAL;
+  if (fwd_bytes) *fwd_bytes = qn::mx_fwd_workspace_bytes(M, K, N, r);
+  if (bwd_bytes) *bwd_bytes = qn::mx_bwd_workspace_bytes(M, K, N, r);
+  return NF4_OK;
+}
+
+int qlora_mx_linear_fwd(int compute_dtype, int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t* X,
+                        const mxfp4_t* W, const uint16_t* A, const uint16_t* B, float c, uint16_t* Y, uint16_t* Z,
+                        void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!dtype_ok(compute_dtype) || !layer_sizes_ok(M, K, N, r) || !mx_ok(W) || W->rows != N || W->cols != K) return NF4_EINVAL;
+  if (!X || !A || !B || !Y || !workspace) return NF4_EINVAL;   // Z may be NULL
+  if (!aligned16(X) || !aligned16(A) || !aligned16(B) || !aligned16(Y) || (Z && !aligned16(Z)) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return NF4_EINVAL;
+  if (workspace_bytes < qn::mx_fwd_workspace_bytes(M, K, N, r)) return NF4_EINVAL;
+  hipError_t e = qn::launch_mx_fwd(M, K, N, r, X, mx_view(W), A, B, c, Y, Z, workspace, static_cast<hipStream_t>(stream),
+                                   compute_dtype);
+  return e == hipSuccess ? NF4_OK : NF4_EHIP;
+}
+
+int qlora_mx_linear_bwd(int compute_dtype, int grad_dtype, int64_t M, int64_t K, int64_t N, int64_t r,
+                        const uint16_t* G, const uint16_t* X, const act8_t* X8, const uint16_t* Z, const mxfp4_t* W,
+                        const uint16_t* A, const uint16_t* B, float c, uint16_t* dX, void* dA, void* dB,
+                        void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!dtype_ok(compute_dtype) || !grad_dtype_ok(grad_dtype, compute_dtype)) return NF4_EINVAL;
+  if (!layer_sizes_ok(M, K, N, r) || !mx_ok(W) || W->rows != N || W->cols != K) return NF4_EINVAL;
+  if ((X == nullptr) == (X8 == nullptr) || (X8 != nullptr && !act8_ok(X8))) return NF4_EINVAL;
+  if (!G || !Z || !A || !B || !dA || !dB || !workspace) return NF4_EINVAL;
+  if (!aligned16(G) || (X && !aligned16(X)) || !aligned16(Z) || !aligned16(A) || !aligned16(B) || !aligned16(dA) ||
+      !aligned16(dB) || (dX && !aligned16(dX)) || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return NF4_EINVAL;
+  if (workspace_bytes < qn::mx_bwd_workspace_bytes(M, K, N, r)) return NF4_EINVAL;
+  qn::Act8View x8;
+  if (X8 != nullptr) x8 = qn::Act8View{X8->codes, X8->absmax};
+  hipError_t e = qn::launch_mx_bwd(M, K, N, r, G, X, x8, Z, mx_view(W), A, B, c, dX, dA, dB, workspace,
+                                   static_cast<hipStream_t>(stream), compute_dtype, grad_dtype != NF4_AB_F32);
   return e == hipSuccess ? NF4_OK : NF4_EHIP;
 }
 

@@ -245,6 +245,27 @@ hipError_t launch_head_loss(int64_t M, int64_t K, int64_t V, const uint16_t* X, 
                             const float* weights, int64_t ignore, float* loss, float* lse, uint16_t* dX, void* ws,
                             hipStream_t stream, int dtype);
 
+// A matrix held in MXFP4 (mxfp4.hpp has its layout).
+struct MxView {
+  uint8_t* codes;
+  uint8_t* scales;
+  int64_t rows, cols;
+};
+// type: of X, one of NF4_OUT_*.  across: X is cols x rows.  ld: X's row stride.
+hipError_t launch_mx_quantize(int type, bool across, const void* X, int64_t ld, MxView m, hipStream_t stream);
+hipError_t launch_mx_dequantize(int type, bool across, MxView m, void* X, int64_t ld, hipStream_t stream);
+// out (p.rows x q.rows, of out_type) = p qᵀ
+int64_t mx_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K);
+hipError_t launch_mx_matmul(MxView p, MxView q, int out_type, void* out, void* ws, hipStream_t stream);
+// The layer on an MXFP4 weight W (N x K).
+int64_t mx_fwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t r);
+int64_t mx_bwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t r);
+hipError_t launch_mx_fwd(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t* X, MxView W, const uint16_t* A,
+                         const uint16_t* B, float c, uint16_t* Y, uint16_t* Z, void* ws, hipStream_t stream, int dtype);
+hipError_t launch_mx_bwd(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t* G, const uint16_t* X, Act8View x8,
+                         const uint16_t* Z, MxView W, const uint16_t* A, const uint16_t* B, float c, uint16_t* dX,
+                         void* dA, void* dB, void* ws, hipStream_t stream, int dtype, bool grad16);
+
 // Dequantize a K x N weight to the 16-bit compute type (dtype), either as
 // stored (K x N) or transposed (N x K).
 // out_ld: row stride of the output (0: N, transposed K).

@@ -363,6 +363,71 @@ int qlora_head_loss(int compute_dtype, int64_t M, int64_t K, int64_t V, const ui
                     const int64_t* targets, const float* weights, int64_t ignore_index, float* loss, float* lse,
                     uint16_t* dX, void* workspace, int64_t workspace_bytes, void* stream);
 
+/* Microscaled 4-bit floating point (MXFP4, the OCP Microscaling formats'
+ * conversion): per row, blocks of 32 consecutive columns (a row's last one filled
+ * up with zeros) share a power of two,
+ *   s = floor(log2 max|x|) - 2, at least -127;
+ *   an element is kept as the nearest to x / 2^s of 0, 0.5, 1, 1.5, 2, 3, 4, 6
+ *   (codes 0 .. 7) and their negatives (codes 8 .. 15), ties to the even code,
+ *   past 6 as 6, the sign kept; it stands for that value times 2^s.
+ * A block holding an infinity or a NaN has scale byte 255 and codes 0, and decodes
+ * to NaN in all its columns.
+ * codes: rows x 16 ceil(cols/32) bytes, two codes a byte, the first column's in the
+ * low half.  scales: the bytes s + 127, in the order in which the matrix cores take
+ * them: 16 rows x 16 blocks are 256 bytes, that of row i and block b at
+ *   ((i/16) ceil(cols/512) + b/16) 256 + 4 (16 (b%4) + i%16) + (b%16)/4;
+ * rows and blocks are filled up to 16 with bytes that are never 255 (0 where
+ * mxfp4_quantize made them). */
+typedef struct mxfp4 {
+  int64_t  rows, cols;
+  uint8_t* codes;     /* 16-byte aligned */
+  uint8_t* scales;    /* 16-byte aligned */
+} mxfp4_t;
+
+/* Host only.  Sizes of the two arrays.  NF4_EINVAL unless rows >= 1, cols >= 8,
+ * cols % 8 == 0 and rows * cols < 2^29 (so for every mxfp4_t below). */
+int mxfp4_sizes(int64_t rows, int64_t cols, int64_t* code_bytes, int64_t* scale_bytes);
+
+/* Quantise X into `out`, or write the values that `in` stands for into X.  type:
+ * X's element type, one of NF4_OUT_* (the values are exact in fp32 and bf16; in
+ * fp16 rounded to nearest even).  transposed 0: X is rows x cols; otherwise X is
+ * cols x rows (a K x N weight held as N rows of K) and rows % 8 == 0.  ld: X's row
+ * stride in elements, at least its row length, ld % 8 == 0, and ld times X's rows
+ * below 2^29; X 16-byte aligned.  Elements past a row's length are neither read nor
+ * written.  One launch, no workspace.  X overlaps neither codes nor scales. */
+int mxfp4_quantize(int type, int transposed, const void* X, int64_t ld, const mxfp4_t* out, void* stream);
+int mxfp4_dequantize(int type, int transposed, const mxfp4_t* in, void* X, int64_t ld, void* stream);
+
+/* C = P Qᵀ for two matrices in MXFP4: P M x K, Q N x K, N % 8 == 0, M * N below 2^29;
+ * C (M x N, dense, 16-byte aligned) of out_type, one of NF4_OUT_*.  Products are
+ * exact, sums are fp32 and rounded once.  Requirements besides: M <= 2^20, N <= 2^24;
+ * workspace 256-byte aligned, at least *bytes. */
+int mxfp4_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t* bytes);
+int mxfp4_matmul(int out_type, const mxfp4_t* P, const mxfp4_t* Q, void* C, void* workspace, int64_t workspace_bytes,
+                 void* stream);
+
+/* The layer on a frozen weight held in MXFP4, W: N x K (rows N, cols K):
+ *   Z = X A,  Y = Q(X) Wᵀ + c Z B
+ * with Q(X) the values that mxfp4_quantize keeps of X's rows.  X M x K, A K x r,
+ * B r x N, Y M x N, Z M x r (NULL: not returned) of compute_dtype.  Sums are fp32;
+ * Z and RNE(c B) enter in the 16-bit type.  Requirements: N % 8 == 0 in place of
+ * N % 64, else qlora_linear_fwd's on sizes; all pointers 16-byte aligned, workspace
+ * 256-byte aligned, at least fwd_bytes.
+ * The backward, given G = dL/dY, takes the derivative of Q as one (what its rounding
+ * drops has none):
+ *   dZ = c G Bᵀ,  dA = Xᵀ dZ,  dB = c Zᵀ G,  dX = G W + dZ Aᵀ (skipped when NULL),
+ * with W's values in compute_dtype.  Exactly one of X (16 bits) and X8 (an 8-bit
+ * checkpoint); Z is required; grad_dtype as in qlora_linear_bwd_ex; workspace at
+ * least bwd_bytes. */
+int qlora_mx_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t r, int64_t* fwd_bytes, int64_t* bwd_bytes);
+int qlora_mx_linear_fwd(int compute_dtype, int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t* X,
+                        const mxfp4_t* W, const uint16_t* A, const uint16_t* B, float c, uint16_t* Y, uint16_t* Z,
+                        void* workspace, int64_t workspace_bytes, void* stream);
+int qlora_mx_linear_bwd(int compute_dtype, int grad_dtype, int64_t M, int64_t K, int64_t N, int64_t r,
+                        const uint16_t* G, const uint16_t* X, const act8_t* X8, const uint16_t* Z, const mxfp4_t* W,
+                        const uint16_t* A, const uint16_t* B, float c, uint16_t* dX, void* dA, void* dB,
+                        void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Synchronise `stream`, then copy the device status word to *host_value.
  * Returns NF4_EHIP if the copy fails, else NF4_OK. */
 int nf4_status_read(const int32_t* status, int32_t* host_value, void* stream);
@@ -389,7 +454,10 @@ int nf4_status_read(const int32_t* status, int32_t* host_value, void* stream);
 #define QK_HEAD_LOGITS  18  /* output head: logits to probabilities      */
 #define QK_HEAD_ROWS    19  /* output head: running sums, loss           */
 #define QK_HEAD_DX      20  /* output head: gradient product             */
-#define QK_NUM_KERNELS  21
+#define QK_MX_QUANT     21  /* MXFP4 quantisation                        */
+#define QK_MX_DEQUANT   22  /* its values                                */
+#define QK_MX_GEMM      23  /* product of two MXFP4 matrices             */
+#define QK_NUM_KERNELS  24
 
 /* When enabled, the library records a pair of hipEvents on the launch
  * stream around every launch of kernel `kernel_id`.  qlora_timer_read

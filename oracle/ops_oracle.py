@@ -1,6 +1,7 @@
 """Plain CPU references (numpy, 64 bits) of the operators around the NF4
 layer: 8-bit activation checkpoints, the gated feed-forward front with its
-backward, and the output head's cross entropy with its gradient.  They share
+backward, the output head's cross entropy with its gradient, microscaled 4-bit
+floating point (MXFP4) and the layer on such a weight.  They share
 no code with the GPU path."""
 from __future__ import annotations
 
@@ -121,3 +122,63 @@ def head_loss(X, W, targets, weights=None, ignore_index: int = -100):
     p[row, at] = -p.sum(axis=1)
     dX = np.where(counted[:, None], (p * w[:, None]) @ W, 0.0)
     return loss, lse, dX
+
+
+MX_BLOCK = 32
+E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def mxfp4_quantize(x: np.ndarray):
+    """Codes (uint8, rows x cols filled up to 32) and scale bytes (uint8, rows x
+    blocks) of a matrix given as float32 or float64: by comparison with every
+    value and, for ties, with the codes' last bits."""
+    x = np.asarray(x, dtype=np.float64)
+    rows, cols = x.shape
+    nb = -(-cols // MX_BLOCK)
+    codes = np.zeros((rows, nb * MX_BLOCK), dtype=np.uint8)
+    scales = np.zeros((rows, nb), dtype=np.uint8)
+    for b in range(nb):
+        blk = np.zeros((rows, MX_BLOCK))
+        part = x[:, b * MX_BLOCK:(b + 1) * MX_BLOCK]
+        blk[:, :part.shape[1]] = part
+        bad = ~np.isfinite(blk).all(axis=1)
+        blk[bad] = 0.0
+        top = np.abs(blk).max(axis=1)
+        _, e = np.frexp(top)                       # top = f 2^e, 0.5 <= f < 1
+        s = np.where(top > 0, np.maximum(e - 3, -127), -127)
+        y = np.ldexp(blk, -s[:, None])
+        gap = np.abs(np.minimum(np.abs(y), 6.0)[:, :, None] - E2M1)
+        gap = gap + 1e-9 * (np.arange(8) % 2) * (gap == gap.min(axis=2, keepdims=True))   # a tie: the even code
+        codes[:, b * MX_BLOCK:(b + 1) * MX_BLOCK] = gap.argmin(axis=2) + 8 * np.signbit(blk)
+        scales[:, b] = np.where(bad, 255, s + 127)
+    return codes, scales
+
+
+def mxfp4_values(codes: np.ndarray, scales: np.ndarray, cols: int) -> np.ndarray:
+    """float64 values, NaN where the scale byte is 255."""
+    v = np.where(codes >= 8, -1.0, 1.0) * E2M1[codes & 7]
+    s = np.where(scales == 255, np.nan, np.ldexp(1.0, scales.astype(np.int64) - 127))
+    return (v * np.repeat(s, MX_BLOCK, axis=1))[:, :cols]
+
+
+def mxfp4_tiled(scales: np.ndarray) -> np.ndarray:
+    """The scale bytes in the order in which they are stored."""
+    rows, nb = scales.shape
+    out = np.zeros(-(-rows // 16) * -(-nb // 16) * 256, dtype=np.uint8)
+    chunks = -(-nb // 16)
+    for i in range(rows):
+        for b in range(nb):
+            out[((i // 16) * chunks + b // 16) * 256 + 4 * (16 * (b % 4) + i % 16) + (b % 16) // 4] = scales[i, b]
+    return out
+
+
+def mx_linear_forward(X, W, A, B, c):
+    """(Y, Z) in float64; W: the N x K values."""
+    Z = X @ A
+    return mxfp4_values(*mxfp4_quantize(X), X.shape[1]) @ W.T + c * (Z @ B), Z
+
+
+def mx_linear_backward(G, X, Z, W, A, B, c):
+    """(dX, dA, dB) in float64."""
+    dZ = c * (G @ B.T)
+    return G @ W + dZ @ A.T, X.T @ dZ, c * (Z.T @ G)
