@@ -22,6 +22,7 @@ KERNEL_IDS = {
     "fwd_gemm": 5, "fwd_gemv": 6, "bwd_dz": 7, "bwd_dx": 8, "bwd_colsum": 9, "dequant_bf16": 10,
     "reduce": 11, "merge": 12, "sgd": 13, "act8_encode": 14, "act8_decode": 15, "gated_fwd": 16, "gated_dy": 17,
     "head_logits": 18, "head_rows": 19, "head_dx": 20, "mx_quant": 21, "mx_dequant": 22, "mx_gemm": 23,
+    "muon": 24,
 }
 C_FUNCTIONS = [
     "nf4_sizes", "nf4_quantize", "nf4_dequantize", "qlora_workspace_bytes",
@@ -33,6 +34,7 @@ C_FUNCTIONS = [
     "qlora_gated_workspace_bytes", "qlora_gated_fwd", "qlora_gated_bwd", "qlora_head_workspace_bytes", "qlora_head_loss",
     "mxfp4_sizes", "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_matmul_workspace_bytes", "mxfp4_matmul",
     "qlora_mx_workspace_bytes", "qlora_mx_linear_fwd", "qlora_mx_linear_bwd",
+    "qlora_muon_workspace_bytes", "qlora_muon_step",
     "nf4_error_string",
 ]
 NF4_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
@@ -56,6 +58,11 @@ class _Act8(ctypes.Structure):
 class _Mx(ctypes.Structure):
     _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("codes", ctypes.c_void_p),
                 ("scales", ctypes.c_void_p)]
+
+
+class _Muon(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_double) for n in ("lr", "momentum", "weight_decay", "eps", "a", "b", "c")] + \
+               [(n, ctypes.c_int32) for n in ("steps", "nesterov", "scaling")]
 
 
 _lib = None
@@ -123,6 +130,9 @@ def lib() -> ctypes.CDLL:
                                           i64, vp]
         L.qlora_mx_linear_bwd.argtypes = [ctypes.c_int, ctypes.c_int, i64, i64, i64, i64, vp, vp, a8, vp, mx, vp, vp,
                                           ctypes.c_float, vp, vp, vp, vp, i64, vp]
+        L.qlora_muon_workspace_bytes.argtypes = [i64, i64, i64, i64p]
+        L.qlora_muon_step.argtypes = [ctypes.c_int, ctypes.c_int, i64, i64, i64] + [vp] * 8 + \
+            [ctypes.POINTER(_Muon), vp, i64, vp]
         L.nf4_error_string.argtypes = [ctypes.c_int]
         L.nf4_error_string.restype = ctypes.c_char_p
         for name in C_FUNCTIONS[:-1]:
@@ -510,6 +520,46 @@ def qlora_sgd_step(A, B, dA, dB, lr: float, A_master=None, B_master=None, stream
     _check(lib().qlora_sgd_step_dt(_COMPUTE[pdt], K, N, r, A.data_ptr(), B.data_ptr(), dA.data_ptr(),
                                    dB.data_ptr(), ctypes.c_float(lr), _ptr(A_master), _ptr(B_master),
                                    _stream(stream)), "qlora_sgd_step_dt")
+
+
+NF4_MUON_SCALE_NONE, NF4_MUON_SCALE_SPECTRAL, NF4_MUON_SCALE_RMS = 0, 1, 2
+_MUON_SCALES = {None: NF4_MUON_SCALE_NONE, "spectral": NF4_MUON_SCALE_SPECTRAL, "rms": NF4_MUON_SCALE_RMS}
+
+
+def qlora_muon_workspace_bytes(K: int, N: int, r: int) -> int:
+    b = ctypes.c_int64()
+    _check(lib().qlora_muon_workspace_bytes(K, N, r, ctypes.byref(b)), "qlora_muon_workspace_bytes")
+    return b.value
+
+
+def qlora_muon_step(A, B, dA, dB, mA, mB, lr: float, momentum: float = 0.95, nesterov: bool = True,
+                    weight_decay: float = 0.0, scaling: str | None = "spectral", steps: int = 5,
+                    coefficients=(3.4445, -4.7750, 2.0315), eps: float = 1e-7, A_master=None, B_master=None,
+                    workspace=None, stream=None) -> None:
+    """In-place step of the bf16 or fp16 adapter (optionally through fp32 masters)
+    along its orthogonalised momentum.  mA, mB: fp32 momenta, updated; dA, dB: fp32 or
+    the adapter's type.  scaling: "spectral" sqrt(max(1, rows / columns)), "rms"
+    0.2 sqrt(max(rows, columns)) or None."""
+    import torch
+    if scaling not in _MUON_SCALES:
+        raise ValueError(f'scaling is "spectral", "rms" or None, got {scaling!r}')
+    K, r = A.shape
+    N = B.shape[1]
+    dt = _compute_dtype(A)
+    gdt, gcode = _grad_code(dA.dtype, dt)
+    for t, n, d, shape in ((A, "A", dt, (K, r)), (B, "B", dt, (r, N)), (dA, "dA", gdt, (K, r)), (dB, "dB", gdt, (r, N)),
+                           (mA, "mA", torch.float32, (K, r)), (mB, "mB", torch.float32, (r, N)),
+                           (A_master, "A_master", torch.float32, (K, r)), (B_master, "B_master", torch.float32, (r, N))):
+        if t is not None or not n.endswith("master"):
+            _require_cuda(t, n, d)
+            _require_shape(t, n, *shape)
+    a, b, c = coefficients
+    o = _Muon(lr, momentum, weight_decay, eps, a, b, c, steps, int(nesterov), _MUON_SCALES[scaling])
+    with _on(A, stream, B, dA, dB, mA, mB, A_master, B_master, workspace) as s:
+        ws = _workspace(workspace, qlora_muon_workspace_bytes(K, N, r), A.device)
+        _check(lib().qlora_muon_step(_COMPUTE[dt], gcode, K, N, r, A.data_ptr(), B.data_ptr(), dA.data_ptr(),
+                                     dB.data_ptr(), mA.data_ptr(), mB.data_ptr(), _ptr(A_master), _ptr(B_master),
+                                     ctypes.byref(o), ws.data_ptr(), ws.numel(), s), "qlora_muon_step")
 
 
 def nf4_status_read(status, stream=None) -> int:

@@ -3,6 +3,7 @@
 // (except nf4_status_read and qlora_timer_read, which exist to wait).
 #include <hip/hip_runtime.h>
 
+#include <cmath>
 #include <mutex>
 #include <vector>
 
@@ -593,6 +594,42 @@ int qlora_sgd_step_dt(int param_dtype, int64_t K, int64_t N, int64_t r, uint16_t
     return NF4_EINVAL;
   hipError_t e =
       qn::launch_sgd(K, N, r, A, B, dA, dB, lr, A_master, B_master, static_cast<hipStream_t>(stream), param_dtype);
+  return e == hipSuccess ? NF4_OK : NF4_EHIP;
+}
+
+static bool muon_shape_ok(int64_t K, int64_t N, int64_t r) {
+  constexpr int64_t kLong = int64_t(1) << 24;
+  return K >= 1 && N >= 1 && r >= 1 && r <= 256 && K <= kLong && N <= kLong && K * r < kMaxOperandElems && r * N < kMaxOperandElems;
+}
+
+int qlora_muon_workspace_bytes(int64_t K, int64_t N, int64_t r, int64_t* bytes) {
+  if (!muon_shape_ok(K, N, r)) return NF4_EINVAL;
+  if (bytes) *bytes = qn::muon_workspace_bytes(K, N, r);
+  return NF4_OK;
+}
+
+int qlora_muon_step(int param_dtype, int grad_dtype, int64_t K, int64_t N, int64_t r, uint16_t* A, uint16_t* B,
+                    const void* dA, const void* dB, float* mA, float* mB, float* A_master, float* B_master,
+                    const qlora_muon_t* options, void* workspace, int64_t workspace_bytes, void* stream) {
+  if (!dtype_ok(param_dtype) || !grad_dtype_ok(grad_dtype, param_dtype) || !muon_shape_ok(K, N, r)) return NF4_EINVAL;
+  if (!A || !B || !dA || !dB || !mA || !mB || !options || !workspace) return NF4_EINVAL;
+  if ((A_master == nullptr) != (B_master == nullptr)) return NF4_EINVAL;
+  const uintptr_t grad_mask = grad_dtype == NF4_AB_F32 ? 3u : 1u;
+  if (((reinterpret_cast<uintptr_t>(A) | reinterpret_cast<uintptr_t>(B)) & 1u) ||
+      ((reinterpret_cast<uintptr_t>(dA) | reinterpret_cast<uintptr_t>(dB)) & grad_mask) ||
+      ((reinterpret_cast<uintptr_t>(mA) | reinterpret_cast<uintptr_t>(mB) | reinterpret_cast<uintptr_t>(A_master) |
+        reinterpret_cast<uintptr_t>(B_master)) & 3u) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return NF4_EINVAL;
+  const qlora_muon_t& o = *options;
+  for (const double v : {o.lr, o.momentum, o.weight_decay, o.eps, o.a, o.b, o.c})
+    if (!std::isfinite(v)) return NF4_EINVAL;
+  if (o.momentum < 0.0 || o.momentum >= 1.0 || !(o.eps > 0.0) || o.steps < 0 || o.steps > 32) return NF4_EINVAL;
+  if (o.scaling != NF4_MUON_SCALE_NONE && o.scaling != NF4_MUON_SCALE_SPECTRAL && o.scaling != NF4_MUON_SCALE_RMS)
+    return NF4_EINVAL;
+  if (workspace_bytes < qn::muon_workspace_bytes(K, N, r)) return NF4_EINVAL;
+  hipError_t e = qn::launch_muon(K, N, r, A, B, dA, dB, mA, mB, A_master, B_master, o, workspace,
+                                 static_cast<hipStream_t>(stream), param_dtype, grad_dtype != NF4_AB_F32);
   return e == hipSuccess ? NF4_OK : NF4_EHIP;
 }
 

@@ -4,6 +4,7 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "../../include/qlora_nf4.h"
 #include "side_jobs.hpp"
 
 namespace qn {
@@ -80,6 +81,12 @@ hipError_t launch_merge(int64_t K, int64_t N, int64_t r, NF4View W, const void* 
 // optionally through fp32 masters.
 hipError_t launch_sgd(int64_t K, int64_t N, int64_t r, uint16_t* A, uint16_t* B, const float* dA, const float* dB,
                       float lr, float* A_master, float* B_master, hipStream_t stream, int dtype = 0);
+
+// A step of A and B along their orthogonalised momentum (muon.hip).
+int64_t muon_workspace_bytes(int64_t K, int64_t N, int64_t r);
+hipError_t launch_muon(int64_t K, int64_t N, int64_t r, uint16_t* A, uint16_t* B, const void* dA, const void* dB,
+                       float* mA, float* mB, float* A_master, float* B_master, const qlora_muon_t& o, void* ws,
+                       hipStream_t stream, int dtype, bool grad16);
 
 // Grouped linears sharing X (see layer.hip).
 int64_t grouped_fwd_workspace_bytes(int64_t M, int64_t K, int g, const int64_t* Ns, int64_t r);

@@ -205,6 +205,36 @@ int qlora_sgd_step_dt(int param_dtype, int64_t K, int64_t N, int64_t r, uint16_t
                       const float* dA, const float* dB, float lr, float* A_master, float* B_master,
                       void* stream);
 
+/* A step of the adapter along its orthogonalised momentum (Muon), in place of
+ * qlora_sgd_step.  For each of A (K x r) and B (r x N), with gradient g and momentum m:
+ *   m <- mu m + (1 - mu) g,   u = (1 - mu) g + mu m where nesterov, else m,
+ *   X <- u / max(|u|_F, eps),  `steps` times X <- a X + (b S + c S^2) X, S = X Xᵀ,
+ *   p <- p (1 - lr weight_decay) - lr s X,
+ * s by `scaling`, for a matrix of rows x columns: NONE 1, SPECTRAL
+ * sqrt(max(1, rows / columns)), RMS 0.2 sqrt(max(rows, columns)).  p is the fp32
+ * master copy where A_master and B_master are given (both or neither), else the
+ * 16-bit parameter; the parameter becomes RNE(p).  m is fp32, updated in place; the
+ * iteration is held in 64 bits.  A gradient or momentum with a value that is not
+ * finite makes its whole matrix NaN.  No element depends on the order in which
+ * anything runs.
+ * param_dtype: NF4_COMPUTE_*; grad_dtype: of dA and dB, NF4_AB_F32 or the parameters'
+ * type.  Requirements: K, N, r >= 1, r <= 256, K and N <= 2^24, K*r and r*N below 2^29,
+ * 0 <= momentum < 1, eps > 0, 0 <= steps <= 32, the numbers finite; pointers aligned
+ * to their element size; workspace 256-byte aligned, at least *bytes.  NF4_EINVAL
+ * otherwise. */
+#define NF4_MUON_SCALE_NONE     0
+#define NF4_MUON_SCALE_SPECTRAL 1
+#define NF4_MUON_SCALE_RMS      2
+typedef struct qlora_muon {
+  double  lr, momentum, weight_decay, eps;
+  double  a, b, c;
+  int32_t steps, nesterov, scaling;
+} qlora_muon_t;
+int qlora_muon_workspace_bytes(int64_t K, int64_t N, int64_t r, int64_t* bytes);
+int qlora_muon_step(int param_dtype, int grad_dtype, int64_t K, int64_t N, int64_t r, uint16_t* A, uint16_t* B,
+                    const void* dA, const void* dB, float* mA, float* mB, float* A_master, float* B_master,
+                    const qlora_muon_t* options, void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Grouped linears sharing one input (e.g. the q, k, v projections, or gate
  * and up: adapters on several projections of one layer, page
  * "qlora-4bit-quantization-finetune" section "训练全流程" (Q and V) and page
@@ -457,7 +487,8 @@ int nf4_status_read(const int32_t* status, int32_t* host_value, void* stream);
 #define QK_MX_QUANT     21  /* MXFP4 quantisation                        */
 #define QK_MX_DEQUANT   22  /* its values                                */
 #define QK_MX_GEMM      23  /* product of two MXFP4 matrices             */
-#define QK_NUM_KERNELS  24
+#define QK_MUON         24  /* orthogonalised adapter step, whole        */
+#define QK_NUM_KERNELS  25
 
 /* When enabled, the library records a pair of hipEvents on the launch
  * stream around every launch of kernel `kernel_id`.  qlora_timer_read

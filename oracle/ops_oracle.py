@@ -1,7 +1,8 @@
 """Plain CPU references (numpy, 64 bits) of the operators around the NF4
 layer: 8-bit activation checkpoints, the gated feed-forward front with its
 backward, the output head's cross entropy with its gradient, microscaled 4-bit
-floating point (MXFP4) and the layer on such a weight.  They share
+floating point (MXFP4) and the layer on such a weight, and the orthogonalised
+adapter step.  They share
 no code with the GPU path."""
 from __future__ import annotations
 
@@ -182,3 +183,27 @@ def mx_linear_backward(G, X, Z, W, A, B, c):
     """(dX, dA, dB) in float64."""
     dZ = c * (G @ B.T)
     return G @ W + dZ @ A.T, X.T @ dZ, c * (Z.T @ G)
+
+
+def newton_schulz(u: np.ndarray, steps: int, coefficients, eps: float) -> np.ndarray:
+    """X <- a X + (b S + c S^2) X with S = X Xᵀ from X = u / max(|u|, eps), as it is written."""
+    a, b, c = coefficients
+    X = np.asarray(u, dtype=np.float64)
+    X = X / max(np.sqrt(np.sum(X * X)), eps)
+    wide = X.shape[0] <= X.shape[1]
+    X = X if wide else X.T
+    for _ in range(steps):
+        S = X @ X.T
+        X = a * X + (b * S + c * (S @ S)) @ X
+    return X if wide else X.T
+
+
+def muon_step(p, g, m, lr, momentum, nesterov, weight_decay, scaling, steps, coefficients, eps):
+    """(p, m) after the step, and the orthogonalised update, in float64."""
+    g, m = np.asarray(g, dtype=np.float64), np.asarray(m, dtype=np.float64)
+    m = momentum * m + (1 - momentum) * g
+    u = (1 - momentum) * g + momentum * m if nesterov else m
+    x = newton_schulz(u, steps, coefficients, eps)
+    rows, cols = x.shape
+    s = {None: 1.0, "spectral": np.sqrt(max(1.0, rows / cols)), "rms": 0.2 * np.sqrt(max(rows, cols))}[scaling]
+    return np.asarray(p, dtype=np.float64) * (1 - lr * weight_decay) - lr * s * x, m, x

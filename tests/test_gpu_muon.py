@@ -1,0 +1,191 @@
+"""The orthogonalised adapter step on the GPU against its 64-bit reference.
+
+With master copies at zero and lr = 1, weight decay 0, scaling None, the new master is
+minus the orthogonalised update rounded once to fp32.  What the kernels add to that
+rounding: u is rounded to fp32 (2^-24 of itself, twice: m and u), which moves the
+update by what the iteration makes of such a change."""
+import numpy as np
+import pytest
+
+import bit_nf4_quantized_10_amd as qn
+from oracle import ops_oracle as oo
+from tests.gpu_util import host, say
+
+pytestmark = pytest.mark.gpu
+HALF = {"bf16": 2.0 ** -8, "f16": 2.0 ** -11}
+COEFFICIENTS = (3.4445, -4.7750, 2.0315)
+
+
+def _torch_type(name):
+    import torch
+    return {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}[name]
+
+
+def _dev(x, name):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(x, dtype=np.float32)).to(_torch_type(name)).cuda()
+
+
+def _gradient(rng, rows, cols, fall=2.0):
+    k = min(rows, cols)
+    s = 10.0 ** np.linspace(0, -fall, k)
+    return (rng.standard_normal((rows, k)) / np.sqrt(rows) * s) @ rng.standard_normal((k, cols)) / np.sqrt(cols)
+
+
+class Case:
+    def __init__(self, K, N, r, name, grad="f32", master=True, seed=0, fall=2.0):
+        rng = np.random.default_rng(seed + K + N + r)
+        self.K, self.N, self.r, self.name = K, N, r, name
+        shapes = {"A": (K, r), "B": (r, N)}
+        self.master = {n: _dev(rng.standard_normal(s) * 0.05, "f32") for n, s in shapes.items()} if master else {"A": None, "B": None}
+        self.p = {n: _dev(host(self.master[n]) if master else rng.standard_normal(s) * 0.05, name) for n, s in shapes.items()}
+        self.g = {n: _dev(_gradient(rng, *s, fall), grad) for n, s in shapes.items()}
+        self.m = {n: _dev(_gradient(rng, *s, fall), "f32") for n, s in shapes.items()}
+
+    def values(self):
+        return {n: tuple(None if t is None else host(t).astype(np.float64) for t in (self.p[n], self.g[n], self.m[n], self.master[n]))
+                for n in ("A", "B")}
+
+    def step(self, lr, **kw):
+        qn.qlora_muon_step(self.p["A"], self.p["B"], self.g["A"], self.g["B"], self.m["A"], self.m["B"], lr,
+                           A_master=self.master["A"], B_master=self.master["B"], **kw)
+
+
+def _moved(u, steps, eps, rel):
+    """Bound, in every element, of what a relative change `rel` of u's elements does to
+    the update: to first order the iteration's derivative, at most its largest slope
+    sum of |a| + 3 |b| + 5 |c| per step for singular values up to 1.15, but no more than
+    the slope a at each step for small ones; the observed largest is measured here by
+    the change that random signs make in the reference, times 8 for the worst of many."""
+    rng = np.random.default_rng(1)
+    base = oo.newton_schulz(u, steps, COEFFICIENTS, eps)
+    worst = 0.0
+    for _ in range(2):
+        other = oo.newton_schulz(u * (1 + 1e-6 * rng.choice([-1.0, 1.0], size=u.shape)), steps, COEFFICIENTS, eps)
+        worst = max(worst, np.abs(other - base).max() / 1e-6)
+    return 8 * worst * rel
+
+
+def check(t, before, lr, momentum=0.95, nesterov=True, weight_decay=0.0, scaling="spectral", steps=5, eps=1e-7):
+    for n in ("A", "B"):
+        p, g, m, master = before[n]
+        full = p if master is None else master
+        want, wm, x = oo.muon_step(full, g, m, lr, momentum, nesterov, weight_decay, scaling, steps, COEFFICIENTS, eps)
+        got_m = host(t.m[n]).astype(np.float64)
+        # momentum: one rounding of the exact sum
+        assert (np.abs(got_m - wm) <= 2.0 ** -24 * np.abs(wm) * 1.01 + 1e-45).all(), n
+        u = (1 - momentum) * g + momentum * wm if nesterov else wm
+        factor = np.abs(lr) * {None: 1.0, "spectral": np.sqrt(max(1.0, x.shape[0] / x.shape[1])),
+                               "rms": 0.2 * np.sqrt(max(x.shape))}[scaling]
+        off = factor * _moved(u, steps, eps, 2.0 ** -23) + 1e-12
+        got = host(t.p[n] if master is None else t.master[n]).astype(np.float64)
+        d = HALF[t.name] if master is None else 2.0 ** -24
+        tiny = 2.0 ** -25 if t.name == "f16" and master is None else 0.0
+        worst = np.max(np.abs(got - want) / (1.01 * d * np.abs(want) + off + tiny))
+        say(f"  {n}: worst error / bound {worst:.3f}, allowed beside the rounding {off:.2e}")
+        assert worst <= 1.0, n
+        if master is not None:
+            rounded = host(t.p[n])
+            np.testing.assert_array_equal(rounded, oo.round16(host(t.master[n]), t.name))
+
+
+@pytest.mark.parametrize("K,N,r", [(1, 1, 1), (8, 8, 8), (64, 200, 1), (40, 24, 17), (300, 1000, 16), (1000, 77, 33),
+                                   (17, 4096, 64), (4096, 2000, 64), (130, 500, 65), (700, 333, 128), (1500, 40, 200),
+                                   (515, 1030, 256)])
+def test_update_itself(K, N, r):
+    import torch
+    say(f"muon update K={K} N={N} r={r}")
+    t = Case(K, N, r, "bf16")
+    for n in ("A", "B"):
+        t.master[n].zero_()
+    before = t.values()
+    t.step(1.0, scaling=None)
+    check(t, before, 1.0, scaling=None)
+    # what orthogonalised means: singular values near one where the direction has any
+    if min(K, r) >= 8:
+        sv = torch.linalg.svdvals(t.master["A"].double())
+        assert 0.3 < float(sv[: min(K, r) // 2].min()) and float(sv.max()) < 1.3
+
+
+@pytest.mark.parametrize("name", ["bf16", "f16"])
+@pytest.mark.parametrize("grad", ["f32", "16"])
+@pytest.mark.parametrize("master", [True, False])
+@pytest.mark.parametrize("K,N,r", [(72, 333, 24), (1024, 512, 64), (333, 72, 100)])
+def test_steps(K, N, r, master, grad, name):
+    say(f"muon step K={K} N={N} r={r} {name} grad {grad} master {master}")
+    t = Case(K, N, r, name, name if grad == "16" else "f32", master)
+    for kw in ({"lr": 0.02, "weight_decay": 0.1}, {"lr": 0.01, "nesterov": False, "scaling": "rms", "momentum": 0.0},
+               {"lr": -0.02, "scaling": None, "momentum": 0.9, "steps": 2}):
+        before = t.values()
+        t.step(**kw)
+        check(t, before, **kw)
+
+
+@pytest.mark.parametrize("steps", [0, 1, 2, 3, 4, 7])
+@pytest.mark.parametrize("r", [16, 80])
+def test_numbers_of_steps(steps, r):
+    say(f"muon {steps} steps, r={r}")
+    t = Case(200, 150, r, "bf16")
+    before = t.values()
+    t.step(0.1, steps=steps)
+    check(t, before, 0.1, steps=steps)
+
+
+@pytest.mark.parametrize("r", [16, 72])
+def test_zero_and_tiny_gradients(r):
+    say(f"muon zero and tiny gradients r={r}")
+    t = Case(120, 136, r, "bf16")
+    for n in ("A", "B"):
+        t.g[n].zero_()
+        t.m[n].zero_()
+    before = t.values()
+    t.step(0.1, weight_decay=0.5)
+    for n in ("A", "B"):
+        np.testing.assert_array_equal(host(t.master[n]), (before[n][3] * (1 - 0.1 * 0.5)).astype(np.float32))
+        assert not host(t.m[n]).any()
+    # below eps the direction is divided by eps, not by its norm
+    t = Case(120, 136, r, "bf16")
+    for n in ("A", "B"):
+        t.g[n].mul_(1e-9)
+        t.m[n].mul_(1e-9)
+    before = t.values()
+    t.step(0.1, scaling=None)
+    check(t, before, 0.1, scaling=None)
+
+
+@pytest.mark.parametrize("r", [8, 100])
+def test_directions_of_any_size_and_rank(r):
+    say(f"muon ranks and sizes r={r}")
+    for scale in (1e-15, 1e15):
+        t = Case(200, 90, r, "bf16")
+        for n in ("A", "B"):
+            t.g[n].mul_(scale)
+            t.m[n].mul_(scale)
+        before = t.values()
+        t.step(0.1, eps=1e-30)
+        check(t, before, 0.1, eps=1e-30)
+    # one direction alone: its singular value goes to near one, the others stay zero
+    t = Case(200, 90, r, "bf16")
+    for n in ("A", "B"):
+        a = host(t.g[n])
+        t.g[n].copy_(_dev(np.outer(a[:, 0], a[0]), "f32"))
+        t.m[n].zero_()
+        t.master[n].zero_()
+    before = t.values()
+    t.step(1.0, scaling=None)
+    check(t, before, 1.0, scaling=None)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("r", [16, 80])
+def test_what_is_not_finite_shows(r, bad):
+    import torch
+    say(f"muon with {bad} r={r}")
+    t = Case(100, 130, r, "bf16")
+    t.g["A"][3, 5] = bad
+    t.step(0.1)
+    assert torch.isnan(t.p["A"]).all() and torch.isnan(t.master["A"]).all()
+    assert torch.isfinite(t.p["B"]).all()
+    t2 = Case(100, 130, r, "bf16")
+    t2.step(0.1)
+    assert torch.equal(t.master["B"], t2.master["B"])
