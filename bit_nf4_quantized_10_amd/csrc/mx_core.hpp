@@ -1,0 +1,356 @@
+// A 256 x 256-tile core for products of MXFP4 matrices with gfx950's scaled matrix
+// instructions: out[m][n] = sum_k act[m][k] w[n][k], fp32 sums, four waves (2 x 2) of
+// 128 x 128 each, one wave per SIMD.
+//
+// It is gemm16.hpp's schedule with 256-element stages: 128 bytes a row as there, so
+// the same copies straight from memory to LDS (three slots of activations, two of
+// weights, 160 KB), the same swizzle and the same 16-byte fragments; a stage is two
+// halves of 64 MFMAs over 128 elements.  v_mfma_scale_f32_16x16x128_f8f6f4 takes the
+// time of a 16-bit one of a quarter of its depth, so the copies, LDS reads and
+// barriers cost a product of that depth no more than they do there.
+// The adapter's 16-bit product comes first, its few fragments straight from memory
+// while the first stages' copies are under way.
+// The scales (mxfp4.hpp) go past LDS: a word a lane and tile of 16 rows holds those
+// of four halves, 16 loads of whole lines a wave and two stages, requested two stages
+// ahead.  A tile past the matrix's end takes the last one's scales: its rows are not
+// stored.
+#pragma once
+
+#include <type_traits>
+
+#include "gemm16.hpp"
+#include "mxfp4.hpp"
+
+namespace qn {
+
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// D[w row 4g + e][act row q] += one step's products; operand bytes `s` of the scales.
+template <int s>
+__device__ __forceinline__ f32x4 mfma_mx(const i32x4& w, const i32x4& a, const f32x4& c, uint32_t sw, uint32_t sa) {
+  const i32x8 w8 = __builtin_shufflevector(w, w, 0, 1, 2, 3, -1, -1, -1, -1);
+  const i32x8 a8 = __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, a8, c, 4, 4, s, static_cast<int>(sw), s, static_cast<int>(sa));
+}
+
+// The same in place.  The compiler's own form may put the sum into other registers, and
+// with all 256 accumulation registers taken it then moves and spills them; the asm ties
+// them.  The s_nop stands for the two wait states that an operand just written by a
+// vector instruction needs, which the compiler does not count for asm; what reads the
+// sums afterwards waits for the last of them (CoreMx::run).
+template <int s>
+__device__ __forceinline__ void mfma_mx_in_place(const i32x4& w, const i32x4& a, f32x4& c, uint32_t sw, uint32_t sa) {
+#define QN_MX_MFMA(sel) \
+  asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 " sel " cbsz:4 blgp:4" \
+               : "+a"(c) : "v"(w), "v"(a), "v"(sw), "v"(sa))
+  if constexpr (s == 0) QN_MX_MFMA("op_sel_hi:[0,0,0]");
+  if constexpr (s == 1) QN_MX_MFMA("op_sel:[1,1,0] op_sel_hi:[0,0,0]");
+  if constexpr (s == 2) QN_MX_MFMA("op_sel_hi:[1,1,0]");
+  if constexpr (s == 3) QN_MX_MFMA("op_sel:[1,1,0] op_sel_hi:[1,1,0]");
+#undef QN_MX_MFMA
+}
+
+struct MxProductArgs {
+  MxView act, w;          // M x K, N x K
+  // adapter term, added to the first split: ext_a (M x r) times ext_b (N x r)ᵀ
+  const uint16_t* ext_a;
+  const uint16_t* ext_b;
+  int64_t r;
+  void* out;              // M x N; a split's fp32 planes [splits][M][N]
+  int64_t chunks_per;     // 512-element chunks a split takes (all of them: no split)
+};
+
+constexpr int kMxStage = 256;   // elements
+
+template <class T>
+struct CoreMx {
+  typedef typename T::v8 v8;
+  typedef __attribute__((address_space(3))) char* lds_bytes;
+  typedef __attribute__((address_space(3))) const i32x4* lds_frag;
+  struct Frags {
+    i32x4 a[8], w[8];
+  };
+  struct Scales {
+    uint32_t a[8], w[8];
+  };
+
+  const MxProductArgs& p;
+  char* smem;
+  int lane, wave, q, g, wm, wn;   // lane = 16 g + q
+  // 32-bit and scalar throughout: compares of 64-bit scalars run on the vector units,
+  // which drags what they select, descriptors too, into vector registers
+  int m0, c0, M, N, nb, chunks;
+  Rsrc r_act, r_w, r_sa, r_sw;
+  uint32_t av[8], wv[8];       // copies: row wave*64 + 8j + lane/8, chunk (lane & 7) ^ (lane >> 3)
+  int chunk;                   // that chunk, a block
+  int pA, pW;                  // LDS bytes of fragment 0 at half 0
+  int ia, iw, ra, rw;          // the wave's first scale tiles, at most the last; tiles after them
+  int s_beg, n_full, last;     // first stage, whole stages from it, blocks in front of this share's end
+  uint32_t so;
+
+  __device__ CoreMx(const MxProductArgs& args, char* s) : p(args), smem(s) {
+    const int t = threadIdx.x;
+    lane = t & 63;
+    wave = __builtin_amdgcn_readfirstlane(t >> 6);
+    q = lane & 15;
+    g = lane >> 4;
+    wm = wave >> 1;
+    wn = wave & 1;
+    M = static_cast<int>(p.act.rows);
+    N = static_cast<int>(p.w.rows);
+    nb = static_cast<int>(mx_blocks(p.act.cols));
+    chunks = static_cast<int>(mx_chunks(p.act.cols));
+    {
+      int64_t m, c;
+      tile_origin<256>(m, c);
+      m0 = static_cast<int>(m);
+      c0 = static_cast<int>(c);
+    }
+    r_act = make_rsrc(p.act.codes, mx_code_bytes(M, p.act.cols));
+    r_w = make_rsrc(p.w.codes, mx_code_bytes(N, p.act.cols));
+    r_sa = make_rsrc(p.act.scales, mx_scale_bytes(M, p.act.cols));
+    r_sw = make_rsrc(p.w.scales, mx_scale_bytes(N, p.act.cols));
+    chunk = (lane & 7) ^ (lane >> 3);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int row = wave * 64 + 8 * j + (lane >> 3);
+      const int m = m0 + row, n = c0 + row;
+      av[j] = m < M ? static_cast<uint32_t>(m * nb + chunk) * 16u : kMasked;
+      wv[j] = n < N ? static_cast<uint32_t>(n * nb + chunk) * 16u : kMasked;
+    }
+    const int la = (M - 1) / 16, lw = (N - 1) / 16;
+    ia = min(m0 / 16 + 8 * wm, la);
+    iw = min(c0 / 16 + 8 * wn, lw);
+    ra = la - ia;
+    rw = lw - iw;
+    pA = (wm * 128 + q) * 128 + ((g ^ (q & 7)) << 4);
+    pW = kG16W + (wn * 128 + q) * 128 + ((g ^ (q & 7)) << 4);
+  }
+
+  __device__ void copy_a(int slot, int j) const {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r_act, (lds_ptr_t)(smem + slot + (wave * 64 + 8 * j) * 128), 16, av[j], so, 0, 0);
+  }
+  __device__ void copy_w(int slot, int j) const {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r_w, (lds_ptr_t)(smem + kG16W + slot + (wave * 64 + 8 * j) * 128), 16, wv[j], so, 0, 0);
+  }
+  // Points the copies at stage u (counted from s_beg; called for every stage in turn):
+  // past the whole stages, blocks past the share's end are masked.  Masks stand in the
+  // lanes' own offsets, since a buffer's range check need not count the scalar part.
+  __device__ __forceinline__ void aim(int u) {
+    so = static_cast<uint32_t>(s_beg + u) * 128u;
+    if (u < n_full) return;
+    const bool past = (s_beg + u) * 8 + chunk >= last;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      av[j] = past ? kMasked : av[j];
+      wv[j] = past ? kMasked : wv[j];
+    }
+  }
+  // Scale x (0 .. 7 act, 8 .. 15 weight tiles) of chunk c.
+  __device__ __forceinline__ uint32_t load_scale(int c, int x) const {
+    return x < 8 ? ld32s(r_sa, 4 * lane, static_cast<uint32_t>((ia + min(x, ra)) * chunks + c) * 256u)
+                 : ld32s(r_sw, 4 * lane, static_cast<uint32_t>((iw + min(x - 8, rw)) * chunks + c) * 256u);
+  }
+  // stage u's chunk, at most the last one
+  __device__ int chunk_at(int u) const { return min((s_beg + u) / 2, chunks - 1); }
+
+  // Fragment x in the order of first use: a0, w0 .. w7, a1 .. a7.
+  __device__ void read(int sa, int sw, int half, int x, Frags& F) const {
+    const lds_bytes base = (lds_bytes)smem;
+    if (x == 0 || x > 8) {
+      const int i = x == 0 ? 0 : x - 8;
+      F.a[i] = *(lds_frag)(base + (pA ^ (half << 6)) + sa + i * 2048);
+    } else {
+      F.w[x - 1] = *(lds_frag)(base + (pW ^ (half << 6)) + sw + (x - 1) * 2048);
+    }
+  }
+
+  // 64 MFMAs from Fc with scale bytes kS; meanwhile the 16 reads into Fn and `side`,
+  // called after every MFMA (i, j).
+  template <int kS, class Side>
+  __device__ __forceinline__ void half(const Frags& Fc, Frags& Fn, const Scales& S, int sa, int sw, int h, f32x4 (&acc)[8][8],
+                                       Side side) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        mfma_mx_in_place<kS>(Fc.w[j], Fc.a[i], acc[i][j], S.w[j], S.a[i]);
+        __builtin_amdgcn_sched_barrier(0);
+        const int x = 4 * i + (j >> 1);
+        if ((j & 1) && x < 16) {
+          read(sa, sw, h, x, Fn);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        side(i, j);
+      }
+    }
+  }
+  template <int kInFlight>
+  __device__ __forceinline__ static void meet() {
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(kInFlight, 0));
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  }
+
+  // Stage u from slots sa and sw; the next one's are sa1 and sw1; activations of stage
+  // u+2 go to sa2, its weights to sw.  kPart 0, 1: the first and second stage of a chunk
+  // with scales S; the first requests the next chunk's into Sn.
+  template <int kPart>
+  __device__ __forceinline__ void stage(int u, int sa, int sa1, int sa2, int sw, int sw1, Frags& F0, Frags& F1,
+                                        const Scales& S, Scales& Sn, f32x4 (&acc)[8][8]) {
+    aim(u + 2);
+    const int next = chunk_at(u + 2);
+    half<2 * kPart>(F0, F1, S, sa, sw, 1, acc, [&](int i, int j) {
+      if ((j & 3) == 2 && i < 4) {
+        copy_a(sa2, 2 * i + (j >> 2));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (kPart == 0 && i >= 4 && (j & 1) == 0) {
+        const int x = 4 * (i - 4) + (j >> 1);
+        if (x < 8) Sn.a[x] = load_scale(next, x);
+        else Sn.w[x - 8] = load_scale(next, x);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    });
+    // every wave has read all of stage u (its second half is in registers) and stage
+    // u+1 has landed; the copies and scales requested since may be in flight
+    meet<kPart == 0 ? 24 : 8>();
+    half<2 * kPart + 1>(F1, F0, S, sa1, sw1, 0, acc, [&](int i, int j) {
+      if ((j & 3) == 2 && i < 4) {
+        copy_w(sw, 2 * i + (j >> 2));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    });
+  }
+
+  // The adapter's product into acc.
+  __device__ __forceinline__ void adapter(f32x4 (&acc)[8][8]) const {
+    const int r = static_cast<int>(p.r);
+    const Rsrc re = make_rsrc(p.ext_a, p.act.rows * p.r * 2), rb = make_rsrc(p.ext_b, p.w.rows * p.r * 2);
+#pragma unroll 1
+    for (int j0 = 0; j0 < r; j0 += 32) {
+      const int e = j0 + 8 * g;
+      v8 fa[8], fw[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int m = m0 + wm * 128 + 16 * i + q, n = c0 + wn * 128 + 16 * i + q;
+        fa[i] = __builtin_bit_cast(v8, ld_b128(re, m < M && e < r ? static_cast<uint32_t>(m * r + e) * 2u : kMasked));
+        fw[i] = __builtin_bit_cast(v8, ld_b128(rb, n < N && e < r ? static_cast<uint32_t>(n * r + e) * 2u : kMasked));
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) acc[i][j] = T::mfma16(fw[j], fa[i], acc[i][j]);
+    }
+  }
+
+  // The whole reduction (blockIdx.z's share): clears and fills acc and releases LDS.
+  // acc[i][j]: rows 16 i + q of the wave's 128, columns 16 j + 4 g .. +3.  Stages come in
+  // pairs, a chunk of scales each; the second of the last pair may be past the end.
+  __device__ __forceinline__ void run(f32x4 (&acc)[8][8]) {
+    const int beg = static_cast<int>(blockIdx.z) * static_cast<int>(p.chunks_per);
+    const int end = min(beg + static_cast<int>(p.chunks_per), chunks);
+    s_beg = 2 * beg;
+    last = min(16 * end, nb);
+    n_full = last / 8 - s_beg;
+    Scales S, Sn;
+    const int first = chunk_at(0);
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      S.a[x] = load_scale(first, x);
+      S.w[x] = load_scale(first, 8 + x);
+    }
+    aim(0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      copy_a(0, j);
+      copy_w(0, j);
+    }
+    aim(1);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) copy_a(kTileBytes, j);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+    if (blockIdx.z == 0) adapter(acc);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) asm volatile("" : "+a"(acc[i][j]));
+    Frags F0, F1;
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(8, 0));
+    __builtin_amdgcn_s_barrier();
+#pragma unroll
+    for (int x = 0; x < 16; ++x) read(0, 0, 0, x, F0);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) copy_w(kTileBytes, j);
+    int sa = 0, sa1 = kTileBytes, sa2 = 2 * kTileBytes;
+    for (int u = 0; u < 2 * (end - beg); u += 2) {
+      // two stages: the weights' slots are back where they were, the activations' moved on twice
+      stage<0>(u, sa, sa1, sa2, 0, kTileBytes, F0, F1, S, Sn, acc);
+      stage<1>(u + 1, sa1, sa2, sa, kTileBytes, 0, F0, F1, S, Sn, acc);
+      S = Sn;
+      const int s = sa;
+      sa = sa2;
+      sa2 = sa1;
+      sa1 = s;
+    }
+    __builtin_amdgcn_s_waitcnt(0);
+    __syncthreads();
+    // the last products' results, and the sums in accumulation registers up to here
+    asm volatile("s_nop 15\n\ts_nop 15");
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) asm volatile("" : "+a"(acc[i][j]));
+  }
+
+  // The tile in 16 bits, through LDS so that every store is of whole lines.
+  __device__ __forceinline__ void store16(const f32x4 (&acc)[8][8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int R = wm * 128 + 16 * i + q;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = wn * 16 + 2 * j + (g >> 1);
+        *reinterpret_cast<uint2*>(smem + R * 512 + ((c ^ (R & 31)) << 4) + 8 * (g & 1)) =
+            make_uint2(T::pack2(acc[i][j][0], acc[i][j][1]), T::pack2(acc[i][j][2], acc[i][j][3]));
+      }
+    }
+    __syncthreads();
+    const int c = lane & 31;
+    const int col = c0 + 8 * c;
+#pragma unroll 4
+    for (int u = 0; u < 32; ++u) {
+      const int R = wave * 64 + 2 * u + (lane >> 5);
+      const uint4 v = *reinterpret_cast<const uint4*>(smem + R * 512 + ((c ^ (R & 31)) << 4));
+      if (m0 + R < M && col < N)
+        __builtin_nontemporal_store(__builtin_bit_cast(u32x4, v),
+                                    reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + static_cast<int64_t>(m0 + R) * N + col));
+    }
+  }
+  // In fp32, into this split's plane.
+  __device__ __forceinline__ void store32(const f32x4 (&acc)[8][8]) const {
+    const Rsrc ro = make_rsrc(static_cast<float*>(p.out) + (static_cast<int64_t>(blockIdx.z) * M + m0) * N + c0,
+                              (static_cast<int64_t>(M - m0) * N - c0) * 4);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = wm * 128 + 16 * i + q;
+      const bool row_ok = m0 + row < M;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int col = wn * 128 + 16 * j + 4 * g;
+        const uint32_t voff = row_ok && c0 + col < N ? static_cast<uint32_t>(row) * (4u * N) + 4u * col : kMasked;
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[i][j]), ro, voff, 0, 0);
+      }
+    }
+  }
+};
+
+}  // namespace
+
+}  // namespace qn

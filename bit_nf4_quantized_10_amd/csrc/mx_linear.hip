@@ -6,10 +6,11 @@
 //
 // Direct kernel: a wave computes 64 x 64 outputs with both operands loaded from memory
 // into its fragments, four steps of 128 elements (one word of scales a row) at a time.
-#include <type_traits>
+#include <hip/hip_ext.h>
 
 #include "common.hpp"
 #include "kernels.hpp"
+#include "mx_core.hpp"
 #include "mxfp4.hpp"
 
 namespace qn {
@@ -18,26 +19,6 @@ namespace {
 
 int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-
-// D[w row 4g + e][act row q] += one step's products; operand bytes `s` of the scales.
-template <int s>
-__device__ __forceinline__ f32x4 mfma_mx(const i32x4& w, const i32x4& a, const f32x4& c, uint32_t sw, uint32_t sa) {
-  const i32x8 w8 = __builtin_shufflevector(w, w, 0, 1, 2, 3, -1, -1, -1, -1);
-  const i32x8 a8 = __builtin_shufflevector(a, a, 0, 1, 2, 3, -1, -1, -1, -1);
-  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, a8, c, 4, 4, s, static_cast<int>(sw), s, static_cast<int>(sa));
-}
-
-struct MxProductArgs {
-  MxView act, w;          // M x K, N x K
-  const uint16_t* ext_a;  // adapter term: M x r times (ext_b: N x r)ᵀ, or null
-  const uint16_t* ext_b;
-  int64_t r;
-  float* part;            // [splits][M][N]
-  int64_t chunks_per;     // 512-element chunks a split takes
-};
-
 template <class T>
 __global__ __launch_bounds__(256) void mx_direct_kernel(MxProductArgs p) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane & 15, g = lane >> 4;
@@ -99,7 +80,7 @@ __global__ __launch_bounds__(256) void mx_direct_kernel(MxProductArgs p) {
         for (int j = 0; j < 4; ++j) acc[i][j] = T::mfma16(fw[j], fa[i], acc[i][j]);
     }
   }
-  float* out = p.part + static_cast<int64_t>(blockIdx.z) * M * N;
+  float* out = static_cast<float*>(p.out) + static_cast<int64_t>(blockIdx.z) * M * N;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int64_t m = m0 + 16 * i + q;
@@ -109,6 +90,16 @@ __global__ __launch_bounds__(256) void mx_direct_kernel(MxProductArgs p) {
       if (m < M && n < N) *reinterpret_cast<f32x4*>(out + m * N + n) = acc[i][j];
     }
   }
+}
+
+template <class T, bool k32>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void mx_tile_kernel(MxProductArgs p) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  CoreMx<T> k(p, smem);
+  f32x4 acc[8][8];
+  k.run(acc);
+  if constexpr (k32) k.store32(acc);
+  else k.store16(acc);
 }
 
 // out = the sum of the splits' fp32 planes in order, in the output's type.
@@ -121,16 +112,58 @@ __global__ __launch_bounds__(256) void mx_sum32_kernel(const float* __restrict__
   }
 }
 
-// Splits of the reduction, by chunks: enough that the device is filled.
+// How a product runs: by the direct kernel or by tiles, in how many splits of the
+// reduction (by chunks); part_bytes: the splits' fp32 planes.
 struct MxPlan {
+  bool tiles;
   int64_t splits, chunks_per, part_bytes;
 };
+#ifndef QN_MX_DIRECT_M
+#define QN_MX_DIRECT_M 64
+#endif
+#ifndef QN_MX_STAGE_US
+#define QN_MX_STAGE_US 1.2
+#endif
 MxPlan plan_mx(int64_t M, int64_t N, int64_t K) {
-  const int64_t tiles = cdiv(M, 64) * cdiv(N, 256), chunks = mx_chunks(K);
-  int64_t s = cdiv(512, tiles);
-  s = s > chunks ? chunks : s;
-  const int64_t per = cdiv(chunks, s), splits = cdiv(chunks, per);
-  return MxPlan{splits, per, align256(splits * M * N * 4)};
+  const int64_t chunks = mx_chunks(K);
+  MxPlan pl{M > QN_MX_DIRECT_M, 1, chunks, 0};
+  if (!pl.tiles) {
+    const int64_t wgs = cdiv(M, 64) * cdiv(N, 256);
+    int64_t s = cdiv(512, wgs);
+    s = s > chunks ? chunks : s;
+    pl.chunks_per = cdiv(chunks, s);
+    pl.splits = cdiv(chunks, pl.chunks_per);
+    pl.part_bytes = align256(pl.splits * M * N * 4);
+    return pl;
+  }
+  // the split of least estimated time, as plan_split16's: rounds of 256 tiles, the
+  // partials through memory twice and one more launch
+  constexpr double kStageUs = QN_MX_STAGE_US, kTileUs = 5.0, kBytesPerUs = 5e6, kLaunchUs = 4.0;
+  const int64_t tiles = cdiv(M, 256) * cdiv(N, 256), plane = M * N * 4;
+  double least = 2 * kStageUs * chunks + kTileUs;
+  if (tiles >= 256) return pl;
+  for (int64_t s = 2; s <= chunks && s <= 64 && s * tiles <= 1024; ++s) {
+    const int64_t per = cdiv(chunks, s), splits = cdiv(chunks, per);
+    if (splits * plane > (int64_t(1) << 28)) break;
+    const double us = cdiv(tiles * splits, 256) * (2 * kStageUs * per + kTileUs) + static_cast<double>(splits * plane) * (2.0 / kBytesPerUs) +
+                      kLaunchUs + 0.1 * splits;
+    if (us >= least) continue;
+    least = us;
+    pl.splits = splits;
+    pl.chunks_per = per;
+    pl.part_bytes = align256(splits * plane);
+  }
+  return pl;
+}
+
+template <class T, bool k32>
+hipError_t launch_mx_tiles_t(const MxProductArgs& p, int64_t splits, hipStream_t stream, const Timer& tm) {
+  static const hipError_t lds_limit = hipFuncSetAttribute(reinterpret_cast<const void*>(&mx_tile_kernel<T, k32>),
+                                                          hipFuncAttributeMaxDynamicSharedMemorySize, kG16Lds);
+  if (lds_limit != hipSuccess) return lds_limit;
+  const dim3 grid(static_cast<unsigned>(cdiv(p.w.rows, 256)), static_cast<unsigned>(cdiv(p.act.rows, 256)), static_cast<unsigned>(splits));
+  hipExtLaunchKernelGGL((mx_tile_kernel<T, k32>), grid, dim3(kThreads), kG16Lds, stream, tm.start(), tm.end(), 0, p);
+  return hipGetLastError();
 }
 
 // out_type: NF4_OUT_*; the adapter's operands are of the 16-bit type dtype.
@@ -138,21 +171,32 @@ hipError_t mx_product(MxView act, MxView w, const uint16_t* ext_a, const uint16_
                       int out_type, void* out, void* ws, hipStream_t stream) {
   const int64_t M = act.rows, N = w.rows;
   const MxPlan pl = plan_mx(M, N, act.cols);
-  MxProductArgs p{act, w, ext_a, ext_b, r, static_cast<float*>(ws), pl.chunks_per};
-  const dim3 grid(static_cast<unsigned>(cdiv(N, 256)), static_cast<unsigned>(cdiv(M, 64)), static_cast<unsigned>(pl.splits));
+  const bool parts = !pl.tiles || pl.splits > 1;
+  MxProductArgs p{act, w, ext_a, ext_b, r, parts ? ws : out, pl.chunks_per};
+  hipError_t e;
   {
-    Timer tm(QK_MX_GEMM, stream);
-    hipLaunchKernelGGL((dtype == kDtypeF16 ? mx_direct_kernel<F16> : mx_direct_kernel<Bf16>), grid, dim3(256), 0, stream, p);
-    tm.stop();
+    const Timer tm(QK_MX_GEMM, stream, true);
+    if (pl.tiles) {
+      const bool k32 = parts || out_type == NF4_OUT_F32;
+      if (dtype == kDtypeF16) e = k32 ? launch_mx_tiles_t<F16, true>(p, pl.splits, stream, tm) : launch_mx_tiles_t<F16, false>(p, pl.splits, stream, tm);
+      else e = k32 ? launch_mx_tiles_t<Bf16, true>(p, pl.splits, stream, tm) : launch_mx_tiles_t<Bf16, false>(p, pl.splits, stream, tm);
+    } else {
+      const dim3 grid(static_cast<unsigned>(cdiv(N, 256)), static_cast<unsigned>(cdiv(M, 64)), static_cast<unsigned>(pl.splits));
+      hipExtLaunchKernelGGL((dtype == kDtypeF16 ? mx_direct_kernel<F16> : mx_direct_kernel<Bf16>), grid, dim3(256), 0, stream,
+                            tm.start(), tm.end(), 0, p);
+      e = hipGetLastError();
+    }
   }
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (e != hipSuccess || !parts) return e;
+  const float* part = static_cast<const float*>(ws);
   if (out_type != NF4_OUT_F32)
-    return launch_split_sum(p.part, pl.splits, M * N, static_cast<uint16_t*>(out), stream,
+    return launch_split_sum(part, pl.splits, M * N, static_cast<uint16_t*>(out), stream,
                             out_type == NF4_OUT_F16 ? kDtypeF16 : kDtypeBf16);
   const int64_t blocks = cdiv(M * N, 1024);
-  hipLaunchKernelGGL(mx_sum32_kernel, dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096)), dim3(256), 0, stream, p.part,
+  Timer tm(QK_REDUCE, stream);
+  hipLaunchKernelGGL(mx_sum32_kernel, dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096)), dim3(256), 0, stream, part,
                      pl.splits, M * N, static_cast<float*>(out));
+  tm.stop();
   return hipGetLastError();
 }
 
@@ -161,7 +205,7 @@ hipError_t mx_product(MxView act, MxView w, const uint16_t* ext_a, const uint16_
 int64_t mx_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K) { return plan_mx(M, N, K).part_bytes; }
 
 hipError_t launch_mx_matmul(MxView p, MxView q, int out_type, void* out, void* ws, hipStream_t stream) {
-  return mx_product(p, q, nullptr, nullptr, 0, kDtypeBf16, out_type, out, ws, stream);
+  return mx_product(p, q, nullptr, nullptr, 0, out_type == NF4_OUT_F16 ? kDtypeF16 : kDtypeBf16, out_type, out, ws, stream);
 }
 
 // Workspace of the forward: Aᵀ, Z's partials, (c B)ᵀ, X's codes and scales, the
