@@ -4,16 +4,20 @@
 //
 // It is gemm16.hpp's schedule with 256-element stages: 128 bytes a row as there, so
 // the same copies straight from memory to LDS (three slots of activations, two of
-// weights, 160 KB), the same swizzle and the same 16-byte fragments; a stage is two
-// halves of 64 MFMAs over 128 elements.  v_mfma_scale_f32_16x16x128_f8f6f4 takes the
-// time of a 16-bit one of a quarter of its depth, so the copies, LDS reads and
-// barriers cost a product of that depth no more than they do there.
-// The adapter's 16-bit product comes first, its few fragments straight from memory
-// while the first stages' copies are under way.
-// The scales (mxfp4.hpp) go past LDS: a word a lane and tile of 16 rows holds those
-// of four halves, 16 loads of whole lines a wave and two stages, requested two stages
-// ahead.  A tile past the matrix's end takes the last one's scales: its rows are not
-// stored.
+// weights, 160 KB) and 16-byte fragments; a stage is two halves of 32 MFMAs over 128
+// elements.  v_mfma_scale_f32_32x32x64_f8f6f4 takes the time of a 16-bit one of a
+// quarter of its depth, and half a dozen other instructions fit between two of them;
+// the 16 x 16 x 128 one with its scales issues twice as often and left no room (1.75
+// us a stage).
+//
+// A lane (i, h) = 32 h + i holds row i of a tile of 32 and in each step one block.  The
+// stored order of the scales (mxfp4.hpp) gives it words of blocks g, 4 + g, 8 + g, 12 + g:
+// with g = h for the first half of a stage and g = 2 + h for the second, the steps of
+// stage p of two take bytes 2p and 2p + 1, and chunks h, 4 + h, 2 + h, 6 + h of the
+// rows' eight.  Scales go past LDS, two words a lane and tile for two stages, requested
+// two stages ahead.  A tile past the matrix's end takes the last one's scales: its rows
+// are not stored.  The adapter's 16-bit product comes first, its few fragments straight
+// from memory while the first stages' copies are under way.
 #pragma once
 
 #include <type_traits>
@@ -28,7 +32,7 @@ namespace {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
-// D[w row 4g + e][act row q] += one step's products; operand bytes `s` of the scales.
+// One 16 x 16 x 128 step, operand bytes `s` of the scales: D[w row 4g + e][act row q].
 template <int s>
 __device__ __forceinline__ f32x4 mfma_mx(const i32x4& w, const i32x4& a, const f32x4& c, uint32_t sw, uint32_t sa) {
   const i32x8 w8 = __builtin_shufflevector(w, w, 0, 1, 2, 3, -1, -1, -1, -1);
@@ -36,15 +40,15 @@ __device__ __forceinline__ f32x4 mfma_mx(const i32x4& w, const i32x4& a, const f
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(w8, a8, c, 4, 4, s, static_cast<int>(sw), s, static_cast<int>(sa));
 }
 
-// The same in place.  The compiler's own form may put the sum into other registers, and
-// with all 256 accumulation registers taken it then moves and spills them; the asm ties
-// them.  The s_nop stands for the two wait states that an operand just written by a
-// vector instruction needs, which the compiler does not count for asm; what reads the
-// sums afterwards waits for the last of them (CoreMx::run).
+// One 32 x 32 x 64 step, in place.  The compiler's own form may put the sum into other
+// registers, and with all 256 accumulation registers taken it then moves and spills
+// them; the asm ties them.  The s_nop stands for the two wait states that an operand just
+// written by a vector instruction needs, which the compiler does not count for asm; what
+// reads the sums afterwards waits for the last of them (CoreMx::run).
 template <int s>
-__device__ __forceinline__ void mfma_mx_in_place(const i32x4& w, const i32x4& a, f32x4& c, uint32_t sw, uint32_t sa) {
+__device__ __forceinline__ void mfma_mx_in_place(const i32x4& w, const i32x4& a, f32x16& c, uint32_t sw, uint32_t sa) {
 #define QN_MX_MFMA(sel) \
-  asm volatile("s_nop 1\n\tv_mfma_scale_f32_16x16x128_f8f6f4 %0, %1, %2, %0, %3, %4 " sel " cbsz:4 blgp:4" \
+  asm volatile("s_nop 1\n\tv_mfma_scale_f32_32x32x64_f8f6f4 %0, %1, %2, %0, %3, %4 " sel " cbsz:4 blgp:4" \
                : "+a"(c) : "v"(w), "v"(a), "v"(sw), "v"(sa))
   if constexpr (s == 0) QN_MX_MFMA("op_sel_hi:[0,0,0]");
   if constexpr (s == 1) QN_MX_MFMA("op_sel:[1,1,0] op_sel_hi:[0,0,0]");
@@ -71,23 +75,22 @@ struct CoreMx {
   typedef __attribute__((address_space(3))) char* lds_bytes;
   typedef __attribute__((address_space(3))) const i32x4* lds_frag;
   struct Frags {
-    i32x4 a[8], w[8];
+    i32x4 a[2][4], w[2][4];      // two steps' tiles
   };
   struct Scales {
-    uint32_t a[8], w[8];
+    uint32_t a[2][4], w[2][4];   // a stage's halves' tiles
   };
 
   const MxProductArgs& p;
   char* smem;
-  int lane, wave, q, g, wm, wn;   // lane = 16 g + q
+  int lane, wave, i32, h, wm, wn;   // lane = 32 h + i32
   // 32-bit and scalar throughout: compares of 64-bit scalars run on the vector units,
   // which drags what they select, descriptors too, into vector registers
   int m0, c0, M, N, nb, chunks;
   Rsrc r_act, r_w, r_sa, r_sw;
-  uint32_t av[8], wv[8];       // copies: row wave*64 + 8j + lane/8, chunk (lane & 7) ^ (lane >> 3)
-  int chunk;                   // that chunk, a block
-  int pA, pW;                  // LDS bytes of fragment 0 at half 0
-  int ia, iw, ra, rw;          // the wave's first scale tiles, at most the last; tiles after them
+  uint32_t av[8], wv[8];       // copies: row wave*64 + 8j + lane/8, chunk_of(j)
+  int pA, pW;                  // LDS bytes of fragment 0 at step 0
+  uint32_t va[4], vw[4];       // bytes of this lane's scale words of the wave's tiles, chunk 0
   int s_beg, n_full, last;     // first stage, whole stages from it, blocks in front of this share's end
   uint32_t so;
 
@@ -95,8 +98,8 @@ struct CoreMx {
     const int t = threadIdx.x;
     lane = t & 63;
     wave = __builtin_amdgcn_readfirstlane(t >> 6);
-    q = lane & 15;
-    g = lane >> 4;
+    i32 = lane & 31;
+    h = lane >> 5;
     wm = wave >> 1;
     wn = wave & 1;
     M = static_cast<int>(p.act.rows);
@@ -113,23 +116,28 @@ struct CoreMx {
     r_w = make_rsrc(p.w.codes, mx_code_bytes(N, p.act.cols));
     r_sa = make_rsrc(p.act.scales, mx_scale_bytes(M, p.act.cols));
     r_sw = make_rsrc(p.w.scales, mx_scale_bytes(N, p.act.cols));
-    chunk = (lane & 7) ^ (lane >> 3);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int row = wave * 64 + 8 * j + (lane >> 3);
       const int m = m0 + row, n = c0 + row;
-      av[j] = m < M ? static_cast<uint32_t>(m * nb + chunk) * 16u : kMasked;
-      wv[j] = n < N ? static_cast<uint32_t>(n * nb + chunk) * 16u : kMasked;
+      av[j] = m < M ? static_cast<uint32_t>(m * nb + chunk_of(j)) * 16u : kMasked;
+      wv[j] = n < N ? static_cast<uint32_t>(n * nb + chunk_of(j)) * 16u : kMasked;
     }
     const int la = (M - 1) / 16, lw = (N - 1) / 16;
-    ia = min(m0 / 16 + 8 * wm, la);
-    iw = min(c0 / 16 + 8 * wn, lw);
-    ra = la - ia;
-    rw = lw - iw;
-    pA = (wm * 128 + q) * 128 + ((g ^ (q & 7)) << 4);
-    pW = kG16W + (wn * 128 + q) * 128 + ((g ^ (q & 7)) << 4);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int ia = m0 / 16 + 8 * wm + 2 * i + (i32 >> 4), iw = c0 / 16 + 8 * wn + 2 * i + (i32 >> 4);
+      va[i] = static_cast<uint32_t>(min(ia, la) * chunks) * 256u + 4 * (16 * h + (i32 & 15));
+      vw[i] = static_cast<uint32_t>(min(iw, lw) * chunks) * 256u + 4 * (16 * h + (i32 & 15));
+    }
+    pA = (wm * 128 + i32) * 128 + ((h ^ swz(i32)) << 4);
+    pW = kG16W + (wn * 128 + i32) * 128 + ((h ^ swz(i32)) << 4);
   }
 
+  // Chunk c of row R lies at c ^ swz(R): 16 lanes' reads, 16 rows of one chunk, fall on
+  // all 64 banks once (R & 7 alone took twice the cycles).
+  __device__ static int swz(int row) { return (row ^ ((row >> 3) & 3)) & 7; }
+  __device__ int chunk_of(int j) const { return (lane & 7) ^ swz(8 * j + (lane >> 3)); }
   __device__ void copy_a(int slot, int j) const {
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r_act, (lds_ptr_t)(smem + slot + (wave * 64 + 8 * j) * 128), 16, av[j], so, 0, 0);
   }
@@ -142,51 +150,67 @@ struct CoreMx {
   __device__ __forceinline__ void aim(int u) {
     so = static_cast<uint32_t>(s_beg + u) * 128u;
     if (u < n_full) return;
-    const bool past = (s_beg + u) * 8 + chunk >= last;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
+      const bool past = (s_beg + u) * 8 + chunk_of(j) >= last;
       av[j] = past ? kMasked : av[j];
       wv[j] = past ? kMasked : wv[j];
     }
   }
-  // Scale x (0 .. 7 act, 8 .. 15 weight tiles) of chunk c.
-  __device__ __forceinline__ uint32_t load_scale(int c, int x) const {
-    return x < 8 ? ld32s(r_sa, 4 * lane, static_cast<uint32_t>((ia + min(x, ra)) * chunks + c) * 256u)
-                 : ld32s(r_sw, 4 * lane, static_cast<uint32_t>((iw + min(x - 8, rw)) * chunks + c) * 256u);
+  // Scale word x of chunk c: of the act (x < 8) or weight tiles, first the words of the
+  // stages' first halves.
+  __device__ __forceinline__ void load_scale(int c, int x, Scales& S) const {
+    const uint32_t at = static_cast<uint32_t>(c) * 256u + ((x >> 2) & 1) * 128u;
+    if (x < 8) S.a[(x >> 2) & 1][x & 3] = ld32s(r_sa, va[x & 3], at);
+    else S.w[(x >> 2) & 1][x & 3] = ld32s(r_sw, vw[x & 3], at);
   }
   // stage u's chunk, at most the last one
   __device__ int chunk_at(int u) const { return min((s_beg + u) / 2, chunks - 1); }
 
-  // Fragment x in the order of first use: a0, w0 .. w7, a1 .. a7.
+  // Fragment x (0 .. 15) of a half, in the order of first use: of each of its steps a0,
+  // w0 .. w3, a1 .. a3.
   __device__ void read(int sa, int sw, int half, int x, Frags& F) const {
     const lds_bytes base = (lds_bytes)smem;
-    if (x == 0 || x > 8) {
-      const int i = x == 0 ? 0 : x - 8;
-      F.a[i] = *(lds_frag)(base + (pA ^ (half << 6)) + sa + i * 2048);
+    const int t = x >> 3, y = x & 7, turn = (t << 6) ^ (half << 5);   // chunk bits 4 and 2
+    if (y == 0 || y > 4) {
+      const int i = y == 0 ? 0 : y - 4;
+      F.a[t][i] = *(lds_frag)(base + (pA ^ turn) + sa + i * 4096);
     } else {
-      F.w[x - 1] = *(lds_frag)(base + (pW ^ (half << 6)) + sw + (x - 1) * 2048);
+      F.w[t][y - 1] = *(lds_frag)(base + (pW ^ turn) + sw + (y - 1) * 4096);
     }
   }
 
-  // 64 MFMAs from Fc with scale bytes kS; meanwhile the 16 reads into Fn and `side`,
-  // called after every MFMA (i, j).
-  template <int kS, class Side>
-  __device__ __forceinline__ void half(const Frags& Fc, Frags& Fn, const Scales& S, int sa, int sw, int h, f32x4 (&acc)[8][8],
+  // 32 MFMAs from Fc, half kHalf of stage kPart; meanwhile the 16 reads of half `next`
+  // into Fn and `side`, called after every MFMA x.
+  template <int kPart, int kHalf, class Side>
+  __device__ __forceinline__ void half(const Frags& Fc, Frags& Fn, const Scales& S, int sa, int sw, int next, f32x16 (&acc)[4][4],
                                        Side side) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        mfma_mx_in_place<kS>(Fc.w[j], Fc.a[i], acc[i][j], S.w[j], S.a[i]);
+      for (int j = 0; j < 4; ++j) {
+        mfma_mx_in_place<2 * kPart>(Fc.w[0][j], Fc.a[0][i], acc[i][j], S.w[kHalf][j], S.a[kHalf][i]);
         __builtin_amdgcn_sched_barrier(0);
-        const int x = 4 * i + (j >> 1);
-        if ((j & 1) && x < 16) {
-          read(sa, sw, h, x, Fn);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        side(i, j);
+        between(sa, sw, next, 4 * i + j, Fn, side);
       }
     }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        mfma_mx_in_place<2 * kPart + 1>(Fc.w[1][j], Fc.a[1][i], acc[i][j], S.w[kHalf][j], S.a[kHalf][i]);
+        __builtin_amdgcn_sched_barrier(0);
+        between(sa, sw, next, 16 + 4 * i + j, Fn, side);
+      }
+    }
+  }
+  template <class Side>
+  __device__ __forceinline__ void between(int sa, int sw, int next, int x, Frags& Fn, Side side) const {
+    if (x < 16) {
+      read(sa, sw, next, x, Fn);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    side(x);
   }
   template <int kInFlight>
   __device__ __forceinline__ static void meet() {
@@ -200,57 +224,60 @@ struct CoreMx {
   // with scales S; the first requests the next chunk's into Sn.
   template <int kPart>
   __device__ __forceinline__ void stage(int u, int sa, int sa1, int sa2, int sw, int sw1, Frags& F0, Frags& F1,
-                                        const Scales& S, Scales& Sn, f32x4 (&acc)[8][8]) {
+                                        const Scales& S, Scales& Sn, f32x16 (&acc)[4][4]) {
     aim(u + 2);
     const int next = chunk_at(u + 2);
-    half<2 * kPart>(F0, F1, S, sa, sw, 1, acc, [&](int i, int j) {
-      if ((j & 3) == 2 && i < 4) {
-        copy_a(sa2, 2 * i + (j >> 2));
+    half<kPart, 0>(F0, F1, S, sa, sw, 1, acc, [&](int x) {
+      if (x < 16 && (x & 1)) {
+        copy_a(sa2, x >> 1);
         __builtin_amdgcn_sched_barrier(0);
       }
-      if (kPart == 0 && i >= 4 && (j & 1) == 0) {
-        const int x = 4 * (i - 4) + (j >> 1);
-        if (x < 8) Sn.a[x] = load_scale(next, x);
-        else Sn.w[x - 8] = load_scale(next, x);
+      if (kPart == 0 && x >= 16) {
+        load_scale(next, x - 16, Sn);
         __builtin_amdgcn_sched_barrier(0);
       }
     });
     // every wave has read all of stage u (its second half is in registers) and stage
     // u+1 has landed; the copies and scales requested since may be in flight
     meet<kPart == 0 ? 24 : 8>();
-    half<2 * kPart + 1>(F1, F0, S, sa1, sw1, 0, acc, [&](int i, int j) {
-      if ((j & 3) == 2 && i < 4) {
-        copy_w(sw, 2 * i + (j >> 2));
+    half<kPart, 1>(F1, F0, S, sa1, sw1, 0, acc, [&](int x) {
+      if (x < 16 && (x & 1)) {
+        copy_w(sw, x >> 1);
         __builtin_amdgcn_sched_barrier(0);
       }
     });
   }
 
   // The adapter's product into acc.
-  __device__ __forceinline__ void adapter(f32x4 (&acc)[8][8]) const {
+  __device__ __forceinline__ void adapter(f32x16 (&acc)[4][4]) const {
     const int r = static_cast<int>(p.r);
     const Rsrc re = make_rsrc(p.ext_a, p.act.rows * p.r * 2), rb = make_rsrc(p.ext_b, p.w.rows * p.r * 2);
 #pragma unroll 1
     for (int j0 = 0; j0 < r; j0 += 32) {
-      const int e = j0 + 8 * g;
-      v8 fa[8], fw[8];
+      v8 fa[2][4], fw[2][4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int m = m0 + wm * 128 + 16 * i + q, n = c0 + wn * 128 + 16 * i + q;
-        fa[i] = __builtin_bit_cast(v8, ld_b128(re, m < M && e < r ? static_cast<uint32_t>(m * r + e) * 2u : kMasked));
-        fw[i] = __builtin_bit_cast(v8, ld_b128(rb, n < N && e < r ? static_cast<uint32_t>(n * r + e) * 2u : kMasked));
+      for (int t = 0; t < 2; ++t) {
+        const int e = j0 + 16 * t + 8 * h;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int m = m0 + wm * 128 + 32 * i + i32, n = c0 + wn * 128 + 32 * i + i32;
+          fa[t][i] = __builtin_bit_cast(v8, ld_b128(re, m < M && e < r ? static_cast<uint32_t>(m * r + e) * 2u : kMasked));
+          fw[t][i] = __builtin_bit_cast(v8, ld_b128(rb, n < N && e < r ? static_cast<uint32_t>(n * r + e) * 2u : kMasked));
+        }
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i)
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) acc[i][j] = T::mfma16(fw[j], fa[i], acc[i][j]);
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[i][j] = T::mfma32(fw[t][j], fa[t][i], acc[i][j]);
     }
   }
 
   // The whole reduction (blockIdx.z's share): clears and fills acc and releases LDS.
-  // acc[i][j]: rows 16 i + q of the wave's 128, columns 16 j + 4 g .. +3.  Stages come in
-  // pairs, a chunk of scales each; the second of the last pair may be past the end.
-  __device__ __forceinline__ void run(f32x4 (&acc)[8][8]) {
+  // acc[i][j][4 x + e]: row 32 i + i32 of the wave's 128, column 32 j + 8 x + 4 h + e.  Stages
+  // come in pairs, a chunk of scales each; the second of the last pair may be past the end.
+  __device__ __forceinline__ void run(f32x16 (&acc)[4][4]) {
     const int beg = static_cast<int>(blockIdx.z) * static_cast<int>(p.chunks_per);
     const int end = min(beg + static_cast<int>(p.chunks_per), chunks);
     s_beg = 2 * beg;
@@ -259,10 +286,7 @@ struct CoreMx {
     Scales S, Sn;
     const int first = chunk_at(0);
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      S.a[x] = load_scale(first, x);
-      S.w[x] = load_scale(first, 8 + x);
-    }
+    for (int x = 0; x < 16; ++x) load_scale(first, x, S);
     aim(0);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -273,14 +297,16 @@ struct CoreMx {
 #pragma unroll
     for (int j = 0; j < 8; ++j) copy_a(kTileBytes, j);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
     if (blockIdx.z == 0) adapter(acc);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) asm volatile("" : "+a"(acc[i][j]));
+      for (int j = 0; j < 4; ++j) asm volatile("" : "+a"(acc[i][j]));
     Frags F0, F1;
     __builtin_amdgcn_s_waitcnt(waitcnt_imm(8, 0));
     __builtin_amdgcn_s_barrier();
@@ -304,22 +330,25 @@ struct CoreMx {
     // the last products' results, and the sums in accumulation registers up to here
     asm volatile("s_nop 15\n\ts_nop 15");
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) asm volatile("" : "+a"(acc[i][j]));
+      for (int j = 0; j < 4; ++j) asm volatile("" : "+a"(acc[i][j]));
   }
 
   // The tile in 16 bits, through LDS so that every store is of whole lines.
-  __device__ __forceinline__ void store16(const f32x4 (&acc)[8][8]) const {
+  __device__ __forceinline__ void store16(const f32x16 (&acc)[4][4]) const {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int R = wm * 128 + 16 * i + q;
+    for (int i = 0; i < 4; ++i) {
+      const int R = wm * 128 + 32 * i + i32;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int c = wn * 16 + 2 * j + (g >> 1);
-        *reinterpret_cast<uint2*>(smem + R * 512 + ((c ^ (R & 31)) << 4) + 8 * (g & 1)) =
-            make_uint2(T::pack2(acc[i][j][0], acc[i][j][1]), T::pack2(acc[i][j][2], acc[i][j][3]));
-      }
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int c = wn * 16 + 4 * j + x;
+          const f32x16& v = acc[i][j];
+          *reinterpret_cast<uint2*>(smem + R * 512 + ((c ^ i32) << 4) + 8 * h) =
+              make_uint2(T::pack2(v[4 * x], v[4 * x + 1]), T::pack2(v[4 * x + 2], v[4 * x + 3]));
+        }
     }
     __syncthreads();
     const int c = lane & 31;
@@ -334,19 +363,23 @@ struct CoreMx {
     }
   }
   // In fp32, into this split's plane.
-  __device__ __forceinline__ void store32(const f32x4 (&acc)[8][8]) const {
+  __device__ __forceinline__ void store32(const f32x16 (&acc)[4][4]) const {
     const Rsrc ro = make_rsrc(static_cast<float*>(p.out) + (static_cast<int64_t>(blockIdx.z) * M + m0) * N + c0,
                               (static_cast<int64_t>(M - m0) * N - c0) * 4);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int row = wm * 128 + 16 * i + q;
+    for (int i = 0; i < 4; ++i) {
+      const int row = wm * 128 + 32 * i + i32;
       const bool row_ok = m0 + row < M;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int col = wn * 128 + 16 * j + 4 * g;
-        const uint32_t voff = row_ok && c0 + col < N ? static_cast<uint32_t>(row) * (4u * N) + 4u * col : kMasked;
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, acc[i][j]), ro, voff, 0, 0);
-      }
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int col = wn * 128 + 32 * j + 8 * x + 4 * h;
+          const f32x16& v = acc[i][j];
+          const uint32_t voff = row_ok && c0 + col < N ? static_cast<uint32_t>(row) * (4u * N) + 4u * col : kMasked;
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, f32x4{v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]}), ro,
+                                                 voff, 0, 0);
+        }
     }
   }
 };

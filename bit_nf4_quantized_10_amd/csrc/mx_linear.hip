@@ -96,7 +96,7 @@ template <class T, bool k32>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void mx_tile_kernel(MxProductArgs p) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
   CoreMx<T> k(p, smem);
-  f32x4 acc[8][8];
+  f32x16 acc[4][4];
   k.run(acc);
   if constexpr (k32) k.store32(acc);
   else k.store16(acc);
