@@ -4,8 +4,7 @@
 // Every product runs on v_mfma_scale_f32_16x16x128_f8f6f4, whose operand is a lane's
 // block of 32 elements with its scale (mxfp4.hpp): nothing is decoded.
 //
-// Direct kernel: a wave computes 64 x 64 outputs with both operands loaded from memory
-// into its fragments, four steps of 128 elements (one word of scales a row) at a time.
+// Many rows run by 256 x 256 tiles (mx_core.hpp), few by mx_gemv.hip's kernel.
 #include <hip/hip_ext.h>
 
 #include "common.hpp"
@@ -19,79 +18,6 @@ namespace {
 
 int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-template <class T>
-__global__ __launch_bounds__(256) void mx_direct_kernel(MxProductArgs p) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane & 15, g = lane >> 4;
-  const int64_t M = p.act.rows, N = p.w.rows, K = p.act.cols;
-  const int64_t nb = mx_blocks(K), chunks = mx_chunks(K);
-  const int64_t n0 = (static_cast<int64_t>(blockIdx.x) * 4 + wave) * 64, m0 = static_cast<int64_t>(blockIdx.y) * 64;
-  if (n0 >= N) return;
-  const Rsrc ra = make_rsrc(p.act.codes, M * nb * 16), rw = make_rsrc(p.w.codes, N * nb * 16);
-  const Rsrc rsa = make_rsrc(p.act.scales, mx_scale_bytes(M, K)), rsw = make_rsrc(p.w.scales, mx_scale_bytes(N, K));
-  f32x4 acc[4][4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  const int64_t c0 = static_cast<int64_t>(blockIdx.z) * p.chunks_per;
-  const int64_t c1 = c0 + p.chunks_per < chunks ? c0 + p.chunks_per : chunks;
-  for (int64_t c = c0; c < c1; ++c) {
-    uint32_t sa[4], sw[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // tiles past the last one are past the buffer's end: zeros
-      sa[i] = ld_b32(rsa, static_cast<uint32_t>(((m0 / 16 + i) * chunks + c) * 256 + 4 * lane));
-      sw[i] = ld_b32(rsw, static_cast<uint32_t>(((n0 / 16 + i) * chunks + c) * 256 + 4 * lane));
-    }
-    auto step = [&](auto tag) {
-      constexpr int s = decltype(tag)::value;
-      const int64_t b = c * 16 + 4 * s + g;
-      i32x4 fa[4], fw[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + 16 * i + q, n = n0 + 16 * i + q;
-        fa[i] = __builtin_bit_cast(i32x4, ld_b128(ra, m < M && b < nb ? static_cast<uint32_t>((m * nb + b) * 16) : kMasked));
-        fw[i] = __builtin_bit_cast(i32x4, ld_b128(rw, n < N && b < nb ? static_cast<uint32_t>((n * nb + b) * 16) : kMasked));
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = mfma_mx<s>(fw[j], fa[i], acc[i][j], sw[j], sa[i]);
-    };
-    step(std::integral_constant<int, 0>{});
-    step(std::integral_constant<int, 1>{});
-    step(std::integral_constant<int, 2>{});
-    step(std::integral_constant<int, 3>{});
-  }
-  if (blockIdx.z == 0 && p.r > 0) {
-    const Rsrc re = make_rsrc(p.ext_a, M * p.r * 2), rb = make_rsrc(p.ext_b, N * p.r * 2);
-    for (int64_t j0 = 0; j0 < p.r; j0 += 32) {
-      const int64_t e = j0 + 8 * g;
-      typename T::v8 fa[4], fw[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + 16 * i + q, n = n0 + 16 * i + q;
-        fa[i] = __builtin_bit_cast(typename T::v8, ld_b128(re, m < M && e < p.r ? static_cast<uint32_t>((m * p.r + e) * 2) : kMasked));
-        fw[i] = __builtin_bit_cast(typename T::v8, ld_b128(rb, n < N && e < p.r ? static_cast<uint32_t>((n * p.r + e) * 2) : kMasked));
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = T::mfma16(fw[j], fa[i], acc[i][j]);
-    }
-  }
-  float* out = static_cast<float*>(p.out) + static_cast<int64_t>(blockIdx.z) * M * N;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t m = m0 + 16 * i + q;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int64_t n = n0 + 16 * j + 4 * g;
-      if (m < M && n < N) *reinterpret_cast<f32x4*>(out + m * N + n) = acc[i][j];
-    }
-  }
-}
-
 template <class T, bool k32>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void mx_tile_kernel(MxProductArgs p) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
@@ -112,34 +38,22 @@ __global__ __launch_bounds__(256) void mx_sum32_kernel(const float* __restrict__
   }
 }
 
-// How a product runs: by the direct kernel or by tiles, in how many splits of the
-// reduction (by chunks); part_bytes: the splits' fp32 planes.
+// Up to this many rows a product runs by mx_gemv.hip's kernel.
+#ifndef QN_MX_ROWS_M
+#define QN_MX_ROWS_M 128
+#endif
+constexpr int64_t kRowsM = QN_MX_ROWS_M;
+
+// Splits of a product by tiles (by chunks of the reduction) and their planes' bytes: the
+// split of least estimated time, as plan_split16's: rounds of 256 tiles, the planes
+// through memory twice and one more launch.
 struct MxPlan {
-  bool tiles;
   int64_t splits, chunks_per, part_bytes;
 };
-#ifndef QN_MX_DIRECT_M
-#define QN_MX_DIRECT_M 64
-#endif
-#ifndef QN_MX_STAGE_US
-#define QN_MX_STAGE_US 1.2
-#endif
 MxPlan plan_mx(int64_t M, int64_t N, int64_t K) {
-  const int64_t chunks = mx_chunks(K);
-  MxPlan pl{M > QN_MX_DIRECT_M, 1, chunks, 0};
-  if (!pl.tiles) {
-    const int64_t wgs = cdiv(M, 64) * cdiv(N, 256);
-    int64_t s = cdiv(512, wgs);
-    s = s > chunks ? chunks : s;
-    pl.chunks_per = cdiv(chunks, s);
-    pl.splits = cdiv(chunks, pl.chunks_per);
-    pl.part_bytes = align256(pl.splits * M * N * 4);
-    return pl;
-  }
-  // the split of least estimated time, as plan_split16's: rounds of 256 tiles, the
-  // partials through memory twice and one more launch
-  constexpr double kStageUs = QN_MX_STAGE_US, kTileUs = 5.0, kBytesPerUs = 5e6, kLaunchUs = 4.0;
-  const int64_t tiles = cdiv(M, 256) * cdiv(N, 256), plane = M * N * 4;
+  constexpr double kStageUs = 1.2, kTileUs = 5.0, kBytesPerUs = 5e6, kLaunchUs = 4.0;
+  const int64_t chunks = mx_chunks(K), tiles = cdiv(M, 256) * cdiv(N, 256), plane = M * N * 4;
+  MxPlan pl{1, chunks, 0};
   double least = 2 * kStageUs * chunks + kTileUs;
   if (tiles >= 256) return pl;
   for (int64_t s = 2; s <= chunks && s <= 64 && s * tiles <= 1024; ++s) {
@@ -149,9 +63,7 @@ MxPlan plan_mx(int64_t M, int64_t N, int64_t K) {
                       kLaunchUs + 0.1 * splits;
     if (us >= least) continue;
     least = us;
-    pl.splits = splits;
-    pl.chunks_per = per;
-    pl.part_bytes = align256(splits * plane);
+    pl = MxPlan{splits, per, align256(splits * plane)};
   }
   return pl;
 }
@@ -166,54 +78,62 @@ hipError_t launch_mx_tiles_t(const MxProductArgs& p, int64_t splits, hipStream_t
   return hipGetLastError();
 }
 
-// out_type: NF4_OUT_*; the adapter's operands are of the 16-bit type dtype.
-hipError_t mx_product(MxView act, MxView w, const uint16_t* ext_a, const uint16_t* ext_b, int64_t r, int dtype,
-                      int out_type, void* out, void* ws, hipStream_t stream) {
-  const int64_t M = act.rows, N = w.rows;
-  const MxPlan pl = plan_mx(M, N, act.cols);
-  const bool parts = !pl.tiles || pl.splits > 1;
-  MxProductArgs p{act, w, ext_a, ext_b, r, parts ? ws : out, pl.chunks_per};
-  hipError_t e;
-  {
-    const Timer tm(QK_MX_GEMM, stream, true);
-    if (pl.tiles) {
-      const bool k32 = parts || out_type == NF4_OUT_F32;
-      if (dtype == kDtypeF16) e = k32 ? launch_mx_tiles_t<F16, true>(p, pl.splits, stream, tm) : launch_mx_tiles_t<F16, false>(p, pl.splits, stream, tm);
-      else e = k32 ? launch_mx_tiles_t<Bf16, true>(p, pl.splits, stream, tm) : launch_mx_tiles_t<Bf16, false>(p, pl.splits, stream, tm);
-    } else {
-      const dim3 grid(static_cast<unsigned>(cdiv(N, 256)), static_cast<unsigned>(cdiv(M, 64)), static_cast<unsigned>(pl.splits));
-      hipExtLaunchKernelGGL((dtype == kDtypeF16 ? mx_direct_kernel<F16> : mx_direct_kernel<Bf16>), grid, dim3(256), 0, stream,
-                            tm.start(), tm.end(), 0, p);
-      e = hipGetLastError();
-    }
-  }
-  if (e != hipSuccess || !parts) return e;
-  const float* part = static_cast<const float*>(ws);
+hipError_t mx_sum(const float* part, int64_t splits, int64_t count, int out_type, void* out, hipStream_t stream) {
   if (out_type != NF4_OUT_F32)
-    return launch_split_sum(part, pl.splits, M * N, static_cast<uint16_t*>(out), stream,
-                            out_type == NF4_OUT_F16 ? kDtypeF16 : kDtypeBf16);
-  const int64_t blocks = cdiv(M * N, 1024);
+    return launch_split_sum(part, splits, count, static_cast<uint16_t*>(out), stream, out_type == NF4_OUT_F16 ? kDtypeF16 : kDtypeBf16);
+  const int64_t blocks = cdiv(count, 1024);
   Timer tm(QK_REDUCE, stream);
-  hipLaunchKernelGGL(mx_sum32_kernel, dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096)), dim3(256), 0, stream, part,
-                     pl.splits, M * N, static_cast<float*>(out));
+  hipLaunchKernelGGL(mx_sum32_kernel, dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096)), dim3(256), 0, stream, part, splits,
+                     count, static_cast<float*>(out));
   tm.stop();
   return hipGetLastError();
 }
 
-}  // namespace
-
-int64_t mx_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K) { return plan_mx(M, N, K).part_bytes; }
-
-hipError_t launch_mx_matmul(MxView p, MxView q, int out_type, void* out, void* ws, hipStream_t stream) {
-  return mx_product(p, q, nullptr, nullptr, 0, out_type == NF4_OUT_F16 ? kDtypeF16 : kDtypeBf16, out_type, out, ws, stream);
+// By tiles.  out_type: NF4_OUT_*; the adapter's operands are of the 16-bit type dtype.
+hipError_t mx_tiles(MxView act, MxView w, const uint16_t* ext_a, const uint16_t* ext_b, int64_t r, int dtype, int out_type,
+                    void* out, void* ws, hipStream_t stream) {
+  const int64_t M = act.rows, N = w.rows;
+  const MxPlan pl = plan_mx(M, N, act.cols);
+  const bool parts = pl.splits > 1;
+  const MxProductArgs p{act, w, ext_a, ext_b, r, parts ? ws : out, pl.chunks_per};
+  hipError_t e;
+  {
+    const Timer tm(QK_MX_GEMM, stream, true);
+    const bool k32 = parts || out_type == NF4_OUT_F32;
+    if (dtype == kDtypeF16) e = k32 ? launch_mx_tiles_t<F16, true>(p, pl.splits, stream, tm) : launch_mx_tiles_t<F16, false>(p, pl.splits, stream, tm);
+    else e = k32 ? launch_mx_tiles_t<Bf16, true>(p, pl.splits, stream, tm) : launch_mx_tiles_t<Bf16, false>(p, pl.splits, stream, tm);
+  }
+  if (e != hipSuccess || !parts) return e;
+  return mx_sum(static_cast<const float*>(ws), pl.splits, M * N, out_type, out, stream);
 }
 
-// Workspace of the forward: Aᵀ, Z's partials, (c B)ᵀ, X's codes and scales, the
-// product's partials, Z for calls that do not pass it.
+}  // namespace
+
+int64_t mx_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+  return M <= kRowsM ? plan_mx_rows(M, K, N, 0).part : plan_mx(M, N, K).part_bytes;
+}
+
+hipError_t launch_mx_matmul(MxView p, MxView q, int out_type, void* out, void* ws, hipStream_t stream) {
+  const int dtype = out_type == NF4_OUT_F16 ? kDtypeF16 : kDtypeBf16;
+  if (p.rows > kRowsM) return mx_tiles(p, q, nullptr, nullptr, 0, dtype, out_type, out, ws, stream);
+  const MxRowsPlan pl = plan_mx_rows(p.rows, p.cols, q.rows, 0);
+  const bool parts = pl.splits > 1;
+  hipError_t e = launch_mx_rows(pl, nullptr, &p, q, p.rows, parts ? ws : out, !parts && out_type != NF4_OUT_F32, stream, dtype);
+  if (e != hipSuccess || !parts) return e;
+  return mx_sum(static_cast<const float*>(ws), pl.splits, p.rows * q.rows, out_type, out, stream);
+}
+
+// Workspace of the forward, few rows: the planes, Z's partials, above 16 rows X's codes
+// and scales; else: Aᵀ, Z's partials, (c B)ᵀ, X's codes and scales, the tiles' planes.
+// Then Z for calls that do not pass it.
+static int64_t mx_kept_bytes(int64_t M, int64_t K) { return align256(mx_code_bytes(M, K)) + align256(mx_scale_bytes(M, K)); }
 int64_t mx_fwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t r) {
+  if (M <= kRowsM) {
+    const MxRowsPlan p = plan_mx_rows(M, K, N, r);
+    return p.part + p.zpart + (M > 16 ? mx_kept_bytes(M, K) : 0) + align256(M * r * 2);
+  }
   const SkinnyPlan p = plan_skinny(M, K, N, r);
-  return p.at_bytes + p.z_part + align256(N * r * 2) + align256(mx_code_bytes(M, K)) + align256(mx_scale_bytes(M, K)) +
-         plan_mx(M, N, K).part_bytes + align256(M * r * 2);
+  return p.at_bytes + p.z_part + align256(N * r * 2) + mx_kept_bytes(M, K) + plan_mx(M, N, K).part_bytes + align256(M * r * 2);
 }
 
 int64_t mx_bwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t r) {
@@ -223,19 +143,31 @@ int64_t mx_bwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t r) {
 
 hipError_t launch_mx_fwd(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t* X, MxView W, const uint16_t* A,
                          const uint16_t* B, float c, uint16_t* Y, uint16_t* Z, void* ws, hipStream_t stream, int dtype) {
-  const SkinnyPlan p = plan_skinny(M, K, N, r);
+  const int type = dtype == kDtypeF16 ? NF4_OUT_F16 : NF4_OUT_BF16;
   char* at = static_cast<char*>(ws);
+  if (Z == nullptr) Z = reinterpret_cast<uint16_t*>(at + mx_fwd_workspace_bytes(M, K, N, r) - align256(M * r * 2));
+  MxView x{nullptr, nullptr, M, K};
+  hipError_t e;
+  if (M <= kRowsM) {
+    const MxRowsPlan pl = plan_mx_rows(M, K, N, r);
+    float* part = reinterpret_cast<float*>(at);
+    float* zpart = reinterpret_cast<float*>(at + pl.part);
+    if (M > 16) {
+      x.codes = reinterpret_cast<uint8_t*>(at + pl.part + pl.zpart);
+      x.scales = x.codes + align256(mx_code_bytes(M, K));
+      if ((e = launch_mx_quantize(type, false, X, K, x, stream)) != hipSuccess) return e;
+    }
+    if ((e = launch_mx_rows(pl, X, M > 16 ? &x : nullptr, W, M, part, false, stream, dtype, X, A, r, zpart)) != hipSuccess) return e;
+    return launch_mx_rows_finish(pl, part, zpart, M, N, r, B, c, Y, Z, stream, dtype);
+  }
+  const SkinnyPlan p = plan_skinny(M, K, N, r);
   char* zpart = at + p.at_bytes;
   uint16_t* cbt = reinterpret_cast<uint16_t*>(zpart + p.z_part);
-  MxView x{reinterpret_cast<uint8_t*>(cbt) + align256(N * r * 2), nullptr, M, K};
+  x.codes = reinterpret_cast<uint8_t*>(cbt) + align256(N * r * 2);
   x.scales = x.codes + align256(mx_code_bytes(M, K));
-  uint8_t* part = x.scales + align256(mx_scale_bytes(M, K));
-  if (Z == nullptr) Z = reinterpret_cast<uint16_t*>(part + plan_mx(M, N, K).part_bytes);
-  const int type = dtype == kDtypeF16 ? NF4_OUT_F16 : NF4_OUT_BF16;
-  hipError_t e = launch_mx_quantize(type, false, X, K, x, stream);
-  if (e != hipSuccess) return e;
+  if ((e = launch_mx_quantize(type, false, X, K, x, stream)) != hipSuccess) return e;
   if ((e = launch_lora_down(M, K, r, X, A, Z, p, at, zpart, stream, N, B, c, cbt, 0, dtype)) != hipSuccess) return e;
-  return mx_product(x, W, Z, cbt, r, dtype, type, Y, part, stream);
+  return mx_tiles(x, W, Z, cbt, r, dtype, type, Y, x.scales + align256(mx_scale_bytes(M, K)), stream);
 }
 
 // dX by the dense 16-bit product with the dequantized weight: the gradient's own
