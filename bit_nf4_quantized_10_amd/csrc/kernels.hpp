@@ -261,21 +261,23 @@ struct MxView {
 // type: of X, one of NF4_OUT_*.  across: X is cols x rows.  ld: X's row stride.
 hipError_t launch_mx_quantize(int type, bool across, const void* X, int64_t ld, MxView m, hipStream_t stream);
 hipError_t launch_mx_dequantize(int type, bool across, MxView m, void* X, int64_t ld, hipStream_t stream);
-// Products for few rows (mx_gemv.hip): tiles of 16 act and weight rows a wave, splits of
-// the reduction and the bytes of their fp32 planes (0: the output is written itself),
-// and the same of Z = X A.
+// Products for fewer rows than tiles want (mx_gemv.hip): which kernel, tiles of 16 act and
+// weight rows a wave, splits of the reduction and the bytes of their fp32 planes (0: the
+// output is written itself), and the same of Z = X A.
+enum { kMxDecode, kMxRows, kMxPanel };
 struct MxRowsPlan {
-  bool decode;       // the layer's up to 16 rows, X quantised on the way
-  int ra, rw;
+  int kind, ra, rw;
   int64_t splits, chunks_per, part;
   int64_t zsplits, z_rpw, zpart;
 };
 MxRowsPlan plan_mx_rows(int64_t M, int64_t K, int64_t N, int64_t r);
-// X: for pl.decode, else act.  out: planes, or with one split
-// the output in 16 bits (out16) or 32.  Xz, A, zpart: the partials of Z, where wanted.
+// Quantises X (M x K) into m; in the same launch Z's partials (pl given) or two transposes.
+hipError_t launch_mx_front(MxView m, const uint16_t* X, hipStream_t stream, int dtype, const MxRowsPlan* pl, const uint16_t* A, int64_t r,
+                           float* zpart, const TJob* side);
+// kMxDecode takes X and quantises it on the way, with Z's partials, the others act.  out:
+// planes, or with one split the output in 16 bits (out16) or 32.
 hipError_t launch_mx_rows(const MxRowsPlan& pl, const uint16_t* X, const MxView* act, MxView w, int64_t M, void* out, bool out16,
-                          hipStream_t stream, int dtype, const uint16_t* Xz = nullptr, const uint16_t* A = nullptr, int64_t r = 0,
-                          float* zpart = nullptr);
+                          hipStream_t stream, int dtype, const uint16_t* A = nullptr, int64_t r = 0, float* zpart = nullptr);
 // Z and Y = the planes' sum + c Z B.
 hipError_t launch_mx_rows_finish(const MxRowsPlan& pl, const float* part, const float* zpart, int64_t M, int64_t N, int64_t r,
                                  const uint16_t* B, float c, uint16_t* Y, uint16_t* Z, hipStream_t stream, int dtype);

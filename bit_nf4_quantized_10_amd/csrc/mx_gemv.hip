@@ -17,6 +17,8 @@
 #include "gemv_parts.hpp"
 #include "kernels.hpp"
 #include "mx_core.hpp"
+#include "mx_quant.hpp"
+#include "side_jobs.hpp"
 
 namespace qn {
 
@@ -29,30 +31,56 @@ struct MxRowsArgs {
   int64_t M, N, K;
   void* out;              // M x N in 16 bits, or fp32 planes [splits][M][N]
   int splits, chunks_per; // chunks a workgroup takes
-  // Z = X A: zsplits workgroups per 16 rows, z_rpw rows of A a wave (0: none)
-  const uint16_t* Xz;
+  // decode kernel: Z = X A in zsplits more workgroups, z_rpw rows of A a wave
   const uint16_t* A;
   int64_t r;
   float* zpart;
   int zsplits, z_rpw;
 };
 
+// In front of a product: X quantised, and the partials of Z = X A in the first workgroups
+// (those of 16 rows and one of zsplits ranges of K, or side_t's transposes).
+struct MxFrontArgs {
+  MxArgs quant;
+  const uint16_t* X;
+  int64_t M, K, r;
+  const uint16_t* A;
+  float* zpart;
+  int zsplits, z_rpw;
+  TJob side[2];
+};
+template <class T, bool kZ>
+__global__ __launch_bounds__(256) void mx_front_kernel(MxFrontArgs p) {
+  __shared__ __attribute__((aligned(16))) float lds[kZ ? 4096 : 32 * 33 / 2];
+  int64_t blk = blockIdx.x;
+  if constexpr (kZ) {
+    const int64_t zwgs = p.zsplits * ((p.M + 15) / 16);
+    if (blk < zwgs) {
+      gemv_zpart<T>(p.X, p.M, blk / p.zsplits * 16, p.K, p.z_rpw, p.A, p.r, p.zpart, blk % p.zsplits, lds);
+      return;
+    }
+    blk -= zwgs;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (blk < p.side[i].nblk) {
+        transpose_block(p.side[i], blk, reinterpret_cast<uint16_t(*)[33]>(lds));
+        return;
+      }
+      blk -= p.side[i].nblk;
+    }
+  }
+  mx_quantize_piece<T>(p.quant, blk);
+}
+
 template <class T, int RA, int RW, bool k16>
 __global__ __launch_bounds__(256) void mx_rows_kernel(MxRowsArgs p) {
   constexpr int kTiles = RA * RW;
-  __shared__ f32x4 red[4 * kTiles < 16 ? 16 : 4 * kTiles][64];   // 16 KB at least: Z's workgroups use it too
+  __shared__ f32x4 red[4 * kTiles][64];
   const int lane = threadIdx.x & 63, q = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int M = static_cast<int>(p.M), N = static_cast<int>(p.N), K = static_cast<int>(p.K);
-  const int zwgs = p.zsplits * ((M + 15) / 16), first = (zwgs + 7) & ~7;
-  int blk = blockIdx.x;
-  if (blk < first) {
-    if (blk < zwgs)
-      gemv_zpart<T>(p.Xz, p.M, blk / p.zsplits * 16, p.K, p.z_rpw, p.A, p.r, p.zpart, blk % p.zsplits,
-                    reinterpret_cast<float*>(red));
-    return;
-  }
-  blk -= first;
+  const int blk = blockIdx.x;
   // row blocks of one weight piece follow each other on one XCD (ids are dealt out to
   // the eight in turn), so that its L2 serves all but the first
   const int groups = (N + 16 * RW - 1) / (16 * RW), mblocks = (M + 16 * RA - 1) / (16 * RA);
@@ -122,6 +150,109 @@ __global__ __launch_bounds__(256) void mx_rows_kernel(MxRowsArgs p) {
     else
       *reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + (static_cast<int64_t>(split) * M + m) * N + n) = v;
   }
+}
+
+// Workgroup: 16 RA activation rows, 64 RW weight rows, 16 RW a wave, and a range of
+// chunks.  Weights go from memory into the wave's own fragments (no other wave wants
+// them), the chunk's activation codes straight into LDS in the order of the fragments;
+// a chunk's loads run while the one before it is multiplied (requested two chunks ahead,
+// the weights gained nothing).  At 100 x 4096 x 11008 (17 us) the multiplications and the
+// LDS reads alone take 9 with the launch, weights, activations and the fp32 planes 2 to 3
+// each.
+__device__ __forceinline__ void copy16(Rsrc r, char* to, uint32_t voff, uint32_t soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_ptr_t)(to), 16, voff, soff, 0, 0);
+}
+constexpr int panel_lds(int ra) { return 2 * 16 * ra * 256; }
+template <class T, int RA, int RW, bool k16>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void mx_panel_kernel(MxRowsArgs p) {
+  extern __shared__ __attribute__((aligned(16))) char smem[];
+  const int lane = threadIdx.x & 63, q = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int M = static_cast<int>(p.M), N = static_cast<int>(p.N), K = static_cast<int>(p.K);
+  const int blk = blockIdx.x;
+  const int groups = (N + 64 * RW - 1) / (64 * RW), mblocks = (M + 16 * RA - 1) / (16 * RA);
+  const int rest = blk >> 3, unit = rest / mblocks * 8 + (blk & 7);   // as mx_rows_kernel
+  if (unit >= groups * p.splits) return;
+  const int m0 = rest % mblocks * (16 * RA), n0 = unit % groups * (64 * RW) + wave * (16 * RW), split = unit / groups;
+  const int nb = static_cast<int>(mx_blocks(K)), chunks = static_cast<int>(mx_chunks(K));
+  const int beg = split * p.chunks_per, end = min(beg + p.chunks_per, chunks);
+  const Rsrc rw = make_rsrc(p.w.codes, mx_code_bytes(N, K)), rsw = make_rsrc(p.w.scales, mx_scale_bytes(N, K));
+  const Rsrc ra = make_rsrc(p.act.codes, mx_code_bytes(M, K)), rsa = make_rsrc(p.act.scales, mx_scale_bytes(M, K));
+  uint32_t vw[RW], va[RA];
+#pragma unroll
+  for (int j = 0; j < RW; ++j) vw[j] = n0 + 16 * j + q < N ? static_cast<uint32_t>((n0 + 16 * j + q) * nb + g) * 16u : kMasked;
+  // this wave copies step `wave` of the chunk
+#pragma unroll
+  for (int i = 0; i < RA; ++i)
+    va[i] = m0 + 16 * i + q < M ? static_cast<uint32_t>((m0 + 16 * i + q) * nb + 4 * wave + g) * 16u : kMasked;
+  struct Loads {
+    i32x4 w[RW][4];
+    uint32_t sw[RW], sa[RA];
+  };
+  // Offsets are a lane's own and a scalar.  Weight blocks past the row's end, of the next
+  // row, meet zeros of X; tiles past the last one take its scales, for rows that are not
+  // stored.
+  const int last_w = (N - 1) / 16, last_a = (M - 1) / 16;
+  auto load = [&](int c, int buf, Loads& L) {
+    const bool in = 16 * c + 4 * wave + g < nb;
+#pragma unroll
+    for (int i = 0; i < RA; ++i) copy16(ra, smem + buf + (4 * i + wave) * 1024, in ? va[i] : kMasked, 256 * c);
+#pragma unroll
+    for (int j = 0; j < RW; ++j) {
+#pragma unroll
+      for (int s = 0; s < 4; ++s) L.w[j][s] = __builtin_bit_cast(i32x4, ld128s(rw, vw[j], 256 * c + 64 * s));
+      L.sw[j] = ld32s(rsw, 4 * lane, static_cast<uint32_t>(min(n0 / 16 + j, last_w) * chunks + c) * 256u);
+    }
+#pragma unroll
+    for (int i = 0; i < RA; ++i) L.sa[i] = ld32s(rsa, 4 * lane, static_cast<uint32_t>(min(m0 / 16 + i, last_a) * chunks + c) * 256u);
+  };
+  f32x4 acc[RA][RW];
+#pragma unroll
+  for (int i = 0; i < RA; ++i)
+#pragma unroll
+    for (int j = 0; j < RW; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  auto step = [&](int c, int buf, const Loads& L, Loads& next) {
+    // this wave's loads of chunk c have landed, and with the barrier everybody's; the
+    // other buffer has been read
+    __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 0));
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    if (c + 1 < end) load(c + 1, 16 * RA * 256 - buf, next);
+    __builtin_amdgcn_sched_barrier(0);
+    auto mul = [&](auto tag) {
+      constexpr int s = decltype(tag)::value;
+      i32x4 fa[RA];
+#pragma unroll
+      for (int i = 0; i < RA; ++i) fa[i] = *reinterpret_cast<const i32x4*>(smem + buf + (4 * i + s) * 1024 + lane * 16);
+#pragma unroll
+      for (int i = 0; i < RA; ++i)
+#pragma unroll
+        for (int j = 0; j < RW; ++j) acc[i][j] = mfma_mx<s>(L.w[j][s], fa[i], acc[i][j], L.sw[j], L.sa[i]);
+    };
+    mul(std::integral_constant<int, 0>{});
+    mul(std::integral_constant<int, 1>{});
+    mul(std::integral_constant<int, 2>{});
+    mul(std::integral_constant<int, 3>{});
+  };
+  Loads l0, l1;
+  load(beg, 0, l0);
+  for (int c = beg; c < end; c += 2) {
+    step(c, 0, l0, l1);
+    if (c + 1 < end) step(c + 1, 16 * RA * 256, l1, l0);
+  }
+#pragma unroll
+  for (int i = 0; i < RA; ++i)
+#pragma unroll
+    for (int j = 0; j < RW; ++j) {
+      const int m = m0 + 16 * i + q, n = n0 + 16 * j + 4 * g;
+      const f32x4& v = acc[i][j];
+      if (m >= M || n >= N) continue;
+      if constexpr (k16)
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + static_cast<int64_t>(m) * N + n) =
+            make_uint2(T::pack2(v[0], v[1]), T::pack2(v[2], v[3]));
+      else
+        *reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + (static_cast<int64_t>(split) * M + m) * N + n) = v;
+    }
 }
 
 // Up to 16 rows of the layer.  Workgroup: 64 RW weight rows, 16 RW a wave, and a range of
@@ -220,9 +351,7 @@ __global__ __launch_bounds__(256) void mx_decode_kernel(MxRowsArgs p) {
 template <class T, int RA, int RW, bool k16>
 void launch_rows_t(const MxRowsArgs& p, hipStream_t stream, const Timer& tm) {
   const int64_t units = cdiv(p.N, 16 * RW) * p.splits, mblocks = cdiv(p.M, 16 * RA);
-  const int64_t zwgs = round_up(p.zsplits * cdiv(p.M, 16), 8);
-  hipExtLaunchKernelGGL((mx_rows_kernel<T, RA, RW, k16>), dim3(static_cast<unsigned>(zwgs + round_up(units, 8) * mblocks)),
-                        dim3(256), 0, stream, tm.start(), tm.end(), 0, p);
+  hipExtLaunchKernelGGL((mx_rows_kernel<T, RA, RW, k16>), dim3(static_cast<unsigned>(round_up(units, 8) * mblocks)), dim3(256), 0, stream, tm.start(), tm.end(), 0, p);
 }
 template <class T, bool k16>
 void launch_rows_w(const MxRowsArgs& p, int ra, int rw, hipStream_t stream, const Timer& tm) {
@@ -241,9 +370,27 @@ void launch_decode(const MxRowsArgs& p, int rw, hipStream_t stream, const Timer&
   const dim3 grid(static_cast<unsigned>(p.zsplits + cdiv(p.N, 64 * rw) * p.splits));
   hipExtLaunchKernelGGL((rw == 1 ? mx_decode_kernel<T, 1> : mx_decode_kernel<T, 2>), grid, dim3(256), 0, stream, tm.start(), tm.end(), 0, p);
 }
+template <class T, int RA, int RW, bool k16>
+hipError_t launch_panel_t(const MxRowsArgs& p, hipStream_t stream, const Timer& tm) {
+  static const hipError_t lds_limit = hipFuncSetAttribute(reinterpret_cast<const void*>(&mx_panel_kernel<T, RA, RW, k16>),
+                                                          hipFuncAttributeMaxDynamicSharedMemorySize, panel_lds(RA));
+  if (lds_limit != hipSuccess) return lds_limit;
+  const dim3 grid(static_cast<unsigned>(round_up(cdiv(p.N, 64 * RW) * p.splits, 8) * cdiv(p.M, 16 * RA)));
+  hipExtLaunchKernelGGL((mx_panel_kernel<T, RA, RW, k16>), grid, dim3(256), panel_lds(RA), stream, tm.start(), tm.end(), 0, p);
+  return hipGetLastError();
+}
+template <class T, int RA>
+hipError_t launch_panel_r(const MxRowsArgs& p, int rw, bool out16, hipStream_t stream, const Timer& tm) {
+  if (rw == 1) return out16 ? launch_panel_t<T, RA, 1, true>(p, stream, tm) : launch_panel_t<T, RA, 1, false>(p, stream, tm);
+  return out16 ? launch_panel_t<T, RA, 2, true>(p, stream, tm) : launch_panel_t<T, RA, 2, false>(p, stream, tm);
+}
+template <class T>
+hipError_t launch_panel(const MxRowsArgs& p, int ra, int rw, bool out16, hipStream_t stream, const Timer& tm) {
+  return ra == 4 ? launch_panel_r<T, 4>(p, rw, out16, stream, tm) : launch_panel_r<T, 8>(p, rw, out16, stream, tm);
+}
 
 #ifndef QN_MXR_WGS
-#define QN_MXR_WGS 512
+#define QN_MXR_WGS 1024
 #endif
 #ifndef QN_MXR_ZSPLITS
 #define QN_MXR_ZSPLITS 8
@@ -251,21 +398,51 @@ void launch_decode(const MxRowsArgs& p, int rw, hipStream_t stream, const Timer&
 
 }  // namespace
 
+// Up to this many rows waves take chunks of their own (mx_rows_kernel): 64 x 4096 x 11008
+// in 15 us, by panels in 17.
+constexpr int64_t kRowsMost = 64;
+
 // r > 0: the layer, whose sums a second launch adds up; else a product alone.
 MxRowsPlan plan_mx_rows(int64_t M, int64_t K, int64_t N, int64_t r) {
   MxRowsPlan p{};
-  p.ra = M <= 16 ? 1 : (M <= 32 ? 2 : 4);
-  p.decode = r > 0 && M <= 16;
-  const int64_t chunks = mx_chunks(K), mb = cdiv(M, 16 * p.ra);
-  const int64_t most = p.decode ? chunks : cdiv(chunks, 4);
-  const int64_t wide = p.decode ? 4 : 1;   // waves side by side
-  p.rw = p.ra == 1 ? (cdiv(N, 16 * wide) * most < 2 * QN_MXR_WGS ? 1 : 2) : (p.ra == 2 ? 2 : (cdiv(N, 32) * mb * most < 2 * QN_MXR_WGS ? 2 : 4));
-  const int64_t groups = cdiv(N, 16 * wide * p.rw) * mb;
-  int64_t s = QN_MXR_WGS / groups;
-  s = s < 1 ? 1 : (s > most ? most : s);
-  while (s > 1 && s * M * N * 4 > INT32_MAX) --s;   // the finish addresses the planes with 31-bit offsets
-  p.chunks_per = cdiv(chunks, s);
-  p.splits = cdiv(chunks, p.chunks_per);
+  const int64_t chunks = mx_chunks(K);
+  // the finish addresses the planes with 31-bit offsets
+  auto fits = [&](int64_t s) { return s * M * N * 4 <= INT32_MAX; };
+  if (M > kRowsMost) {
+    p.kind = kMxPanel;
+    // the least estimated time: a start, chunks one after another on a CU (by tiles of 64 or
+    // 128 rows and 64 or 128 columns), the planes through memory twice and the launch that adds
+    // them; from calls of 64 .. 1024 rows, K 2056 and 4096, N 1336 .. 22016
+    constexpr double kStartUs[2][2] = {{6.2, 6.5}, {7.3, 8.2}}, kChunkUs[2][2] = {{1.15, 1.9}, {1.9, 2.1}};
+    constexpr double kBytesPerUs = 5e6, kLaunchUs = 4.0;
+    double least = 0.0;
+    for (int ra = 4; ra <= 8; ra += 4)
+      for (int rw = 1; rw <= 2; ++rw)
+        for (int64_t s = 1; s <= chunks && s <= 8; ++s) {
+          const int64_t per = cdiv(chunks, s);
+          if (cdiv(chunks, per) != s || (s > 1 && !fits(s))) continue;
+          const int64_t rounds = cdiv(cdiv(N, 64 * rw) * cdiv(M, 16 * ra) * s, 256);
+          const double us = kStartUs[ra / 8][rw - 1] + kChunkUs[ra / 8][rw - 1] * static_cast<double>(rounds * per) +
+                            (r > 0 || s > 1 ? kLaunchUs + static_cast<double>(s * M * N) * 8.0 / kBytesPerUs : 0.0);
+          if (least > 0.0 && us >= least) continue;
+          least = us;
+          p.ra = ra;
+          p.rw = rw;
+          p.splits = s;
+          p.chunks_per = per;
+        }
+  } else {
+    p.kind = r > 0 && M <= 16 ? kMxDecode : kMxRows;
+    p.ra = M <= 16 ? 1 : (M <= 32 ? 2 : 4);
+    const int64_t most = p.kind == kMxDecode ? chunks : cdiv(chunks, 4);
+    const int64_t wide = p.kind == kMxDecode ? 4 : 1;   // waves side by side
+    p.rw = p.ra == 1 ? (cdiv(N, 16 * wide) * most < 2 * QN_MXR_WGS ? 1 : 2) : (p.ra == 2 ? 2 : (cdiv(N, 32) * most < 2 * QN_MXR_WGS ? 2 : 4));
+    int64_t s = QN_MXR_WGS / cdiv(N, 16 * wide * p.rw);
+    s = s < 1 ? 1 : (s > most ? most : s);
+    while (s > 1 && !fits(s)) --s;
+    p.chunks_per = cdiv(chunks, s);
+    p.splits = cdiv(chunks, p.chunks_per);
+  }
   if (r > 0) {
     p.z_rpw = round_up(cdiv(K, 4 * QN_MXR_ZSPLITS), 32);
     p.zsplits = cdiv(K, 4 * p.z_rpw);
@@ -275,20 +452,48 @@ MxRowsPlan plan_mx_rows(int64_t M, int64_t K, int64_t N, int64_t r) {
   return p;
 }
 
+hipError_t launch_mx_front(MxView m, const uint16_t* X, hipStream_t stream, int dtype, const MxRowsPlan* pl, const uint16_t* A, int64_t r,
+                           float* zpart, const TJob* side) {
+  MxFrontArgs p{};
+  p.quant = MxArgs{X, m.cols, m.codes, m.scales, m.rows, m.cols, mx_chunks(m.cols)};
+  p.X = X;
+  p.M = m.rows;
+  p.K = m.cols;
+  p.r = r;
+  p.A = A;
+  p.zpart = zpart;
+  int64_t more = 0;
+  if (pl != nullptr) {
+    p.zsplits = static_cast<int>(pl->zsplits);
+    p.z_rpw = static_cast<int>(pl->z_rpw);
+    more = pl->zsplits * cdiv(m.rows, 16);
+  } else {
+    p.side[0] = side[0];
+    p.side[1] = side[1];
+    more = side[0].nblk + side[1].nblk;
+  }
+  auto* k = dtype == kDtypeF16 ? (pl != nullptr ? mx_front_kernel<F16, true> : mx_front_kernel<F16, false>)
+                               : (pl != nullptr ? mx_front_kernel<Bf16, true> : mx_front_kernel<Bf16, false>);
+  Timer tm(QK_MX_QUANT, stream);
+  hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(more + cdiv(m.rows, 16) * p.quant.chunks)), dim3(256), 0, stream, p);
+  tm.stop();
+  return hipGetLastError();
+}
+
 hipError_t launch_mx_rows(const MxRowsPlan& pl, const uint16_t* X, const MxView* act, MxView w, int64_t M, void* out, bool out16,
-                          hipStream_t stream, int dtype, const uint16_t* Xz, const uint16_t* A, int64_t r, float* zpart) {
+                          hipStream_t stream, int dtype, const uint16_t* A, int64_t r, float* zpart) {
   const MxRowsArgs p{X, act != nullptr ? *act : MxView{}, w, M, w.rows, w.cols, out, static_cast<int>(pl.splits), static_cast<int>(pl.chunks_per),
-                     Xz, A, r, zpart, static_cast<int>(pl.zsplits), static_cast<int>(pl.z_rpw)};
+                     A, r, zpart, static_cast<int>(pl.zsplits), static_cast<int>(pl.z_rpw)};
   const Timer tm(QK_MX_GEMM, stream, true);
   auto go = [&](auto tag) {
     typedef decltype(tag) T;
-    if (pl.decode) launch_decode<T>(p, pl.rw, stream, tm);
+    if (pl.kind == kMxPanel) return launch_panel<T>(p, pl.ra, pl.rw, out16, stream, tm);
+    if (pl.kind == kMxDecode) launch_decode<T>(p, pl.rw, stream, tm);
     else if (out16) launch_rows_w<T, true>(p, pl.ra, pl.rw, stream, tm);
     else launch_rows_w<T, false>(p, pl.ra, pl.rw, stream, tm);
+    return hipGetLastError();
   };
-  if (dtype == kDtypeF16) go(F16{});
-  else go(Bf16{});
-  return hipGetLastError();
+  return dtype == kDtypeF16 ? go(F16{}) : go(Bf16{});
 }
 
 hipError_t launch_mx_rows_finish(const MxRowsPlan& pl, const float* part, const float* zpart, int64_t M, int64_t N, int64_t r,

@@ -38,11 +38,10 @@ __global__ __launch_bounds__(256) void mx_sum32_kernel(const float* __restrict__
   }
 }
 
-// Up to this many rows a product runs by mx_gemv.hip's kernel.
-#ifndef QN_MX_ROWS_M
-#define QN_MX_ROWS_M 128
-#endif
-constexpr int64_t kRowsM = QN_MX_ROWS_M;
+// Products run by mx_gemv.hip's kernels up to 64 rows or 2^21 outputs, and by tiles above.
+// The layer, in a graph: 512 rows at 4096 x 4096 35 us and by tiles 42; 256 rows at
+// 4096 x 11008 47 and 42; 777 rows at 2056 x 1336 23 and 33; 1024 at 4096 x 4096 47 and 42.
+bool few_rows(int64_t M, int64_t N) { return M <= 64 || M * N <= (int64_t(1) << 21); }
 
 // Splits of a product by tiles (by chunks of the reduction) and their planes' bytes: the
 // split of least estimated time, as plan_split16's: rounds of 256 tiles, the planes
@@ -110,12 +109,12 @@ hipError_t mx_tiles(MxView act, MxView w, const uint16_t* ext_a, const uint16_t*
 }  // namespace
 
 int64_t mx_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-  return M <= kRowsM ? plan_mx_rows(M, K, N, 0).part : plan_mx(M, N, K).part_bytes;
+  return few_rows(M, N) ? plan_mx_rows(M, K, N, 0).part : plan_mx(M, N, K).part_bytes;
 }
 
 hipError_t launch_mx_matmul(MxView p, MxView q, int out_type, void* out, void* ws, hipStream_t stream) {
   const int dtype = out_type == NF4_OUT_F16 ? kDtypeF16 : kDtypeBf16;
-  if (p.rows > kRowsM) return mx_tiles(p, q, nullptr, nullptr, 0, dtype, out_type, out, ws, stream);
+  if (!few_rows(p.rows, q.rows)) return mx_tiles(p, q, nullptr, nullptr, 0, dtype, out_type, out, ws, stream);
   const MxRowsPlan pl = plan_mx_rows(p.rows, p.cols, q.rows, 0);
   const bool parts = pl.splits > 1;
   hipError_t e = launch_mx_rows(pl, nullptr, &p, q, p.rows, parts ? ws : out, !parts && out_type != NF4_OUT_F32, stream, dtype);
@@ -128,9 +127,9 @@ hipError_t launch_mx_matmul(MxView p, MxView q, int out_type, void* out, void* w
 // Then Z for calls that do not pass it.
 static int64_t mx_kept_bytes(int64_t M, int64_t K) { return align256(mx_code_bytes(M, K)) + align256(mx_scale_bytes(M, K)); }
 int64_t mx_fwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t r) {
-  if (M <= kRowsM) {
+  if (few_rows(M, N)) {
     const MxRowsPlan p = plan_mx_rows(M, K, N, r);
-    return p.part + p.zpart + (M > 16 ? mx_kept_bytes(M, K) : 0) + align256(M * r * 2);
+    return p.part + p.zpart + (p.kind != kMxDecode ? mx_kept_bytes(M, K) : 0) + align256(M * r * 2);
   }
   const SkinnyPlan p = plan_skinny(M, K, N, r);
   return p.at_bytes + p.z_part + align256(N * r * 2) + mx_kept_bytes(M, K) + plan_mx(M, N, K).part_bytes + align256(M * r * 2);
@@ -148,16 +147,17 @@ hipError_t launch_mx_fwd(int64_t M, int64_t K, int64_t N, int64_t r, const uint1
   if (Z == nullptr) Z = reinterpret_cast<uint16_t*>(at + mx_fwd_workspace_bytes(M, K, N, r) - align256(M * r * 2));
   MxView x{nullptr, nullptr, M, K};
   hipError_t e;
-  if (M <= kRowsM) {
+  if (few_rows(M, N)) {
     const MxRowsPlan pl = plan_mx_rows(M, K, N, r);
     float* part = reinterpret_cast<float*>(at);
     float* zpart = reinterpret_cast<float*>(at + pl.part);
-    if (M > 16) {
+    const bool decode = pl.kind == kMxDecode;
+    if (!decode) {
       x.codes = reinterpret_cast<uint8_t*>(at + pl.part + pl.zpart);
       x.scales = x.codes + align256(mx_code_bytes(M, K));
-      if ((e = launch_mx_quantize(type, false, X, K, x, stream)) != hipSuccess) return e;
+      if ((e = launch_mx_front(x, X, stream, dtype, &pl, A, r, zpart, nullptr)) != hipSuccess) return e;
     }
-    if ((e = launch_mx_rows(pl, X, M > 16 ? &x : nullptr, W, M, part, false, stream, dtype, X, A, r, zpart)) != hipSuccess) return e;
+    if ((e = launch_mx_rows(pl, X, decode ? nullptr : &x, W, M, part, false, stream, dtype, A, r, zpart)) != hipSuccess) return e;
     return launch_mx_rows_finish(pl, part, zpart, M, N, r, B, c, Y, Z, stream, dtype);
   }
   const SkinnyPlan p = plan_skinny(M, K, N, r);
@@ -165,8 +165,11 @@ hipError_t launch_mx_fwd(int64_t M, int64_t K, int64_t N, int64_t r, const uint1
   uint16_t* cbt = reinterpret_cast<uint16_t*>(zpart + p.z_part);
   x.codes = reinterpret_cast<uint8_t*>(cbt) + align256(N * r * 2);
   x.scales = x.codes + align256(mx_code_bytes(M, K));
-  if ((e = launch_mx_quantize(type, false, X, K, x, stream)) != hipSuccess) return e;
-  if ((e = launch_lora_down(M, K, r, X, A, Z, p, at, zpart, stream, N, B, c, cbt, 0, dtype)) != hipSuccess) return e;
+  // Aᵀ and (c B)ᵀ ride along in the launch that quantises X
+  TJob tj[2];
+  lora_transposes(K, r, A, reinterpret_cast<uint16_t*>(at), N, B, c, cbt, 0, dtype, tj);
+  if ((e = launch_mx_front(x, X, stream, dtype, nullptr, nullptr, 0, nullptr, tj)) != hipSuccess) return e;
+  if ((e = launch_lora_down(M, K, r, X, A, Z, p, at, zpart, stream, N, B, c, cbt, 0, dtype, true)) != hipSuccess) return e;
   return mx_tiles(x, W, Z, cbt, r, dtype, type, Y, x.scales + align256(mx_scale_bytes(M, K)), stream);
 }
 
