@@ -37,18 +37,17 @@ struct MuonJob {
   float* mom;
   float* master;        // may be null
   float* u;
-  double* part;         // Gram partials [chunks][pairs][64][64]
-  double* mat;          // G, the next G, H, T, Q, the next Q: rp x rp each
-  int64_t len, len_p;
-  int64_t chunk;        // of len_p, elements a Gram workgroup takes
-  int chunks, tall;
+  double* part;         // Gram partials, by chunk
+  double* mat;          // G, the next G, H, T, Q, the next Q: rp x rp each (r <= 64: G, Q alone)
+  int64_t len, len_p;   // len_p: up to a multiple of 64
+  int chunk, chunks;    // of len_p, elements a Gram workgroup takes
+  int tall;
   double step;          // lr times the shape's factor
 };
 struct MuonArgs {
   MuonJob j[2];
   int r, rp, tiles;     // rp: r up to 16; tiles: 64-wide tiles of it
-  int f16, grad16;
-  int nesterov;
+  int nesterov, steps;
   double momentum, decay, eps, a, b, c;   // decay: 1 - lr wd
 };
 
@@ -57,28 +56,118 @@ __device__ __forceinline__ const MuonJob& job_of(const MuonArgs& p, int64_t firs
   if (second) blk -= first;
   return p.j[second];
 }
+__device__ __forceinline__ f64x4 mfma64(double a, double b, const f64x4& c) {
+  return __builtin_amdgcn_mfma_f64_16x16x4f64(a, b, c, 0, 0, 0);
+}
 
-// m and u, element by element of the filled-up matrix.
+// The gradient's element type: NF4_AB_*.
+template <int kGrad>
+__device__ __forceinline__ float muon_grad(Rsrc r, uint32_t at) {
+  if (kGrad == NF4_AB_F32) return ld_f32(r, at == kMasked ? kMasked : 4 * at);
+  const uint32_t h = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(r, at == kMasked ? kMasked : 2 * at, 0, 0));
+  return kGrad == NF4_AB_F16 ? F16::widen(h) : Bf16::widen(h);
+}
+// m updated and u, of element `at` of the matrix.
+__device__ __forceinline__ float muon_direction(const MuonArgs& p, const MuonJob& J, uint32_t at, float g, float m0) {
+  const double mu = p.momentum, nu = 1.0 - mu;
+  const float m = static_cast<float>(mu * m0 + nu * g);
+  J.mom[at] = m;
+  return p.nesterov ? static_cast<float>(nu * g + mu * m) : m;
+}
+
+// r <= 64.  Workgroup: one chunk of the long side; per 64 of it m and u, element by element
+// in the order in memory, u into LDS as [long][rank], and its wave's 16 of the Gram
+// matrix's upper tiles.  The waves are added in LDS in order.
+template <int NT, int kGrad>
+__global__ __launch_bounds__(256) void muon_gram64_kernel(MuonArgs p, int64_t first) {
+  constexpr int kPairs = NT * (NT + 1) / 2, kRp = 16 * NT, kLd = kRp + 1, kLoads = kRp / 4;
+  __shared__ float tile[64 * kLd];
+  __shared__ double red[kPairs * 256];
+  int64_t blk = blockIdx.x;
+  const MuonJob& J = job_of(p, first, blk);
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6, q = lane & 15, g = lane >> 4;
+  f64x4 acc[kPairs];
+#pragma unroll
+  for (int x = 0; x < kPairs; ++x) acc[x] = f64x4{0, 0, 0, 0};
+  const int64_t beg = blk * J.chunk, end = min(J.len_p, beg + J.chunk);
+  const uint32_t r = p.r, len = static_cast<uint32_t>(J.len);
+  const Rsrc rg = make_rsrc(J.grad, int64_t(r) * len * (kGrad == NF4_AB_F32 ? 4 : 2)), rm = make_rsrc(J.mom, int64_t(r) * len * 4);
+  for (int64_t l0 = beg; l0 < end; l0 += 64) {
+    float gv[kLoads], mv[kLoads];
+    uint32_t at[kLoads];
+    auto place = [&](int k, int& l, int& c) {   // this thread's k-th element: long l0 + l, rank c
+      const int e = t + 256 * k;
+      l = J.tall ? e / kRp : e & 63;
+      c = J.tall ? e - l * kRp : e >> 6;
+    };
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      int l, c;
+      place(k, l, c);
+      const uint32_t L = static_cast<uint32_t>(l0) + l;
+      at[k] = L < len && c < static_cast<int>(r) ? (J.tall ? L * r + c : c * len + L) : kMasked;
+      gv[k] = muon_grad<kGrad>(rg, at[k]);
+      mv[k] = ld_f32(rm, at[k] == kMasked ? kMasked : 4 * at[k]);
+    }
+    __syncthreads();   // the last 64 have been multiplied
+#pragma unroll
+    for (int k = 0; k < kLoads; ++k) {
+      int l, c;
+      place(k, l, c);
+      const float u = at[k] != kMasked ? muon_direction(p, J, at[k], gv[k], mv[k]) : 0.0f;
+      J.u[J.tall ? (l0 + l) * kRp + c : c * J.len_p + l0 + l] = u;
+      tile[l * kLd + c] = u;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      double f[NT];
+#pragma unroll
+      for (int i = 0; i < NT; ++i) f[i] = static_cast<double>(tile[(16 * wave + 4 * s + g) * kLd + 16 * i + q]);
+#pragma unroll
+      for (int i = 0, x = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = i; j < NT; ++j, ++x) acc[x] = mfma64(f[i], f[j], acc[x]);
+    }
+  }
+  // lane: rows 16 i + g + 4 e, column 16 j + q
+  for (int w = 0; w < 4; ++w) {
+    if (wave == w) {
+#pragma unroll
+      for (int x = 0; x < kPairs; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          double& at = red[x * 256 + (g + 4 * e) * 16 + q];
+          at = w == 0 ? acc[x][e] : at + acc[x][e];
+        }
+    }
+    __syncthreads();
+  }
+  for (int i = t; i < kPairs * 256; i += 256) J.part[blk * (kPairs * 256) + i] = red[i];
+}
+
+// r > 64: m and u, element by element of the filled-up matrix.
+template <int kGrad>
 __global__ __launch_bounds__(256) void muon_momentum_kernel(MuonArgs p, int64_t first) {
   int64_t blk = blockIdx.x;
   const MuonJob& J = job_of(p, first, blk);
   const uint32_t row_p = J.tall ? p.rp : static_cast<uint32_t>(J.len_p);
   const uint32_t rows = J.tall ? static_cast<uint32_t>(J.len) : p.r, cols = J.tall ? p.r : static_cast<uint32_t>(J.len);
-  const int64_t count = J.len_p * p.rp;
-  const double mu = p.momentum, nu = 1.0 - mu;
+  const uint32_t count = static_cast<uint32_t>(J.len_p * p.rp);
+  const Rsrc rg = make_rsrc(J.grad, int64_t(rows) * cols * (kGrad == NF4_AB_F32 ? 4 : 2)), rm = make_rsrc(J.mom, int64_t(rows) * cols * 4);
+  float g[4], m[4];
+  uint32_t at[4];
+#pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int64_t i = blk * 1024 + k * 256 + threadIdx.x;
-    if (i >= count) return;
-    const uint32_t y = static_cast<uint32_t>(i) / row_p, x = static_cast<uint32_t>(i) - y * row_p;
-    float u = 0.0f;
-    if (y < rows && x < cols) {
-      const int64_t at = static_cast<int64_t>(y) * cols + x;
-      const float g = p.grad16 ? widen_of(static_cast<const uint16_t*>(J.grad)[at], p.f16) : static_cast<const float*>(J.grad)[at];
-      const float m = static_cast<float>(mu * J.mom[at] + nu * g);
-      J.mom[at] = m;
-      u = p.nesterov ? static_cast<float>(nu * g + mu * m) : m;
-    }
-    J.u[i] = u;
+    const uint32_t i = static_cast<uint32_t>(blk) * 1024 + k * 256 + threadIdx.x, y = i / row_p, x = i - y * row_p;
+    at[k] = i < count && y < rows && x < cols ? y * cols + x : kMasked;
+    g[k] = muon_grad<kGrad>(rg, at[k]);
+    m[k] = ld_f32(rm, at[k] == kMasked ? kMasked : 4 * at[k]);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t i = static_cast<uint32_t>(blk) * 1024 + k * 256 + threadIdx.x;
+    if (i < count) J.u[i] = at[k] != kMasked ? muon_direction(p, J, at[k], g[k], m[k]) : 0.0f;
   }
 }
 
@@ -97,8 +186,8 @@ __device__ __forceinline__ void gram_load(const MuonJob& J, int rp, int64_t l0, 
   }
 }
 
-// Workgroup: one 64 x 64 tile pair (I <= J) of the Gram matrix over one chunk; its waves
-// take every fourth 16 and are added in LDS in order.
+// r > 64.  Workgroup: one 64 x 64 tile pair (I <= J) of the Gram matrix over one chunk; its
+// waves take every fourth 16 and are added in LDS in order.
 __global__ __launch_bounds__(256) void muon_gram_kernel(MuonArgs p, int64_t first) {
   __shared__ double red[64 * 64];
   int64_t blk = blockIdx.x;
@@ -127,8 +216,7 @@ __global__ __launch_bounds__(256) void muon_gram_kernel(MuonArgs p, int64_t firs
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f64_16x16x4f64(static_cast<double>(a[i][s]), static_cast<double>(b[j][s]), acc[i][j], 0, 0, 0);
+        for (int j = 0; j < 4; ++j) acc[i][j] = mfma64(static_cast<double>(a[i][s]), static_cast<double>(b[j][s]), acc[i][j]);
   }
   // lane: rows 16 i + g + 4 e, column 16 j + q
   for (int w = 0; w < 4; ++w) {
@@ -149,135 +237,318 @@ __global__ __launch_bounds__(256) void muon_gram_kernel(MuonArgs p, int64_t firs
   for (int i = t; i < 4096; i += 256) out[i] = red[i];
 }
 
-// G (both halves) from the partials, in order of the chunks.
-__global__ __launch_bounds__(256) void muon_sum_kernel(MuonArgs p, int64_t first) {
+// G (both halves) from the partials: a workgroup adds 32 elements, each of its eight rows of
+// threads the chunks x, x + 8, .., and then the eight in order.  kSide: tiles of 16 (r <= 64,
+// with `side` of them) or of 64.
+template <int kSide>
+__global__ __launch_bounds__(256) void muon_sum_kernel(MuonArgs p, int side, int64_t first) {
+  __shared__ double red[8][32];
   int64_t blk = blockIdx.x;
   const MuonJob& J = job_of(p, first, blk);
-  const int pairs = p.tiles * (p.tiles + 1) / 2;
-  const int at = static_cast<int>(blk) * 256 + threadIdx.x;   // of pairs * 4096
+  const int pairs = side * (side + 1) / 2, plane = pairs * kSide * kSide;
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5, at = static_cast<int>(blk) * 32 + x;
   double s = 0.0;
-  for (int c = 0; c < J.chunks; ++c) s += J.part[static_cast<int64_t>(c) * pairs * 4096 + at];
-  int pair = at >> 12, I = 0;
-  while (pair >= p.tiles - I) pair -= p.tiles - I++;
-  const int i = 64 * I + ((at >> 6) & 63), j = 64 * (I + pair) + (at & 63);
+#pragma unroll 4
+  for (int c = y; c < J.chunks; c += 8) s += J.part[static_cast<int64_t>(c) * plane + at];
+  red[y][x] = s;
+  __syncthreads();
+  if (y != 0) return;
+  for (int k = 1; k < 8; ++k) s += red[k][x];
+  int pair = at / (kSide * kSide), I = 0;
+  while (pair >= side - I) pair -= side - I++;
+  const int i = kSide * I + (at / kSide) % kSide, j = kSide * (I + pair) + at % kSide;
   if (i >= p.rp || j >= p.rp) return;
   J.mat[i * p.rp + j] = s;
   J.mat[j * p.rp + i] = s;
 }
 
-// 1 / max(|u|, eps)^2 from the Gram matrix's diagonal.
-__device__ __forceinline__ double muon_scale(const double* G, int rp, double eps) {
+// 1 / max(|u|, eps)^2 from the Gram matrix's diagonal (d: its first element, rows ld apart).
+__device__ __forceinline__ double muon_scale(const double* d, int ld, int rp, double eps) {
   double s = 0.0;
-  for (int i = threadIdx.x & 63; i < rp; i += 64) s += G[i * rp + i];
+  for (int i = threadIdx.x & 63; i < rp; i += 64) s += d[i * (ld + 1)];
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) s += __shfl_xor(s, x, 64);
   const double n = sqrt(s), m = n > eps ? n : (n == n ? eps : n);
   return 1.0 / (m * m);
 }
 
-// Which r x r products a launch computes: H = G G; T = G P and the next Q = Q P; the
+// r <= 64: the whole iteration of one matrix in one workgroup, G, P, Q and S = G P in LDS.
+// Everything is symmetric, so only the upper tiles are computed, a wave each, and stored
+// twice; all operands are read along their rows (68 a row: 64 lanes on all banks), P's
+// once for its three products.  Bound by the matrix unit of one CU, 32 flops a cycle and
+// SIMD: at r = 64 the 17 products, 64 deep, three tiles a SIMD, take 22 us of it.
+template <int NT>
+__global__ __launch_bounds__(64 * (NT * (NT + 1) / 2)) void muon_iterate64_kernel(MuonArgs p) {
+  constexpr int kRp = 16 * NT, kLd = 68, kThreads = 64 * (NT * (NT + 1) / 2), kDeep = kRp / 4;
+  extern __shared__ double lds[];
+  double *G = lds, *P = G + kRp * kLd, *Q = P + kRp * kLd, *S = Q + kRp * kLd;
+  double* mat = p.j[blockIdx.x].mat;
+  const int t = threadIdx.x, lane = t & 63, q = lane & 15, g = lane >> 4;
+  int pair = __builtin_amdgcn_readfirstlane(t >> 6), I = 0;
+  while (pair >= NT - I) pair -= NT - I++;
+  const int i0 = 16 * I, j0 = 16 * (I + pair);
+  for (int i = t; i < kRp * kRp; i += kThreads) G[(i / kRp) * kLd + i % kRp] = mat[i];
+  __syncthreads();
+  const double sc = muon_scale(G, kLd, kRp, p.eps);
+  __syncthreads();
+  for (int i = t; i < kRp * kRp; i += kThreads) {
+    const int at = (i / kRp) * kLd + i % kRp;
+    G[at] *= sc;
+    Q[at] = i / kRp == i % kRp ? 1.0 : 0.0;
+  }
+  __syncthreads();
+  const int ra = (i0 + q) * kLd + g, rb = (j0 + q) * kLd + g;
+  auto put = [&](double* M, const f64x4& v) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = i0 + g + 4 * e, j = j0 + q;
+      if (i > j) continue;   // a diagonal tile's lower half comes from its upper
+      M[i * kLd + j] = v[e];
+      M[j * kLd + i] = v[e];
+    }
+  };
+  struct Rows {
+    double v[kDeep];
+  };
+  auto rows = [&](const double* at) {
+    Rows R;
+#pragma unroll
+    for (int k = 0; k < kDeep; ++k) R.v[k] = at[4 * k];
+    return R;
+  };
+  // two chains, so that a wave need not wait for its own last product
+  auto product = [&](const Rows& a, const Rows& b) {
+    f64x4 x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < kDeep; k += 2) {
+      x = mfma64(a.v[k], b.v[k], x);
+      y = mfma64(a.v[k + 1], b.v[k + 1], y);
+    }
+    return x + y;
+  };
+  f64x4 gt;   // this wave's tile of G
+#pragma unroll
+  for (int e = 0; e < 4; ++e) gt[e] = G[(i0 + g + 4 * e) * kLd + j0 + q];
+  for (int step = 0; step < p.steps; ++step) {
+    const bool last = step + 1 == p.steps;
+    const Rows ga = rows(G + ra);
+    f64x4 pt = product(ga, rows(G + rb));
+#pragma unroll
+    for (int e = 0; e < 4; ++e) pt[e] = (i0 + g + 4 * e == j0 + q ? p.a : 0.0) + p.b * gt[e] + p.c * pt[e];
+    put(P, pt);
+    __syncthreads();
+    const Rows pb = rows(P + rb);
+    f64x4 qt = pt;
+    if (step > 0) qt = product(rows(Q + ra), pb);
+    if (!last) put(S, product(ga, pb));
+    __syncthreads();
+    put(Q, qt);          // read again after the next barrier but one
+    if (last) break;
+    gt = product(rows(S + ra), pb);
+    put(G, gt);          // read before the last barrier
+    __syncthreads();
+  }
+  __syncthreads();
+  // Q / |u|, after G
+  const double root = sqrt(sc);
+  for (int i = t; i < kRp * kRp; i += kThreads) mat[kRp * kRp + i] = root * Q[(i / kRp) * kLd + i % kRp];
+}
+
+// r > 64: which r x r products a launch computes: H = G G; T = G P and the next Q = Q P; the
 // next G = T P.
 enum { kSquare = 0, kMixed = 1, kNext = 2 };
 
 // A wave: one 16 x 16 tile.  All operands are symmetric up to rounding, so both are read
-// along their rows.  step 0: G carries its scale still, Q is the identity.
-__global__ __launch_bounds__(256) void muon_product_kernel(MuonArgs p, int what, int step, int64_t first) {
+// along their rows.  kFirst: G carries its scale still, Q is the identity.  last: Q gets its
+// 1 / |u|.
+template <int kWhat, bool kFirst>
+__global__ __launch_bounds__(256) void muon_product_kernel(MuonArgs p, int step, const double* scales, int64_t first) {
   int64_t blk = blockIdx.x;
+  const bool second = blk >= first;
   const MuonJob& J = job_of(p, first, blk);
   const int lane = threadIdx.x & 63, q = lane & 15, g = lane >> 4, rp = p.rp, side = rp / 16;
   const int plane = rp * rp;
   const int now = step & 1, then = 1 - now;
   const double *G = J.mat + now * plane, *Q = J.mat + (4 + now) * plane;
   double *H = J.mat + 2 * plane, *T = J.mat + 3 * plane, *Gn = J.mat + then * plane, *Qn = J.mat + (4 + then) * plane;
-  const double sc = step == 0 ? muon_scale(G, rp, p.eps) : 1.0;
+  const double sc = scales[second], g1 = kFirst ? sc : 1.0;
   const int tile = static_cast<int>(blk) * 4 + (threadIdx.x >> 6);
   if (tile >= side * side) return;
   const int i0 = 16 * (tile / side), j0 = 16 * (tile % side);
-  auto poly = [&](int i, int j) { return (i == j ? p.a : 0.0) + p.b * sc * G[i * rp + j] + p.c * H[i * rp + j]; };
+  const double *ga = (kWhat == kNext ? T : G) + (i0 + q) * rp + 4 * g, *gb = G + (j0 + q) * rp + 4 * g;
+  const double *hb = H + (j0 + q) * rp + 4 * g, *qa = Q + (i0 + q) * rp + 4 * g;
   f64x4 x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
-  for (int k0 = 0; k0 < rp; k0 += 16) {
+  struct Rows {
+    f64x4 a, b, h, q;
+  };
+  auto load = [&](int k0, Rows& R) {
+    R.a = *reinterpret_cast<const f64x4*>(ga + k0);
+    R.b = *reinterpret_cast<const f64x4*>(gb + k0);
+    if (kWhat != kSquare) R.h = *reinterpret_cast<const f64x4*>(hb + k0);
+    if (kWhat == kMixed && !kFirst) R.q = *reinterpret_cast<const f64x4*>(qa + k0);
+  };
+  auto mul = [&](int k0, const Rows& R) {
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const int k = k0 + 4 * g + s;
-      const double gi = what == kNext ? T[(i0 + q) * rp + k] : sc * G[(i0 + q) * rp + k];
-      const double oj = what == kSquare ? sc * G[(j0 + q) * rp + k] : poly(j0 + q, k);
-      x = __builtin_amdgcn_mfma_f64_16x16x4f64(gi, oj, x, 0, 0, 0);
-      if (what == kMixed && step > 0) y = __builtin_amdgcn_mfma_f64_16x16x4f64(Q[(i0 + q) * rp + k], oj, y, 0, 0, 0);
+      const double gi = kWhat == kNext ? R.a[s] : g1 * R.a[s];
+      const double oj = kWhat == kSquare ? g1 * R.b[s] : (k0 + 4 * g + s == j0 + q ? p.a : 0.0) + p.b * g1 * R.b[s] + p.c * R.h[s];
+      x = mfma64(gi, oj, x);
+      if (kWhat == kMixed && !kFirst) y = mfma64(R.q[s], oj, y);
     }
+  };
+  // four steps' rows requested together
+  for (int k0 = 0; k0 < rp; k0 += 64) {
+    Rows R[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (k0 + 16 * u < rp) load(k0 + 16 * u, R[u]);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (k0 + 16 * u < rp) mul(k0 + 16 * u, R[u]);
   }
-  double* out = what == kSquare ? H : (what == kMixed ? T : Gn);
+  double* out = kWhat == kSquare ? H : (kWhat == kMixed ? T : Gn);
+  const double root = step + 1 == p.steps ? sqrt(sc) : 1.0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int i = i0 + g + 4 * e, j = j0 + q;
-    if (what == kMixed) Qn[i * rp + j] = step == 0 ? poly(i, j) : y[e];
+    if (kWhat == kMixed)
+      Qn[i * rp + j] = root * (kFirst ? (i == j ? p.a : 0.0) + p.b * g1 * G[i * rp + j] + p.c * H[i * rp + j] : y[e]);
     out[i * rp + j] = x[e];
   }
 }
 
-// X = U Q / |u| and the parameters.
-__device__ __forceinline__ void muon_update(const MuonArgs& p, const MuonJob& J, int64_t at, double x) {
-  const float old = J.master != nullptr ? J.master[at] : widen_of(J.param[at], p.f16);
-  const float v = static_cast<float>(static_cast<double>(old) * p.decay - J.step * x);
-  if (J.master != nullptr) J.master[at] = v;
-  J.param[at] = half_of(v, p.f16);
+// r > 64: the scales of both matrices; without a step also Q.
+__global__ __launch_bounds__(64) void muon_scale_kernel(MuonArgs p, double* scales) {
+  const int rp = p.rp;
+  const double s = muon_scale(p.j[blockIdx.x].mat, rp, rp, p.eps);
+  if (threadIdx.x == 0) scales[blockIdx.x] = s;
+  if (p.steps == 0)
+    for (int i = threadIdx.x; i < rp * rp; i += 64) p.j[blockIdx.x].mat[4 * rp * rp + i] = i / rp == i % rp ? sqrt(s) : 0.0;
 }
 
-// Workgroup: 16 of the long side, wave w the 16-wide tiles w, w + 4, .. of the rank.
-__global__ __launch_bounds__(256) void muon_apply_kernel(MuonArgs p, const double* scales, int q_at, int64_t first) {
-  int64_t blk = blockIdx.x;
-  const bool second = blk >= first;
-  const MuonJob& J = job_of(p, first, blk);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane & 15, g = lane >> 4, rp = p.rp;
-  const double* Q = J.mat + static_cast<int64_t>(q_at) * rp * rp;
-  const double sc = sqrt(scales[second]);
-  const int64_t l0 = blk * 16;
-  for (int c0 = 16 * wave; c0 < rp; c0 += 64) {
-    f64x4 x = {0, 0, 0, 0};
-    for (int k0 = 0; k0 < rp; k0 += 4) {
-      const int k = k0 + g;
-      const double qv = q_at < 0 ? (k == c0 + q ? 1.0 : 0.0) : Q[k * rp + c0 + q];
-      if (J.tall)
-        x = __builtin_amdgcn_mfma_f64_16x16x4f64(static_cast<double>(J.u[(l0 + q) * rp + k]), qv, x, 0, 0, 0);
-      else
-        x = __builtin_amdgcn_mfma_f64_16x16x4f64(qv, static_cast<double>(J.u[k * J.len_p + l0 + q]), x, 0, 0, 0);
+// X = U Q and the parameters.  Workgroup: 64 of the long side, a wave 16; Q (symmetric, so
+// both layouts read it along its rows) passes through LDS in 64 x 64 pieces.  Bound by
+// memory: u, the parameters and their copies once.
+template <bool kF16, bool kMaster, bool kTall>
+__device__ __forceinline__ void muon_apply(const MuonArgs& p, const MuonJob& J, int64_t blk, const double* Q, double* qs) {
+  constexpr int kLd = 65;
+  const int t = threadIdx.x, lane = t & 63, wave = t >> 6, q = lane & 15, g = lane >> 4, rp = p.rp;
+  const int64_t l0 = blk * 64 + 16 * wave;
+  const uint32_t r = p.r, len = static_cast<uint32_t>(J.len);
+  const Rsrc rq = make_rsrc(Q, static_cast<int64_t>(rp) * rp * 8), ru = make_rsrc(J.u, J.len_p * rp * 4);
+  const Rsrc ro = make_rsrc(kMaster ? static_cast<const void*>(J.master) : J.param, int64_t(r) * len * (kMaster ? 4 : 2));
+  for (int c0 = 0; c0 < rp; c0 += 64) {
+    const int cn = min(rp - c0, 64);
+    // the old values of this lane's outputs.  tall: long g + 4 e, rank q; wide: the other way
+    uint32_t at[4][4];
+    float old[4][4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t l = static_cast<uint32_t>(l0) + (kTall ? g + 4 * e : q), c = c0 + 16 * j + (kTall ? q : g + 4 * e);
+        at[j][e] = l < len && c < r ? (kTall ? l * r + c : c * len + l) : kMasked;
+        old[j][e] = muon_grad<kMaster ? NF4_AB_F32 : (kF16 ? NF4_AB_F16 : NF4_AB_BF16)>(ro, at[j][e]);
+      }
+    f64x4 x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) x[j] = f64x4{0, 0, 0, 0};
+    for (int k0 = 0; k0 < rp; k0 += 64) {
+      const int kn = min(rp - k0, 64);
+      float u[4][4];
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const int k = k0 + 16 * kk + (kTall ? 4 * g + s : 4 * s + g);
+          const uint32_t L = static_cast<uint32_t>(l0) + q;
+          u[kk][s] = ld_f32(ru, k < rp ? (kTall ? L * rp + k : static_cast<uint32_t>(k) * static_cast<uint32_t>(J.len_p) + L) * 4 : kMasked);
+        }
+      uint2 qv[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int c = (t >> 6) + 4 * i, k = t & 63;
+        qv[i] = ld_b64(rq, c < cn && k < kn ? static_cast<uint32_t>((c0 + c) * rp + k0 + k) * 8 : kMasked);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 16; ++i) qs[((t >> 6) + 4 * i) * kLd + (t & 63)] = __builtin_bit_cast(double, qv[i]);
+      __syncthreads();
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk) {
+        if (16 * kk >= kn) break;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+          const int k = 16 * kk + (kTall ? 4 * g + s : 4 * s + g);
+          const double ud = static_cast<double>(u[kk][s]);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if (16 * j >= cn) break;
+            const double w = qs[(16 * j + q) * kLd + k];
+            x[j] = kTall ? mfma64(ud, w, x[j]) : mfma64(w, ud, x[j]);
+          }
+        }
+      }
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      // tall: long g + 4 e, rank q; wide: rank g + 4 e, long q
-      const int64_t l = l0 + (J.tall ? g + 4 * e : q);
-      const int c = c0 + (J.tall ? q : g + 4 * e);
-      if (l < J.len && c < p.r) muon_update(p, J, J.tall ? l * p.r + c : c * J.len + l, sc * x[e]);
-    }
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (at[j][e] == kMasked) continue;
+        const float v = static_cast<float>(static_cast<double>(old[j][e]) * p.decay - J.step * x[j][e]);
+        if (kMaster) J.master[at[j][e]] = v;
+        J.param[at[j][e]] = half_of(v, kF16);
+      }
   }
 }
-
-// The scales of both matrices, before G is overwritten.
-__global__ __launch_bounds__(64) void muon_scale_kernel(MuonArgs p, double* scales) {
-  const double s = muon_scale(p.j[blockIdx.x].mat, p.rp, p.eps);
-  if (threadIdx.x == 0) scales[blockIdx.x] = s;
+template <bool kF16, bool kMaster>
+__global__ __launch_bounds__(256) void muon_apply_kernel(MuonArgs p, int q_at, int64_t first) {
+  __shared__ double qs[64 * 65];
+  int64_t blk = blockIdx.x;
+  const MuonJob& J = job_of(p, first, blk);
+  const double* Q = J.mat + static_cast<int64_t>(q_at) * p.rp * p.rp;
+  if (J.tall) muon_apply<kF16, kMaster, true>(p, J, blk, Q, qs);
+  else muon_apply<kF16, kMaster, false>(p, J, blk, Q, qs);
 }
 
 struct MuonSizes {
-  int64_t len_p, chunk, u, part, mat;
-  int chunks;
+  int64_t len_p, u, part, mat;
+  int chunk, chunks;
 };
-MuonSizes muon_sizes(int64_t len, int64_t r) {
+// Chunks of both matrices so that about 256 workgroups run.
+MuonSizes muon_sizes(int64_t len, int64_t other, int64_t r) {
   MuonSizes s;
   const int64_t rp = round_up(r, 16), tiles = cdiv(rp, 64), pairs = tiles * (tiles + 1) / 2;
-  s.len_p = round_up(len, 16);
-  int64_t chunks = cdiv(96, pairs);
-  s.chunk = round_up(cdiv(s.len_p, chunks), 64);
-  s.chunks = static_cast<int>(cdiv(s.len_p, s.chunk));
+  s.len_p = round_up(len, 64);
+  const int64_t chunk = round_up(cdiv(s.len_p + round_up(other, 64), cdiv(256, pairs)), 64);
+  s.chunk = static_cast<int>(chunk);
+  s.chunks = static_cast<int>(cdiv(s.len_p, chunk));
+  const int64_t side = rp / 16;
+  const int64_t plane = tiles == 1 ? side * (side + 1) / 2 * 256 : pairs * 4096;
   s.u = align256(s.len_p * rp * 4);
-  s.part = align256(static_cast<int64_t>(s.chunks) * pairs * 4096 * 8);
-  s.mat = align256(6 * rp * rp * 8);
+  s.part = align256(s.chunks * plane * 8);
+  s.mat = align256((tiles == 1 ? 2 : 6) * rp * rp * 8);
   return s;
+}
+
+template <int NT>
+hipError_t launch_muon64(const MuonArgs& p, int grad, int64_t c0, int64_t c1, hipStream_t stream) {
+  constexpr int kPairs = NT * (NT + 1) / 2, kLds = 4 * 16 * NT * 68 * 8;
+  static const hipError_t lds_limit = hipFuncSetAttribute(reinterpret_cast<const void*>(&muon_iterate64_kernel<NT>),
+                                                          hipFuncAttributeMaxDynamicSharedMemorySize, kLds);
+  if (lds_limit != hipSuccess) return lds_limit;
+  auto* k = grad == NF4_AB_F32 ? muon_gram64_kernel<NT, NF4_AB_F32>
+                               : (grad == NF4_AB_F16 ? muon_gram64_kernel<NT, NF4_AB_F16> : muon_gram64_kernel<NT, NF4_AB_BF16>);
+  hipLaunchKernelGGL(k, dim3(static_cast<unsigned>(c0 + c1)), dim3(256), 0, stream, p, c0);
+  hipLaunchKernelGGL(muon_sum_kernel<16>, dim3(2 * kPairs * 8), dim3(256), 0, stream, p, NT, int64_t(kPairs) * 8);
+  hipLaunchKernelGGL(muon_iterate64_kernel<NT>, dim3(2), dim3(64 * kPairs), kLds, stream, p);
+  return hipGetLastError();
 }
 
 }  // namespace
 
 int64_t muon_workspace_bytes(int64_t K, int64_t N, int64_t r) {
-  const MuonSizes a = muon_sizes(K, r), b = muon_sizes(N, r);
+  const MuonSizes a = muon_sizes(K, N, r), b = muon_sizes(N, K, r);
   return 256 + a.u + a.part + a.mat + b.u + b.part + b.mat;
 }
 
@@ -288,11 +559,12 @@ hipError_t launch_muon(int64_t K, int64_t N, int64_t r, uint16_t* A, uint16_t* B
   p.r = static_cast<int>(r);
   p.rp = static_cast<int>(round_up(r, 16));
   p.tiles = (p.rp + 63) / 64;
-  p.f16 = dtype == kDtypeF16;
-  p.grad16 = grad16;
+  const bool f16 = dtype == kDtypeF16;
+  const int grad = !grad16 ? NF4_AB_F32 : (f16 ? NF4_AB_F16 : NF4_AB_BF16);
   p.momentum = o.momentum;
   p.decay = 1.0 - o.lr * o.weight_decay;
   p.nesterov = o.nesterov != 0;
+  p.steps = o.steps;
   p.eps = o.eps;
   p.a = o.a;
   p.b = o.b;
@@ -302,7 +574,7 @@ hipError_t launch_muon(int64_t K, int64_t N, int64_t r, uint16_t* A, uint16_t* B
   MuonSizes s[2];
   for (int i = 0; i < 2; ++i) {
     const int64_t len = i ? N : K;
-    s[i] = muon_sizes(len, r);
+    s[i] = muon_sizes(len, i ? K : N, r);
     MuonJob& J = p.j[i];
     J.param = i ? B : A;
     J.grad = i ? dB : dA;
@@ -325,20 +597,41 @@ hipError_t launch_muon(int64_t K, int64_t N, int64_t r, uint16_t* A, uint16_t* B
     J.mat = reinterpret_cast<double*>(at);
     at += s[i].mat;
   }
-  const int64_t pairs = static_cast<int64_t>(p.tiles) * (p.tiles + 1) / 2;
   auto grid = [](int64_t a, int64_t b) { return dim3(static_cast<unsigned>(a + b)); };
   Timer tm(QK_MUON, stream);
-  const int64_t m0 = cdiv(s[0].len_p * p.rp, 1024), m1 = cdiv(s[1].len_p * p.rp, 1024);
-  hipLaunchKernelGGL(muon_momentum_kernel, grid(m0, m1), dim3(256), 0, stream, p, m0);
-  hipLaunchKernelGGL(muon_gram_kernel, grid(s[0].chunks * pairs, s[1].chunks * pairs), dim3(256), 0, stream, p, s[0].chunks * pairs);
-  hipLaunchKernelGGL(muon_sum_kernel, grid(pairs * 16, pairs * 16), dim3(256), 0, stream, p, pairs * 16);
-  hipLaunchKernelGGL(muon_scale_kernel, dim3(2), dim3(64), 0, stream, p, scales);
-  const int64_t side = p.rp / 16, wgs = cdiv(side * side, 4);
-  for (int i = 0; i < o.steps; ++i)
-    for (int what = kSquare; what <= (i + 1 < o.steps ? kNext : kMixed); ++what)
-      hipLaunchKernelGGL(muon_product_kernel, grid(wgs, wgs), dim3(256), 0, stream, p, what, i, wgs);
-  hipLaunchKernelGGL(muon_apply_kernel, grid(s[0].len_p / 16, s[1].len_p / 16), dim3(256), 0, stream, p,
-                     static_cast<const double*>(scales), o.steps == 0 ? -1 : 4 + (o.steps & 1), s[0].len_p / 16);
+  int q_at = 1;
+  if (p.tiles == 1) {
+    hipError_t e;
+    switch (p.rp / 16) {
+      case 1: e = launch_muon64<1>(p, grad, s[0].chunks, s[1].chunks, stream); break;
+      case 2: e = launch_muon64<2>(p, grad, s[0].chunks, s[1].chunks, stream); break;
+      case 3: e = launch_muon64<3>(p, grad, s[0].chunks, s[1].chunks, stream); break;
+      default: e = launch_muon64<4>(p, grad, s[0].chunks, s[1].chunks, stream); break;
+    }
+    if (e != hipSuccess) return e;
+  } else {
+    const int64_t pairs = static_cast<int64_t>(p.tiles) * (p.tiles + 1) / 2;
+    const int64_t m0 = cdiv(s[0].len_p * p.rp, 1024), m1 = cdiv(s[1].len_p * p.rp, 1024);
+    auto* mk = grad == NF4_AB_F32 ? muon_momentum_kernel<NF4_AB_F32>
+                                  : (grad == NF4_AB_F16 ? muon_momentum_kernel<NF4_AB_F16> : muon_momentum_kernel<NF4_AB_BF16>);
+    hipLaunchKernelGGL(mk, grid(m0, m1), dim3(256), 0, stream, p, m0);
+    hipLaunchKernelGGL(muon_gram_kernel, grid(s[0].chunks * pairs, s[1].chunks * pairs), dim3(256), 0, stream, p, s[0].chunks * pairs);
+    hipLaunchKernelGGL(muon_sum_kernel<64>, grid(pairs * 128, pairs * 128), dim3(256), 0, stream, p, p.tiles, pairs * 128);
+    hipLaunchKernelGGL(muon_scale_kernel, dim3(2), dim3(64), 0, stream, p, scales);
+    const int64_t side = p.rp / 16, wgs = cdiv(side * side, 4);
+    auto product = [&](auto* k, int i) {
+      hipLaunchKernelGGL(k, grid(wgs, wgs), dim3(256), 0, stream, p, i, static_cast<const double*>(scales), wgs);
+    };
+    for (int i = 0; i < o.steps; ++i) {
+      product(i == 0 ? muon_product_kernel<kSquare, true> : muon_product_kernel<kSquare, false>, i);
+      product(i == 0 ? muon_product_kernel<kMixed, true> : muon_product_kernel<kMixed, false>, i);
+      if (i + 1 < o.steps) product(i == 0 ? muon_product_kernel<kNext, true> : muon_product_kernel<kNext, false>, i);
+    }
+    q_at = 4 + (o.steps & 1);
+  }
+  auto* ak = f16 ? (A_master ? muon_apply_kernel<true, true> : muon_apply_kernel<true, false>)
+                 : (A_master ? muon_apply_kernel<false, true> : muon_apply_kernel<false, false>);
+  hipLaunchKernelGGL(ak, grid(s[0].len_p / 64, s[1].len_p / 64), dim3(256), 0, stream, p, q_at, s[0].len_p / 64);
   tm.stop();
   return hipGetLastError();
 }
