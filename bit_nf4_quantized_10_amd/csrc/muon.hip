@@ -77,12 +77,12 @@ __device__ __forceinline__ float muon_direction(const MuonArgs& p, const MuonJob
 
 // r <= 64.  Workgroup: one chunk of the long side; per 64 of it m and u, element by element
 // in the order in memory, u into LDS as [long][rank], and its wave's 16 of the Gram
-// matrix's upper tiles.  The waves are added in LDS in order.
+// matrix's upper tiles.
 template <int NT, int kGrad>
 __global__ __launch_bounds__(256) void muon_gram64_kernel(MuonArgs p, int64_t first) {
   constexpr int kPairs = NT * (NT + 1) / 2, kRp = 16 * NT, kLd = kRp + 1, kLoads = kRp / 4;
   __shared__ float tile[64 * kLd];
-  __shared__ double red[kPairs * 256];
+  __shared__ double red[2][kPairs * 256];
   int64_t blk = blockIdx.x;
   const MuonJob& J = job_of(p, first, blk);
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6, q = lane & 15, g = lane >> 4;
@@ -131,19 +131,21 @@ __global__ __launch_bounds__(256) void muon_gram64_kernel(MuonArgs p, int64_t fi
     }
   }
   // lane: rows 16 i + g + 4 e, column 16 j + q
-  for (int w = 0; w < 4; ++w) {
-    if (wave == w) {
+  // the sum of the waves, (0 + 2) + (1 + 3)
+#pragma unroll
+  for (int w = 0; w < 4; w += 2) {
+    if ((wave & 2) == w) {
 #pragma unroll
       for (int x = 0; x < kPairs; ++x)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          double& at = red[x * 256 + (g + 4 * e) * 16 + q];
+          double& at = red[wave & 1][x * 256 + (g + 4 * e) * 16 + q];
           at = w == 0 ? acc[x][e] : at + acc[x][e];
         }
     }
     __syncthreads();
   }
-  for (int i = t; i < kPairs * 256; i += 256) J.part[blk * (kPairs * 256) + i] = red[i];
+  for (int i = t; i < kPairs * 256; i += 256) J.part[blk * (kPairs * 256) + i] = red[0][i] + red[1][i];
 }
 
 // r > 64: m and u, element by element of the filled-up matrix.
@@ -358,62 +360,75 @@ __global__ __launch_bounds__(64 * (NT * (NT + 1) / 2)) void muon_iterate64_kerne
 // next G = T P.
 enum { kSquare = 0, kMixed = 1, kNext = 2 };
 
-// A wave: one 16 x 16 tile.  All operands are symmetric up to rounding, so both are read
-// along their rows.  kFirst: G carries its scale still, Q is the identity.  last: Q gets its
-// 1 / |u|.
+// Workgroup: one upper 16 x 16 tile, stored twice (everything is symmetric; both operands are
+// read along their rows); its waves every fourth 16 of the depth, all rows requested at
+// once, since what the launch before wrote comes from far, and added in LDS in order.
+// (A wave a tile, 16 requests after another: 10 to 19 us a launch at r = 256, now 7 to 12.)
+// kFirst: G carries its scale still, Q is the identity.  The last step's Q gets its 1 / |u|.
 template <int kWhat, bool kFirst>
 __global__ __launch_bounds__(256) void muon_product_kernel(MuonArgs p, int step, const double* scales, int64_t first) {
+  constexpr bool kQ = kWhat == kMixed && !kFirst;
+  __shared__ f64x4 red[kQ ? 2 : 1][4][64];
   int64_t blk = blockIdx.x;
   const bool second = blk >= first;
   const MuonJob& J = job_of(p, first, blk);
-  const int lane = threadIdx.x & 63, q = lane & 15, g = lane >> 4, rp = p.rp, side = rp / 16;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, q = lane & 15, g = lane >> 4, rp = p.rp, side = rp / 16;
   const int plane = rp * rp;
   const int now = step & 1, then = 1 - now;
   const double *G = J.mat + now * plane, *Q = J.mat + (4 + now) * plane;
   double *H = J.mat + 2 * plane, *T = J.mat + 3 * plane, *Gn = J.mat + then * plane, *Qn = J.mat + (4 + then) * plane;
   const double sc = scales[second], g1 = kFirst ? sc : 1.0;
-  const int tile = static_cast<int>(blk) * 4 + (threadIdx.x >> 6);
-  if (tile >= side * side) return;
-  const int i0 = 16 * (tile / side), j0 = 16 * (tile % side);
-  const double *ga = (kWhat == kNext ? T : G) + (i0 + q) * rp + 4 * g, *gb = G + (j0 + q) * rp + 4 * g;
-  const double *hb = H + (j0 + q) * rp + 4 * g, *qa = Q + (i0 + q) * rp + 4 * g;
-  f64x4 x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
+  int pair = static_cast<int>(blk), I = 0;
+  while (pair >= side - I) pair -= side - I++;
+  const int i0 = 16 * I, j0 = 16 * (I + pair);
   struct Rows {
     f64x4 a, b, h, q;
   };
-  auto load = [&](int k0, Rows& R) {
-    R.a = *reinterpret_cast<const f64x4*>(ga + k0);
-    R.b = *reinterpret_cast<const f64x4*>(gb + k0);
-    if (kWhat != kSquare) R.h = *reinterpret_cast<const f64x4*>(hb + k0);
-    if (kWhat == kMixed && !kFirst) R.q = *reinterpret_cast<const f64x4*>(qa + k0);
-  };
-  auto mul = [&](int k0, const Rows& R) {
+  Rows R[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int k = 16 * (4 * u + wave) + 4 * g, ia = (i0 + q) * rp + k, jb = (j0 + q) * rp + k;
+    if (16 * (4 * u + wave) >= rp) break;
+    R[u].a = *reinterpret_cast<const f64x4*>((kWhat == kNext ? T : G) + ia);
+    R[u].b = *reinterpret_cast<const f64x4*>(G + jb);
+    if (kWhat != kSquare) R[u].h = *reinterpret_cast<const f64x4*>(H + jb);
+    if (kQ) R[u].q = *reinterpret_cast<const f64x4*>(Q + ia);
+  }
+  f64x4 x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    if (16 * (4 * u + wave) >= rp) break;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-      const double gi = kWhat == kNext ? R.a[s] : g1 * R.a[s];
-      const double oj = kWhat == kSquare ? g1 * R.b[s] : (k0 + 4 * g + s == j0 + q ? p.a : 0.0) + p.b * g1 * R.b[s] + p.c * R.h[s];
+      const double gi = kWhat == kNext ? R[u].a[s] : g1 * R[u].a[s];
+      const double oj = kWhat == kSquare
+                            ? g1 * R[u].b[s]
+                            : (16 * (4 * u + wave) + 4 * g + s == j0 + q ? p.a : 0.0) + p.b * g1 * R[u].b[s] + p.c * R[u].h[s];
       x = mfma64(gi, oj, x);
-      if (kWhat == kMixed && !kFirst) y = mfma64(R.q[s], oj, y);
+      if (kQ) y = mfma64(R[u].q[s], oj, y);
     }
-  };
-  // four steps' rows requested together
-  for (int k0 = 0; k0 < rp; k0 += 64) {
-    Rows R[4];
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (k0 + 16 * u < rp) load(k0 + 16 * u, R[u]);
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      if (k0 + 16 * u < rp) mul(k0 + 16 * u, R[u]);
+  }
+  red[0][wave][lane] = x;
+  if (kQ) red[kQ][wave][lane] = y;
+  __syncthreads();
+  if (wave != 0) return;
+  for (int w = 1; w < 4; ++w) {
+    x += red[0][w][lane];
+    if (kQ) y += red[kQ][w][lane];
   }
   double* out = kWhat == kSquare ? H : (kWhat == kMixed ? T : Gn);
   const double root = step + 1 == p.steps ? sqrt(sc) : 1.0;
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
     const int i = i0 + g + 4 * e, j = j0 + q;
-    if (kWhat == kMixed)
-      Qn[i * rp + j] = root * (kFirst ? (i == j ? p.a : 0.0) + p.b * g1 * G[i * rp + j] + p.c * H[i * rp + j] : y[e]);
+    if (i > j) continue;
+    if (kWhat == kMixed) {
+      const double v = root * (kFirst ? (i == j ? p.a : 0.0) + p.b * g1 * G[i * rp + j] + p.c * H[i * rp + j] : y[e]);
+      Qn[i * rp + j] = v;
+      Qn[j * rp + i] = v;
+    }
     out[i * rp + j] = x[e];
+    out[j * rp + i] = x[e];
   }
 }
 
@@ -456,14 +471,24 @@ __device__ __forceinline__ void muon_apply(const MuonArgs& p, const MuonJob& J, 
     for (int k0 = 0; k0 < rp; k0 += 64) {
       const int kn = min(rp - k0, 64);
       float u[4][4];
+      const uint32_t L = static_cast<uint32_t>(l0) + q;
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
+      for (int kk = 0; kk < 4; ++kk) {
+        if constexpr (kTall) {
+          const int k = k0 + 16 * kk + 4 * g;
+          const uint4 v = ld_b128(ru, k < rp ? (L * rp + k) * 4 : kMasked);
+          u[kk][0] = __builtin_bit_cast(float, v.x);
+          u[kk][1] = __builtin_bit_cast(float, v.y);
+          u[kk][2] = __builtin_bit_cast(float, v.z);
+          u[kk][3] = __builtin_bit_cast(float, v.w);
+        } else {
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-          const int k = k0 + 16 * kk + (kTall ? 4 * g + s : 4 * s + g);
-          const uint32_t L = static_cast<uint32_t>(l0) + q;
-          u[kk][s] = ld_f32(ru, k < rp ? (kTall ? L * rp + k : static_cast<uint32_t>(k) * static_cast<uint32_t>(J.len_p) + L) * 4 : kMasked);
+          for (int s = 0; s < 4; ++s) {
+            const uint32_t k = k0 + 16 * kk + 4 * s + g;
+            u[kk][s] = ld_f32(ru, k < static_cast<uint32_t>(rp) ? (k * static_cast<uint32_t>(J.len_p) + L) * 4 : kMasked);
+          }
         }
+      }
       uint2 qv[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
@@ -618,7 +643,7 @@ hipError_t launch_muon(int64_t K, int64_t N, int64_t r, uint16_t* A, uint16_t* B
     hipLaunchKernelGGL(muon_gram_kernel, grid(s[0].chunks * pairs, s[1].chunks * pairs), dim3(256), 0, stream, p, s[0].chunks * pairs);
     hipLaunchKernelGGL(muon_sum_kernel<64>, grid(pairs * 128, pairs * 128), dim3(256), 0, stream, p, p.tiles, pairs * 128);
     hipLaunchKernelGGL(muon_scale_kernel, dim3(2), dim3(64), 0, stream, p, scales);
-    const int64_t side = p.rp / 16, wgs = cdiv(side * side, 4);
+    const int64_t side = p.rp / 16, wgs = side * (side + 1) / 2;
     auto product = [&](auto* k, int i) {
       hipLaunchKernelGGL(k, grid(wgs, wgs), dim3(256), 0, stream, p, i, static_cast<const double*>(scales), wgs);
     };
