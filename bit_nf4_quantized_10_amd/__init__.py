@@ -8,6 +8,7 @@ not built, every call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from dataclasses import dataclass
 
@@ -198,6 +199,14 @@ class _on:
             self.scope.__exit__(*e)
 
 
+def _require_dense(t, name: str, dtype, *shape) -> None:
+    """A contiguous device tensor of that type and shape."""
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return
+    _require_cuda(t, name, dtype)
+    _require_shape(t, name, *shape)
+
+
 def _require_shape(t, name: str, *shape) -> None:
     if tuple(t.shape) != shape:
         raise ValueError(f"{name} must be {' x '.join(map(str, shape))}, got {tuple(t.shape)}")
@@ -324,8 +333,13 @@ class NF4State:
             _require_part(self.absmax, name, "absmax", "torch.float32", n1, device)
 
 
+_DTYPE_NAMES = {}   # torch dtype -> its name, whose formatting costs a microsecond
+
+
 def _require_part(t, name: str, part: str, dtype: str, count: int, device) -> None:
-    if t is None or t.device != device or str(t.dtype) != dtype or t.numel() < count or not t.is_contiguous():
+    if t is not None and t.dtype not in _DTYPE_NAMES:
+        _DTYPE_NAMES[t.dtype] = str(t.dtype)
+    if t is None or t.device != device or _DTYPE_NAMES[t.dtype] != dtype or t.numel() < count or not t.is_contiguous():
         raise ValueError(f"{name}.{part} must be {count} contiguous {dtype} on {device}")
 
 
@@ -526,6 +540,7 @@ NF4_MUON_SCALE_NONE, NF4_MUON_SCALE_SPECTRAL, NF4_MUON_SCALE_RMS = 0, 1, 2
 _MUON_SCALES = {None: NF4_MUON_SCALE_NONE, "spectral": NF4_MUON_SCALE_SPECTRAL, "rms": NF4_MUON_SCALE_RMS}
 
 
+@functools.lru_cache(maxsize=4096)
 def qlora_muon_workspace_bytes(K: int, N: int, r: int) -> int:
     b = ctypes.c_int64()
     _check(lib().qlora_muon_workspace_bytes(K, N, r, ctypes.byref(b)), "qlora_muon_workspace_bytes")
@@ -551,8 +566,7 @@ def qlora_muon_step(A, B, dA, dB, mA, mB, lr: float, momentum: float = 0.95, nes
                            (mA, "mA", torch.float32, (K, r)), (mB, "mB", torch.float32, (r, N)),
                            (A_master, "A_master", torch.float32, (K, r)), (B_master, "B_master", torch.float32, (r, N))):
         if t is not None or not n.endswith("master"):
-            _require_cuda(t, n, d)
-            _require_shape(t, n, *shape)
+            _require_dense(t, n, d, *shape)
     a, b, c = coefficients
     o = _Muon(lr, momentum, weight_decay, eps, a, b, c, steps, int(nesterov), _MUON_SCALES[scaling])
     with _on(A, stream, B, dA, dB, mA, mB, A_master, B_master, workspace) as s:
@@ -665,11 +679,10 @@ def _grad_code(grad_dtype, dt) -> tuple:
 
 def _out(t, name: str, dtype, device, *shape):
     """A given output, checked, or a new one."""
-    import torch
     if t is None:
-        return torch.empty(*shape, dtype=dtype, device=device)
-    _require_cuda(t, name, dtype)
-    _require_shape(t, name, *shape)
+        import torch
+        return torch.empty(shape, dtype=dtype, device=device)
+    _require_dense(t, name, dtype, *shape)
     return t
 
 
@@ -891,6 +904,7 @@ class MXFP4:
         _require_part(self.scales, name, "scales", "torch.uint8", scales, device)
 
 
+@functools.lru_cache(maxsize=4096)
 def mxfp4_sizes(rows: int, cols: int) -> tuple[int, int]:
     """Bytes of the codes and of the scales of a rows x cols matrix."""
     c, s = ctypes.c_int64(), ctypes.c_int64()
@@ -905,10 +919,13 @@ def empty_mxfp4(rows: int, cols: int, device="cuda") -> MXFP4:
                  torch.empty(s, dtype=torch.uint8, device=device))
 
 
+_ELEMENTS = {"torch.float32": NF4_OUT_F32, "torch.bfloat16": NF4_OUT_BF16, "torch.float16": NF4_OUT_F16}
+
+
 def _element_code(dtype) -> int:
     """NF4_OUT_* code of a torch dtype."""
-    import torch
-    code = {torch.float32: NF4_OUT_F32, torch.bfloat16: NF4_OUT_BF16, torch.float16: NF4_OUT_F16}.get(dtype)
+    name = _DTYPE_NAMES.get(dtype) or _DTYPE_NAMES.setdefault(dtype, str(dtype))
+    code = _ELEMENTS.get(name)
     if code is None:
         raise ValueError(f"the element type is fp32, bf16 or fp16, got {dtype}")
     return code
@@ -963,6 +980,7 @@ def mxfp4_dequantize(kept: MXFP4, dtype=None, transpose: bool = False, out=None,
     return out
 
 
+@functools.lru_cache(maxsize=4096)
 def mxfp4_matmul_workspace_bytes(M: int, N: int, K: int) -> int:
     b = ctypes.c_int64()
     _check(lib().mxfp4_matmul_workspace_bytes(M, N, K, ctypes.byref(b)), "mxfp4_matmul_workspace_bytes")
@@ -987,6 +1005,7 @@ def mxfp4_matmul(P: MXFP4, Q: MXFP4, dtype=None, out=None, workspace=None, strea
     return out
 
 
+@functools.lru_cache(maxsize=4096)
 def qlora_mx_workspace_bytes(M: int, K: int, N: int, r: int) -> tuple[int, int]:
     f, b = ctypes.c_int64(), ctypes.c_int64()
     _check(lib().qlora_mx_workspace_bytes(M, K, N, r, ctypes.byref(f), ctypes.byref(b)), "qlora_mx_workspace_bytes")
@@ -1001,8 +1020,7 @@ def qlora_mx_linear_fwd(X, W: MXFP4, A, B, c: float, Y=None, Z=None, workspace=N
     dt = _compute_dtype(X)
     M, (N, K), r = X.shape[0], W.shape, A.shape[1]
     for t, n, shape in ((X, "X", (M, K)), (A, "A", (K, r)), (B, "B", (r, N))):
-        _require_cuda(t, n, dt)
-        _require_shape(t, n, *shape)
+        _require_dense(t, n, dt, *shape)
     W.check("W", X.device)
     with _on(X, stream, A, B, Y, Z, workspace) as s:
         Y = _out(Y, "Y", dt, X.device, M, N)
@@ -1025,8 +1043,7 @@ def qlora_mx_linear_bwd(G, X, Z, W: MXFP4, A, B, c: float, need_dx: bool = True,
     dt = _compute_dtype(G)
     M, (N, K), r = G.shape[0], W.shape, A.shape[1]
     for t, n, shape in ((G, "G", (M, N)), (Z, "Z", (M, r)), (A, "A", (K, r)), (B, "B", (r, N))):
-        _require_cuda(t, n, dt)
-        _require_shape(t, n, *shape)
+        _require_dense(t, n, dt, *shape)
     if X.dtype != dt:
         raise ValueError(f"X must be of {dt}, got {X.dtype}")
     if not isinstance(X, Act8):

@@ -439,6 +439,7 @@ MxRowsPlan plan_mx_rows(int64_t M, int64_t K, int64_t N, int64_t r) {
     p.rw = p.ra == 1 ? (cdiv(N, 16 * wide) * most < 2 * QN_MXR_WGS ? 1 : 2) : (p.ra == 2 ? 2 : (cdiv(N, 32) * most < 2 * QN_MXR_WGS ? 2 : 4));
     int64_t s = QN_MXR_WGS / cdiv(N, 16 * wide * p.rw);
     s = s < 1 ? 1 : (s > most ? most : s);
+    if (r == 0 && chunks <= 16) s = 1;   // four chunks a wave cost less than the launch that adds planes
     while (s > 1 && !fits(s)) --s;
     p.chunks_per = cdiv(chunks, s);
     p.splits = cdiv(chunks, p.chunks_per);
