@@ -406,8 +406,7 @@ int qlora_head_loss(int compute_dtype, int64_t M, int64_t K, int64_t V, const ui
  * low half.  scales: the bytes s + 127, in the order in which the matrix cores take
  * them: 16 rows x 16 blocks are 256 bytes, that of row i and block b at
  *   ((i/16) ceil(cols/512) + b/16) 256 + 4 (16 (b%4) + i%16) + (b%16)/4;
- * rows and blocks are filled up to 16 with bytes that are never 255 (0 where
- * mxfp4_quantize made them). */
+ * rows and blocks are filled up to 16 with bytes 0, columns up to 32 with codes 0. */
 typedef struct mxfp4 {
   int64_t  rows, cols;
   uint8_t* codes;     /* 16-byte aligned */

@@ -189,3 +189,86 @@ def test_what_is_not_finite_shows(r, bad):
     t2 = Case(100, 130, r, "bf16")
     t2.step(0.1)
     assert torch.equal(t.master["B"], t2.master["B"])
+
+
+@pytest.mark.parametrize("K,N,r", [(1000, 77, 33), (64, 500, 64), (300, 130, 100)])
+def test_unaligned_tensors_and_what_lies_around_them(K, N, r):
+    """Tensors that start one element into their memory; their neighbours stay."""
+    import torch
+    say(f"muon unaligned K={K} N={N} r={r}")
+    t, u = Case(K, N, r, "bf16"), Case(K, N, r, "bf16")
+    around = []
+    for d in (u.p, u.g, u.m, u.master):
+        for n in ("A", "B"):
+            v = d[n]
+            buf = torch.full((v.numel() + 65,), 3.0, dtype=v.dtype, device="cuda")
+            buf[1:1 + v.numel()].copy_(v.flatten())
+            d[n] = buf[1:1 + v.numel()].view(v.shape)
+            around.append((buf, v.numel()))
+    n = qn.qlora_muon_workspace_bytes(K, N, r)
+    ws = torch.full((n + 512,), 255, dtype=torch.uint8, device="cuda")
+    t.step(0.1)
+    u.step(0.1, workspace=ws[:n])
+    assert (ws[n:] == 255).all()
+    for d, e in ((t.p, u.p), (t.m, u.m), (t.master, u.master)):
+        assert all(torch.equal(d[k], e[k]) for k in ("A", "B"))
+    for buf, count in around:
+        assert float(buf[0]) == 3.0 and (buf[1 + count:] == 3.0).all()
+
+
+@pytest.mark.parametrize("r", [16, 64, 130])
+def test_replayed_steps(r):
+    """Three replays of a captured step, with eager work between, are three eager steps."""
+    import torch
+    say(f"muon graph r={r}")
+    t, u = Case(700, 300, r, "bf16"), Case(700, 300, r, "bf16")
+    before = {k: {n: d[n].clone() for n in ("A", "B")} for k, d in (("p", u.p), ("m", u.m), ("master", u.master))}
+    g = torch.cuda.CUDAGraph()
+    u.step(0.02)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        u.step(0.02)
+    for k, d in (("p", u.p), ("m", u.m), ("master", u.master)):
+        for n in ("A", "B"):
+            d[n].copy_(before[k][n])
+    for _ in range(3):
+        t.step(0.02)
+        g.replay()
+        torch.cuda.synchronize()
+        Case(40, 50, r, "f16").step(0.1)
+        for d, e in ((t.p, u.p), (t.m, u.m), (t.master, u.master)):
+            assert all(torch.equal(d[n], e[n]) for n in ("A", "B"))
+
+
+def test_streams_at_once():
+    import torch
+    say("muon on three streams")
+    shapes = [(700, 300, 16), (4096, 2000, 64), (300, 500, 100)]
+    want = [Case(*s, "bf16") for s in shapes]
+    for t in want:
+        t.step(0.02)
+    got = [Case(*s, "bf16") for s in shapes]
+    torch.cuda.synchronize()
+    for t in got:
+        t.step(0.02, stream=torch.cuda.Stream())
+    torch.cuda.synchronize()
+    for t, u in zip(want, got):
+        assert all(torch.equal(t.master[n], u.master[n]) and torch.equal(t.m[n], u.m[n]) for n in ("A", "B"))
+
+
+def test_longest_matrices():
+    """2^24 - 1 rows of one rank: the update is the scaled direction."""
+    import torch
+    say("muon of the longest matrices")
+    K = (1 << 24) - 1
+    g = torch.Generator(device="cuda").manual_seed(3)
+    A, B = torch.zeros(K, 1, dtype=torch.bfloat16, device="cuda"), torch.zeros(1, K, dtype=torch.bfloat16, device="cuda")
+    dA, dB = torch.randn(K, 1, generator=g, device="cuda"), torch.randn(1, K, generator=g, device="cuda")
+    mA, mB, MA, MB = (torch.zeros_like(v) for v in (dA, dB, dA, dB))
+    qn.qlora_muon_step(A, B, dA, dB, mA, mB, 1.0, scaling=None, A_master=MA, B_master=MB)
+    x = 1.0
+    for _ in range(5):
+        x = COEFFICIENTS[0] * x + COEFFICIENTS[1] * x ** 3 + COEFFICIENTS[2] * x ** 5
+    for d, M in ((dA, MA), (dB, MB)):
+        want = -x * d.double() / d.double().square().sum().sqrt()
+        assert float((M - want).abs().max()) <= 1e-6 * float(want.abs().max())
