@@ -450,7 +450,7 @@ __device__ __forceinline__ void muon_apply(const MuonArgs& p, const MuonJob& J, 
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6, q = lane & 15, g = lane >> 4, rp = p.rp;
   const int64_t l0 = blk * 64 + 16 * wave;
   const uint32_t r = p.r, len = static_cast<uint32_t>(J.len);
-  const Rsrc rq = make_rsrc(Q, static_cast<int64_t>(rp) * rp * 8), ru = make_rsrc(J.u, J.len_p * rp * 4);
+  const Rsrc rq = make_rsrc(Q, static_cast<int64_t>(rp) * rp * 8);
   const Rsrc ro = make_rsrc(kMaster ? static_cast<const void*>(J.master) : J.param, int64_t(r) * len * (kMaster ? 4 : 2));
   for (int c0 = 0; c0 < rp; c0 += 64) {
     const int cn = min(rp - c0, 64);
@@ -471,22 +471,19 @@ __device__ __forceinline__ void muon_apply(const MuonArgs& p, const MuonJob& J, 
     for (int k0 = 0; k0 < rp; k0 += 64) {
       const int kn = min(rp - k0, 64);
       float u[4][4];
-      const uint32_t L = static_cast<uint32_t>(l0) + q;
+      // u, filled up, may pass 2 GiB; past kn the last 16 again, unused
 #pragma unroll
       for (int kk = 0; kk < 4; ++kk) {
+        const int64_t k = k0 + min(16 * kk, kn - 16);
         if constexpr (kTall) {
-          const int k = k0 + 16 * kk + 4 * g;
-          const uint4 v = ld_b128(ru, k < rp ? (L * rp + k) * 4 : kMasked);
-          u[kk][0] = __builtin_bit_cast(float, v.x);
-          u[kk][1] = __builtin_bit_cast(float, v.y);
-          u[kk][2] = __builtin_bit_cast(float, v.z);
-          u[kk][3] = __builtin_bit_cast(float, v.w);
+          const float4 v = *reinterpret_cast<const float4*>(J.u + (l0 + q) * rp + k + 4 * g);
+          u[kk][0] = v.x;
+          u[kk][1] = v.y;
+          u[kk][2] = v.z;
+          u[kk][3] = v.w;
         } else {
 #pragma unroll
-          for (int s = 0; s < 4; ++s) {
-            const uint32_t k = k0 + 16 * kk + 4 * s + g;
-            u[kk][s] = ld_f32(ru, k < static_cast<uint32_t>(rp) ? (k * static_cast<uint32_t>(J.len_p) + L) * 4 : kMasked);
-          }
+          for (int s = 0; s < 4; ++s) u[kk][s] = J.u[(k + 4 * s + g) * J.len_p + l0 + q];
         }
       }
       uint2 qv[16];
@@ -590,7 +587,8 @@ hipError_t launch_muon(int64_t K, int64_t N, int64_t r, uint16_t* A, uint16_t* B
   p.decay = 1.0 - o.lr * o.weight_decay;
   p.nesterov = o.nesterov != 0;
   p.steps = o.steps;
-  p.eps = o.eps;
+  // a norm is zero or at least an fp32 number's 2^-149; kept where 1 / eps^2 is finite too
+  p.eps = std::fmax(o.eps, 1e-60);
   p.a = o.a;
   p.b = o.b;
   p.c = o.c;

@@ -272,3 +272,53 @@ def test_longest_matrices():
     for d, M in ((dA, MA), (dB, MB)):
         want = -x * d.double() / d.double().square().sum().sqrt()
         assert float((M - want).abs().max()) <= 1e-6 * float(want.abs().max())
+
+
+@pytest.mark.parametrize("r", [16, 80])
+@pytest.mark.parametrize("eps", [2.2250738585072014e-308, 1e-200, 1e30])
+def test_any_eps(r, eps):
+    """Zeros stay zeros however small eps, whose square may be 0; a large one divides."""
+    import torch
+    say(f"muon eps={eps} r={r}")
+    t = Case(90, 70, r, "bf16")
+    for d in (t.g, t.m):
+        for n in ("A", "B"):
+            d[n].zero_()
+    before = t.values()
+    t.step(0.1, eps=eps)
+    check(t, before, 0.1, eps=max(eps, 1e-150))
+    t = Case(90, 70, r, "bf16")
+    before = t.values()
+    t.step(0.1, eps=eps)
+    check(t, before, 0.1, eps=max(eps, 1e-150))
+
+
+@pytest.mark.parametrize("K,N,r", [(11_300_000, 64, 33), (64, 11_300_000, 33), ((1 << 24) - 3, 100, 20), (100, (1 << 24) - 3, 20)])
+def test_directions_past_two_gibibytes(K, N, r):
+    """The direction, its rank filled up to a multiple of 16, takes more memory than its
+    matrix: the last rows and columns are stepped like the first."""
+    import torch
+    say(f"muon of a direction past 2 GiB, {K} x {N}, rank {r}")
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    shapes = ((K, r), (r, N))
+    A, B = (torch.zeros(*s, dtype=torch.bfloat16, device="cuda") for s in shapes)
+    dA, dB = (torch.randn(*s, generator=gen, device="cuda") for s in shapes)
+    mA, mB, MA, MB = (torch.zeros(*s, device="cuda") for s in shapes + shapes)
+    qn.qlora_muon_step(A, B, dA, dB, mA, mB, 1.0, momentum=0.0, nesterov=False, scaling=None, A_master=MA, B_master=MB)
+    a, b, c = COEFFICIENTS
+    for U, M in ((dA, MA), (dB.T, MB.T)):
+        n = U.shape[0]
+        G = torch.zeros(r, r, dtype=torch.float64, device="cuda")
+        for i in range(0, n, 1 << 20):
+            x = U[i:i + (1 << 20)].double().contiguous()
+            G += x.T.contiguous() @ x
+        norm = float(G.trace()) ** 0.5
+        G = host(G) / norm ** 2
+        Q = np.eye(r)
+        for _ in range(5):
+            P = a * np.eye(r) + b * G + c * G @ G
+            Q, G = Q @ P, P @ G @ P
+        for part in (slice(0, 200), slice(n // 2, n // 2 + 200), slice(max(n - 200, 0), n)):
+            want = -host(U[part]).astype(np.float64) @ Q / norm
+            # u is the gradient itself; what is left are 64-bit sums and one rounding
+            assert np.abs(host(M[part]) - want).max() <= 2.0 ** -24 * np.abs(want).max() * 1.01 + 1e-10 * np.abs(want).max()
