@@ -389,12 +389,8 @@ hipError_t launch_panel(const MxRowsArgs& p, int ra, int rw, bool out16, hipStre
   return ra == 4 ? launch_panel_r<T, 4>(p, rw, out16, stream, tm) : launch_panel_r<T, 8>(p, rw, out16, stream, tm);
 }
 
-#ifndef QN_MXR_WGS
-#define QN_MXR_WGS 1024
-#endif
-#ifndef QN_MXR_ZSPLITS
-#define QN_MXR_ZSPLITS 8
-#endif
+constexpr int64_t kWgs = 1024;   // workgroups wanted: four a CU
+constexpr int64_t kZSplits = 8;  // of K, in Z's partials
 
 }  // namespace
 
@@ -436,8 +432,8 @@ MxRowsPlan plan_mx_rows(int64_t M, int64_t K, int64_t N, int64_t r) {
     p.ra = M <= 16 ? 1 : (M <= 32 ? 2 : 4);
     const int64_t most = p.kind == kMxDecode ? chunks : cdiv(chunks, 4);
     const int64_t wide = p.kind == kMxDecode ? 4 : 1;   // waves side by side
-    p.rw = p.ra == 1 ? (cdiv(N, 16 * wide) * most < 2 * QN_MXR_WGS ? 1 : 2) : (p.ra == 2 ? 2 : (cdiv(N, 32) * most < 2 * QN_MXR_WGS ? 2 : 4));
-    int64_t s = QN_MXR_WGS / cdiv(N, 16 * wide * p.rw);
+    p.rw = p.ra == 1 ? (cdiv(N, 16 * wide) * most < 2 * kWgs ? 1 : 2) : (p.ra == 2 ? 2 : (cdiv(N, 32) * most < 2 * kWgs ? 2 : 4));
+    int64_t s = kWgs / cdiv(N, 16 * wide * p.rw);
     s = s < 1 ? 1 : (s > most ? most : s);
     if (r == 0 && chunks <= 16) s = 1;   // four chunks a wave cost less than the launch that adds planes
     while (s > 1 && !fits(s)) --s;
@@ -445,7 +441,7 @@ MxRowsPlan plan_mx_rows(int64_t M, int64_t K, int64_t N, int64_t r) {
     p.splits = cdiv(chunks, p.chunks_per);
   }
   if (r > 0) {
-    p.z_rpw = round_up(cdiv(K, 4 * QN_MXR_ZSPLITS), 32);
+    p.z_rpw = round_up(cdiv(K, 4 * kZSplits), 32);
     p.zsplits = cdiv(K, 4 * p.z_rpw);
     p.zpart = round_up(p.zsplits * M * r * 4, 256);
   }

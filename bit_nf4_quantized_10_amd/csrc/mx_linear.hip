@@ -41,7 +41,9 @@ __global__ __launch_bounds__(256) void mx_sum32_kernel(const float* __restrict__
 // Products run by mx_gemv.hip's kernels up to 64 rows or 2^21 outputs, and by tiles above.
 // The layer, in a graph: 512 rows at 4096 x 4096 35 us and by tiles 42; 256 rows at
 // 4096 x 11008 47 and 42; 777 rows at 2056 x 1336 23 and 33; 1024 at 4096 x 4096 47 and 42.
-bool few_rows(int64_t M, int64_t N) { return M <= 64 || M * N <= (int64_t(1) << 21); }
+// Up to 2^17 rows, which the launch that adds their planes and Z's partials takes in one
+// grid and with 31-bit offsets.
+bool few_rows(int64_t M, int64_t N) { return M <= 64 || (M * N <= (int64_t(1) << 21) && M <= (int64_t(1) << 17)); }
 
 // Splits of a product by tiles (by chunks of the reduction) and their planes' bytes: the
 // split of least estimated time, as plan_split16's: rounds of 256 tiles, the planes

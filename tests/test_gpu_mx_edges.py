@@ -279,3 +279,24 @@ def test_widest_layer(M):
     for n in (slice(0, 600), slice(N // 2, N // 2 + 600), slice(N - 600, N)):
         want = X.numpy().astype(np.float64) @ w[n].T + X.numpy()[:, :1].astype(np.float64) * B.numpy()[:1, n]
         np.testing.assert_array_equal(host(Y[:, n]), oo.round16(want, "bf16"))
+
+
+@pytest.mark.parametrize("M,N,K", [(262144, 8, 1032), (131072, 16, 1032), (65536, 32, 2056)])
+def test_many_rows_of_few_columns(M, N, K):
+    """Whole numbers throughout: X of -2 .. 2, one 1 a column of A, c B of -2 .. 2."""
+    import torch
+    say(f"mx layer of {M} rows, {N} columns")
+    r = 256
+    rng = np.random.default_rng(M + N)
+    codes, scales = _whole(rng, N, K, 0, 0)
+    W, w = _state(codes, scales, K), oo.mxfp4_values(codes, scales, K)
+    X = torch.randint(-2, 3, (M, K), device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)).bfloat16()
+    a = np.zeros((K, r), dtype=np.float32)
+    a[rng.integers(0, K, size=r), np.arange(r)] = 1.0
+    b = rng.integers(-2, 3, size=(r, N)).astype(np.float32)
+    A, B = (torch.from_numpy(v).bfloat16().cuda() for v in (a, b))
+    Y, Z = qn.qlora_mx_linear_fwd(X, W, A, B, 1.0)
+    for rows in (slice(0, 300), slice(M // 2 - 150, M // 2 + 150), slice(M - 300, M)):
+        x = host(X[rows]).astype(np.float64)
+        np.testing.assert_array_equal(host(Z[rows]), x @ a)
+        np.testing.assert_array_equal(host(Y[rows]), oo.round16(x @ w.T + x @ a @ b, "bf16"))
