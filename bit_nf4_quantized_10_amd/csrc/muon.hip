@@ -67,58 +67,76 @@ __device__ __forceinline__ float muon_grad(Rsrc r, uint32_t at) {
   const uint32_t h = static_cast<uint16_t>(__builtin_amdgcn_raw_buffer_load_b16(r, at == kMasked ? kMasked : 2 * at, 0, 0));
   return kGrad == NF4_AB_F16 ? F16::widen(h) : Bf16::widen(h);
 }
-// m updated and u, of element `at` of the matrix.
-__device__ __forceinline__ float muon_direction(const MuonArgs& p, const MuonJob& J, uint32_t at, float g, float m0) {
-  const double mu = p.momentum, nu = 1.0 - mu;
-  const float m = static_cast<float>(mu * m0 + nu * g);
-  J.mom[at] = m;
-  return p.nesterov ? static_cast<float>(nu * g + mu * m) : m;
+// m updated and u, of an element.
+struct MuonDirection {
+  double mu, nu, ug, um;
+  __device__ explicit MuonDirection(const MuonArgs& p)
+      : mu(p.momentum), nu(1.0 - p.momentum), ug(p.nesterov ? nu : 0.0), um(p.nesterov ? mu : 1.0) {}
+  __device__ __forceinline__ float step(float g, float& m) const {
+    m = static_cast<float>(mu * m + nu * g);
+    return static_cast<float>(ug * g + um * m);
+  }
+};
+
+// Everybody's LDS accesses are done; stores to memory may be under way, which
+// __syncthreads() would wait for.
+__device__ __forceinline__ void meet_lds() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
 // r <= 64.  Workgroup: one chunk of the long side; per 64 of it m and u, element by element
 // in the order in memory, u into LDS as [long][rank], and its wave's 16 of the Gram
-// matrix's upper tiles.
-template <int NT, int kGrad>
-__global__ __launch_bounds__(256) void muon_gram64_kernel(MuonArgs p, int64_t first) {
+// matrix's upper tiles; the next 64 are requested meanwhile.
+template <int NT, int kGrad, bool kTall>
+__device__ __forceinline__ void muon_gram64(const MuonArgs& p, const MuonJob& J, int64_t blk, float* tile, double* red) {
   constexpr int kPairs = NT * (NT + 1) / 2, kRp = 16 * NT, kLd = kRp + 1, kLoads = kRp / 4;
-  __shared__ float tile[64 * kLd];
-  __shared__ double red[2][kPairs * 256];
-  int64_t blk = blockIdx.x;
-  const MuonJob& J = job_of(p, first, blk);
   const int t = threadIdx.x, lane = t & 63, wave = t >> 6, q = lane & 15, g = lane >> 4;
-  f64x4 acc[kPairs];
-#pragma unroll
-  for (int x = 0; x < kPairs; ++x) acc[x] = f64x4{0, 0, 0, 0};
-  const int64_t beg = blk * J.chunk, end = min(J.len_p, beg + J.chunk);
+  const int64_t beg = blk * J.chunk, end = min(J.len_p, beg + J.chunk), len_p = J.len_p;
   const uint32_t r = p.r, len = static_cast<uint32_t>(J.len);
   const Rsrc rg = make_rsrc(J.grad, int64_t(r) * len * (kGrad == NF4_AB_F32 ? 4 : 2)), rm = make_rsrc(J.mom, int64_t(r) * len * 4);
-  for (int64_t l0 = beg; l0 < end; l0 += 64) {
-    float gv[kLoads], mv[kLoads];
+  const MuonDirection dir(p);
+  float* const u_out = J.u;
+  auto place = [&](int k, int& l, int& c) {   // this thread's k-th element: long l0 + l, rank c
+    const int e = t + 256 * k;
+    l = kTall ? e / kRp : e & 63;
+    c = kTall ? e - l * kRp : e >> 6;
+  };
+  struct Loads {
+    float g[kLoads], m[kLoads];
     uint32_t at[kLoads];
-    auto place = [&](int k, int& l, int& c) {   // this thread's k-th element: long l0 + l, rank c
-      const int e = t + 256 * k;
-      l = J.tall ? e / kRp : e & 63;
-      c = J.tall ? e - l * kRp : e >> 6;
-    };
+  };
+  auto load = [&](int64_t l0, Loads& v) {
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) {
       int l, c;
       place(k, l, c);
       const uint32_t L = static_cast<uint32_t>(l0) + l;
-      at[k] = L < len && c < static_cast<int>(r) ? (J.tall ? L * r + c : c * len + L) : kMasked;
-      gv[k] = muon_grad<kGrad>(rg, at[k]);
-      mv[k] = ld_f32(rm, at[k] == kMasked ? kMasked : 4 * at[k]);
+      v.at[k] = L < len && c < static_cast<int>(r) ? (kTall ? L * r + c : c * len + L) : kMasked;
+      v.g[k] = muon_grad<kGrad>(rg, v.at[k]);
+      v.m[k] = ld_f32(rm, v.at[k] == kMasked ? kMasked : 4 * v.at[k]);
     }
-    __syncthreads();   // the last 64 have been multiplied
+  };
+  f64x4 acc[kPairs];
+#pragma unroll
+  for (int x = 0; x < kPairs; ++x) acc[x] = f64x4{0, 0, 0, 0};
+  Loads v;
+  load(beg, v);
+  for (int64_t l0 = beg; l0 < end; l0 += 64) {
+    meet_lds();   // the last 64 have been multiplied
 #pragma unroll
     for (int k = 0; k < kLoads; ++k) {
       int l, c;
       place(k, l, c);
-      const float u = at[k] != kMasked ? muon_direction(p, J, at[k], gv[k], mv[k]) : 0.0f;
-      J.u[J.tall ? (l0 + l) * kRp + c : c * J.len_p + l0 + l] = u;
+      // masked elements are zeros, whose u is zero, and a masked store is dropped
+      const float u = dir.step(v.g[k], v.m[k]);
+      __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, v.m[k]), rm, v.at[k] == kMasked ? kMasked : 4 * v.at[k], 0, 0);
+      u_out[kTall ? (l0 + l) * kRp + c : c * len_p + l0 + l] = u;
       tile[l * kLd + c] = u;
     }
-    __syncthreads();
+    if (l0 + 64 < end) load(l0 + 64, v);
+    meet_lds();
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
       double f[NT];
@@ -139,13 +157,23 @@ __global__ __launch_bounds__(256) void muon_gram64_kernel(MuonArgs p, int64_t fi
       for (int x = 0; x < kPairs; ++x)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          double& at = red[wave & 1][x * 256 + (g + 4 * e) * 16 + q];
+          double& at = red[((wave & 1) * kPairs + x) * 256 + (g + 4 * e) * 16 + q];
           at = w == 0 ? acc[x][e] : at + acc[x][e];
         }
     }
-    __syncthreads();
+    meet_lds();
   }
-  for (int i = t; i < kPairs * 256; i += 256) J.part[blk * (kPairs * 256) + i] = red[0][i] + red[1][i];
+  double* part = J.part + blk * (kPairs * 256);
+  for (int i = t; i < kPairs * 256; i += 256) part[i] = red[i] + red[kPairs * 256 + i];
+}
+template <int NT, int kGrad>
+__global__ __launch_bounds__(256) void muon_gram64_kernel(MuonArgs p, int64_t first) {
+  constexpr int kPairs = NT * (NT + 1) / 2;
+  __shared__ float tile[64 * (16 * NT + 1)];
+  __shared__ double red[2 * kPairs * 256];
+  const int64_t blk = blockIdx.x;
+  if (blk < first) muon_gram64<NT, kGrad, true>(p, p.j[0], blk, tile, red);
+  else muon_gram64<NT, kGrad, false>(p, p.j[1], blk - first, tile, red);
 }
 
 // r > 64: m and u, element by element of the filled-up matrix.
@@ -153,6 +181,8 @@ template <int kGrad>
 __global__ __launch_bounds__(256) void muon_momentum_kernel(MuonArgs p, int64_t first) {
   int64_t blk = blockIdx.x;
   const MuonJob& J = job_of(p, first, blk);
+  const MuonDirection dir(p);
+  float* const u_out = J.u;
   const uint32_t row_p = J.tall ? p.rp : static_cast<uint32_t>(J.len_p);
   const uint32_t rows = J.tall ? static_cast<uint32_t>(J.len) : p.r, cols = J.tall ? p.r : static_cast<uint32_t>(J.len);
   const uint32_t count = static_cast<uint32_t>(J.len_p * p.rp);
@@ -169,7 +199,9 @@ __global__ __launch_bounds__(256) void muon_momentum_kernel(MuonArgs p, int64_t 
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const uint32_t i = static_cast<uint32_t>(blk) * 1024 + k * 256 + threadIdx.x;
-    if (i < count) J.u[i] = at[k] != kMasked ? muon_direction(p, J, at[k], g[k], m[k]) : 0.0f;
+    const float u = dir.step(g[k], m[k]);   // zero where masked
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, m[k]), rm, at[k] == kMasked ? kMasked : 4 * at[k], 0, 0);
+    if (i < count) u_out[i] = u;
   }
 }
 
@@ -526,11 +558,9 @@ __device__ __forceinline__ void muon_apply(const MuonArgs& p, const MuonJob& J, 
 template <bool kF16, bool kMaster>
 __global__ __launch_bounds__(256) void muon_apply_kernel(MuonArgs p, int q_at, int64_t first) {
   __shared__ double qs[64 * 65];
-  int64_t blk = blockIdx.x;
-  const MuonJob& J = job_of(p, first, blk);
-  const double* Q = J.mat + static_cast<int64_t>(q_at) * p.rp * p.rp;
-  if (J.tall) muon_apply<kF16, kMaster, true>(p, J, blk, Q, qs);
-  else muon_apply<kF16, kMaster, false>(p, J, blk, Q, qs);
+  const int64_t blk = blockIdx.x, q0 = static_cast<int64_t>(q_at) * p.rp * p.rp;
+  if (blk < first) muon_apply<kF16, kMaster, true>(p, p.j[0], blk, p.j[0].mat + q0, qs);
+  else muon_apply<kF16, kMaster, false>(p, p.j[1], blk - first, p.j[1].mat + q0, qs);
 }
 
 struct MuonSizes {
