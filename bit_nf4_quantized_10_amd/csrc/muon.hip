@@ -88,7 +88,9 @@ __device__ __forceinline__ void meet_lds() {
 
 // r <= 64.  Workgroup: one chunk of the long side; per 64 of it m and u, element by element
 // in the order in memory, u into LDS as [long][rank], and its wave's 16 of the Gram
-// matrix's upper tiles; the next 64 are requested meanwhile.
+// matrix's upper tiles; the next 64 are requested meanwhile.  8192 and 22016 long at rank
+// 64: 13 us for 23 MB read and 15 written (7.5 at a copy's rate), a workgroup a CU of two
+// turns; with a branch around every element and nothing requested ahead 17.
 template <int NT, int kGrad, bool kTall>
 __device__ __forceinline__ void muon_gram64(const MuonArgs& p, const MuonJob& J, int64_t blk, float* tile, double* red) {
   constexpr int kPairs = NT * (NT + 1) / 2, kRp = 16 * NT, kLd = kRp + 1, kLoads = kRp / 4;
@@ -310,7 +312,9 @@ __device__ __forceinline__ double muon_scale(const double* d, int ld, int rp, do
 // Everything is symmetric, so only the upper tiles are computed, a wave each, and stored
 // twice; all operands are read along their rows (68 a row: 64 lanes on all banks), P's
 // once for its three products.  Bound by the matrix unit of one CU, 32 flops a cycle and
-// SIMD: at r = 64 the 17 products, 64 deep, three tiles a SIMD, take 22 us of it.
+// SIMD: at r = 64 the 17 products, 64 deep, three tiles a SIMD, take 22 us of the 41; LDS
+// reads take about 7, the rest are 15 barriers, start and end.  More CUs would meet in
+// memory three times a step, at 2 to 3 us each.
 template <int NT>
 __global__ __launch_bounds__(64 * (NT * (NT + 1) / 2)) void muon_iterate64_kernel(MuonArgs p) {
   constexpr int kRp = 16 * NT, kLd = 68, kThreads = 64 * (NT * (NT + 1) / 2), kDeep = kRp / 4;
@@ -475,7 +479,8 @@ __global__ __launch_bounds__(64) void muon_scale_kernel(MuonArgs p, double* scal
 
 // X = U Q and the parameters.  Workgroup: 64 of the long side, a wave 16; Q (symmetric, so
 // both layouts read it along its rows) passes through LDS in 64 x 64 pieces.  Bound by
-// memory: u, the parameters and their copies once.
+// memory: u, the parameters and their copies once (27 MB at 8192 and 22016 long, rank 64:
+// 15.5 us, of it two waits for memory and 3.4 us of 64-bit products).
 template <bool kF16, bool kMaster, bool kTall>
 __device__ __forceinline__ void muon_apply(const MuonArgs& p, const MuonJob& J, int64_t blk, const double* Q, double* qs) {
   constexpr int kLd = 65;

