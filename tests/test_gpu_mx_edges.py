@@ -300,3 +300,44 @@ def test_many_rows_of_few_columns(M, N, K):
         x = host(X[rows]).astype(np.float64)
         np.testing.assert_array_equal(host(Z[rows]), x @ a)
         np.testing.assert_array_equal(host(Y[rows]), oo.round16(x @ w.T + x @ a @ b, "bf16"))
+
+
+@pytest.mark.parametrize("M,K,N,r", [((1 << 20), 8, 8, 8), ((1 << 20), 24, 40, 16), (1, 8, (1 << 24) - 8, 8), (40, 16, 1 << 22, 16),
+                                     (1, (1 << 22), 8, 8), (700, (1 << 19) + 8, 8, 8)])
+def test_longest_sides_in_whole_numbers(M, K, N, r):
+    """Forward and backward with one side at the end of its range.  A and B hold a 1 a row
+    or column at most, G few elements, so that every sum is exact and Z and dZ are whole
+    numbers of at most eight bits."""
+    import torch
+    say(f"mx layer M={M} K={K} N={N} r={r}")
+    rng = np.random.default_rng(M % 1000 + K % 1000 + N % 1000)
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    codes, scales = _whole(rng, N, K, 0, 0)
+    W, w = _state(codes, scales, K), torch.from_numpy(oo.mxfp4_values(codes, scales, K)).cuda()
+
+    def sparse(rows, cols, count, high):
+        v = torch.zeros(rows * cols, dtype=torch.float64, device="cuda")
+        at = torch.randint(0, rows * cols, (count,), device="cuda", generator=gen)
+        v[at] = torch.randint(-high, high + 1, (count,), device="cuda", generator=gen).double()
+        return v.view(rows, cols)
+
+    x = torch.randint(-2, 3, (M, K), device="cuda", generator=gen).double() if K < 1 << 12 else sparse(M, K, 60 * M, 2)
+    x[:, :1] = 2.0       # every row's first block has scale 1/2; the others hold -2 .. 2 too
+    a, b, g = sparse(K, r, 64, 1), sparse(r, N, min(r * N, 4096), 1), sparse(M, N, min(M * N // 2 + 1, 30 * max(1, M // 100)), 1)
+    X, A, B, G = (v.bfloat16() for v in (x, a, b, g))
+    Y, Z = qn.qlora_mx_linear_fwd(X, W, A, B, 1.0)
+    z = x @ a
+    assert float(z.abs().max()) <= 256
+    assert torch.equal(Z.double(), z)
+    for i in range(0, N, 1 << 18):
+        n = slice(i, i + (1 << 18))
+        for j in range(0, M, 1 << 18):
+            m = slice(j, j + (1 << 18))
+            want = x[m] @ w[n].T.contiguous() + z[m] @ b[:, n].contiguous()
+            assert torch.equal(Y[m, n], want.float().bfloat16())
+    dX, dA, dB = qn.qlora_mx_linear_bwd(G, X, Z, W, A, B, 1.0)
+    dz = g @ b.T.contiguous()
+    assert float(dz.abs().max()) <= 256
+    assert torch.equal(dA.double(), x.T.contiguous() @ dz)
+    assert torch.equal(dB.double(), z.T.contiguous() @ g)
+    assert torch.equal(dX, (g @ w + dz @ a.T.contiguous()).float().bfloat16())
