@@ -221,7 +221,7 @@ int qlora_sgd_step_dt(int param_dtype, int64_t K, int64_t N, int64_t r, uint16_t
  * type.  Requirements: K, N, r >= 1, r <= 256, K and N <= 2^24, K*r and r*N below 2^29,
  * 0 <= momentum < 1, eps > 0, 0 <= steps <= 32, the numbers finite; pointers aligned
  * to their element size; workspace 256-byte aligned, at least *bytes.  NF4_EINVAL
- * otherwise. */
+ * otherwise.  No two of the arrays overlap. */
 #define NF4_MUON_SCALE_NONE     0
 #define NF4_MUON_SCALE_SPECTRAL 1
 #define NF4_MUON_SCALE_RMS      2
@@ -430,7 +430,8 @@ int mxfp4_dequantize(int type, int transposed, const mxfp4_t* in, void* X, int64
 /* C = P Qᵀ for two matrices in MXFP4: P M x K, Q N x K, N % 8 == 0, M * N below 2^29;
  * C (M x N, dense, 16-byte aligned) of out_type, one of NF4_OUT_*.  Products are
  * exact, sums are fp32 and rounded once.  Requirements besides: M <= 2^20, N <= 2^24;
- * workspace 256-byte aligned, at least *bytes. */
+ * workspace 256-byte aligned, at least *bytes.  C overlaps neither operand nor the
+ * workspace. */
 int mxfp4_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K, int64_t* bytes);
 int mxfp4_matmul(int out_type, const mxfp4_t* P, const mxfp4_t* Q, void* C, void* workspace, int64_t workspace_bytes,
                  void* stream);
@@ -447,7 +448,8 @@ int mxfp4_matmul(int out_type, const mxfp4_t* P, const mxfp4_t* Q, void* C, void
  *   dZ = c G Bᵀ,  dA = Xᵀ dZ,  dB = c Zᵀ G,  dX = G W + dZ Aᵀ (skipped when NULL),
  * with W's values in compute_dtype.  Exactly one of X (16 bits) and X8 (an 8-bit
  * checkpoint); Z is required; grad_dtype as in qlora_linear_bwd_ex; workspace at
- * least bwd_bytes. */
+ * least bwd_bytes.  Outputs overlap neither the inputs nor each other nor the
+ * workspace. */
 int qlora_mx_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t r, int64_t* fwd_bytes, int64_t* bwd_bytes);
 int qlora_mx_linear_fwd(int compute_dtype, int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t* X,
                         const mxfp4_t* W, const uint16_t* A, const uint16_t* B, float c, uint16_t* Y, uint16_t* Z,
