@@ -150,14 +150,17 @@ hipError_t launch_gemv(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_
                        hipStream_t stream, int dtype = 0);
 // dZ = c G Bᵀ: split partials, then their sum (with defer != nullptr that sum
 // is not launched but returned, for the caller to run in a later launch).
+// dZ_lo (M x r, may be null): what dZ's rounding leaves out, in 16 bits.
 hipError_t launch_dz(int64_t M, int64_t N, int64_t r, const uint16_t* G, const uint16_t* B, float c, uint16_t* dZ,
-                     const SkinnyPlan& p, void* part_ws, hipStream_t stream, int dtype = 0, RdJob* defer = nullptr);
+                     const SkinnyPlan& p, void* part_ws, hipStream_t stream, int dtype = 0, RdJob* defer = nullptr,
+                     uint16_t* dZ_lo = nullptr);
 // dA and dB: fp32, or with grad16 of the layer's 16-bit type.  x8 (codes
-// non-null): X is kept in 8 bits, and the X argument is not read.
+// non-null): X is kept in 8 bits, and the X argument is not read.  dZ_lo (may be
+// null): dA = Xᵀ (dZ + dZ_lo).
 hipError_t launch_colsums(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t* X, const uint16_t* G,
                           const uint16_t* Z, const uint16_t* dZ, float c, void* dA, void* dB, const SkinnyPlan& p,
                           void* da_ws, void* db_ws, hipStream_t stream, int dtype = 0, bool grad16 = false,
-                          Act8View x8 = {});
+                          Act8View x8 = {}, const uint16_t* dZ_lo = nullptr);
 
 hipError_t launch_fwd(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t* X, NF4View W,
                       const uint16_t* A, const uint16_t* B, float c, uint16_t* Y, uint16_t* Z,

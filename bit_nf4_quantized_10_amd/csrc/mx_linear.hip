@@ -140,7 +140,7 @@ int64_t mx_fwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t r) {
 
 int64_t mx_bwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t r) {
   const SkinnyPlan p = plan_skinny(M, K, N, r);
-  return p.dz_part + align256(M * r * 2) + p.da_part + p.db_part + align256(K * N * 2) + plan_split16(M, K, N).part_bytes;
+  return p.dz_part + 2 * align256(M * r * 2) + p.da_part + p.db_part + align256(K * N * 2) + plan_split16(M, K, N).part_bytes;
 }
 
 hipError_t launch_mx_fwd(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t* X, MxView W, const uint16_t* A,
@@ -177,19 +177,23 @@ hipError_t launch_mx_fwd(int64_t M, int64_t K, int64_t N, int64_t r, const uint1
 }
 
 // dX by the dense 16-bit product with the dequantized weight: the gradient's own
-// rounding to four bits would be another derivative.
+// rounding to four bits would be another derivative.  dA takes dZ in two 16-bit parts:
+// where few channels of X are far above the others, few rows of dZ make most of dA, and
+// dZ's rounding alone would be up to three times dA's own.  In dX, dZ's part is small.
 hipError_t launch_mx_bwd(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t* G, const uint16_t* X, Act8View x8,
                          const uint16_t* Z, MxView W, const uint16_t* A, const uint16_t* B, float c, uint16_t* dX,
                          void* dA, void* dB, void* ws, hipStream_t stream, int dtype, bool grad16) {
   const SkinnyPlan p = plan_skinny(M, K, N, r);
   char* dz_part = static_cast<char*>(ws);
   uint16_t* dz16 = reinterpret_cast<uint16_t*>(dz_part + p.dz_part);
-  char* da_part = reinterpret_cast<char*>(dz16) + align256(M * r * 2);
+  uint16_t* dz_lo = dz16 + align256(M * r * 2) / 2;
+  char* da_part = reinterpret_cast<char*>(dz_lo) + align256(M * r * 2);
   char* db_part = da_part + p.da_part;
   uint16_t* wd = reinterpret_cast<uint16_t*>(db_part + p.db_part);
-  hipError_t e = launch_dz(M, N, r, G, B, c, dz16, p, dz_part, stream, dtype);
+  hipError_t e = launch_dz(M, N, r, G, B, c, dz16, p, dz_part, stream, dtype, nullptr, dz_lo);
   if (e != hipSuccess) return e;
-  if ((e = launch_colsums(M, K, N, r, X, G, Z, dz16, c, dA, dB, p, da_part, db_part, stream, dtype, grad16, x8)) != hipSuccess)
+  if ((e = launch_colsums(M, K, N, r, X, G, Z, dz16, c, dA, dB, p, da_part, db_part, stream, dtype, grad16, x8,
+                          dz_lo)) != hipSuccess)
     return e;
   if (dX == nullptr) return hipGetLastError();
   if ((e = launch_mx_dequantize(dtype == kDtypeF16 ? NF4_OUT_F16 : NF4_OUT_BF16, true, W, wd, N, stream)) != hipSuccess) return e;

@@ -634,13 +634,15 @@ hipError_t launch_lora_down(int64_t M, int64_t K, int64_t r, const uint16_t* X, 
 }
 
 hipError_t launch_dz(int64_t M, int64_t N, int64_t r, const uint16_t* G, const uint16_t* B, float c, uint16_t* dZ,
-                     const SkinnyPlan& p, void* part_ws, hipStream_t stream, int dtype, RdJob* defer) {
+                     const SkinnyPlan& p, void* part_ws, hipStream_t stream, int dtype, RdJob* defer, uint16_t* dZ_lo) {
   float* part = static_cast<float*>(part_ws);
   Timer tm(QK_BWD_DZ, stream);
   hipError_t e = launch_rowsum(G, B, M, r, N, p.dz_splits, p.dz_per, part, stream, 0, 0, dtype);
   tm.stop();
   if (e != hipSuccess) return e;
-  const RdJob jz = rdjob(part, p.dz_splits, M, r, c, false, nullptr, dZ, dtype);
+  RdJob jz = rdjob(part, p.dz_splits, M, r, c, false, nullptr, dZ, dtype);
+  jz.ext_lo = dZ_lo;
+  jz.ext_ld = r;
   if (defer != nullptr) {
     *defer = jz;
     return hipSuccess;
@@ -651,10 +653,12 @@ hipError_t launch_dz(int64_t M, int64_t N, int64_t r, const uint16_t* G, const u
 // dA = Xᵀ dZ (K x r) and dB = c Zᵀ G (r x N).
 hipError_t launch_colsums(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t* X, const uint16_t* G,
                           const uint16_t* Z, const uint16_t* dZ, float c, void* dA, void* dB, const SkinnyPlan& p,
-                          void* da_ws, void* db_ws, hipStream_t stream, int dtype, bool grad16, Act8View x8) {
+                          void* da_ws, void* db_ws, hipStream_t stream, int dtype, bool grad16, Act8View x8,
+                          const uint16_t* dZ_lo) {
   const int64_t jc = cdiv(r, 64);
   CsJob ja{X, K, K, dZ, static_cast<float*>(da_ws), cdiv(K, 64), jc, p.da_per, 0, r, r};
   set_act8(ja, x8);
+  ja.v_lo = dZ_lo;
   CsJob jb{G, N, N, Z, static_cast<float*>(db_ws), cdiv(N, 64), jc, p.db_per, 0, r, r};
   ja.nblk = ja.col_blocks * jc * p.da_splits;
   jb.nblk = jb.col_blocks * jc * p.db_splits;

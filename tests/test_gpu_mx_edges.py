@@ -341,3 +341,22 @@ def test_longest_sides_in_whole_numbers(M, K, N, r):
     assert torch.equal(dA.double(), x.T.contiguous() @ dz)
     assert torch.equal(dB.double(), z.T.contiguous() @ g)
     assert torch.equal(dX, (g @ w + dz @ a.T.contiguous()).float().bfloat16())
+
+
+@pytest.mark.parametrize("name", ["bf16", "f16"])
+def test_gradient_of_a_where_few_channels_are_large(name):
+    """dA comes from dZ before its rounding: two 16-bit parts hold it within half a step
+    of half a step."""
+    import torch
+    from tests.test_gpu_mx_linear import F32, HALF, TINY, close
+    say(f"mx dA with large channels {name}")
+    t = Case(300, 520, 264, 16, name)
+    t.X[:, 7] *= 40.0
+    t.X[:, 300] *= 100.0
+    t.x = host(t.X).astype(np.float64)
+    Y, Z = t.forward()
+    dX, dA, dB = t.backward(Z, need_dx=False)
+    _, want, _ = oo.mx_linear_backward(t.g, t.x, host(Z).astype(np.float64), t.w, t.a, t.b, t.c)
+    dz = abs(t.c) * np.abs(t.g @ t.b.T)
+    near = HALF[name] ** 2 * dz + 1.01 * abs(t.c) * t.N * F32 * (np.abs(t.g) @ np.abs(t.b).T) + TINY[name]
+    close(dA, want, 1.01 * (np.abs(t.x).T @ near) + 2 * t.M * F32 * (np.abs(t.x).T @ dz), "dA")
