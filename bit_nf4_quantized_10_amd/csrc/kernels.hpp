@@ -284,6 +284,14 @@ hipError_t launch_mx_rows(const MxRowsPlan& pl, const uint16_t* X, const MxView*
 // Z and Y = the planes' sum + c Z B.
 hipError_t launch_mx_rows_finish(const MxRowsPlan& pl, const float* part, const float* zpart, int64_t M, int64_t N, int64_t r,
                                  const uint16_t* B, float c, uint16_t* Y, uint16_t* Z, hipStream_t stream, int dtype);
+// dX by a product that decodes W itself (mx_back.hip).  splits 0: W is dequantised, and the
+// product dense; else ranges of the reduction, rows of W each, and their planes' bytes.
+struct MxBackPlan {
+  int64_t splits, per, part;
+};
+MxBackPlan plan_mx_back(int64_t M, int64_t K, int64_t N);
+hipError_t launch_mx_back(const MxBackPlan& pl, int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t* G, const uint16_t* dZ,
+                          MxView W, const uint16_t* A, uint16_t* dX, float* part, hipStream_t stream, int dtype);
 // out (p.rows x q.rows, of out_type) = p qᵀ
 int64_t mx_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K);
 hipError_t launch_mx_matmul(MxView p, MxView q, int out_type, void* out, void* ws, hipStream_t stream);

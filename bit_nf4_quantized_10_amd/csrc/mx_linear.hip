@@ -140,7 +140,9 @@ int64_t mx_fwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t r) {
 
 int64_t mx_bwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t r) {
   const SkinnyPlan p = plan_skinny(M, K, N, r);
-  return p.dz_part + 2 * align256(M * r * 2) + p.da_part + p.db_part + align256(K * N * 2) + plan_split16(M, K, N).part_bytes;
+  const MxBackPlan back = plan_mx_back(M, K, N);
+  return p.dz_part + 2 * align256(M * r * 2) + p.da_part + p.db_part +
+         (back.splits > 0 ? back.part : align256(K * N * 2) + plan_split16(M, K, N).part_bytes);
 }
 
 hipError_t launch_mx_fwd(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t* X, MxView W, const uint16_t* A,
@@ -176,8 +178,9 @@ hipError_t launch_mx_fwd(int64_t M, int64_t K, int64_t N, int64_t r, const uint1
   return mx_tiles(x, W, Z, cbt, r, dtype, type, Y, x.scales + align256(mx_scale_bytes(M, K)), stream);
 }
 
-// dX by the dense 16-bit product with the dequantized weight: the gradient's own
-// rounding to four bits would be another derivative.  dA takes dZ in two 16-bit parts:
+// dX in 16 bits, by the dense product with the dequantized weight or, smaller calls, by
+// one that decodes it (mx_back.hip): the gradient's own rounding to four bits would be
+// another derivative.  dA takes dZ in two 16-bit parts:
 // where few channels of X are far above the others, few rows of dZ make most of dA, and
 // dZ's rounding alone would be up to three times dA's own.  In dX, dZ's part is small.
 hipError_t launch_mx_bwd(int64_t M, int64_t K, int64_t N, int64_t r, const uint16_t* G, const uint16_t* X, Act8View x8,
@@ -196,6 +199,8 @@ hipError_t launch_mx_bwd(int64_t M, int64_t K, int64_t N, int64_t r, const uint1
                           dz_lo)) != hipSuccess)
     return e;
   if (dX == nullptr) return hipGetLastError();
+  const MxBackPlan back = plan_mx_back(M, K, N);
+  if (back.splits > 0) return launch_mx_back(back, M, K, N, r, G, dz16, W, A, dX, reinterpret_cast<float*>(wd), stream, dtype);
   if ((e = launch_mx_dequantize(dtype == kDtypeF16 ? NF4_OUT_F16 : NF4_OUT_BF16, true, W, wd, N, stream)) != hipSuccess) return e;
   return launch_gated_dx(M, K, N, r, G, wd, dz16, A, dX, stream, dtype, reinterpret_cast<char*>(wd) + align256(K * N * 2));
 }

@@ -12,9 +12,10 @@ from tests.test_gpu_mxfp4 import TYPES, _round, _state, _torch_type, _whole
 
 pytestmark = pytest.mark.gpu
 # one shape for each kernel and plan of the products: up to 16 rows, waves with chunks of
-# their own, panels of 64 and 128 rows, tiles with and without a split, whole and ragged
+# their own, panels of 64 and 128 rows, tiles with and without a split, whole and ragged;
+# dX decoding W, in one range and in several, and by the dense product (the last)
 SHAPES = [(3, 520, 264, 16), (16, 4104, 4096, 64), (30, 1032, 520, 8), (50, 2056, 1000, 24), (100, 1032, 1336, 40),
-          (300, 520, 2056, 16), (777, 264, 1336, 24), (1100, 1032, 2056, 24), (2100, 264, 1032, 256), (4000, 40, 4104, 8)]
+          (300, 520, 2056, 16), (777, 264, 1336, 24), (1100, 1032, 2056, 24), (2100, 264, 1032, 256), (4000, 40, 4104, 8), (2600, 1032, 3400, 24)]
 
 
 @pytest.mark.parametrize("M,N,K", [(1024, 2056, 8), (1030, 2064, 40), (1500, 1544, 256), (513, 4104, 264), (2048, 1032, 520),
