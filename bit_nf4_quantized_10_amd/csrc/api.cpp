@@ -625,6 +625,8 @@ int qlora_muon_step(int param_dtype, int grad_dtype, int64_t K, int64_t N, int64
   for (const double v : {o.lr, o.momentum, o.weight_decay, o.eps, o.a, o.b, o.c})
     if (!std::isfinite(v)) return NF4_EINVAL;
   if (o.momentum < 0.0 || o.momentum >= 1.0 || !(o.eps > 0.0) || o.steps < 0 || o.steps > 32) return NF4_EINVAL;
+  // the Gram matrix's rounding grows by a^2 a step (muon.hip)
+  if (std::pow(std::fabs(o.a), 2.0 * o.steps) > 0x1p29) return NF4_EINVAL;
   if (o.scaling != NF4_MUON_SCALE_NONE && o.scaling != NF4_MUON_SCALE_SPECTRAL && o.scaling != NF4_MUON_SCALE_RMS)
     return NF4_EINVAL;
   if (workspace_bytes < qn::muon_workspace_bytes(K, N, r)) return NF4_EINVAL;

@@ -9,10 +9,14 @@
 //   P = a I + b G + c G^2,   Q <- Q P,   G <- P G P,      X = U Q / |u|,
 // and the long matrix is read twice (Gram, product) instead of twice a step.  G's
 // rounding errors are absolute where the iteration on X itself has relative ones, and
-// a small singular value's part of G grows twelvefold a step; G, Q and P are
-// therefore 64-bit throughout (v_mfma_f64_16x16x4_f64; an error of 2^-53 comes out below
-// 1e-10), as are the sums of both long products.  The trace of U ᵀU is |u|^2, so the
-// norm costs no pass of its own.
+// a small singular value's part of G grows by a^2 a step, twelvefold; G, Q and P are
+// therefore 64-bit throughout (v_mfma_f64_16x16x4_f64), as are the sums of both long
+// products.  A direction that U lacks has an eigenvalue of a few 2^-53 in G, of either
+// sign; near -1, where no real one lies, the polynomial would run away (at the default
+// coefficients after some 18 steps).  Steps end where a^(2 steps) passes 2^29: there the
+// update is off by at most 1e-8 of its largest element, by 2e-12 after five default
+// steps (U of rank 1 to 8, with equal columns, with singular values down to 1e-8).  The
+// trace of U ᵀU is |u|^2, so the norm costs no pass of its own.
 #include <cmath>
 
 #include "common.hpp"

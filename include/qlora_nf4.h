@@ -214,12 +214,15 @@ int qlora_sgd_step_dt(int param_dtype, int64_t K, int64_t N, int64_t r, uint16_t
  * sqrt(max(1, rows / columns)), RMS 0.2 sqrt(max(rows, columns)).  p is the fp32
  * master copy where A_master and B_master are given (both or neither), else the
  * 16-bit parameter; the parameter becomes RNE(p).  m is fp32, updated in place; the
- * iteration is held in 64 bits.  A gradient or momentum with a value that is not
- * finite makes its whole matrix NaN.  No element depends on the order in which
+ * iteration is held in 64 bits.  It runs on X's Gram matrix, whose rounding in
+ * directions that u lacks (fewer tokens than the rank, equal columns) grows by a^2 a
+ * step: |a|^(2 steps) is at most 2^29, 8 steps at a = 3.4445, and what that makes of it
+ * stays below 2^-24 of the largest element.  A gradient or momentum with a value that
+ * is not finite makes its whole matrix NaN.  No element depends on the order in which
  * anything runs.
  * param_dtype: NF4_COMPUTE_*; grad_dtype: of dA and dB, NF4_AB_F32 or the parameters'
  * type.  Requirements: K, N, r >= 1, r <= 256, K and N <= 2^24, K*r and r*N below 2^29,
- * 0 <= momentum < 1, eps > 0, 0 <= steps <= 32, the numbers finite; pointers aligned
+ * 0 <= momentum < 1, eps > 0, 0 <= steps <= 32, |a|^(2 steps) <= 2^29, the numbers finite; pointers aligned
  * to their element size; workspace 256-byte aligned, at least *bytes.  NF4_EINVAL
  * otherwise.  No two of the arrays overlap. */
 #define NF4_MUON_SCALE_NONE     0

@@ -322,3 +322,42 @@ def test_directions_past_two_gibibytes(K, N, r):
             want = -host(U[part]).astype(np.float64) @ Q / norm
             # u is the gradient itself; what is left are 64-bit sums and one rounding
             assert np.abs(host(M[part]) - want).max() <= 2.0 ** -24 * np.abs(want).max() * 1.01 + 1e-10 * np.abs(want).max()
+
+
+@pytest.mark.parametrize("coefficients,steps", [(COEFFICIENTS, 8), ((2.0, -1.5, 0.5), 14), ((1.5, -0.5, 0.0), 24)])
+@pytest.mark.parametrize("K,N,r,rank", [(200, 8, 16, 1), (17, 1000, 64, 4), (300, 40, 64, 0), (8, 700, 80, 3), (500, 130, 200, 2),
+                                        (40, 300, 256, 0)])
+def test_low_rank_directions_at_the_last_step(K, N, r, rank, coefficients, steps):
+    """Whole numbers of that rank (0: pairs of equal columns of A, rows of B), or with fewer
+    rows than the rank, so that the direction is exactly its gradient: what is left is one
+    rounding to fp32 and the Gram matrix's, below 2^-24 of the largest element."""
+    say(f"muon of rank {rank}: K={K} N={N} r={r}, {steps} steps")
+    rng = np.random.default_rng(K + N + r)
+    t = Case(K, N, r, "bf16")
+    for n, (rows, cols) in (("A", (K, r)), ("B", (r, N))):
+        k = rank or r // 2
+        v = rng.integers(-3, 4, size=(rows if n == "A" else cols, k)).astype(np.float64)
+        v = v @ rng.integers(-3, 4, size=(k, r)) if rank else v.repeat(2, axis=1)
+        v[0, 0] += not v.any()
+        t.g[n].copy_(_dev(v if n == "A" else v.T, "f32"))
+        t.master[n].zero_()
+    before = t.values()
+    t.step(1.0, scaling=None, momentum=0.0, nesterov=False, steps=steps, coefficients=coefficients)
+    for n in ("A", "B"):
+        want = -oo.newton_schulz(before[n][1], steps, coefficients, 1e-7)
+        got = host(t.master[n]).astype(np.float64)
+        worst = np.abs(got - want).max() / np.abs(want).max() * 2.0 ** 24
+        say(f"  {n}: off by {worst:.3f} x 2^-24 of the largest element")
+        assert (np.abs(got - want) <= 1.01 * 2.0 ** -24 * (np.abs(want) + np.abs(want).max())).all(), n
+
+
+def test_steps_past_the_last_are_refused():
+    t = Case(100, 90, 16, "bf16")
+    before = t.values()
+    for kw in ({"steps": 9}, {"steps": 32}, {"steps": 33}, {"steps": 5, "coefficients": (8.0, -20.0, 13.0)}):
+        with pytest.raises(qn.NF4Error):
+            t.step(0.1, **kw)
+    after = t.values()
+    for n in ("A", "B"):
+        for a, b in zip(before[n], after[n]):
+            np.testing.assert_array_equal(a, b)
