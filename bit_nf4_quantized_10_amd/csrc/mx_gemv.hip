@@ -17,6 +17,7 @@
 #include "gemv_parts.hpp"
 #include "kernels.hpp"
 #include "mx_core.hpp"
+#include "mx_offsets.hpp"
 #include "mx_quant.hpp"
 #include "side_jobs.hpp"
 
@@ -180,9 +181,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void m
   const int beg = split * p.chunks_per, end = min(beg + p.chunks_per, chunks);
   const Rsrc rw = make_rsrc(p.w.codes, mx_code_bytes(N, K)), rsw = make_rsrc(p.w.scales, mx_scale_bytes(N, K));
   const Rsrc ra = make_rsrc(p.act.codes, mx_code_bytes(M, K)), rsa = make_rsrc(p.act.scales, mx_scale_bytes(M, K));
-  uint32_t vw[RW], va[RA];
-#pragma unroll
-  for (int j = 0; j < RW; ++j) vw[j] = n0 + 16 * j + q < N ? static_cast<uint32_t>((n0 + 16 * j + q) * nb + g) * 16u : kMasked;
+  uint32_t va[RA];
   // this wave copies step `wave` of the chunk
 #pragma unroll
   for (int i = 0; i < RA; ++i)
@@ -191,9 +190,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void m
     i32x4 w[RW][4];
     uint32_t sw[RW], sa[RA];
   };
-  // Offsets are a lane's own and a scalar.  Weight blocks past the row's end, of the next
-  // row, meet zeros of X; tiles past the last one take its scales, for rows that are not
-  // stored.
+  // Offsets are a lane's own and a scalar, masks in the lane's own (mx_offsets.hpp); tiles
+  // past the last one take its scales, for rows that are not stored.
   const int last_w = (N - 1) / 16, last_a = (M - 1) / 16;
   auto load = [&](int c, int buf, Loads& L) {
     const bool in = 16 * c + 4 * wave + g < nb;
@@ -202,7 +200,10 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void m
 #pragma unroll
     for (int j = 0; j < RW; ++j) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) L.w[j][s] = __builtin_bit_cast(i32x4, ld128s(rw, vw[j], 256 * c + 64 * s));
+      for (int s = 0; s < 4; ++s) {
+        const MxOffset at = mx_code_offset(n0 + 16 * j + q, N, nb, c, s, g);
+        L.w[j][s] = __builtin_bit_cast(i32x4, ld128s(rw, at.lane, at.scalar));
+      }
       L.sw[j] = ld32s(rsw, 4 * lane, static_cast<uint32_t>(min(n0 / 16 + j, last_w) * chunks + c) * 256u);
     }
 #pragma unroll
