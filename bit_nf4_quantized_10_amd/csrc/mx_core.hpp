@@ -28,6 +28,7 @@
 #include <type_traits>
 
 #include "gemm16.hpp"
+#include "mx_offsets.hpp"
 #include "mxfp4.hpp"
 
 namespace qn {
@@ -149,9 +150,9 @@ struct CoreMx {
   }
   // Points the copies at stage u (counted from s_beg; called for every stage in turn):
   // past the whole stages, blocks past the share's end are masked.  Masks stand in the
-  // lanes' own offsets, since a buffer's range check need not count the scalar part.
+  // lanes' own offsets, and the scalar part stays within the rows (mx_offsets.hpp).
   __device__ __forceinline__ void aim(int u) {
-    so = static_cast<uint32_t>(s_beg + u) * 128u;
+    so = mx_stage_offset(s_beg + u, last);
     if (u < n_full) return;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
