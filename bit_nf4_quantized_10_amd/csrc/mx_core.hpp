@@ -65,10 +65,11 @@ __device__ __forceinline__ void mfma_mx_in_place(const i32x4& w, const i32x4& a,
 
 struct MxProductArgs {
   MxView act, w;          // M x K, N x K
-  // adapter term, added to the first split: ext_a (M x r) times ext_b (N x r)ᵀ
+  // adapter term, added to the first split: c times ext_a (M x r) times ext_b (N x r)ᵀ
   const uint16_t* ext_a;
   const uint16_t* ext_b;
   int64_t r;
+  float c;
   void* out;              // M x N; a split's fp32 planes [splits][M][N]
   int64_t chunks_per;     // 512-element chunks a split takes (all of them: no split)
 };
@@ -252,7 +253,7 @@ struct CoreMx {
     });
   }
 
-  // The adapter's product into acc, 32 of its rank at a time.
+  // 32 of the adapter's rank.
   struct Adapter {
     v8 a[2][4], w[2][4];
   };
@@ -270,13 +271,64 @@ struct CoreMx {
       }
     }
   }
-  __device__ __forceinline__ void adapter_add(const Adapter& A, f32x16 (&acc)[4][4]) const {
+  // A sum in vector registers; kFresh: from zero.  s_nop: as mfma_mx_in_place's.
+  template <bool kFresh>
+  __device__ __forceinline__ static void adapter_mfma(const v8& w, const v8& a, f32x16& x) {
+    if constexpr (kFresh) {
+      if constexpr (T::kDtype == 1) asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_f16 %0, %1, %2, 0" : "=&v"(x) : "v"(w), "v"(a));
+      else asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, 0" : "=&v"(x) : "v"(w), "v"(a));
+    } else {
+      if constexpr (T::kDtype == 1) asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_f16 %0, %1, %2, %0" : "+v"(x) : "v"(w), "v"(a));
+      else asm volatile("s_nop 1\n\tv_mfma_f32_32x32x16_bf16 %0, %1, %2, %0" : "+v"(x) : "v"(w), "v"(a));
+    }
+  }
+  // 64 more of the rank, of which A0 and A1 hold 32 each.
+  __device__ __forceinline__ void adapter_add(const Adapter& A0, const Adapter& A1, f32x16 (&acc)[4][4]) const {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < 4; ++t) {
+      const Adapter& A = t < 2 ? A0 : A1;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = T::mfma32(A.w[t][j], A.a[t][i], acc[i][j]);
+        for (int j = 0; j < 4; ++j) acc[i][j] = T::mfma32(A.w[t & 1][j], A.a[t & 1][i], acc[i][j]);
+    }
+  }
+  // acc = c times the product, whose last 64 (both; else 32) of the rank these are; more: acc
+  // holds the others' sums.  c comes in fp32, as in the few rows' path: c B or c Z in 16 bits
+  // could pass their range, and a row's result would depend on the rows beside it.  A tile's
+  // sum is in vector registers (asm, since the compiler takes accumulation registers, whence
+  // all elements are moved to be scaled and back: 2.6 us a round of 256 x 256 tiles more) and
+  // scaled while the next two tiles' are computed: behind 32 vector instructions, the first
+  // behind four matrix instructions with their waits, where reading it wants 11 wait states.
+  // 1.1 us a round more than unscaled: 2048 x 8192 x 22016, rank 64, 206 -> 209 us a call,
+  // 4096 x 4096 x 11008, rank 16, 119 -> 122.
+  __device__ __forceinline__ void adapter_last(const Adapter& A0, const Adapter& A1, bool more, bool both, f32x16 (&acc)[4][4]) const {
+    f32x16 x[3];
+#pragma unroll
+    for (int k = 0; k < 18; ++k) {
+      if (k < 16) {
+        f32x16& y = x[k % 3];
+        const int i = k >> 2, j = k & 3;
+        if (more) {
+          y = acc[i][j];
+          adapter_mfma<false>(A0.w[0][j], A0.a[0][i], y);
+        } else {
+          adapter_mfma<true>(A0.w[0][j], A0.a[0][i], y);
+        }
+        adapter_mfma<false>(A0.w[1][j], A0.a[1][i], y);
+        if (both) {
+          adapter_mfma<false>(A1.w[0][j], A1.a[0][i], y);
+          adapter_mfma<false>(A1.w[1][j], A1.a[1][i], y);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (k >= 2) {
+        f32x16& to = acc[(k - 2) >> 2][(k - 2) & 3];
+        to = x[(k - 2) % 3] * p.c;
+        asm volatile("" : "+a"(to));
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
   }
 
   // The whole reduction (blockIdx.z's share): clears and fills acc and releases LDS.
@@ -311,17 +363,18 @@ struct CoreMx {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
-    if (r > 0) {
-      adapter_add(A0, acc);
-      if (r > 32) adapter_add(A1, acc);
-#pragma unroll 1
-      for (int j0 = 64; j0 < r; j0 += 32) {
-        adapter_load(j0, r, A0);
-        adapter_add(A0, acc);
+      for (int j = 0; j < 4; ++j) {
+        acc[i][j] = f32x16{0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+        asm volatile("" : "+a"(acc[i][j]));
       }
+    if (r > 0) {
+#pragma unroll 1
+      for (int j0 = 64; j0 < r; j0 += 64) {
+        adapter_add(A0, A1, acc);
+        adapter_load(j0, r, A0);
+        adapter_load(j0 + 32, r, A1);
+      }
+      adapter_last(A0, A1, r > 64, r > 32, acc);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)

@@ -92,12 +92,12 @@ hipError_t mx_sum(const float* part, int64_t splits, int64_t count, int out_type
 }
 
 // By tiles.  out_type: NF4_OUT_*; the adapter's operands are of the 16-bit type dtype.
-hipError_t mx_tiles(MxView act, MxView w, const uint16_t* ext_a, const uint16_t* ext_b, int64_t r, int dtype, int out_type,
+hipError_t mx_tiles(MxView act, MxView w, const uint16_t* ext_a, const uint16_t* ext_b, int64_t r, float c, int dtype, int out_type,
                     void* out, void* ws, hipStream_t stream) {
   const int64_t M = act.rows, N = w.rows;
   const MxPlan pl = plan_mx(M, N, act.cols);
   const bool parts = pl.splits > 1;
-  const MxProductArgs p{act, w, ext_a, ext_b, r, parts ? ws : out, pl.chunks_per};
+  const MxProductArgs p{act, w, ext_a, ext_b, r, c, parts ? ws : out, pl.chunks_per};
   hipError_t e;
   {
     const Timer tm(QK_MX_GEMM, stream, true);
@@ -117,7 +117,7 @@ int64_t mx_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K) {
 
 hipError_t launch_mx_matmul(MxView p, MxView q, int out_type, void* out, void* ws, hipStream_t stream) {
   const int dtype = out_type == NF4_OUT_F16 ? kDtypeF16 : kDtypeBf16;
-  if (!few_rows(p.rows, q.rows)) return mx_tiles(p, q, nullptr, nullptr, 0, dtype, out_type, out, ws, stream);
+  if (!few_rows(p.rows, q.rows)) return mx_tiles(p, q, nullptr, nullptr, 0, 0.0f, dtype, out_type, out, ws, stream);
   const MxRowsPlan pl = plan_mx_rows(p.rows, p.cols, q.rows, 0);
   const bool parts = pl.splits > 1;
   hipError_t e = launch_mx_rows(pl, nullptr, &p, q, p.rows, parts ? ws : out, !parts && out_type != NF4_OUT_F32, stream, dtype);
@@ -126,7 +126,7 @@ hipError_t launch_mx_matmul(MxView p, MxView q, int out_type, void* out, void* w
 }
 
 // Workspace of the forward, few rows: the planes, Z's partials, above 16 rows X's codes
-// and scales; else: Aᵀ, Z's partials, (c B)ᵀ, X's codes and scales, the tiles' planes.
+// and scales; else: Aᵀ, Z's partials, Bᵀ, X's codes and scales, the tiles' planes.
 // Then Z for calls that do not pass it.
 static int64_t mx_kept_bytes(int64_t M, int64_t K) { return align256(mx_code_bytes(M, K)) + align256(mx_scale_bytes(M, K)); }
 int64_t mx_fwd_workspace_bytes(int64_t M, int64_t K, int64_t N, int64_t r) {
@@ -167,15 +167,15 @@ hipError_t launch_mx_fwd(int64_t M, int64_t K, int64_t N, int64_t r, const uint1
   }
   const SkinnyPlan p = plan_skinny(M, K, N, r);
   char* zpart = at + p.at_bytes;
-  uint16_t* cbt = reinterpret_cast<uint16_t*>(zpart + p.z_part);
-  x.codes = reinterpret_cast<uint8_t*>(cbt) + align256(N * r * 2);
+  uint16_t* bt = reinterpret_cast<uint16_t*>(zpart + p.z_part);
+  x.codes = reinterpret_cast<uint8_t*>(bt) + align256(N * r * 2);
   x.scales = x.codes + align256(mx_code_bytes(M, K));
-  // Aᵀ and (c B)ᵀ ride along in the launch that quantises X
+  // Aᵀ and Bᵀ ride along in the launch that quantises X
   TJob tj[2];
-  lora_transposes(K, r, A, reinterpret_cast<uint16_t*>(at), N, B, c, cbt, 0, dtype, tj);
+  lora_transposes(K, r, A, reinterpret_cast<uint16_t*>(at), N, B, 1.0f, bt, 0, dtype, tj);
   if ((e = launch_mx_front(x, X, stream, dtype, nullptr, nullptr, 0, nullptr, tj)) != hipSuccess) return e;
-  if ((e = launch_lora_down(M, K, r, X, A, Z, p, at, zpart, stream, N, B, c, cbt, 0, dtype, true)) != hipSuccess) return e;
-  return mx_tiles(x, W, Z, cbt, r, dtype, type, Y, x.scales + align256(mx_scale_bytes(M, K)), stream);
+  if ((e = launch_lora_down(M, K, r, X, A, Z, p, at, zpart, stream, N, B, 1.0f, bt, 0, dtype, true)) != hipSuccess) return e;
+  return mx_tiles(x, W, Z, bt, r, c, dtype, type, Y, x.scales + align256(mx_scale_bytes(M, K)), stream);
 }
 
 // dX in 16 bits, by the dense product with the dequantized weight or, smaller calls, by

@@ -133,3 +133,31 @@ def test_rows_that_are_not_finite_stay_their_own():
         assert torch.isnan(Y[1]).all()
         rest = torch.arange(M, device="cuda") != 1
         assert torch.equal(Y[rest], clean[rest])
+
+
+@pytest.mark.parametrize("name,c", [("bf16", 1.0 / 3), ("f16", 1.0 / 3), ("f16", 3e4), ("f16", 1e-7), ("f16", -7e-5), ("bf16", 1e-39)])
+@pytest.mark.parametrize("K,N,r", [(264, 2056, 16), (4104, 2056, 96)])
+def test_the_adapter_is_scaled_alike_on_every_path(K, N, r, name, c):
+    """A row's adapter term does not depend on the rows beside it: c multiplies the fp32 sum
+    Z B, and neither c B nor c Z is rounded to 16 bits (c B here passes fp16's largest
+    number, or its normal numbers).  W is zero and Z B whole numbers, so Y = RNE(fl32(c) Z B)
+    with one rounding to fp32 before it."""
+    import torch
+    say(f"mx adapter scaled by {c} {name} K={K} r={r}")
+    rng = np.random.default_rng(K + r)
+    M = 1100
+    x = np.zeros((M, K), dtype=np.float32)
+    x[:, 7] = rng.integers(-2, 3, size=M)
+    x[:, 40] = rng.integers(-900, 900, size=M) // 4 * 4 * (rng.random(M) < 0.5)
+    a = np.zeros((K, r), dtype=np.float32)
+    a[7, 0] = a[40, 1] = a[7, r - 1] = 1.0
+    b = rng.integers(-3, 4, size=(r, N)).astype(np.float32)
+    X, A, B = (_dev(v, name) for v in (x, a, b))
+    W = qn.mxfp4_quantize(torch.zeros(N, K, device="cuda"))
+    x = host(X).astype(np.float64)
+    with np.errstate(over="ignore", under="ignore"):
+        want = oo.round16((np.float32(c) * (x @ a @ b).astype(np.float32)).astype(np.float32), name)
+    for rows in (3, 16, 40, 100, M):      # in the product, waves with chunks of their own, panels, tiles
+        Y, Z = qn.qlora_mx_linear_fwd(X[:rows].contiguous(), W, A, B, c)
+        np.testing.assert_array_equal(host(Z), x[:rows] @ a)
+        np.testing.assert_array_equal(host(Y), want[:rows], err_msg=f"{rows} rows")
