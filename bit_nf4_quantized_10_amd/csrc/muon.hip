@@ -302,14 +302,15 @@ __global__ __launch_bounds__(256) void muon_sum_kernel(MuonArgs p, int side, int
   J.mat[j * p.rp + i] = s;
 }
 
-// 1 / max(|u|, eps)^2 from the Gram matrix's diagonal (d: its first element, rows ld apart).
+// 1 / max(|u|, eps)^2 from the Gram matrix's diagonal (d: its first element, rows ld apart);
+// NaN where u is not finite, which 1 / infinity would hide from an update without a step.
 __device__ __forceinline__ double muon_scale(const double* d, int ld, int rp, double eps) {
   double s = 0.0;
   for (int i = threadIdx.x & 63; i < rp; i += 64) s += d[i * (ld + 1)];
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) s += __shfl_xor(s, x, 64);
   const double n = sqrt(s), m = n > eps ? n : (n == n ? eps : n);
-  return 1.0 / (m * m);
+  return (1.0 + 0.0 * n) / (m * m);
 }
 
 // r <= 64: the whole iteration of one matrix in one workgroup, G, P, Q and S = G P in LDS.

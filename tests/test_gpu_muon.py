@@ -361,3 +361,18 @@ def test_steps_past_the_last_are_refused():
     for n in ("A", "B"):
         for a, b in zip(before[n], after[n]):
             np.testing.assert_array_equal(a, b)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("where", ["gradient", "momentum"])
+@pytest.mark.parametrize("r", [16, 64, 80])
+@pytest.mark.parametrize("steps", [0, 1, 2])
+def test_what_is_not_finite_shows_after_any_number_of_steps(steps, r, where, bad):
+    """The whole matrix, without a step too, where an infinite norm alone would leave zeros."""
+    import torch
+    say(f"muon with {bad} in a {where}, {steps} steps, r={r}")
+    t = Case(100, 130, r, "bf16")
+    (t.g if where == "gradient" else t.m)["B"][5, 7] = bad
+    t.step(0.1, steps=steps)
+    assert torch.isnan(t.p["B"]).all() and torch.isnan(t.master["B"]).all()
+    assert torch.isfinite(t.p["A"]).all() and torch.isfinite(t.m["A"]).all()
