@@ -554,8 +554,10 @@ def qlora_muon_step(A, B, dA, dB, mA, mB, lr: float, momentum: float = 0.95, nes
     """In-place step of the bf16 or fp16 adapter (optionally through fp32 masters)
     along its orthogonalised momentum.  mA, mB: fp32 momenta, updated; dA, dB: fp32 or
     the adapter's type.  scaling: "spectral" sqrt(max(1, rows / columns)), "rms"
-    0.2 sqrt(max(rows, columns)) or None.  steps: at most 32, with |a|^(2 steps) <= 2^29
-    for the first coefficient a (8 for the default ones)."""
+    0.2 sqrt(max(rows, columns)) or None, of A (K x r) and B (r x N) as they are:
+    "spectral" is sqrt(K / r) for A and 1 for B (K, N >= r), where for adapters stored
+    output x input it would be 1 for A and sqrt(N / r) for B.  steps: at most 32, with
+    |a|^(2 steps) <= 2^29 for the first coefficient a (8 for the default ones)."""
     import torch
     if scaling not in _MUON_SCALES:
         raise ValueError(f'scaling is "spectral", "rms" or None, got {scaling!r}')

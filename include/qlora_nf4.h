@@ -211,7 +211,11 @@ int qlora_sgd_step_dt(int param_dtype, int64_t K, int64_t N, int64_t r, uint16_t
  *   X <- u / max(|u|_F, eps),  `steps` times X <- a X + (b S + c S^2) X, S = X Xᵀ,
  *   p <- p (1 - lr weight_decay) - lr s X,
  * s by `scaling`, for a matrix of rows x columns: NONE 1, SPECTRAL
- * sqrt(max(1, rows / columns)), RMS 0.2 sqrt(max(rows, columns)).  p is the fp32
+ * sqrt(max(1, rows / columns)), RMS 0.2 sqrt(max(rows, columns)).  Rows and columns are
+ * those of A and B as they are stored here, input x output: SPECTRAL gives A (K x r)
+ * sqrt(K / r) and B (r x N) 1 where K, N >= r, as for any matrix of that shape.  Where
+ * adapters are stored output x input, the same formula gives A 1 and B sqrt(N / r); that
+ * is another step, which no value here selects.  p is the fp32
  * master copy where A_master and B_master are given (both or neither), else the
  * 16-bit parameter; the parameter becomes RNE(p).  m is fp32, updated in place; the
  * iteration is held in 64 bits.  It runs on X's Gram matrix, whose rounding in

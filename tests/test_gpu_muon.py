@@ -376,3 +376,19 @@ def test_what_is_not_finite_shows_after_any_number_of_steps(steps, r, where, bad
     t.step(0.1, steps=steps)
     assert torch.isnan(t.p["B"]).all() and torch.isnan(t.master["B"]).all()
     assert torch.isfinite(t.p["A"]).all() and torch.isfinite(t.m["A"]).all()
+
+
+@pytest.mark.parametrize("scaling,a,b", [("spectral", 8.0, 1.0), ("rms", 0.2 * np.sqrt(1024.0), 0.2 * np.sqrt(400.0)), (None, 1.0, 1.0)])
+def test_scalings_go_by_the_stored_rows_and_columns(scaling, a, b):
+    """A is 1024 x 16, B 16 x 400: the factors as the header names them."""
+    say(f"muon scaling {scaling}")
+    steps = {}
+    for s in (scaling, None):
+        t = Case(1024, 400, 16, "bf16")
+        for n in ("A", "B"):
+            t.master[n].zero_()
+        t.step(1.0, scaling=s)
+        steps[s] = {n: host(t.master[n]).astype(np.float64) for n in ("A", "B")}
+    for n, f in (("A", a), ("B", b)):
+        # two roundings to fp32
+        assert (np.abs(steps[scaling][n] - f * steps[None][n]) <= 2.02 * 2.0 ** -24 * f * np.abs(steps[None][n])).all(), n
