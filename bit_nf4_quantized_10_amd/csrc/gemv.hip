@@ -73,6 +73,23 @@ __device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
   return *reinterpret_cast<lp>(static_cast<uintptr_t>(addr));
 }
 
+template <int R>
+struct GvStep {
+  uint4 c[2];   // 16 code bytes of one row per load (row order of the LDS stage)
+  uint4 x[R];   // activation fragments X[16 rt + q][k + 8g .. k + 8g + 7]
+  int q;        // second-level code of the table this lane builds
+  float s2;
+};
+
+// Workgroup (4 waves) = one 128-column strip; wave w covers rows
+// [(split*4 + w) * rpw, +rpw) in steps of 32.  Lane (q, g): columns
+// n0 + 8q .. +7, rows 8g .. 8g+7 of each step.  Per step a wave copies its
+// 2 KB of codes (two 16-byte loads per lane, whole 64-byte row pieces) into
+// its LDS stage, each lane builds one of the step's 64 block tables, and the
+// lane reads its eight 4-byte code words back in MFMA order.  Each weight is
+// one byte-select add and one 16-bit table lookup, pairs packed with v_perm;
+// column t of the lane feeds the MFMA of tile t.  part[split][m][n] = sum of
+// the 4 waves (fixed order).
 // kTwo: two weights of N columns each (the gated block's), `pairs` strip pairs
 // of the first, then of the second; the partials are M x 2N, side by side.
 // R > 1 (kTwo only): a workgroup multiplies each decoded fragment with R tiles

@@ -108,23 +108,6 @@ __device__ __forceinline__ void gemv_zpart(const uint16_t* __restrict__ X, int64
   }
 }
 
-template <int R>
-struct GvStep {
-  uint4 c[2];   // 16 code bytes of one row per load (row order of the LDS stage)
-  uint4 x[R];   // activation fragments X[16 rt + q][k + 8g .. k + 8g + 7]
-  int q;        // second-level code of the table this lane builds
-  float s2;
-};
-
-// Workgroup (4 waves) = one 128-column strip; wave w covers rows
-// [(split*4 + w) * rpw, +rpw) in steps of 32.  Lane (q, g): columns
-// n0 + 8q .. +7, rows 8g .. 8g+7 of each step.  Per step a wave copies its
-// 2 KB of codes (two 16-byte loads per lane, whole 64-byte row pieces) into
-// its LDS stage, each lane builds one of the step's 64 block tables, and the
-// lane reads its eight 4-byte code words back in MFMA order.  Each weight is
-// one byte-select add and one 16-bit table lookup, pairs packed with v_perm;
-// column t of the lane feeds the MFMA of tile t.  part[split][m][n] = sum of
-// the 4 waves (fixed order).
 // Y = sum_s part[s] + c Z B, 16-row tiles.  Workgroup (4 waves) = 512
 // columns, row tile blockIdx.y / 4 and its row phase e; lane (q, g) of wave w owns columns
 // n0 + 128w + 8q .. +7 and row 4g + e.  A workgroup requests at its start
