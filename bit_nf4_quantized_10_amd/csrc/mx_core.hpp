@@ -300,8 +300,8 @@ struct CoreMx {
   // all elements are moved to be scaled and back: 2.6 us a round of 256 x 256 tiles more) and
   // scaled while the next two tiles' are computed: behind 32 vector instructions, the first
   // behind four matrix instructions with their waits, where reading it wants 11 wait states.
-  // 1.1 us a round more than unscaled: 2048 x 8192 x 22016, rank 64, 206 -> 209 us a call,
-  // 4096 x 4096 x 11008, rank 16, 119 -> 122.
+  // 0.8 us a round more than unscaled: 2048 x 8192 x 22016, rank 64, 203 -> 206 us a call,
+  // 4096 x 4096 x 11008, rank 16, 123 -> 126.
   __device__ __forceinline__ void adapter_last(const Adapter& A0, const Adapter& A1, bool more, bool both, f32x16 (&acc)[4][4]) const {
     f32x16 x[3];
 #pragma unroll
@@ -373,6 +373,9 @@ struct CoreMx {
         adapter_add(A0, A1, acc);
         adapter_load(j0, r, A0);
         adapter_load(j0 + 32, r, A1);
+        // here, so that a rank of up to 64 waits below for its own loads alone, not for as many
+        // as this loop would leave under way
+        __builtin_amdgcn_s_waitcnt(waitcnt_imm(0, 15));
       }
       adapter_last(A0, A1, r > 64, r > 32, acc);
     }
