@@ -93,7 +93,7 @@ __device__ __forceinline__ void meet_lds() {
 // r <= 64.  Workgroup: one chunk of the long side; per 64 of it m and u, element by element
 // in the order in memory, u into LDS as [long][rank], and its wave's 16 of the Gram
 // matrix's upper tiles; the next 64 are requested meanwhile.  8192 and 22016 long at rank
-// 64: 13 us for 23 MB read and 15 written (7.5 at a copy's rate), a workgroup a CU of two
+// 64: 13 us for 15.5 MB read and 15.5 written (6 at a copy's rate), a workgroup a CU of two
 // turns; with a branch around every element and nothing requested ahead 17.
 template <int NT, int kGrad, bool kTall>
 __device__ __forceinline__ void muon_gram64(const MuonArgs& p, const MuonJob& J, int64_t blk, float* tile, double* red) {
@@ -182,7 +182,8 @@ __global__ __launch_bounds__(256) void muon_gram64_kernel(MuonArgs p, int64_t fi
   else muon_gram64<NT, kGrad, false>(p, p.j[1], blk - first, tile, red);
 }
 
-// r > 64: m and u, element by element of the filled-up matrix.
+// r > 64: m and u, element by element of the filled-up matrix; 11 us at 8192 and 22016 long,
+// rank 128 (62 MB), 20 at 256: a copy's rate or a little more.
 template <int kGrad>
 __global__ __launch_bounds__(256) void muon_momentum_kernel(MuonArgs p, int64_t first) {
   int64_t blk = blockIdx.x;
@@ -227,7 +228,9 @@ __device__ __forceinline__ void gram_load(const MuonJob& J, int rp, int64_t l0, 
 }
 
 // r > 64.  Workgroup: one 64 x 64 tile pair (I <= J) of the Gram matrix over one chunk; its
-// waves take every fourth 16 and are added in LDS in order.
+// waves take every fourth 16 and are added in LDS in order.  8192 and 22016 long: 29 us at
+// rank 128, 77 at 256, the 64-bit matrix unit busy for 36 and 44 % of it; each pair reads its
+// rows of U again (31 and 124 MB, most of it from the caches).
 __global__ __launch_bounds__(256) void muon_gram_kernel(MuonArgs p, int64_t first) {
   __shared__ double red[64 * 64];
   int64_t blk = blockIdx.x;
@@ -485,7 +488,10 @@ __global__ __launch_bounds__(64) void muon_scale_kernel(MuonArgs p, double* scal
 // X = U Q and the parameters.  Workgroup: 64 of the long side, a wave 16; Q (symmetric, so
 // both layouts read it along its rows) passes through LDS in 64 x 64 pieces.  Bound by
 // memory: u, the parameters and their copies once (27 MB at 8192 and 22016 long, rank 64:
-// 15.5 us, of it two waits for memory and 3.4 us of 64-bit products).
+// 15.5 us, of it two waits for memory and 3.4 us of 64-bit products).  Above rank 64 by its
+// products and what feeds them, 44 us at rank 128 and 150 at 256: the matrix unit busy for 34
+// and 38 % of it, the vector units (u to 64 bits, addresses) for half, u read once per 64 of
+// the rank.
 template <bool kF16, bool kMaster, bool kTall>
 __device__ __forceinline__ void muon_apply(const MuonArgs& p, const MuonJob& J, int64_t blk, const double* Q, double* qs) {
   constexpr int kLd = 65;

@@ -8,7 +8,9 @@
 // W are mxfp4_dequantize's, so are their roundings to fp16.  The adapter's product runs as
 // more steps of the first range, A's rows read as they lie.
 // Bound by the decoding and the waits of two waves a SIMD: 0.6 PFLOP/s at 800 x 4096 x
-// 4096, where the dense product of many tiles reaches 1.4.
+// 4096, where the dense product of many tiles reaches 1.4.  128 x 8192 x 22016 82 us, each
+// block decoded twice, once per 64 rows: vector units 35 %, matrix units 26 %, loads waited
+// for 55 % of the waves' time.
 #include <hip/hip_ext.h>
 
 #include "common.hpp"
@@ -158,8 +160,8 @@ void launch_back_t(const MxBackArgs& p, bool out16, hipStream_t stream, const Ti
 
 // Up to 256 rows, where W's dequantised copy costs most, or 2^33 products.  Whole backward
 // this way and by the dense product, us: 1 row, 4096 x 4096 22 and 44; 128 rows, 8192 x
-// 22016 120 and 237, 256 183 and 263, 400 298 and 303; 777 x 2056 x 1336 45 and 56; 2048^3
-// 57 and 69; 1024 x 4096 x 4096 82 and 84; 333 x 22016 x 2048 99 and 86; 4096 x 512 x 8192
+// 22016 115 and 237, 256 180 and 263, 400 298 and 303; 777 x 2056 x 1336 44 and 56; 2048^3
+// 57 and 69; 1024 x 4096 x 4096 79 and 84; 333 x 22016 x 2048 99 and 86; 4096 x 512 x 8192
 // 115 and 110.
 MxBackPlan plan_mx_back(int64_t M, int64_t K, int64_t N) {
   constexpr int64_t kWgs = 512;   // workgroups wanted: two a CU

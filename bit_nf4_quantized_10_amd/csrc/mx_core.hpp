@@ -19,10 +19,12 @@
 // are not stored.  The adapter's 16-bit product comes first, its few fragments straight
 // from memory while the first stages' copies are under way.
 //
-// Bound by the matrix unit and its power limit in the loop (1.2 us a stage, 4.9 PFLOP/s at a
-// reduction of 16384) and by bare starts and stores around it, about 10 us a round of 256
-// tiles: 4096^3 34 to 36 us (4.0 to 3.8 PFLOP/s), 2048 x 8192 x 22016 171, with an adapter of
-// rank 64 186 (190 with the adapter's loads behind the copies).
+// Bound by the matrix unit and its power limit in the loop and by bare starts and stores
+// around it.  A stage takes 1.7 us with all CUs at work (5.0 PFLOP/s; 4096 x 4096, reductions
+// of 2048 to 32768) and 1.1 with a quarter of them, a round of 256 tiles 8 to 10 us besides:
+// 4096^3 34 to 37 us (4.0 to 3.7 PFLOP/s), a reduction of 16384 117 to 121 (4.6, the matrix
+// unit busy for 76 % of it), 2048 x 8192 x 22016 168; the layer's forward there with an
+// adapter of rank 64 206, X's quantisation and Z among it.
 #pragma once
 
 #include <type_traits>

@@ -159,7 +159,7 @@ __global__ __launch_bounds__(256) void mx_rows_kernel(MxRowsArgs p) {
 // chunks.  Weights go from memory into the wave's own fragments (no other wave wants
 // them), the chunk's activation codes straight into LDS in the order of the fragments;
 // a chunk's loads run while the one before it is multiplied (requested two chunks ahead,
-// the weights gained nothing).  At 100 x 4096 x 11008 (17 us) the multiplications and the
+// the weights gained nothing).  At 100 x 4096 x 11008 (15 us) the multiplications and the
 // LDS reads alone take 9 with the launch, weights, activations and the fp32 planes 2 to 3
 // each.
 __device__ __forceinline__ void copy16(Rsrc r, char* to, uint32_t voff, uint32_t soff) {

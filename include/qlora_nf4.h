@@ -447,13 +447,15 @@ int mxfp4_matmul(int out_type, const mxfp4_t* P, const mxfp4_t* Q, void* C, void
  *   Z = X A,  Y = Q(X) Wᵀ + c Z B
  * with Q(X) the values that mxfp4_quantize keeps of X's rows.  X M x K, A K x r,
  * B r x N, Y M x N, Z M x r (NULL: not returned) of compute_dtype.  Sums are fp32;
- * Z enters in the 16-bit type, and c multiplies the fp32 sum Z B.  Requirements: N % 8 == 0 in place of
+ * Z enters in the 16-bit type, as it is returned, and c multiplies the fp32 sum Z B.
+ * Requirements: N % 8 == 0 in place of
  * N % 64, else qlora_linear_fwd's on sizes; all pointers 16-byte aligned, workspace
  * 256-byte aligned, at least fwd_bytes.
  * The backward, given G = dL/dY, takes the derivative of Q as one (what its rounding
  * drops has none):
  *   dZ = c G Bᵀ,  dA = Xᵀ dZ,  dB = c Zᵀ G,  dX = G W + dZ Aᵀ (skipped when NULL),
- * with W's values in compute_dtype.  Exactly one of X (16 bits) and X8 (an 8-bit
+ * with W's values in compute_dtype; dZ enters dX in that type, dA in two such parts.
+ * Exactly one of X (16 bits) and X8 (an 8-bit
  * checkpoint); Z is required; grad_dtype as in qlora_linear_bwd_ex; workspace at
  * least bwd_bytes.  Outputs overlap neither the inputs nor each other nor the
  * workspace. */
