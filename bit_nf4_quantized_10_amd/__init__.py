@@ -1041,9 +1041,11 @@ def qlora_mx_linear_bwd(G, X, Z, W: MXFP4, A, B, c: float, need_dx: bool = True,
                         dB=None, workspace=None, stream=None):
     """Backward of qlora_mx_linear_fwd with the derivative of Q taken as one:
     dZ = c G Bᵀ, dA = Xᵀ dZ, dB = c Zᵀ G, dX = G W + dZ Aᵀ.  Returns (dX or None,
-    dA, dB).  X may be an Act8.  grad_dtype: of dA and dB, float32 (the default) or
-    G's dtype."""
+    dA, dB).  Z: the forward's.  X may be an Act8.  grad_dtype: of dA and dB, float32 (the
+    default) or G's dtype."""
     dt = _compute_dtype(G)
+    if Z is None:
+        raise ValueError("Z is required: the forward's, with return_z")
     M, (N, K), r = G.shape[0], W.shape, A.shape[1]
     for t, n, shape in ((G, "G", (M, N)), (Z, "Z", (M, r)), (A, "A", (K, r)), (B, "B", (r, N))):
         _require_dense(t, n, dt, *shape)

@@ -160,3 +160,12 @@ def test_workspaces_over_the_whole_range():
                     fwd, bwd = qn.qlora_mx_workspace_bytes(M, K, N, r)
                     assert 0 < fwd < 1 << 34 and 0 < bwd < 1 << 34, (M, K, N, r)
                 assert 0 <= qn.mxfp4_matmul_workspace_bytes(M, N, K) < 1 << 34
+
+
+def test_backward_without_z_says_so():
+    """return_z=False keeps Z from the caller, and the backward does not form it again."""
+    torch = pytest.importorskip("torch")
+    x = torch.zeros(8, 64, dtype=torch.bfloat16)
+    kept = qn.MXFP4(8, 64, torch.zeros(8 * 32, dtype=torch.uint8), torch.zeros(256, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="Z is required"):
+        qn.qlora_mx_linear_bwd(x[:, :8].contiguous(), x, None, kept, x.T.contiguous(), x[:, :8].contiguous(), C)
