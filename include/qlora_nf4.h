@@ -226,9 +226,9 @@ int qlora_sgd_step_dt(int param_dtype, int64_t K, int64_t N, int64_t r, uint16_t
  * anything runs.
  * param_dtype: NF4_COMPUTE_*; grad_dtype: of dA and dB, NF4_AB_F32 or the parameters'
  * type.  Requirements: K, N, r >= 1, r <= 256, K and N <= 2^24, K*r and r*N below 2^29,
- * 0 <= momentum < 1, eps > 0, 0 <= steps <= 32, |a|^(2 steps) <= 2^29, the numbers finite; pointers aligned
- * to their element size; workspace 256-byte aligned, at least *bytes.  NF4_EINVAL
- * otherwise.  No two of the arrays overlap. */
+ * 0 <= momentum < 1, eps > 0, 0 <= steps <= 32, |a|^(2 steps) <= 2^29, the numbers
+ * finite; pointers aligned to their element size; workspace 256-byte aligned, at least
+ * *bytes.  NF4_EINVAL otherwise.  No two of the arrays overlap. */
 #define NF4_MUON_SCALE_NONE     0
 #define NF4_MUON_SCALE_SPECTRAL 1
 #define NF4_MUON_SCALE_RMS      2
@@ -448,9 +448,8 @@ int mxfp4_matmul(int out_type, const mxfp4_t* P, const mxfp4_t* Q, void* C, void
  * with Q(X) the values that mxfp4_quantize keeps of X's rows.  X M x K, A K x r,
  * B r x N, Y M x N, Z M x r (NULL: not returned) of compute_dtype.  Sums are fp32;
  * Z enters in the 16-bit type, as it is returned, and c multiplies the fp32 sum Z B.
- * Requirements: N % 8 == 0 in place of
- * N % 64, else qlora_linear_fwd's on sizes; all pointers 16-byte aligned, workspace
- * 256-byte aligned, at least fwd_bytes.
+ * Requirements: N % 8 == 0 in place of N % 64, else qlora_linear_fwd's on sizes; all
+ * pointers 16-byte aligned, workspace 256-byte aligned, at least fwd_bytes.
  * The backward, given G = dL/dY, takes the derivative of Q as one (what its rounding
  * drops has none):
  *   dZ = c G Bᵀ,  dA = Xᵀ dZ,  dB = c Zᵀ G,  dX = G W + dZ Aᵀ (skipped when NULL),

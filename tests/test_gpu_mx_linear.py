@@ -161,3 +161,26 @@ def test_the_adapter_is_scaled_alike_on_every_path(K, N, r, name, c):
         Y, Z = qn.qlora_mx_linear_fwd(X[:rows].contiguous(), W, A, B, c)
         np.testing.assert_array_equal(host(Z), x[:rows] @ a)
         np.testing.assert_array_equal(host(Y), want[:rows], err_msg=f"{rows} rows")
+
+
+@pytest.mark.parametrize("name", ["bf16", "f16"])
+@pytest.mark.parametrize("r", [8, 32, 40, 64, 72, 128, 136, 200, 256])
+@pytest.mark.parametrize("M,K,N", [(1100, 264, 2056), (257, 2056, 8264)])
+def test_every_rank_by_tiles_in_whole_numbers(M, K, N, r, name):
+    """The adapter's products in parts of 64, the last one of 32 or less: with whole numbers
+    and c = 1/2 every sum is exact."""
+    import torch
+    from tests.test_gpu_mxfp4 import _whole
+    say(f"mx tiles M={M} K={K} N={N} r={r} {name}")
+    rng = np.random.default_rng(M + r)
+    codes, scales = _whole(rng, N, K, 0, 0)
+    W, w = _state(codes, scales, K), oo.mxfp4_values(codes, scales, K)
+    x = rng.integers(-2, 3, size=(M, K)).astype(np.float32)
+    x[:, ::32] = 2.0          # every block's scale is 1/2, and -2 .. 2 are kept as they are
+    a = np.zeros((K, r), dtype=np.float32)
+    a[rng.integers(0, K, size=r), np.arange(r)] = rng.choice([-1.0, 1.0], size=r)
+    b = rng.integers(-3, 4, size=(r, N)).astype(np.float32)
+    Y, Z = qn.qlora_mx_linear_fwd(_dev(x, name), W, _dev(a, name), _dev(b, name), 0.5)
+    z = x.astype(np.float64) @ a
+    np.testing.assert_array_equal(host(Z), z)
+    np.testing.assert_array_equal(host(Y), oo.round16(x @ w.T + 0.5 * (z @ b), name))
